@@ -444,6 +444,154 @@ int wkv7_forward_epilogue(const wkv7_desc *desc, const void *r, const void *w, c
                           const void *g, const wkv7_epilogue_params *params, void *out,
                           float *sT, void *stream);
 
+/*
+ * ---- The short causal convolution and the selective state-space scan ---------
+ * The two operators of a state-space mixing layer, beside the WKV7 recurrence
+ * and its decay-only form ("Paper Review: RWKV-7 Goose", Background information
+ * on delta rule: RWKV-6 and Mamba 2 forget by a diagonal decay): the scan's
+ * transition is diagonal too, but its decay depends on channel, state and token.
+ * At W = 2 without the activation the convolution is the token shift in front
+ * of a time-mixing layer (weight[d] = (mu_d, 1 - mu_d)).
+ *
+ * The conventions at the top of this file hold (device pointers, 16-byte
+ * alignment, row-major layouts without gaps, fp32 states and learned vectors,
+ * asynchronous work on `stream`, synchronous validation that launches nothing
+ * on error), with channels in place of heads: token tensors are [B][T][D].
+ * Work goes to the current device: make the tensors' device current first.
+ * D is any width; widths whose rows hold whole 16-byte (convolution) pieces run
+ * fastest.  Calls share no scratch; a workspace may be used again by a later
+ * call on the same stream, not by two calls that can overlap (two captured
+ * graphs replayed on different streams need one each).
+ *
+ * `lengths` (int32 [B], 4-byte aligned, or NULL = T each) gives the valid
+ * tokens of every batch row, clamped to [0, T]: what the inputs hold at and
+ * behind a row's length (NaN included) is not used, outputs there are 0, and
+ * the state behind the sequence is the one after the row's last valid token.
+ */
+
+/* W: 2, 3 or 4 taps.  silu: 0 or 1. */
+typedef struct {
+    int32_t B, T, D, W;
+    int32_t dtype;      /* wkv7_dtype */
+    int32_t silu;
+} wkv7_conv_desc;
+
+/*
+ * The convolution, per channel d and token t:
+ *     pre_t = bias[d] + sum_k weight[d][k] x_{t-(W-1)+k}
+ *     y_t   = pre_t, or pre_t sigmoid(pre_t) with desc->silu
+ *   weight   fp32 [D][W]; bias fp32 [D] or NULL
+ *   x, y     [B][T][D]
+ *   s0       [B][W-1][D] (dtype) the inputs before the first token, oldest
+ *            first, or NULL (zeros)
+ *   sT       [B][W-1][D] (dtype) the last W - 1 inputs, or NULL
+ */
+int wkv7_conv_forward(const wkv7_conv_desc *desc, const float *weight, const float *bias,
+                      const int32_t *lengths, const void *x, const void *s0, void *y, void *sT,
+                      void *stream);
+
+/* Device scratch of wkv7_conv_backward; 0 on an invalid descriptor. */
+size_t wkv7_conv_backward_workspace_bytes(const wkv7_conv_desc *desc);
+
+/*
+ * Gradients of <dy, y> + <dsT, sT> (dsT NULL = 0): dx [B][T][D] and ds0
+ * [B][W-1][D] (or NULL) in dtype, dweight fp32 [D][W], dbias fp32 [D] (required
+ * with a bias, else NULL).  The sums over tokens and rows are fp32 in a fixed
+ * order: repeated calls agree bit for bit.
+ */
+int wkv7_conv_backward(const wkv7_conv_desc *desc, const float *weight, const float *bias,
+                       const int32_t *lengths, const void *x, const void *s0, const void *dy,
+                       const void *dsT, void *dx, float *dweight, float *dbias, void *ds0,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
+/* One token: x, y [B][D]; state [B][W-1][D] is read and moved on in place
+   (desc->T is ignored).  y may not overlap x or state. */
+int wkv7_conv_step(const wkv7_conv_desc *desc, const float *weight, const float *bias,
+                   const void *x, void *state, void *y, void *stream);
+
+/* N: 8, 16, 32 or 64 states per channel.  G groups of D / G neighbouring
+   channels, each with its own B and C (D a multiple of G).  ckpt_bits: 0 (no
+   checkpoints), 8 or 32. */
+typedef struct {
+    int32_t B, T, D, N, G;
+    int32_t dtype;      /* wkv7_dtype */
+    int32_t ckpt_bits;
+} wkv7_ssm_desc;
+
+/* The learned parts (device pointers to fp32, 16-byte aligned) and settings. */
+typedef struct {
+    const float *A;        /* [D][N], finite; negative for a decaying state */
+    const float *dskip;    /* [D] or NULL: no skip term */
+    const float *dt_bias;  /* [D] or NULL: 0 */
+    const int32_t *lengths;
+    int32_t softplus;      /* 1: D_t = log(1 + exp(dt_t + dt_bias)); 0: dt_t + dt_bias itself */
+} wkv7_ssm_params;
+
+/* Where wkv7_ssm_backward writes. */
+typedef struct {
+    void *dx, *ddt;          /* [B][T][D], dtype */
+    void *dBm, *dCm;         /* [B][T][G][N], dtype */
+    void *dz;                /* [B][T][D], dtype; required with z, else NULL */
+    float *dA;               /* [D][N] */
+    float *ddskip, *ddt_bias;/* [D]; required with dskip / dt_bias, else NULL */
+    float *dh0;              /* [B][D][N] or NULL */
+} wkv7_ssm_grads;
+
+/* Bytes of the checkpoints of the state entering every 16 tokens (entry m: the
+   state before token 16m), NB = ceil(T / 16):
+     ckpt_bits 32   fp32 [B][NB][D][N];
+     ckpt_bits 8    int8 codes [B][NB][D][N], then from the next 16-byte boundary
+                    fp32 scales [B][NB][D]; a state is code * scale.  A channel's
+                    scale is the largest magnitude of its N states over 127 and a
+                    code the nearest whole number (ties to even), so a state is
+                    off by at most half a scale.  Channels below 1e-35 are stored
+                    as 0; one that holds an infinity or a NaN reads back as NaN.
+   0 for ckpt_bits 0 and on an invalid descriptor. */
+size_t wkv7_ssm_ckpt_bytes(const wkv7_ssm_desc *desc);
+
+/* Device scratch of wkv7_ssm_forward (0: none needed) and wkv7_ssm_backward;
+   0 on an invalid descriptor. */
+size_t wkv7_ssm_forward_workspace_bytes(const wkv7_ssm_desc *desc);
+size_t wkv7_ssm_backward_workspace_bytes(const wkv7_ssm_desc *desc);
+
+/*
+ * The scan, per channel d (group g = d / (D / G)) and token t, from h = h0:
+ *     D_t    = softplus(dt_t + dt_bias)              u_t = D_t x_t
+ *     h[n]   = exp(D_t A[d][n]) h[n] + u_t Bm_t[g][n]
+ *     y_t    = (sum_n Cm_t[g][n] h[n] + dskip x_t) * (z_t sigmoid(z_t) with z)
+ *   x, dt, z, y   [B][T][D]; z may be NULL
+ *   Bm, Cm        [B][T][G][N]
+ *   h0, hT        fp32 [B][D][N]: the initial state (NULL = zeros) and the state
+ *                 behind the sequence (or NULL)
+ *   ckpt          required when desc->ckpt_bits is not 0, else NULL
+ * All arithmetic is fp32.
+ */
+int wkv7_ssm_forward(const wkv7_ssm_desc *desc, const wkv7_ssm_params *params, const void *x,
+                     const void *dt, const void *Bm, const void *Cm, const void *z,
+                     const float *h0, void *y, float *hT, void *ckpt, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of <dy, y> + <dhT, hT> (dhT NULL = 0), from the forward's inputs
+ * and its checkpoints (desc->ckpt_bits 8 or 32; h0 is their first entry).  The
+ * states inside a block of 16 tokens are formed again from the block's
+ * checkpoint; with 8 bits the gradients are those of states rounded there, and
+ * dh0 is taken through the rounding unchanged.  Sums run in a fixed order:
+ * repeated calls agree bit for bit.
+ */
+int wkv7_ssm_backward(const wkv7_ssm_desc *desc, const wkv7_ssm_params *params, const void *x,
+                      const void *dt, const void *Bm, const void *Cm, const void *z,
+                      const void *dy, const float *dhT, const void *ckpt,
+                      const wkv7_ssm_grads *grads, void *workspace, size_t workspace_bytes,
+                      void *stream);
+
+/* One token on resident states: x, dt, z, y [B][D], Bm, Cm [B][G][N], state
+   fp32 [B][D][N] read and overwritten.  desc->T and ckpt_bits are ignored;
+   params->lengths must be NULL. */
+int wkv7_ssm_step(const wkv7_ssm_desc *desc, const wkv7_ssm_params *params, const void *x,
+                  const void *dt, const void *Bm, const void *Cm, const void *z, float *state,
+                  void *y, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

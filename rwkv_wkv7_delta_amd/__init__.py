@@ -12,6 +12,12 @@ evolves as ``S <- S (diag(w_t) + a_t b_t^T) + v_t k_t^T`` and ``y_t = S r_t``
 ``a = b = None`` selects the decay-only recurrence ``S <- S diag(w_t) + v_t k_t^T``
 (a = b = 0; RWKV-6-style vector-decay linear attention), with specialised
 kernels that skip the removal terms; its backward returns ``da = db = None``.
+
+Beside the recurrence stand the two operators of a state-space mixing layer
+(``mixers.py``): the short causal convolution (``conv_forward``,
+``conv_backward``, ``conv_step``; at two taps the token shift) and the selective
+scan (``ssm_forward``, ``ssm_backward``, ``ssm_step``), whose training forward
+keeps state checkpoints in 32 or 8 bits.
 """
 
 from __future__ import annotations
@@ -43,7 +49,10 @@ EXPORTED = ("wkv7_abi_version", "wkv7_status_string", "wkv7_tape_bytes", "wkv7_c
             "wkv7_forward_split_static",
             "wkv7_backward", "wkv7_backward_ckpt", "wkv7_backward_adjoint", "wkv7_backward_gradients",
             "wkv7_backward_overlapped", "wkv7_decode_step", "wkv7_epilogue",
-            "wkv7_forward_epilogue")
+            "wkv7_forward_epilogue", "wkv7_conv_forward", "wkv7_conv_backward_workspace_bytes",
+            "wkv7_conv_backward", "wkv7_conv_step", "wkv7_ssm_ckpt_bytes",
+            "wkv7_ssm_forward_workspace_bytes", "wkv7_ssm_backward_workspace_bytes",
+            "wkv7_ssm_forward", "wkv7_ssm_backward", "wkv7_ssm_step")
 
 
 class WKV7Error(RuntimeError):
@@ -69,6 +78,27 @@ WKV7_SPLIT_NONE, WKV7_SPLIT_MAPS, WKV7_SPLIT_SEQUENTIAL = 0, 1, 2
 class Desc(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("H", ctypes.c_int32),
                 ("N", ctypes.c_int32), ("dtype", ctypes.c_int32), ("chunk_len", ctypes.c_int32)]
+
+
+class ConvDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("W", ctypes.c_int32), ("dtype", ctypes.c_int32), ("silu", ctypes.c_int32)]
+
+
+class SsmDesc(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("D", ctypes.c_int32),
+                ("N", ctypes.c_int32), ("G", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("ckpt_bits", ctypes.c_int32)]
+
+
+class SsmParams(ctypes.Structure):
+    _fields_ = [("A", ctypes.c_void_p), ("dskip", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p),
+                ("lengths", ctypes.c_void_p), ("softplus", ctypes.c_int32)]
+
+
+class SsmGradPointers(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_void_p) for name in
+                ("dx", "ddt", "dBm", "dCm", "dz", "dA", "ddskip", "ddt_bias", "dh0")]
 
 
 _lib = None
@@ -126,6 +156,21 @@ def lib():
         L.wkv7_epilogue.restype = ctypes.c_int
         L.wkv7_forward_epilogue.argtypes = [D] + [P] * 7 + [P, E, P, P, P]
         L.wkv7_forward_epilogue.restype = ctypes.c_int
+        CD, SD = ctypes.POINTER(ConvDesc), ctypes.POINTER(SsmDesc)
+        SP, SG = ctypes.POINTER(SsmParams), ctypes.POINTER(SsmGradPointers)
+        for name, args, res in (
+                ("wkv7_conv_forward", [CD] + [P] * 8, ctypes.c_int),
+                ("wkv7_conv_backward_workspace_bytes", [CD], Z),
+                ("wkv7_conv_backward", [CD] + [P] * 11 + [P, Z, P], ctypes.c_int),
+                ("wkv7_conv_step", [CD] + [P] * 6, ctypes.c_int),
+                ("wkv7_ssm_ckpt_bytes", [SD], Z),
+                ("wkv7_ssm_forward_workspace_bytes", [SD], Z),
+                ("wkv7_ssm_backward_workspace_bytes", [SD], Z),
+                ("wkv7_ssm_forward", [SD, SP] + [P] * 9 + [P, Z, P], ctypes.c_int),
+                ("wkv7_ssm_backward", [SD, SP] + [P] * 8 + [SG, P, Z, P], ctypes.c_int),
+                ("wkv7_ssm_step", [SD, SP] + [P] * 8, ctypes.c_int)):
+            fn = getattr(L, name)
+            fn.argtypes, fn.restype = args, res
         _lib = L
     return _lib
 
@@ -436,3 +481,7 @@ def decode_step(r, w, k, v, a, b, state, out=None):
     if st != WKV7_OK:
         raise WKV7Error(st, "wkv7_decode_step")
     return y
+
+
+from .mixers import (SsmGrads, conv_backward, conv_forward, conv_step, ssm_backward,  # noqa: E402,F401
+                     ssm_ckpt_bytes, ssm_forward, ssm_split_ckpt, ssm_step)

@@ -21,7 +21,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["wkv7_api.cpp", "wkv7_seq.hip", "wkv7_chunk_fwd.hip", "wkv7_bwd.hip", "wkv7_static.hip",
-           "wkv7_epilogue.hip", "wkv7_chunk128.hip"]
+           "wkv7_epilogue.hip", "wkv7_chunk128.hip", "wkv7_ssm_api.cpp", "wkv7_ssm.hip",
+           "wkv7_ssm_bwd.hip", "wkv7_conv.hip"]
 
 COMMON = [
     f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC",

@@ -1,0 +1,400 @@
+// wkv7_conv.hip -- the short causal convolution along a sequence: prompts
+// (forward), gradients, single tokens.
+//
+// Per channel d with W = 2, 3 or 4 taps:
+//   pre_t = bias + sum_k weight[d][k] x_{t-(W-1)+k},   y_t = pre_t, or pre_t sigmoid(pre_t)
+// with the W - 1 inputs before the first token from a state (zero without one);
+// the state behind the sequence is its last W - 1 inputs.  W = 2 without the
+// activation is a token shift (each channel mixes the previous token in).
+//
+// Bound by HBM: every kernel reads each token tensor once and writes each
+// output once.  A thread owns a few neighbouring channels (16 bytes of a row
+// where the width allows; rows of other widths element by element) and steps
+// along a run of tokens with the last W - 1 inputs in registers, so that a
+// token row is read by one run only, but for the W - 1 rows before a run.
+// fp32 arithmetic, outputs rounded once.
+
+#include "wkv7_ssm_device.h"
+#include "wkv7_ssm_internal.h"
+
+namespace wkv7 {
+
+namespace {
+
+constexpr int kConvThreads = 256;
+
+// Weights of the thread's channels, transposed to taps; zero behind the width.
+template <int W, int V>
+__device__ __forceinline__ void load_weights(const ConvArgs& p, int c, float (&w)[W][V], float (&bias)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const bool in = c + i < p.D;
+        const size_t at = (size_t)(in ? c + i : 0);
+#pragma unroll
+        for (int k = 0; k < W; ++k) w[k][i] = in ? p.weight[at * W + k] : 0.f;
+        bias[i] = in && p.bias ? p.bias[at] : 0.f;
+    }
+}
+
+// Input number t of batch row b (t in [1 - W, T)): the state before the first
+// token.  The loaded piece holds valid memory's values for any t in that range.
+template <typename T, int W, int V, bool kVec>
+__device__ __forceinline__ void load_input(const ConvArgs& p, int b, int t, int c, Piece<T, V>& r, bool& zero) {
+    const T* const X = static_cast<const T*>(p.x);
+    const T* const S0 = static_cast<const T*>(p.s0);
+    zero = t < 0 && !S0;
+    if (t >= 0 || !S0) {
+        r.template load<kVec>(X + ((size_t)b * p.T + (t > 0 ? t : 0)) * p.D, c, p.D);
+    } else {
+        r.template load<kVec>(S0 + ((size_t)b * (W - 1) + (t + W - 1)) * p.D, c, p.D);
+    }
+}
+
+template <typename T, int W, int V, bool kVec>
+__global__ __launch_bounds__(kConvThreads) void conv_fwd_kernel(const ConvArgs p, unsigned cols, unsigned runs,
+                                                               int run, unsigned items) {
+    const unsigned id = blockIdx.x * kConvThreads + threadIdx.x;
+    if (id >= items) return;
+    const unsigned rr = id / cols;
+    const int c = (int)(id % cols) * V;
+    const int b = (int)(rr / runs), t0 = (int)(rr % runs) * run;
+    const int t1 = t0 + run < p.T ? t0 + run : p.T;
+    const int len = row_length(p.lengths, b, p.T);
+    float w[W][V], bias[V], hist[W - 1][V];
+    load_weights<W, V>(p, c, w, bias);
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) {
+        Piece<T, V> r;
+        bool zero;
+        load_input<T, W, V, kVec>(p, b, t0 - (W - 1) + k, c, r, zero);
+        const bool keep = !zero && t0 - (W - 1) + k < len;
+#pragma unroll
+        for (int i = 0; i < V; ++i) hist[k][i] = keep ? r.get(i) : 0.f;
+    }
+    const T* xp = static_cast<const T*>(p.x) + ((size_t)b * p.T + t0) * p.D;
+    T* yp = static_cast<T*>(p.y) + ((size_t)b * p.T + t0) * p.D;
+    constexpr int U = 4;   // rows loaded together
+    for (int t = t0; t < t1; t += U) {
+        Piece<T, V> r[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            r[u].template load<kVec>(xp + (size_t)(t + u < t1 ? u : t1 - 1 - t) * p.D, c, p.D);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (t + u < t1) {
+                const bool in = t + u < len;
+                float out[V];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float x = r[u].get(i);
+                    float pre = bias[i];
+#pragma unroll
+                    for (int k = 0; k < W - 1; ++k) pre = fmaf(w[k][i], hist[k][i], pre);
+                    pre = fmaf(w[W - 1][i], x, pre);
+#pragma unroll
+                    for (int k = 0; k + 1 < W - 1; ++k) hist[k][i] = hist[k + 1][i];
+                    hist[W - 2][i] = x;
+                    if (p.silu) pre *= sigmoid(pre);
+                    out[i] = in ? pre : 0.f;
+                }
+                store_piece<kVec>(yp + (size_t)u * p.D, c, p.D, out);
+            }
+        }
+        xp += (size_t)U * p.D;
+        yp += (size_t)U * p.D;
+    }
+}
+
+// The state behind each row: its last W - 1 inputs, copied (one thread per
+// channel; also the whole answer when there are no tokens).
+template <typename T, int W>
+__global__ __launch_bounds__(kConvThreads) void conv_state_kernel(const ConvArgs p) {
+    const int64_t id = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
+    if (id >= (int64_t)p.B * (W - 1) * p.D) return;
+    const int c = (int)(id % p.D);
+    const int k = (int)(id / p.D % (W - 1)), b = (int)(id / p.D / (W - 1));
+    const int t = row_length(p.lengths, b, p.T) - (W - 1) + k;
+    T v = 0;
+    if (t >= 0) v = static_cast<const T*>(p.x)[((size_t)b * p.T + t) * p.D + c];
+    else if (p.s0) v = static_cast<const T*>(p.s0)[((size_t)b * (W - 1) + t + W - 1) * p.D + c];
+    static_cast<T*>(p.sT)[id] = v;
+}
+
+// One token: y from the state and the input, the state moved on in place.
+template <typename T, int W, int V, bool kVec>
+__global__ __launch_bounds__(kConvThreads) void conv_step_kernel(const ConvArgs p, unsigned cols, unsigned items) {
+    const unsigned id = blockIdx.x * kConvThreads + threadIdx.x;
+    if (id >= items) return;
+    const int c = (int)(id % cols) * V;
+    const size_t b = id / cols;
+    float w[W][V], bias[V], in[W][V], out[V];
+    Piece<T, V> r[W];
+    T* const S = static_cast<T*>(p.sT) + b * (W - 1) * p.D;
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) r[k].template load<kVec>(S + (size_t)k * p.D, c, p.D);
+    r[W - 1].template load<kVec>(static_cast<const T*>(p.x) + b * p.D, c, p.D);
+    load_weights<W, V>(p, c, w, bias);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        float pre = bias[i];
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            in[k][i] = r[k].get(i);
+            pre = fmaf(w[k][i], in[k][i], pre);
+        }
+        out[i] = p.silu ? pre * sigmoid(pre) : pre;
+    }
+#pragma unroll
+    for (int k = 0; k < W - 1; ++k) store_piece<kVec>(S + (size_t)k * p.D, c, p.D, in[k + 1]);
+    store_piece<kVec>(static_cast<T*>(p.y) + b * p.D, c, p.D, out);
+}
+
+// Gradients.  e_t = dy_t, times the activation's slope at pre_t:
+//   dx_t = sum_k weight[k] e_{t+(W-1)-k} (+ dsT where x_t is in the last state)
+//   dweight[k] = sum_t e_t x_{t-(W-1)+k},   dbias = sum_t e_t
+// A wave takes 64 column pieces of one run of tokens, a workgroup four runs; a
+// run steps W - 1 tokens past its end for the e that its last dx need, and the
+// first run of a row W - 1 tokens before the first for ds0.  The sums over a
+// run stay in registers; the workgroup's four meet in LDS, the workgroups in a
+// second kernel, in a fixed order.
+template <typename T, int W, int V, bool kVec>
+__global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvBwdArgs q, unsigned cblocks, int runs) {
+    constexpr int R = kConvThreads / 64, M = W + 1;
+    __shared__ float s_part[R][M][64 * V];
+    const ConvArgs& p = q.f;
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const unsigned cb = blockIdx.x % cblocks, part = blockIdx.x / cblocks;
+    const int c = (int)(cb * 64 + lane) * V;
+    const int64_t r0 = (int64_t)part * R + wave;
+    const bool some = c < p.D && r0 < (int64_t)p.B * runs;
+    float w[W][V], bias[V], dw[W][V], db[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        db[i] = 0.f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) dw[k][i] = 0.f;
+    }
+    if (some) {
+        const int b = (int)(r0 / runs), rr = (int)(r0 % runs);
+        const int t0 = rr * q.run, t1 = t0 + q.run < p.T ? t0 + q.run : p.T;
+        const int len = row_length(p.lengths, b, p.T);
+        const T* const X = static_cast<const T*>(p.x) + (size_t)b * p.T * p.D;
+        const T* const DY = static_cast<const T*>(q.dy) + (size_t)b * p.T * p.D;
+        load_weights<W, V>(p, c, w, bias);
+        float hist[W - 1][V];   // x of the W - 1 tokens before t
+        float eh[W - 1][V];     // e of the W - 1 tokens before t
+#pragma unroll
+        for (int k = 0; k < W - 1; ++k) {
+            Piece<T, V> r;
+            bool zero;
+            load_input<T, W, V, kVec>(p, b, t0 - (W - 1) + k, c, r, zero);
+            const bool keep = !zero && t0 - (W - 1) + k < len;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                hist[k][i] = keep ? r.get(i) : 0.f;
+                eh[k][i] = 0.f;
+            }
+        }
+        // Token t gives dx of input t - (W - 1): inputs before t0 belong to the
+        // run before (or, in a row's first run, to the state).
+        const int stop = t1 + W - 1;
+        constexpr int U = 4;
+        for (int t = t0; t < stop; t += U) {
+            Piece<T, V> rx[U], ry[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const size_t row = (size_t)(t + u < p.T ? t + u : p.T - 1) * p.D;
+                rx[u].template load<kVec>(X + row, c, p.D);
+                ry[u].template load<kVec>(DY + row, c, p.D);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int tt = t + u;
+                if (tt < stop) {
+                    const bool in = tt < len, own = in && tt < t1;
+                    const int src = tt - (W - 1);
+                    float g[V];
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        const float x = in ? rx[u].get(i) : 0.f;
+                        float e = in ? ry[u].get(i) : 0.f;
+                        if (p.silu) {
+                            float pre = bias[i];
+#pragma unroll
+                            for (int k = 0; k < W - 1; ++k) pre = fmaf(w[k][i], hist[k][i], pre);
+                            pre = fmaf(w[W - 1][i], x, pre);
+                            const float s = sigmoid(pre);
+                            e = in ? e * (s * fmaf(pre, 1.f - s, 1.f)) : 0.f;
+                        }
+                        const float eo = own ? e : 0.f;
+#pragma unroll
+                        for (int k = 0; k < W - 1; ++k) dw[k][i] = fmaf(eo, hist[k][i], dw[k][i]);
+                        dw[W - 1][i] = fmaf(eo, x, dw[W - 1][i]);
+                        db[i] += eo;
+                        // x_{tt-(W-1)} meets tap W-1 at its own token, tap 0 at tt.
+                        float s = w[0][i] * e;
+#pragma unroll
+                        for (int k = 0; k < W - 1; ++k) s = fmaf(w[W - 1 - k][i], eh[k][i], s);
+                        g[i] = s;
+#pragma unroll
+                        for (int k = 0; k + 1 < W - 1; ++k) {
+                            hist[k][i] = hist[k + 1][i];
+                            eh[k][i] = eh[k + 1][i];
+                        }
+                        hist[W - 2][i] = x;
+                        eh[W - 2][i] = e;
+                    }
+                    const bool past = src < 0;   // an input of the state
+                    if (src >= t0 || (past && rr == 0)) {
+                        // Inputs len - (W-1) .. len - 1 are the last state's.
+                        const int k = src - (len - (W - 1));
+                        if (q.dsT && k >= 0 && src < len) {
+                            Piece<T, V> r;
+                            r.template load<kVec>(static_cast<const T*>(q.dsT) + ((size_t)b * (W - 1) + k) * p.D, c, p.D);
+#pragma unroll
+                            for (int i = 0; i < V; ++i) g[i] += r.get(i);
+                        }
+                        if (!past) {
+                            if (src >= len) {
+#pragma unroll
+                                for (int i = 0; i < V; ++i) g[i] = 0.f;
+                            }
+                            store_piece<kVec>(static_cast<T*>(q.dx) + ((size_t)b * p.T + src) * p.D, c, p.D, g);
+                        } else if (q.ds0) {
+                            store_piece<kVec>(static_cast<T*>(q.ds0) + ((size_t)b * (W - 1) + src + W - 1) * p.D, c,
+                                              p.D, g);
+                        }
+                    }
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+#pragma unroll
+        for (int k = 0; k < W; ++k) s_part[wave][k][lane * V + i] = dw[k][i];
+        s_part[wave][W][lane * V + i] = db[i];
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < 64 * V * M; e += kConvThreads) {
+        const int cc = e / M, k = e % M;
+        const int ch = (int)(cb * 64 * V) + cc;
+        if (ch < p.D) {
+            float s = 0.f;
+#pragma unroll
+            for (int r = 0; r < R; ++r) s += s_part[r][k][cc];
+            q.part[((size_t)part * p.D + ch) * M + k] = s;
+        }
+    }
+}
+
+// dweight and dbias: the sum over the parts, in order.  A workgroup takes 16
+// elements of [D][W + 1], 16 lanes of parts each.
+template <int W>
+__global__ __launch_bounds__(256) void conv_params_kernel(const float* __restrict__ part, int parts, int D,
+                                                          float* dweight, float* dbias) {
+    constexpr int M = W + 1;
+    __shared__ float s_sum[16][17];
+    const size_t total = (size_t)D * M;
+    const int l = threadIdx.x % 16, k = threadIdx.x / 16;
+    const size_t e = (size_t)blockIdx.x * 16 + l;
+    float s = 0.f;
+    if (e < total)
+        for (int i = k; i < parts; i += 16) s += part[i * total + e];
+    s_sum[k][l] = s;
+    __syncthreads();
+    if (k == 0 && e < total) {
+        for (int i = 1; i < 16; ++i) s += s_sum[i][l];
+        const size_t c = e / M, t = e % M;
+        if (t < W) dweight[c * W + t] = s;
+        else if (dbias) dbias[c] = s;
+    }
+}
+
+constexpr int kRun = 16;   // tokens of a forward run
+
+template <typename T, int W, int V, bool kVec>
+hipError_t fwd_v(const ConvArgs& p, hipStream_t stream) {
+    const unsigned cols = (unsigned)((p.D + V - 1) / V), runs = (unsigned)((p.T + kRun - 1) / kRun);
+    const uint64_t items = (uint64_t)cols * runs * p.B;
+    if (items == 0) return hipSuccess;
+    if (items > (1ull << 31)) return hipErrorInvalidValue;
+    const unsigned grid = (unsigned)((items + kConvThreads - 1) / kConvThreads);
+    conv_fwd_kernel<T, W, V, kVec><<<grid, kConvThreads, 0, stream>>>(p, cols, runs, kRun, (unsigned)items);
+    return hipGetLastError();
+}
+
+template <typename T, int W, int V, bool kVec>
+hipError_t step_v(const ConvArgs& p, hipStream_t stream) {
+    const unsigned cols = (unsigned)((p.D + V - 1) / V);
+    const uint64_t items = (uint64_t)cols * p.B;
+    if (items > (1ull << 31)) return hipErrorInvalidValue;
+    const unsigned grid = (unsigned)((items + kConvThreads - 1) / kConvThreads);
+    conv_step_kernel<T, W, V, kVec><<<grid, kConvThreads, 0, stream>>>(p, cols, (unsigned)items);
+    return hipGetLastError();
+}
+
+template <typename T, int W, int V, bool kVec>
+hipError_t bwd_v(const ConvBwdArgs& q, hipStream_t stream) {
+    const ConvArgs& p = q.f;
+    const unsigned cblocks = (unsigned)((p.D + 64 * V - 1) / (64 * V));
+    const int runs = (p.T + q.run - 1) / q.run;
+    if ((uint64_t)cblocks * q.parts > (1ull << 30)) return hipErrorInvalidValue;
+    conv_bwd_kernel<T, W, V, kVec><<<dim3(cblocks * q.parts), kConvThreads, 0, stream>>>(q, cblocks, runs);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const size_t total = (size_t)p.D * (W + 1);
+    conv_params_kernel<W><<<dim3((unsigned)((total + 15) / 16)), 256, 0, stream>>>(q.part, q.parts, p.D, q.dweight,
+                                                                                q.dbias);
+    return hipGetLastError();
+}
+
+// The gradient of the state when there are no tokens: sT = s0.
+template <typename T>
+__global__ __launch_bounds__(kConvThreads) void conv_pass_kernel(const T* __restrict__ from, T* to, uint64_t n) {
+    const uint64_t id = (uint64_t)blockIdx.x * kConvThreads + threadIdx.x;
+    if (id < n) to[id] = from ? from[id] : (T)0;
+}
+
+template <typename T, int W>
+hipError_t fwd_w(const ConvArgs& p, hipStream_t stream) {
+    constexpr int V = 16 / sizeof(T);
+    hipError_t e = p.D % V == 0 ? fwd_v<T, W, V, true>(p, stream) : fwd_v<T, W, 1, true>(p, stream);
+    if (e != hipSuccess || !p.sT) return e;
+    const uint64_t n = (uint64_t)p.B * (W - 1) * p.D;
+    conv_state_kernel<T, W><<<dim3((unsigned)((n + kConvThreads - 1) / kConvThreads)), kConvThreads, 0, stream>>>(p);
+    return hipGetLastError();
+}
+template <typename T, int W>
+hipError_t step_w(const ConvArgs& p, hipStream_t stream) {
+    constexpr int V = 16 / sizeof(T);
+    return p.D % V == 0 ? step_v<T, W, V, true>(p, stream) : step_v<T, W, 1, true>(p, stream);
+}
+template <typename T, int W>
+hipError_t bwd_w(const ConvBwdArgs& q, hipStream_t stream) {
+    constexpr int V = 4;
+    const uint64_t n = (uint64_t)q.f.B * (W - 1) * q.f.D;
+    if (q.f.T == 0 && q.ds0 && n > 0) {
+        conv_pass_kernel<T><<<dim3((unsigned)((n + kConvThreads - 1) / kConvThreads)), kConvThreads, 0, stream>>>(
+            static_cast<const T*>(q.dsT), static_cast<T*>(q.ds0), n);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return q.f.D % V == 0 ? bwd_v<T, W, V, true>(q, stream) : bwd_v<T, W, 1, true>(q, stream);
+}
+
+}  // namespace
+
+#define WKV7_CONV_DISPATCH(fn, p, q)                                                          \
+    switch ((p).W) {                                                                          \
+        case 2: return (p).bf16 ? fn<bf16_t, 2>(q, stream) : fn<float, 2>(q, stream);         \
+        case 3: return (p).bf16 ? fn<bf16_t, 3>(q, stream) : fn<float, 3>(q, stream);         \
+        case 4: return (p).bf16 ? fn<bf16_t, 4>(q, stream) : fn<float, 4>(q, stream);         \
+        default: return hipErrorInvalidValue;                                                 \
+    }
+
+hipError_t launch_conv_forward(const ConvArgs& p, hipStream_t stream) { WKV7_CONV_DISPATCH(fwd_w, p, p) }
+hipError_t launch_conv_step(const ConvArgs& p, hipStream_t stream) { WKV7_CONV_DISPATCH(step_w, p, p) }
+hipError_t launch_conv_backward(const ConvBwdArgs& q, hipStream_t stream) { WKV7_CONV_DISPATCH(bwd_w, q.f, q) }
+
+}  // namespace wkv7

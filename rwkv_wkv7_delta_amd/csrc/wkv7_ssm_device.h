@@ -1,0 +1,171 @@
+// wkv7_ssm_device.h -- device helpers of the selective scan and the short
+// causal convolution.
+#pragma once
+
+#include "wkv7_device.h"
+
+namespace wkv7 {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+__device__ __forceinline__ float exp2_raw(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float exp_raw(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+__device__ __forceinline__ float sigmoid(float x) {
+    return __builtin_amdgcn_rcpf(1.f + exp_raw(-x));
+}
+
+// log(1 + exp(x)).  With e = exp(x) and u = fl(1 + e), log(u) e / (u - 1) is
+// log(1 + e) to a few rounding errors for every e: the error of u cancels
+// between the logarithm and u - 1 (which is exact).  Above 20, x itself to
+// fp32 rounding.
+__device__ __forceinline__ float softplus(float x) {
+    const float e = exp_raw(fminf(x, 20.f));
+    const float u = 1.f + e;
+    const float l = u == 1.f ? e : __builtin_amdgcn_logf(u) * kLn2 * (e * __builtin_amdgcn_rcpf(u - 1.f));
+    return x > 20.f ? x : (x != x ? x : l);
+}
+
+// V consecutive elements of a token row as loaded, so that a prefetch does not
+// wait for them.  kVec: whole pieces at their natural alignment (c a multiple
+// of V, clamped into the row by the caller's limit); else element by element,
+// every address clamped to lim - 1.
+template <typename T, int V>
+struct Piece {
+    static constexpr int kBytes = V * (int)sizeof(T);
+    static constexpr int kWords = (kBytes + 3) / 4;
+    uint32_t w[kWords];
+
+    template <bool kVec>
+    __device__ __forceinline__ void load(const T* row, int c, int lim) {
+        if constexpr (kVec) {
+            const T* p = row + (c < lim ? c : lim - V);
+            if constexpr (kBytes == 2) {
+                w[0] = *reinterpret_cast<const uint16_t*>(p);
+            } else if constexpr (kBytes == 4) {
+                w[0] = *reinterpret_cast<const uint32_t*>(p);
+            } else if constexpr (kBytes == 8) {
+                const uint2 u = *reinterpret_cast<const uint2*>(p);
+                w[0] = u.x; w[1] = u.y;
+            } else {
+#pragma unroll
+                for (int i = 0; i < kWords; i += 4) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
+                    w[i] = u.x; w[i + 1] = u.y; w[i + 2] = u.z; w[i + 3] = u.w;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int k = c + i < lim ? c + i : lim - 1;
+                if constexpr (sizeof(T) == 4) {
+                    w[i] = __float_as_uint(row[k]);
+                } else if (i % 2 == 0) {
+                    w[i / 2] = row[k];
+                } else {
+                    w[i / 2] |= (uint32_t)row[k] << 16;
+                }
+            }
+        }
+    }
+    __device__ __forceinline__ float get(int i) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else return i % 2 == 0 ? bf16_lo(w[i / 2]) : bf16_hi(w[i / 2]);
+    }
+};
+
+template <bool kVec, int V>
+__device__ __forceinline__ void store_piece(float* row, int c, int lim, const float (&x)[V]) {
+    if constexpr (kVec && V % 4 == 0) {
+        if (c < lim) {
+#pragma unroll
+            for (int i = 0; i < V; i += 4)
+                *reinterpret_cast<float4*>(row + c + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        }
+    } else if constexpr (kVec && V == 2) {
+        if (c < lim) *reinterpret_cast<float2*>(row + c) = make_float2(x[0], x[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (c + i < lim) row[c + i] = x[i];
+    }
+}
+template <bool kVec, int V>
+__device__ __forceinline__ void store_piece(bf16_t* row, int c, int lim, const float (&x)[V]) {
+    if constexpr (kVec && V == 8) {
+        if (c < lim)
+            *reinterpret_cast<uint4*>(row + c) =
+                make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                           pack_bf16x2(x[6], x[7]));
+    } else if constexpr (kVec && V == 4) {
+        if (c < lim)
+            *reinterpret_cast<uint2*>(row + c) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+    } else if constexpr (kVec && V == 2) {
+        if (c < lim) *reinterpret_cast<uint32_t*>(row + c) = pack_bf16x2(x[0], x[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            if (c + i < lim) row[c + i] = f2bf(x[i]);
+    }
+}
+
+// Sum and maximum over each aligned group of P = 2, 4, 8 or 16 lanes, in every lane.
+template <int P>
+__device__ __forceinline__ float group_sum(float x) {
+    if constexpr (P == 2) return x + __builtin_amdgcn_update_dpp(0.0f, x, 0xB1, 0xF, 0xF, false);
+    else return lanes_sum<P>(x);
+}
+template <int P>
+__device__ __forceinline__ float group_max(float x) {
+    x = fmaxf(x, __builtin_amdgcn_update_dpp(0.0f, x, 0xB1, 0xF, 0xF, false));
+    if (P >= 4) x = fmaxf(x, __builtin_amdgcn_update_dpp(0.0f, x, 0x4E, 0xF, 0xF, false));
+    if (P >= 8) x = fmaxf(x, __builtin_amdgcn_update_dpp(0.0f, x, 0x141, 0xF, 0xF, false));
+    if (P >= 16) x = fmaxf(x, __builtin_amdgcn_update_dpp(0.0f, x, 0x140, 0xF, 0xF, false));
+    return x;
+}
+
+// Valid tokens of batch row b: lengths[b] clamped to [0, T], or T.
+__device__ __forceinline__ int row_length(const int32_t* lengths, int b, int T) {
+    if (!lengths) return T;
+    const int n = lengths[b];
+    return n < 0 ? 0 : n > T ? T : n;
+}
+
+// ---- state checkpoints --------------------------------------------------------
+// 32 bits: fp32 [B][blocks][D][N].  8 bits: int8 codes of the same shape, then,
+// from a 16-byte boundary, fp32 scales [B][blocks][D]: one scale for the N
+// states of a channel, its largest magnitude over 127, so a code is off by at
+// most half a scale.  A row whose largest magnitude is below 1e-35 is stored as
+// zeros; one that holds an infinity or a NaN gets a NaN scale, so what is read
+// back is NaN and never plausible.
+__device__ __forceinline__ size_t ckpt_scale_offset(size_t codes) { return (codes + 15) / 16 * 16; }
+
+// Four states of a channel whose N states lie over P lanes: the codes packed
+// into a word, and the scale.
+template <int P>
+__device__ __forceinline__ uint32_t encode8(const float (&h)[4], float& scale) {
+    float m = 0.f, bad = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        m = fmaxf(m, fabsf(h[i]));
+        bad = fmaf(h[i], 0.f, bad);   // NaN if any of them is not finite
+    }
+    m = group_max<P>(m);
+    bad = group_sum<P>(bad);
+    const bool some = m >= 1e-35f && bad == 0.f;
+    const float inv = some ? 127.f / m : 0.f;
+    scale = bad == 0.f ? (some ? m / 127.f : 0.f) : bad;
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int q = some ? (int)rintf(h[i] * inv) : 0;
+        w |= (uint32_t)(q & 0xff) << (8 * i);
+    }
+    return w;
+}
+__device__ __forceinline__ void decode8(uint32_t w, float scale, float (&h)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = (float)(int8_t)(w >> (8 * i)) * scale;
+}
+
+}  // namespace wkv7
