@@ -39,14 +39,14 @@ __device__ __forceinline__ void load_weights(const ConvArgs& p, int c, float (&w
 // Input number t of batch row b (t in [1 - W, T)): the state before the first
 // token.  The loaded piece holds valid memory's values for any t in that range.
 template <typename T, int W, int V, bool kVec>
-__device__ __forceinline__ void load_input(const ConvArgs& p, int b, int t, int c, Piece<T, V>& r, bool& zero) {
+__device__ __forceinline__ void load_input(const ConvArgs& p, int b, int t, int c, Piece<T, V, kVec>& r, bool& zero) {
     const T* const X = static_cast<const T*>(p.x);
     const T* const S0 = static_cast<const T*>(p.s0);
     zero = t < 0 && !S0;
     if (t >= 0 || !S0) {
-        r.template load<kVec>(X + ((size_t)b * p.T + (t > 0 ? t : 0)) * p.D, c, p.D);
+        r.load(X + ((size_t)b * p.T + (t > 0 ? t : 0)) * p.D, c, p.D);
     } else {
-        r.template load<kVec>(S0 + ((size_t)b * (W - 1) + (t + W - 1)) * p.D, c, p.D);
+        r.load(S0 + ((size_t)b * (W - 1) + (t + W - 1)) * p.D, c, p.D);
     }
 }
 
@@ -64,7 +64,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_fwd_kernel(const ConvArgs p
     load_weights<W, V>(p, c, w, bias);
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
-        Piece<T, V> r;
+        Piece<T, V, kVec> r;
         bool zero;
         load_input<T, W, V, kVec>(p, b, t0 - (W - 1) + k, c, r, zero);
         const bool keep = !zero && t0 - (W - 1) + k < len;
@@ -75,10 +75,10 @@ __global__ __launch_bounds__(kConvThreads) void conv_fwd_kernel(const ConvArgs p
     T* yp = static_cast<T*>(p.y) + ((size_t)b * p.T + t0) * p.D;
     constexpr int U = 4;   // rows loaded together
     for (int t = t0; t < t1; t += U) {
-        Piece<T, V> r[U];
+        Piece<T, V, kVec> r[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            r[u].template load<kVec>(xp + (size_t)(t + u < t1 ? u : t1 - 1 - t) * p.D, c, p.D);
+            r[u].load(xp + (size_t)(t + u < t1 ? u : t1 - 1 - t) * p.D, c, p.D);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (t + u < t1) {
@@ -128,11 +128,11 @@ __global__ __launch_bounds__(kConvThreads) void conv_step_kernel(const ConvArgs 
     const int c = (int)(id % cols) * V;
     const size_t b = id / cols;
     float w[W][V], bias[V], in[W][V], out[V];
-    Piece<T, V> r[W];
+    Piece<T, V, kVec> r[W];
     T* const S = static_cast<T*>(p.sT) + b * (W - 1) * p.D;
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) r[k].template load<kVec>(S + (size_t)k * p.D, c, p.D);
-    r[W - 1].template load<kVec>(static_cast<const T*>(p.x) + b * p.D, c, p.D);
+    for (int k = 0; k < W - 1; ++k) r[k].load(S + (size_t)k * p.D, c, p.D);
+    r[W - 1].load(static_cast<const T*>(p.x) + b * p.D, c, p.D);
     load_weights<W, V>(p, c, w, bias);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -185,7 +185,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvBwdArg
         float eh[W - 1][V];     // e of the W - 1 tokens before t
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) {
-            Piece<T, V> r;
+            Piece<T, V, kVec> r;
             bool zero;
             load_input<T, W, V, kVec>(p, b, t0 - (W - 1) + k, c, r, zero);
             const bool keep = !zero && t0 - (W - 1) + k < len;
@@ -200,12 +200,12 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvBwdArg
         const int stop = t1 + W - 1;
         constexpr int U = 4;
         for (int t = t0; t < stop; t += U) {
-            Piece<T, V> rx[U], ry[U];
+            Piece<T, V, kVec> rx[U], ry[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const size_t row = (size_t)(t + u < p.T ? t + u : p.T - 1) * p.D;
-                rx[u].template load<kVec>(X + row, c, p.D);
-                ry[u].template load<kVec>(DY + row, c, p.D);
+                rx[u].load(X + row, c, p.D);
+                ry[u].load(DY + row, c, p.D);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -249,8 +249,8 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvBwdArg
                         // Inputs len - (W-1) .. len - 1 are the last state's.
                         const int k = src - (len - (W - 1));
                         if (q.dsT && k >= 0 && src < len) {
-                            Piece<T, V> r;
-                            r.template load<kVec>(static_cast<const T*>(q.dsT) + ((size_t)b * (W - 1) + k) * p.D, c, p.D);
+                            Piece<T, V, kVec> r;
+                            r.load(static_cast<const T*>(q.dsT) + ((size_t)b * (W - 1) + k) * p.D, c, p.D);
 #pragma unroll
                             for (int i = 0; i < V; ++i) g[i] += r.get(i);
                         }

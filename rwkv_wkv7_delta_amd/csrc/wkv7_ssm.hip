@@ -6,15 +6,13 @@
 //   h_t[n] = exp(D_t A[n]) h_{t-1}[n] + u_t B_t[n]
 //   y_t = (sum_n C_t[n] h_t[n] + dskip x_t) * z_t sigmoid(z_t)
 //
-// A channel's N states lie over P = N / 4 lanes, four per lane, so a workgroup
-// of 256 lanes takes 1024 / N channels of one group and one batch row.  It
-// walks the tokens in tiles of 16: every thread loads a piece of one token row
-// (x, dt, z) and of B and C, one tile ahead, forms D and u once per token and
-// channel and leaves them in LDS as fp32; every lane then steps its four states
-// through the tile (exponential as 2^(D A log2 e)); the read-out is summed over
-// the channel's lanes by DPP and goes back through LDS to the threads that hold
-// the row pieces, which add the skip term, gate and store whole pieces.
-// Everything is fp32; only the stored outputs are rounded.
+// The layout over a workgroup is wkv7_ssm_tile.h's.  In interval i the staging
+// waves leave D and u of tile i in LDS and finish tile i - 2: they add up the P
+// partial read-outs of every token and channel, add the skip term, gate and
+// store; they also write the checkpoints (8-bit codes are formed here).  The
+// step waves run tile i - 1: per token and state a product for the exponent, a
+// 2^x, the two products of the update and one of the read-out.  Everything is
+// fp32; only the stored outputs are rounded.
 //
 // Tokens at or behind a row's length take D = u = 0 and B = C = 0: the state
 // passes unchanged (2^0 = 1), whatever the padding holds, and y is stored as 0.
@@ -25,40 +23,28 @@
 // sum D of every segment but the last; the second composes its own entry state
 // from them and h0 and runs its segment with outputs.
 
-#include "wkv7_ssm_device.h"
-#include "wkv7_ssm_internal.h"
+#include "wkv7_ssm_tile.h"
 
 namespace wkv7 {
 
 namespace {
 
-constexpr int kTile = kSsmChunk;
-
-template <int N>
-struct Shape {
-    static constexpr int P = N / kSsmStates;              // lanes per channel
-    static constexpr int CH = kSsmThreads / P;            // channels per workgroup
-    static constexpr int EPT = CH * kTile / kSsmThreads;  // channels of a thread's row piece
-    static constexpr int BC = kTile * N / kSsmThreads > 0 ? kTile * N / kSsmThreads : 1;
-    static constexpr int YS = CH + 16;                    // row stride of the read-outs in LDS
-};
-
-// A thread's share of one tile as loaded.
-template <typename T, int N>
+// A staging thread's share of one tile as loaded.
+template <typename T, int N, bool kVec>
 struct Loaded {
-    Piece<T, Shape<N>::EPT> x, dt, z;
-    Piece<T, Shape<N>::BC> b, c;
+    Piece<T, Shape<N>::EPT, kVec> x, dt, z;
+    Piece<T, Shape<N>::BC, true> b, c;
 };
 
-template <typename T, int N, bool kVec, bool kMap>
-__global__ __launch_bounds__(kSsmThreads) void ssm_fwd_kernel(const SsmArgs p, int blocks) {
+template <typename T, int N, bool kVec, bool kMap, bool kCkpt>
+__global__ __launch_bounds__(2 * kStepThreads) void ssm_fwd_kernel(const SsmArgs p, int blocks) {
     using S = Shape<N>;
     constexpr int EPT = S::EPT, BC = S::BC, P = S::P, CH = S::CH;
-    __shared__ float2 s_du[2][kTile][CH];
-    __shared__ __attribute__((aligned(16))) float s_b[2][kTile][N], s_c[2][kTile][N];
-    __shared__ float s_y[2][kTile][S::YS];
+    __shared__ __attribute__((aligned(16))) float2 s_du[2][kTile][CH];
+    __shared__ __attribute__((aligned(16))) float s_b[2][kTile][N], s_c[2][kMap ? 1 : kTile][N];
+    __shared__ __attribute__((aligned(16))) float s_y[2][kMap ? 1 : kTile][kMap ? 1 : P][S::YS];
+    __shared__ __attribute__((aligned(16))) float s_h[2][kCkpt ? CH : 1][S::HS];   // states entering a tile
 
-    const int tid = threadIdx.x;
     unsigned blk = blockIdx.x;
     const int j = blk % blocks;
     blk /= blocks;
@@ -69,150 +55,216 @@ __global__ __launch_bounds__(kSsmThreads) void ssm_fwd_kernel(const SsmArgs p, i
     const int c0 = g * Dg + j * CH, cend = (g + 1) * Dg;   // the group's channels end at cend
     const int t_begin = seg * p.seg_len;
     const int t_end = seg == p.nseg - 1 ? p.T : t_begin + p.seg_len;
-    const int len = row_length(p.lengths, b, p.T);
+    const int tiles = (t_end - t_begin + kTile - 1) / kTile;
+    const int intervals = (tiles + 5) / 4 * 4;   // tiles + 2, to a multiple of 4
 
-    // The row piece this thread stages, and the B, C elements.
-    const int pt = tid / 16, pc = c0 + (tid % 16) * EPT;
-    const int be = tid * BC, bt = be / N, bn = be % N;
-    const bool has_bc = bt < kTile;
-    const T* const X = static_cast<const T*>(p.x);
-    const T* const DT = static_cast<const T*>(p.dt);
-    const T* const Z = static_cast<const T*>(p.z);
-    const T* const Bm = static_cast<const T*>(p.Bm);
-    const T* const Cm = static_cast<const T*>(p.Cm);
+    if (threadIdx.x < kStepThreads) {
+        // ---- step waves: tile i - 1 in interval i --------------------------------
+        const StepLane<N> at(threadIdx.x);
+        const int ch = c0 + at.cl < cend ? c0 + at.cl : cend - 1;
+        const bool live = c0 + at.cl < cend;
+        const size_t chn = ((size_t)b * p.D + ch) * N + at.n0;   // into [B][D][N]
+        float a2[4], h[4] = {0.f, 0.f, 0.f, 0.f}, dsum = 0.f;
+        load_cols<4>(p.A + (size_t)ch * N + at.n0, a2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a2[i] *= kLog2e;
+        if constexpr (!kMap) {
+            if (p.h0) load_cols<4>(p.h0 + chn, h);
+            const size_t BDN = (size_t)p.B * p.D * N, BD = (size_t)p.B * p.D;
+            for (int s = 0; s < seg; ++s) {
+                float e[4];
+                load_cols<4>(p.seg_h + s * BDN + chn, e);
+                const float d = p.seg_d[s * BD + chn / N];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) h[i] = fmaf(exp2_raw(d * a2[i]), h[i], e[i]);
+            }
+        }
+        for (int i = 0; i < intervals; ++i) {
+            __syncthreads();
+            if (i >= tiles) continue;
+            const int k = i & 1;
+            float b4[4], c4[4];
+            load_cols<4>(&s_b[k][at.t][at.n0], b4);
+            if constexpr (!kMap) {
+                load_cols<4>(&s_c[k][at.t][at.n0], c4);
+                if constexpr (kCkpt) store_cols<4>(&s_h[k][at.cl][at.n0], h);
+            }
+            // All of the tile's D and u at once: read per token, each read's
+            // latency showed between two tokens.
+            float2 d16[kTile];
+#pragma unroll
+            for (int t = 0; t < kTile; ++t) d16[t] = s_du[k][t][at.cl];
+            __builtin_amdgcn_sched_barrier(0);
+            each_token([&](auto tok) {
+                constexpr int t = decltype(tok)::v;
+                const float2 du = d16[t];
+                float a[4], x[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    a[n] = exp2_raw(du.x * a2[n]);
+                    x[n] = row_bcast<t>(b4[n]) * du.y;
+                }
+                if constexpr (kMap) {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) h[n] = fmaf(a[n], h[n], x[n]);
+                    dsum += du.x;
+                } else {
+                    s_y[k][t][at.part][at.cl] = step_read<t>(h, a, x, c4);
+                }
+            });
+        }
+        if (live) {
+            if constexpr (kMap) {
+                store_cols<4>(p.seg_h + (size_t)seg * p.B * p.D * N + chn, h);
+                if (at.n0 == 0) p.seg_d[(size_t)seg * p.B * p.D + chn / N] = dsum;
+            } else if (seg == p.nseg - 1 && p.hT) {
+                store_cols<4>(p.hT + chn, h);
+            }
+        }
+        return;
+    }
+
+    // ---- staging waves: tile i in interval i, the outputs of tile i - 2 -------------
+    const int tid = threadIdx.x - kStepThreads;
+    const int len = row_length(p.lengths, b, p.T);
+    const int pt = tid / 16, pl = (tid % 16) * EPT;   // the thread's row piece
+    const int be = tid * BC, bt = be / N, bn = be % N;              // and its elements of B and C
     float bias[EPT], skip[EPT];
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
-        const int c = pc + i < cend ? pc + i : cend - 1;
+        const int c = c0 + pl + i < cend ? c0 + pl + i : cend - 1;
         bias[i] = p.dt_bias ? p.dt_bias[c] : 0.f;
         skip[i] = p.dskip ? p.dskip[c] : 0.f;
     }
-
-    // The channel and states this lane steps.
-    const int cl = tid / P, n0 = (tid % P) * kSsmStates, ch = c0 + cl;
-    const bool live = ch < cend;
-    const size_t chn = ((size_t)b * p.D + (live ? ch : cend - 1)) * N + n0;   // into [B][D][N]
-    float a2[4], h[4] = {0.f, 0.f, 0.f, 0.f}, dsum = 0.f;
-    {
-        const float4 a = *reinterpret_cast<const float4*>(p.A + (size_t)(live ? ch : cend - 1) * N + n0);
-        a2[0] = a.x * kLog2e; a2[1] = a.y * kLog2e; a2[2] = a.z * kLog2e; a2[3] = a.w * kLog2e;
-    }
-    if constexpr (!kMap) {
-        if (p.h0) load_cols<4>(p.h0 + chn, h);
-        const size_t BDN = (size_t)p.B * p.D * N, BD = (size_t)p.B * p.D;
-        for (int s = 0; s < seg; ++s) {
-            float e[4];
-            load_cols<4>(p.seg_h + s * BDN + chn, e);
-            const float d = p.seg_d[s * BD + chn / N];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = fmaf(exp2_raw(d * a2[i]), h[i], e[i]);
-        }
-    }
-
-    auto load = [&](Loaded<T, N>& r, int t0) {
-        const int t = t0 + pt < p.T ? t0 + pt : p.T - 1;
-        const size_t row = ((size_t)b * p.T + t) * p.D;
-        r.x.template load<kVec>(X + row, pc, cend);
-        r.dt.template load<kVec>(DT + row, pc, cend);
-        if (!kMap && Z) r.z.template load<kVec>(Z + row, pc, cend);
-        if (has_bc) {
-            const int tb = t0 + bt < p.T ? t0 + bt : p.T - 1;
-            const size_t off = (((size_t)b * p.T + tb) * p.G + g) * N;
-            r.b.template load<true>(Bm + off, bn, N);
-            if (!kMap) r.c.template load<true>(Cm + off, bn, N);
-        }
-    };
-    // The read-outs of the tile at t0 (in s_y[buf]) to y.
-    T* const Y = static_cast<T*>(p.y);
-    auto write_out = [&](const Piece<T, EPT>& xr, const Piece<T, EPT>& zr, int t0, int buf) {
-        const int t = t0 + pt;
-        if (t >= t_end) return;
-        float out[EPT];
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) {
-            float v = fmaf(skip[i], xr.get(i), s_y[buf][pt][(tid % 16) * EPT + i]);
-            if (Z) {
-                const float z = zr.get(i);
-                v *= z * sigmoid(z);
-            }
-            out[i] = t < len ? v : 0.f;
-        }
-        store_piece<kVec>(Y + ((size_t)b * p.T + t) * p.D, pc, cend, out);
-    };
-
-    Loaded<T, N> cur;
-    Piece<T, EPT> px, pz;   // the previous tile's x and z
-    if (t_begin < t_end) load(cur, t_begin);
     const int nck = (p.T + kTile - 1) / kTile;
-    int buf = 0;
-    for (int t0 = t_begin; t0 < t_end; t0 += kTile, buf ^= 1) {
-        {
-            const bool in = t0 + pt < len && t0 + pt < t_end;
+    const bool gate = p.z != nullptr;
+
+    // A tile's rows of a token tensor as a buffer: the workgroup's channels of
+    // its first row to those of its last; rows behind the segment read as 0 and
+    // are not written.  So nothing that touches memory in the loop below is
+    // conditional, and each wait covers exactly the loads it needs.
+    const uint32_t at = (uint32_t)(((size_t)pt * p.D + pl) * sizeof(T));
+    const uint32_t at_bc = bt < kTile ? (uint32_t)(((size_t)bt * p.G * N + bn) * sizeof(T)) : kNowhere;
+    const int valid = cend - c0 - pl;
+    const int row = p.D * (int)sizeof(T), tail = (cend - c0) * (int)sizeof(T);
+    const int row_bc = p.G * N * (int)sizeof(T), tail_bc = N * (int)sizeof(T);
+    const size_t first = (((size_t)b * p.T + t_begin) * p.D + c0) * sizeof(T);
+    const size_t first_bc = (((size_t)b * p.T + t_begin) * p.G + g) * N * sizeof(T);
+    const char *x_at = static_cast<const char*>(p.x) + first, *dt_at = static_cast<const char*>(p.dt) + first,
+               *z_at = static_cast<const char*>(gate ? p.z : p.x) + first,
+               *b_at = static_cast<const char*>(p.Bm) + first_bc, *c_at = static_cast<const char*>(p.Cm) + first_bc;
+    char* y_at = static_cast<char*>(p.y) + (int64_t)first - 2 * (int64_t)kTile * row;   // written two tiles later
+    auto load = [&](Loaded<T, N, kVec>& r, int left) {   // left: rows from the tile's first to the segment's end
+        const int n = left < kTile ? left : kTile;
+        const int bytes = n > 0 ? (n - 1) * row + tail : 0, bytes_bc = n > 0 ? (n - 1) * row_bc + tail_bc : 0;
+        r.x.load(buffer_of(x_at, bytes), at);
+        r.dt.load(buffer_of(dt_at, bytes), at);
+        if constexpr (!kMap) r.z.load(buffer_of(z_at, gate ? bytes : 0), at);
+        r.b.load(buffer_of(b_at, bytes_bc), at_bc);
+        if constexpr (!kMap) r.c.load(buffer_of(c_at, bytes_bc), at_bc);
+        x_at += kTile * (int64_t)row;
+        dt_at += kTile * (int64_t)row;
+        z_at += kTile * (int64_t)row;
+        b_at += kTile * (int64_t)row_bc;
+        c_at += kTile * (int64_t)row_bc;
+    };
+    auto stage = [&](const Loaded<T, N, kVec>& r, int tile) {
+        const int t0 = t_begin + tile * kTile, k = tile & 1;
+        float d[EPT];
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) {
-                const float v = cur.dt.get(i) + bias[i];
-                const float d = p.softplus ? softplus(v) : v;
-                s_du[buf][pt][(tid % 16) * EPT + i] =
-                    in ? make_float2(d, d * cur.x.get(i)) : make_float2(0.f, 0.f);
-            }
-            if (has_bc) {
-                const bool inb = t0 + bt < len && t0 + bt < t_end;
+        for (int i = 0; i < EPT; ++i) d[i] = r.dt.get(i) + bias[i];
+        if (p.softplus) {
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) d[i] = softplus(d[i]);
+        }
+        const int end = len < t_end ? len : t_end;
+        if (t0 + kTile <= end) {
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) s_du[k][pt][pl + i] = make_float2(d[i], d[i] * r.x.get(i));
+            if (bt < kTile) {
 #pragma unroll
                 for (int i = 0; i < BC; ++i) {
-                    s_b[buf][bt][bn + i] = inb ? cur.b.get(i) : 0.f;
-                    if (!kMap) s_c[buf][bt][bn + i] = inb ? cur.c.get(i) : 0.f;
+                    s_b[k][bt][bn + i] = r.b.get(i);
+                    if (!kMap) s_c[k][bt][bn + i] = r.c.get(i);
+                }
+            }
+        } else {
+            const bool in = t0 + pt < end, inb = t0 + bt < end;
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) {
+                const float u = d[i] * r.x.get(i);
+                s_du[k][pt][pl + i] = make_float2(in ? d[i] : 0.f, in ? u : 0.f);
+            }
+            if (bt < kTile) {
+#pragma unroll
+                for (int i = 0; i < BC; ++i) {
+                    s_b[k][bt][bn + i] = inb ? r.b.get(i) : 0.f;
+                    if (!kMap) s_c[k][bt][bn + i] = inb ? r.c.get(i) : 0.f;
                 }
             }
         }
+    };
+    // The read-outs of a stepped tile, and the checkpoint of the state entering it.
+    auto write_out = [&](const Piece<T, EPT, kVec>& xr, const Piece<T, EPT, kVec>& zr, int tile) {
+        const int t0 = t_begin + tile * kTile, k = tile & 1;
+        float out[EPT];
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) out[i] = s_y[k][pt][0][pl + i];
+#pragma unroll
+        for (int q = 1; q < P; ++q)
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) out[i] += s_y[k][pt][q][pl + i];
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) out[i] = fmaf(skip[i], xr.get(i), out[i]);
+        if (gate) {
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) out[i] *= zr.get(i) * sigmoid(zr.get(i));
+        }
+        if (t0 + kTile > len) {
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) out[i] = t0 + pt < len ? out[i] : 0.f;
+        }
+        const int left = tile >= 0 ? t_end - t0 : 0, n = left < kTile ? left : kTile;
+        store_piece<T, kVec>(buffer_of(y_at, n > 0 ? (n - 1) * row + tail : 0), at, valid, out);
+        y_at += kTile * (int64_t)row;
+        if constexpr (kCkpt) {
+            const int hc = tid / P, n0 = (tid % P) * kSsmStates;
+            float h[4], scale;
+            load_cols<4>(&s_h[k][hc][n0], h);
+            const uint32_t w = encode8<P>(h, scale);
+            const bool wide = p.ckpt_bits == 32;
+            const int bytes = n > 0 ? (cend - c0) * N : 0;
+            const size_t crow = ((size_t)b * nck + (tile >= 0 ? t0 / kTile : 0)) * p.D + c0;   // the first channel's
+            char* const base = static_cast<char*>(p.ckpt);
+            const size_t scales = ckpt_scale_offset((size_t)p.B * nck * p.D * N);
+            store_piece<float, true>(buffer_of(base + crow * N * 4, wide ? 4 * bytes : 0), 4u * (hc * N + n0), 1, h);
+            __builtin_amdgcn_raw_buffer_store_b32(w, buffer_of(base + crow * N, wide ? 0 : bytes), hc * N + n0, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(
+                __float_as_uint(scale), buffer_of(base + scales + crow * 4, wide || n <= 0 ? 0 : 4 * (cend - c0)),
+                n0 == 0 ? 4u * hc : kNowhere, 0, 0);
+        }
+    };
+
+    // Two tiles of loads in flight, and the x and z of the two tiles whose
+    // read-outs are still to come: four sets of registers in turn (moving a set
+    // that is still being loaded would wait for it).  Behind the last tile and
+    // before the first the loads and stores meet empty buffers, and what is
+    // staged is not read.
+    Loaded<T, N, kVec> r0, r1, r2, r3;
+    load(r0, t_end - t_begin);
+    load(r1, t_end - t_begin - kTile);
+    r2 = r0, r3 = r0;
+    auto interval = [&](int i, const Loaded<T, N, kVec>& r, Loaded<T, N, kVec>& old) {
+        stage(r, i);
+        if constexpr (!kMap) write_out(old.x, old.z, i - 2);
+        load(old, t_end - t_begin - (i + 2) * kTile);
         __syncthreads();
-        if constexpr (!kMap) {
-            if (t0 > t_begin) write_out(px, pz, t0 - kTile, buf ^ 1);
-            px = cur.x;
-            pz = cur.z;
-            if (p.ckpt_bits && live) {
-                const size_t at = (((size_t)b * nck + t0 / kTile) * p.D + ch) * N + n0;
-                if (p.ckpt_bits == 32) {
-                    store_cols<4>(static_cast<float*>(p.ckpt) + at, h);
-                } else {
-                    float scale;
-                    const uint32_t w = encode8<P>(h, scale);
-                    *reinterpret_cast<uint32_t*>(static_cast<char*>(p.ckpt) + at) = w;
-                    if (n0 == 0)
-                        reinterpret_cast<float*>(static_cast<char*>(p.ckpt) +
-                                                 ckpt_scale_offset((size_t)p.B * nck * p.D * N))[at / N] = scale;
-                }
-            }
-        }
-        if (t0 + kTile < t_end) load(cur, t0 + kTile);
-        float keep = 0.f;
-#pragma unroll
-        for (int t = 0; t < kTile; ++t) {
-            const float2 du = s_du[buf][t][cl];
-            const float4 b4 = *reinterpret_cast<const float4*>(&s_b[buf][t][n0]);
-            const float bb[4] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = fmaf(exp2_raw(du.x * a2[i]), h[i], du.y * bb[i]);
-            if constexpr (kMap) {
-                dsum += du.x;
-            } else {
-                const float4 c4 = *reinterpret_cast<const float4*>(&s_c[buf][t][n0]);
-                const float y = group_sum<P>(dot4(make_float4(h[0], h[1], h[2], h[3]), c4));
-                keep = t % P == tid % P ? y : keep;
-                if (t % P == P - 1) s_y[buf][t - (P - 1) + tid % P][cl] = keep;
-            }
-        }
-    }
-    if constexpr (kMap) {
-        if (live) {
-            store_cols<4>(p.seg_h + (size_t)seg * p.B * p.D * N + chn, h);
-            if (n0 == 0) p.seg_d[(size_t)seg * p.B * p.D + chn / N] = dsum;
-        }
-    } else {
-        if (t_begin < t_end) {
-            __syncthreads();
-            write_out(px, pz, t_begin + (t_end - t_begin - 1) / kTile * kTile, buf ^ 1);
-        }
-        if (seg == p.nseg - 1 && p.hT && live) store_cols<4>(p.hT + chn, h);
+    };
+    for (int i = 0; i < intervals; i += 4) {
+        interval(i, r0, r2);
+        interval(i + 1, r1, r3);
+        interval(i + 2, r2, r0);
+        interval(i + 3, r3, r1);
     }
 }
 
@@ -253,23 +305,28 @@ __global__ __launch_bounds__(kSsmThreads) void ssm_step_kernel(const SsmArgs p) 
     }
 }
 
-template <typename T, int N>
-hipError_t launch_fwd(const SsmArgs& p, hipStream_t stream) {
-    using S = Shape<N>;
-    const int Dg = p.D / p.G, blocks = (Dg + S::CH - 1) / S::CH;
+template <typename T, int N, bool kVec>
+hipError_t launch_fwd_v(const SsmArgs& p, int blocks, hipStream_t stream) {
+    constexpr int threads = 2 * kStepThreads;
     const unsigned per = (unsigned)p.B * p.G * blocks;
-    const bool vec = Dg % S::EPT == 0;   // every piece whole and aligned
     if (p.nseg > 1) {
-        const dim3 grid(per * (p.nseg - 1));
-        if (vec) ssm_fwd_kernel<T, N, true, true><<<grid, kSsmThreads, 0, stream>>>(p, blocks);
-        else ssm_fwd_kernel<T, N, false, true><<<grid, kSsmThreads, 0, stream>>>(p, blocks);
+        ssm_fwd_kernel<T, N, kVec, true, false><<<dim3(per * (p.nseg - 1)), threads, 0, stream>>>(p, blocks);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     const dim3 grid(per * p.nseg);
-    if (vec) ssm_fwd_kernel<T, N, true, false><<<grid, kSsmThreads, 0, stream>>>(p, blocks);
-    else ssm_fwd_kernel<T, N, false, false><<<grid, kSsmThreads, 0, stream>>>(p, blocks);
+    if (p.ckpt_bits && p.T > 0) ssm_fwd_kernel<T, N, kVec, false, true><<<grid, threads, 0, stream>>>(p, blocks);
+    else ssm_fwd_kernel<T, N, kVec, false, false><<<grid, threads, 0, stream>>>(p, blocks);
     return hipGetLastError();
+}
+
+template <typename T, int N>
+hipError_t launch_fwd(const SsmArgs& p, hipStream_t stream) {
+    using S = Shape<N>;
+    const int Dg = p.D / p.G, blocks = (Dg + S::CH - 1) / S::CH;
+    // Whole, aligned pieces where the width of a group holds them.
+    return Dg % S::EPT == 0 ? launch_fwd_v<T, N, true>(p, blocks, stream)
+                            : launch_fwd_v<T, N, false>(p, blocks, stream);
 }
 
 template <typename T, int N>

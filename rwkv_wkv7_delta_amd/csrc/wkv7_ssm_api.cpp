@@ -72,7 +72,7 @@ int check_ssm(const wkv7_ssm_desc* d) {
     if (d->N != 8 && d->N != 16 && d->N != 32 && d->N != 64) return WKV7_ERR_UNSUPPORTED;
     if (d->dtype != WKV7_F32 && d->dtype != WKV7_BF16) return WKV7_ERR_UNSUPPORTED;
     if (d->ckpt_bits != 0 && d->ckpt_bits != 8 && d->ckpt_bits != 32) return WKV7_ERR_UNSUPPORTED;
-    if (d->T > INT32_MAX - 64 || d->D > (1 << 28)) return WKV7_ERR_UNSUPPORTED;
+    if (d->T > INT32_MAX - 64 || d->D > (1 << 24)) return WKV7_ERR_UNSUPPORTED;
     const int64_t blocks = ((int64_t)d->T + 15) / 16, most = (int64_t)1 << 40;
     // A launch has at most B G ceil(D / G / channels) workgroups per segment.
     if (!product_fits(d->B, d->T, d->D, 1, most) || !product_fits(d->B, blocks, d->D, d->N, most) ||

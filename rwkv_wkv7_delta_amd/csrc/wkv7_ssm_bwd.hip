@@ -45,10 +45,10 @@ struct Shape {
     static constexpr int YS = CH + 16;                    // row stride of the per-channel sums in LDS
 };
 
-template <typename T, int N>
+template <typename T, int N, bool kVec>
 struct Loaded {
-    Piece<T, Shape<N>::EPT> x, dt, z, dy;
-    Piece<T, Shape<N>::BC> b, c;
+    Piece<T, Shape<N>::EPT, kVec> x, dt, z, dy;
+    Piece<T, Shape<N>::BC, true> b, c;
 };
 
 // Sums v[0..7] over the lanes of a wave that share lane % P: lane l returns in
@@ -138,18 +138,18 @@ __global__ __launch_bounds__(kSsmThreads, 2) void ssm_bwd_kernel(const SsmBwdArg
         }
     }
 
-    auto load = [&](Loaded<T, N>& r, int t0) {
+    auto load = [&](Loaded<T, N, kVec>& r, int t0) {
         const int t = t0 + pt < p.T ? t0 + pt : p.T - 1;
         const size_t row = ((size_t)b * p.T + t) * p.D;
-        if (!kMap) r.x.template load<kVec>(X + row, pc, cend);
-        r.dt.template load<kVec>(DT + row, pc, cend);
-        r.dy.template load<kVec>(DY + row, pc, cend);
-        if (Z) r.z.template load<kVec>(Z + row, pc, cend);
+        if (!kMap) r.x.load(X + row, pc, cend);
+        r.dt.load(DT + row, pc, cend);
+        r.dy.load(DY + row, pc, cend);
+        if (Z) r.z.load(Z + row, pc, cend);
         if (has_bc) {
             const int tb = t0 + bt < p.T ? t0 + bt : p.T - 1;
             const size_t off = (((size_t)b * p.T + tb) * p.G + g) * N;
-            if (!kMap) r.b.template load<true>(Bm + off, bn, N);
-            r.c.template load<true>(Cm + off, bn, N);
+            if (!kMap) r.b.load(Bm + off, bn, N);
+            r.c.load(Cm + off, bn, N);
         }
     };
 
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(kSsmThreads, 2) void ssm_bwd_kernel(const SsmBwdArg
         }
     };
 
-    Loaded<T, N> cur;
+    Loaded<T, N, kVec> cur;
     // The last tile (none when there are no tokens).
     const int t_last = t_begin < t_end ? t_begin + (t_end - t_begin - 1) / kTile * kTile : t_begin - kTile;
     if (t_begin < t_end) load(cur, t_last);

@@ -15,28 +15,32 @@ __device__ __forceinline__ float sigmoid(float x) {
     return __builtin_amdgcn_rcpf(1.f + exp_raw(-x));
 }
 
-// log(1 + exp(x)).  With e = exp(x) and u = fl(1 + e), log(u) e / (u - 1) is
-// log(1 + e) to a few rounding errors for every e: the error of u cancels
-// between the logarithm and u - 1 (which is exact).  Above 20, x itself to
-// fp32 rounding.
+// log(1 + exp(x)) = max(x, 0) + log(1 + e) with e = exp(-|x|) in (0, 1].  With
+// u = fl(1 + e), log(1 + e) = log(u) + (e - (u - 1)) / u to second order in the
+// rounding of u; u - 1 is exact, and the divisor is left out: the term is below
+// 2^-24 where u is 1 or more, so that changes the sum by less than half a unit
+// in its last place.  For e below 2^-24 the logarithm is 0 and the term is e.
 __device__ __forceinline__ float softplus(float x) {
-    const float e = exp_raw(fminf(x, 20.f));
+    const float e = exp_raw(-fabsf(x));
     const float u = 1.f + e;
-    const float l = u == 1.f ? e : __builtin_amdgcn_logf(u) * kLn2 * (e * __builtin_amdgcn_rcpf(u - 1.f));
-    return x > 20.f ? x : (x != x ? x : l);
+    return fmaxf(x, 0.f) + fmaf(__builtin_amdgcn_logf(u), kLn2, e - (u - 1.f));
 }
 
-// V consecutive elements of a token row as loaded, so that a prefetch does not
-// wait for them.  kVec: whole pieces at their natural alignment (c a multiple
-// of V, clamped into the row by the caller's limit); else element by element,
-// every address clamped to lim - 1.
-template <typename T, int V>
+// ---- token rows ---------------------------------------------------------------
+// Pieces of V consecutive elements, kept as loaded so that a prefetch does not
+// wait for them.  kVec: whole pieces at their natural alignment; else element by
+// element.
+typedef uint32_t vu2 __attribute__((ext_vector_type(2)));
+typedef uint32_t vu4 __attribute__((ext_vector_type(4)));
+
+template <typename T, int V, bool kVec>
 struct Piece {
     static constexpr int kBytes = V * (int)sizeof(T);
-    static constexpr int kWords = (kBytes + 3) / 4;
+    static constexpr int kWords = kVec ? (kBytes + 3) / 4 : V;
     uint32_t w[kWords];
 
-    template <bool kVec>
+    // From a row in memory; c is a multiple of V with kVec.  Addresses at or
+    // behind `lim` are clamped into the row.
     __device__ __forceinline__ void load(const T* row, int c, int lim) {
         if constexpr (kVec) {
             const T* p = row + (c < lim ? c : lim - V);
@@ -58,18 +62,37 @@ struct Piece {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const int k = c + i < lim ? c + i : lim - 1;
-                if constexpr (sizeof(T) == 4) {
-                    w[i] = __float_as_uint(row[k]);
-                } else if (i % 2 == 0) {
-                    w[i / 2] = row[k];
-                } else {
-                    w[i / 2] |= (uint32_t)row[k] << 16;
-                }
+                if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(row[k]);
+                else w[i] = row[k];
+            }
+        }
+    }
+    // At byte `at` of a buffer; what lies outside it reads as 0.
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t at) {
+        if constexpr (!kVec) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if constexpr (sizeof(T) == 4) w[i] = __builtin_amdgcn_raw_buffer_load_b32(r, at + 4 * i, 0, 0);
+                else w[i] = __builtin_amdgcn_raw_buffer_load_b16(r, at + 2 * i, 0, 0);
+            }
+        } else if constexpr (kBytes == 2) {
+            w[0] = __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0);
+        } else if constexpr (kBytes == 4) {
+            w[0] = __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
+        } else if constexpr (kBytes == 8) {
+            const vu2 u = __builtin_bit_cast(vu2, __builtin_amdgcn_raw_buffer_load_b64(r, at, 0, 0));
+            w[0] = u.x; w[1] = u.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; i += 4) {
+                const vu4 u = __builtin_bit_cast(vu4, __builtin_amdgcn_raw_buffer_load_b128(r, at + 4 * i, 0, 0));
+                w[i] = u.x; w[i + 1] = u.y; w[i + 2] = u.z; w[i + 3] = u.w;
             }
         }
     }
     __device__ __forceinline__ float get(int i) const {
         if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+        else if constexpr (!kVec) return bf16_lo(w[i]);
         else return i % 2 == 0 ? bf16_lo(w[i / 2]) : bf16_hi(w[i / 2]);
     }
 };
@@ -107,6 +130,52 @@ __device__ __forceinline__ void store_piece(bf16_t* row, int c, int lim, const f
         for (int i = 0; i < V; ++i)
             if (c + i < lim) row[c + i] = f2bf(x[i]);
     }
+}
+
+// The same into a buffer, of the first `valid` elements (kVec: all or none);
+// what lies outside the buffer is dropped.
+constexpr uint32_t kNowhere = 0x7ffffff0u;   // behind the end of every buffer here
+
+template <typename T, bool kVec, int V>
+__device__ __forceinline__ void store_piece(__amdgpu_buffer_rsrc_t r, uint32_t at, int valid, const float (&x)[V]) {
+    if constexpr (!kVec) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const uint32_t o = i < valid ? at + i * (uint32_t)sizeof(T) : kNowhere;
+            if constexpr (sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[i]), r, o, 0, 0);
+            else __builtin_amdgcn_raw_buffer_store_b16(f2bf(x[i]), r, o, 0, 0);
+        }
+    } else {
+        const uint32_t o = valid > 0 ? at : kNowhere;
+        constexpr int kWords = V * (int)sizeof(T) / 4;
+        if constexpr (kWords == 0) {
+            __builtin_amdgcn_raw_buffer_store_b16(f2bf(x[0]), r, o, 0, 0);
+        } else {
+            uint32_t w[kWords];
+#pragma unroll
+            for (int i = 0; i < kWords; ++i) {
+                if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(x[i]);
+                else w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+            }
+            if constexpr (kWords == 1) {
+                __builtin_amdgcn_raw_buffer_store_b32(w[0], r, o, 0, 0);
+            } else if constexpr (kWords == 2) {
+                const vu2 u = {w[0], w[1]};
+                __builtin_amdgcn_raw_buffer_store_b64(u, r, o, 0, 0);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kWords; i += 4) {
+                    const vu4 u = {w[i], w[i + 1], w[i + 2], w[i + 3]};
+                    __builtin_amdgcn_raw_buffer_store_b128(u, r, o + 4 * i, 0, 0);
+                }
+            }
+        }
+    }
+}
+
+// `bytes` at p as a buffer (0: every access lies outside, nothing is touched).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, bytes, 0x00020000);
 }
 
 // Sum and maximum over each aligned group of P = 2, 4, 8 or 16 lanes, in every lane.

@@ -9,7 +9,7 @@
 namespace wkv7 {
 
 constexpr int kSsmChunk = 16;      // tokens per state checkpoint and per kernel tile
-constexpr int kSsmThreads = 256;   // threads of a scan workgroup
+constexpr int kSsmThreads = 256;   // lanes that hold a scan workgroup's states
 constexpr int kSsmStates = 4;      // states of a channel per lane
 
 // Channels that one scan workgroup takes: N / 4 lanes per channel.
