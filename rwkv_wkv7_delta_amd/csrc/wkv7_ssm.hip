@@ -32,27 +32,23 @@ namespace {
 // A staging thread's share of one tile as loaded.
 template <typename T, int N, bool kVec>
 struct Loaded {
-    Piece<T, Shape<N>::EPT, kVec> x, dt, z;
-    Piece<T, Shape<N>::BC, true> b, c;
+    Piece<T, Shape<N, kSsmStates>::EPT, kVec> x, dt, z;
+    Piece<T, Shape<N, kSsmStates>::BC, true> b, c;
 };
 
 template <typename T, int N, bool kVec, bool kMap, bool kCkpt>
 __global__ __launch_bounds__(2 * kStepThreads) void ssm_fwd_kernel(const SsmArgs p, int blocks) {
-    using S = Shape<N>;
+    using S = Shape<N, kSsmStates>;
     constexpr int EPT = S::EPT, BC = S::BC, P = S::P, CH = S::CH;
     __shared__ __attribute__((aligned(16))) float2 s_du[2][kTile][CH];
     __shared__ __attribute__((aligned(16))) float s_b[2][kTile][N], s_c[2][kMap ? 1 : kTile][N];
     __shared__ __attribute__((aligned(16))) float s_y[2][kMap ? 1 : kTile][kMap ? 1 : P][S::YS];
     __shared__ __attribute__((aligned(16))) float s_h[2][kCkpt ? CH : 1][S::HS];   // states entering a tile
 
-    unsigned blk = blockIdx.x;
-    const int j = blk % blocks;
-    blk /= blocks;
-    const int g = blk % p.G;
-    blk /= p.G;
-    const int b = blk % p.B, seg = blk / p.B;
+    const Place pos(blocks, p.G, p.B);
+    const int g = pos.g, b = pos.b, seg = pos.seg;
     const int Dg = p.D / p.G;
-    const int c0 = g * Dg + j * CH, cend = (g + 1) * Dg;   // the group's channels end at cend
+    const int c0 = g * Dg + pos.j * CH, cend = (g + 1) * Dg;   // the group's channels end at cend
     const int t_begin = seg * p.seg_len;
     const int t_end = seg == p.nseg - 1 ? p.T : t_begin + p.seg_len;
     const int tiles = (t_end - t_begin + kTile - 1) / kTile;
@@ -60,7 +56,7 @@ __global__ __launch_bounds__(2 * kStepThreads) void ssm_fwd_kernel(const SsmArgs
 
     if (threadIdx.x < kStepThreads) {
         // ---- step waves: tile i - 1 in interval i --------------------------------
-        const StepLane<N> at(threadIdx.x);
+        const StepLane<N, kSsmStates> at(threadIdx.x);
         const int ch = c0 + at.cl < cend ? c0 + at.cl : cend - 1;
         const bool live = c0 + at.cl < cend;
         const size_t chn = ((size_t)b * p.D + ch) * N + at.n0;   // into [B][D][N]
@@ -145,7 +141,7 @@ __global__ __launch_bounds__(2 * kStepThreads) void ssm_fwd_kernel(const SsmArgs
     // conditional, and each wait covers exactly the loads it needs.
     const uint32_t at = (uint32_t)(((size_t)pt * p.D + pl) * sizeof(T));
     const uint32_t at_bc = bt < kTile ? (uint32_t)(((size_t)bt * p.G * N + bn) * sizeof(T)) : kNowhere;
-    const int valid = cend - c0 - pl;
+    const int valid = cend - c0 - pl, here = cend - c0 < CH ? cend - c0 : CH;
     const int row = p.D * (int)sizeof(T), tail = (cend - c0) * (int)sizeof(T);
     const int row_bc = p.G * N * (int)sizeof(T), tail_bc = N * (int)sizeof(T);
     const size_t first = (((size_t)b * p.T + t_begin) * p.D + c0) * sizeof(T);
@@ -233,14 +229,14 @@ __global__ __launch_bounds__(2 * kStepThreads) void ssm_fwd_kernel(const SsmArgs
             load_cols<4>(&s_h[k][hc][n0], h);
             const uint32_t w = encode8<P>(h, scale);
             const bool wide = p.ckpt_bits == 32;
-            const int bytes = n > 0 ? (cend - c0) * N : 0;
+            const int bytes = n > 0 ? here * N : 0;
             const size_t crow = ((size_t)b * nck + (tile >= 0 ? t0 / kTile : 0)) * p.D + c0;   // the first channel's
             char* const base = static_cast<char*>(p.ckpt);
             const size_t scales = ckpt_scale_offset((size_t)p.B * nck * p.D * N);
             store_piece<float, true>(buffer_of(base + crow * N * 4, wide ? 4 * bytes : 0), 4u * (hc * N + n0), 1, h);
             __builtin_amdgcn_raw_buffer_store_b32(w, buffer_of(base + crow * N, wide ? 0 : bytes), hc * N + n0, 0, 0);
             __builtin_amdgcn_raw_buffer_store_b32(
-                __float_as_uint(scale), buffer_of(base + scales + crow * 4, wide || n <= 0 ? 0 : 4 * (cend - c0)),
+                __float_as_uint(scale), buffer_of(base + scales + crow * 4, wide || n <= 0 ? 0 : 4 * here),
                 n0 == 0 ? 4u * hc : kNowhere, 0, 0);
         }
     };
@@ -322,7 +318,7 @@ hipError_t launch_fwd_v(const SsmArgs& p, int blocks, hipStream_t stream) {
 
 template <typename T, int N>
 hipError_t launch_fwd(const SsmArgs& p, hipStream_t stream) {
-    using S = Shape<N>;
+    using S = Shape<N, kSsmStates>;
     const int Dg = p.D / p.G, blocks = (Dg + S::CH - 1) / S::CH;
     // Whole, aligned pieces where the width of a group holds them.
     return Dg % S::EPT == 0 ? launch_fwd_v<T, N, true>(p, blocks, stream)

@@ -72,7 +72,8 @@ int check_ssm(const wkv7_ssm_desc* d) {
     if (d->N != 8 && d->N != 16 && d->N != 32 && d->N != 64) return WKV7_ERR_UNSUPPORTED;
     if (d->dtype != WKV7_F32 && d->dtype != WKV7_BF16) return WKV7_ERR_UNSUPPORTED;
     if (d->ckpt_bits != 0 && d->ckpt_bits != 8 && d->ckpt_bits != 32) return WKV7_ERR_UNSUPPORTED;
-    if (d->T > INT32_MAX - 64 || d->D > (1 << 24)) return WKV7_ERR_UNSUPPORTED;
+    // A tile of sixteen rows is addressed with 32-bit byte offsets.
+    if (d->T > INT32_MAX - 64 || d->D > (1 << 24) || (int64_t)d->G * d->N > (1 << 22)) return WKV7_ERR_UNSUPPORTED;
     const int64_t blocks = ((int64_t)d->T + 15) / 16, most = (int64_t)1 << 40;
     // A launch has at most B G ceil(D / G / channels) workgroups per segment.
     if (!product_fits(d->B, d->T, d->D, 1, most) || !product_fits(d->B, blocks, d->D, d->N, most) ||
@@ -82,8 +83,8 @@ int check_ssm(const wkv7_ssm_desc* d) {
     return WKV7_OK;
 }
 
-int64_t channel_blocks(const wkv7_ssm_desc* d) {
-    const int ch = wkv7::ssm_channels(d->N);
+int64_t channel_blocks(const wkv7_ssm_desc* d, bool backward) {
+    const int ch = backward ? wkv7::ssm_bwd_channels(d->N) : wkv7::ssm_channels(d->N);
     return ((int64_t)d->D / d->G + ch - 1) / ch;
 }
 
@@ -97,9 +98,9 @@ constexpr int kUnits = 256;          // compute units of the device
 constexpr int kMaxSegments = 32;
 constexpr int kMinSegmentTokens = 128;
 
-SsmPlan plan_ssm(const wkv7_ssm_desc* d) {
+SsmPlan plan_ssm(const wkv7_ssm_desc* d, bool backward) {
     const SsmPlan none{1, d->T};
-    const int64_t wgs = (int64_t)d->B * d->G * channel_blocks(d);
+    const int64_t wgs = (int64_t)d->B * d->G * channel_blocks(d, backward);
     if (wgs == 0 || d->T == 0) return none;
     int64_t n = 2 * kUnits / wgs;
     if (n > d->T / kMinSegmentTokens) n = d->T / kMinSegmentTokens;
@@ -119,7 +120,7 @@ size_t segment_floats(const wkv7_ssm_desc* d, const SsmPlan& s) {
 }
 // Floats of the backward's partial sums of dB and dC, dA, and the vectors.
 size_t part_bc_floats(const wkv7_ssm_desc* d) {
-    const int64_t blocks = channel_blocks(d);
+    const int64_t blocks = channel_blocks(d, true);
     return blocks > 1 ? (size_t)blocks * d->B * d->T * d->G * 2 * d->N : 0;
 }
 size_t part_a_floats(const wkv7_ssm_desc* d, const SsmPlan& s) { return (size_t)s.nseg * d->B * d->D * d->N; }
@@ -210,13 +211,13 @@ size_t wkv7_ssm_ckpt_bytes(const wkv7_ssm_desc* desc) {
 
 size_t wkv7_ssm_forward_workspace_bytes(const wkv7_ssm_desc* desc) {
     if (check_ssm(desc) != WKV7_OK) return 0;
-    const SsmPlan s = plan_ssm(desc);
+    const SsmPlan s = plan_ssm(desc, false);
     return s.nseg > 1 ? segment_floats(desc, s) * sizeof(float) : 0;
 }
 
 size_t wkv7_ssm_backward_workspace_bytes(const wkv7_ssm_desc* desc) {
     if (check_ssm(desc) != WKV7_OK) return 0;
-    return backward_floats(desc, plan_ssm(desc)) * sizeof(float);
+    return backward_floats(desc, plan_ssm(desc, true)) * sizeof(float);
 }
 
 int wkv7_ssm_forward(const wkv7_ssm_desc* desc, const wkv7_ssm_params* params, const void* x,
@@ -233,7 +234,7 @@ int wkv7_ssm_forward(const wkv7_ssm_desc* desc, const wkv7_ssm_params* params, c
           opt(workspace)) ||
         (tokens && (ckpt != nullptr) != (desc->ckpt_bits != 0)))
         return WKV7_ERR_INVALID_ARG;
-    const SsmPlan s = plan_ssm(desc);
+    const SsmPlan s = plan_ssm(desc, false);
     const size_t need = s.nseg > 1 ? segment_floats(desc, s) * sizeof(float) : 0;
     if (need > 0 && (!workspace || workspace_bytes < need)) return WKV7_ERR_WORKSPACE;
     if (!tokens && !hT) return WKV7_OK;
@@ -258,7 +259,7 @@ int wkv7_ssm_backward(const wkv7_ssm_desc* desc, const wkv7_ssm_params* params, 
         !(opt(z) && opt(dhT) && opt(grads->dh0) && opt(workspace)) || !req(grads->dA) ||
         !both(grads->ddskip, params->dskip) || !both(grads->ddt_bias, params->dt_bias))
         return WKV7_ERR_INVALID_ARG;
-    const SsmPlan s = plan_ssm(desc);
+    const SsmPlan s = plan_ssm(desc, true);
     const size_t need = backward_floats(desc, s) * sizeof(float);
     if (need > 0 && (!workspace || workspace_bytes < need)) return WKV7_ERR_WORKSPACE;
     float* const bc = static_cast<float*>(workspace);

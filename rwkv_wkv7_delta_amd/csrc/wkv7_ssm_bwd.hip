@@ -10,335 +10,425 @@
 //   dx_t = du_t D_t + dy_t dskip    dskip: sum_{b,t} dy_t x_t   dh0 = a_0 g_0
 // and the slope of the softplus on dD_t.
 //
-// The lanes own channels and states as in the forward, walking the 16-token
-// tiles last to first.  A tile starts from the checkpoint of the state entering
-// it: the lane steps its four states through the tile keeping a_t and h_t in
-// registers (no state is read or written per token), then runs the adjoint
-// back.  Sums over a channel's states are DPP sums over its P lanes.  Sums over
-// channels (dB, dC) fold eight values over the wave's channel lanes at once:
-// v_permlane32_swap and v_permlane16_swap halve the values as they add, DPP
-// rotations add the rest; the waves meet in LDS, and the channel blocks of a
-// group in a second kernel that adds their partial sums in a fixed order (no
-// atomics).  dA and the per-channel vectors are summed over tiles in registers,
-// over batch rows and segments by the second kernel.
+// The layout over a workgroup is wkv7_ssm_tile.h's, the tiles taken last to
+// first.  A tile starts from the checkpoint of the state entering it (decoded by
+// the staging waves): a step lane steps its states through the tile keeping a_t
+// and h_t in registers (no state is read or written per token), then runs the
+// adjoint back.  Sums over channels (dB, dC) fold a lane's values over the
+// sixteen channels of its row by DPP, halving the values as they add; sums over
+// states fold over the wave's rows by lane swaps; the rest meets in LDS, and the
+// channel blocks of a group in a second kernel that adds their partial sums in a
+// fixed order (no atomics).  dA and the per-channel vectors are summed over
+// tiles in registers, over batch rows and segments by the second kernel.
 //
 // Time segments (few channels): the adjoint is affine too, carry_left =
 // exp(A sum D) carry_right + e; a first launch finds e and sum D of every
 // segment but the first, the second composes its own entry from dhT.
 
-#include "wkv7_ssm_device.h"
-#include "wkv7_ssm_internal.h"
+#include "wkv7_ssm_tile.h"
 
 namespace wkv7 {
 
 namespace {
 
-constexpr int kTile = kSsmChunk;
-constexpr int kWaves = kSsmThreads / 64;
-
+// States per lane: two, so that the 2 x 16 states and transitions of a tile stay
+// in registers beside everything else and a workgroup takes few enough channels
+// to spread over the device; four at N = 64, whose channels would not fit a
+// workgroup's sixteen rows otherwise.
 template <int N>
-struct Shape {
-    static constexpr int P = N / kSsmStates;              // lanes per channel
-    static constexpr int CH = kSsmThreads / P;            // channels per workgroup
-    static constexpr int EPT = CH * kTile / kSsmThreads;  // channels of a thread's row piece
-    static constexpr int BC = kTile * N / kSsmThreads > 0 ? kTile * N / kSsmThreads : 1;
-    static constexpr int YS = CH + 16;                    // row stride of the per-channel sums in LDS
-};
+constexpr int kStates = N == 64 ? 4 : 2;
 
 template <typename T, int N, bool kVec>
 struct Loaded {
-    Piece<T, Shape<N>::EPT, kVec> x, dt, z, dy;
-    Piece<T, Shape<N>::BC, true> b, c;
+    static constexpr int S = kStates<N>;
+    Piece<T, Shape<N, S>::EPT, kVec> x, dt, z, dy;
+    Piece<T, Shape<N, S>::BC, true> b, c;
+    Piece<float, S, true> h;       // entry states: fp32,
+    uint32_t codes, scale;         // or codes and their scale
 };
 
-// Sums v[0..7] over the lanes of a wave that share lane % P: lane l returns in
-// q[k] the sum of v[4k + 2 bit4(l) + bit5(l)].
-template <int P>
-__device__ __forceinline__ void fold8(const float (&v)[8], float (&q)[2]) {
-    float w[4];
+// What a staging thread keeps of a tile until its gradients come back.
+template <int EPT>
+struct Kept {
+    float x[EPT], d[EPT], slope[EPT], dy[EPT], w[EPT];   // w: dz per read-out
+};
+
+template <int kCtrl>
+__device__ __forceinline__ float dpp(float x) {
+    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), kCtrl, 0xF, 0xF, true));
+}
+
+// Sums of 2 S values over the sixteen lanes of every row, folded: each step adds
+// a lane's partner (row_ror:8, row_half_mirror, quad_perm) and, while there are
+// two values, keeps one of them by a bit of the lane.  Lane l returns the sum of
+// value 2 bit2 + bit3 (S = 2), 4 bit1 + 2 bit2 + bit3 (S = 4).
+template <int S>
+__device__ __forceinline__ float fold_row(const float (&v)[2 * S], bool bit3, bool bit2, bool bit1) {
+    float x[S], y[S / 2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[2 * i]),
-                                                        __float_as_uint(v[2 * i + 1]), false, false);
-        w[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+    for (int i = 0; i < S; ++i) {
+        const float p = v[2 * i] + dpp<0x128>(v[2 * i]), q = v[2 * i + 1] + dpp<0x128>(v[2 * i + 1]);
+        x[i] = bit3 ? q : p;
     }
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(w[2 * k]),
-                                                        __float_as_uint(w[2 * k + 1]), false, false);
-        float x = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-        if (P <= 8) x += __builtin_amdgcn_update_dpp(0.0f, x, 0x128, 0xF, 0xF, false);   // row_ror 8
-        if (P <= 4) x += __builtin_amdgcn_update_dpp(0.0f, x, 0x124, 0xF, 0xF, false);   // row_ror 4
-        if (P <= 2) x += __builtin_amdgcn_update_dpp(0.0f, x, 0x122, 0xF, 0xF, false);   // row_ror 2
-        q[k] = x;
+    for (int i = 0; i < S / 2; ++i) {
+        const float p = x[2 * i] + dpp<0x141>(x[2 * i]), q = x[2 * i + 1] + dpp<0x141>(x[2 * i + 1]);
+        y[i] = bit2 ? q : p;
     }
+    float z = y[0] + dpp<0x4E>(y[0]);
+    if constexpr (S == 4) {
+        const float q = y[1] + dpp<0x4E>(y[1]);
+        z = bit1 ? q : z;
+    }
+    return z + dpp<0xB1>(z);
+}
+
+// Sums of four values over the wave's four rows: row r returns the sum of value
+// 0, 2, 1, 3 for r = 0, 1, 2, 3.
+__device__ __forceinline__ float fold_rows(float v0, float v1, float v2, float v3) {
+    const auto a = __builtin_amdgcn_permlane32_swap(__float_as_uint(v0), __float_as_uint(v1), false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v2), __float_as_uint(v3), false, false);
+    const float p = __uint_as_float(a[0]) + __uint_as_float(a[1]), q = __uint_as_float(b[0]) + __uint_as_float(b[1]);
+    const auto c = __builtin_amdgcn_permlane16_swap(__float_as_uint(p), __float_as_uint(q), false, false);
+    return __uint_as_float(c[0]) + __uint_as_float(c[1]);
 }
 
 template <typename T, int N, bool kVec, bool kMap>
-__global__ __launch_bounds__(kSsmThreads, 2) void ssm_bwd_kernel(const SsmBwdArgs q, int blocks) {
-    using S = Shape<N>;
-    constexpr int EPT = S::EPT, BC = S::BC, P = S::P, CH = S::CH;
-    // Per token and channel: D, u, dy; then du, sum r A (and the read-out).
-    __shared__ float2 s_du[kTile][CH];
-    __shared__ float s_dy[kTile][CH];
-    __shared__ __attribute__((aligned(16))) float s_b[kTile][N], s_c[kTile][N];
-    __shared__ float s_o[kMap ? 1 : 3][kMap ? 1 : kTile][S::YS];
-    __shared__ float s_red[kMap ? 1 : kWaves][kMap ? 1 : kTile][2 * N];
+__global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmBwdArgs q, int blocks) {
+    constexpr int S = kStates<N>;
+    using Sh = Shape<N, S>;
+    constexpr int EPT = Sh::EPT, BC = Sh::BC, P = Sh::P, CH = Sh::CH, HS = Sh::HS;
+    constexpr int PW = P / 4;                  // waves that share a channel
+    constexpr int CG = CH / 16;                // groups of 16 channels
+    constexpr int OS = 64 + 16;                // row stride of the sums over states
+    __shared__ __attribute__((aligned(16))) float2 s_du[2][kTile][CH];
+    __shared__ __attribute__((aligned(16))) float s_dy[2][kTile][CH];
+    __shared__ __attribute__((aligned(16))) float s_b[2][kMap ? 1 : kTile][N], s_c[2][kTile][N];
+    __shared__ __attribute__((aligned(16))) float s_h[2][kMap ? 1 : CH][HS];
+    // Per token: sums over a wave's states of du, of r A, and the read-out; and
+    // the sums over 16 channels of dB and dC.
+    __shared__ __attribute__((aligned(16))) float s_o[2][kMap ? 1 : 3][kMap ? 1 : kTile][OS];
+    __shared__ __attribute__((aligned(16))) float s_red[2][kMap ? 1 : CG][kMap ? 1 : kTile][2 * N];
 
     const SsmArgs& p = q.f;
-    const int tid = threadIdx.x, wave = tid / 64, lane = tid % 64;
-    unsigned blk = blockIdx.x;
-    const int j = blk % blocks;
-    blk /= blocks;
-    const int g = blk % p.G;
-    blk /= p.G;
-    const int b = blk % p.B, seg = (int)(blk / p.B) + (kMap ? 1 : 0);
+    const Place pos(blocks, p.G, p.B);
+    const int g = pos.g, b = pos.b, j = pos.j, seg = pos.seg + (kMap ? 1 : 0);
     const int Dg = p.D / p.G;
     const int c0 = g * Dg + j * CH, cend = (g + 1) * Dg;
     const int t_begin = seg * p.seg_len;
     const int t_end = seg == p.nseg - 1 ? p.T : t_begin + p.seg_len;
-    const int len = row_length(p.lengths, b, p.T);
+    const int tiles = (t_end - t_begin + kTile - 1) / kTile;
+    const int intervals = (tiles + 5) / 4 * 4;   // tiles + 2, to a multiple of 4
+    const size_t BDN = (size_t)p.B * p.D * N, BD = (size_t)p.B * p.D;
+    const bool gate = p.z != nullptr;
 
-    const int pt = tid / 16, pl = (tid % 16) * EPT, pc = c0 + pl;
+    if (threadIdx.x < kStepThreads) {
+        // ---- step waves: the i-th tile from the end in interval i + 1 ---------------
+        const StepLane<N, S> at(threadIdx.x);
+        const int wave = threadIdx.x / 64, l = threadIdx.x % 16, row = threadIdx.x / 16 % 4;
+        const bool bit3 = l & 8, bit2 = l & 4, bit1 = l & 2;
+        const bool live = c0 + at.cl < cend;
+        const int ch = live ? c0 + at.cl : cend - 1;
+        const size_t chn = ((size_t)b * p.D + ch) * N + at.n0;
+        float A[S], a2[S], dA[S], carry[S], dsum = 0.f;
+        load_cols<S>(p.A + (size_t)ch * N + at.n0, A);
+#pragma unroll
+        for (int n = 0; n < S; ++n) {
+            a2[n] = A[n] * kLog2e;
+            dA[n] = carry[n] = 0.f;
+        }
+        if constexpr (!kMap) {
+            if (q.dhT) load_cols<S>(q.dhT + chn, carry);
+            for (int s = p.nseg - 1; s > seg; --s) {
+                float e[S];
+                load_cols<S>(p.seg_h + (s - 1) * BDN + chn, e);
+                const float d = p.seg_d[(s - 1) * BD + chn / N];
+#pragma unroll
+                for (int n = 0; n < S; ++n) carry[n] = fmaf(exp2_raw(d * a2[n]), carry[n], e[n]);
+            }
+        }
+        // Where the lane leaves its folded sums: row r of the wave holds value 0,
+        // 2, 1, 3 of a fold over the rows; a lane of a row the state (and dB or
+        // dC) that fold_row names.
+        const int col = wave * 16 + l;
+        const int second = row >> 1, later = row & 1;   // of (sb, sr), (t, t - 1)
+        const int n_red = S == 2 ? at.n0 + (bit3 ? 1 : 0) + (bit2 ? N : 0)
+                                 : at.n0 + (bit3 ? 1 : 0) + (bit2 ? 2 : 0) + (bit1 ? N : 0);
+        for (int i = 0; i < intervals; ++i) {
+            __syncthreads();
+            if (i >= tiles) continue;
+            const int k = i & 1;
+            float c4[S];
+            load_cols<S>(&s_c[k][at.t][at.n0], c4);
+            if constexpr (kMap) {
+                each_token_back([&](auto tok) {
+                    constexpr int t = decltype(tok)::v;
+                    const float d = s_du[k][t][at.cl].x, dyt = s_dy[k][t][at.cl];
+#pragma unroll
+                    for (int n = 0; n < S; ++n)
+                        carry[n] = exp2_raw(d * a2[n]) * (carry[n] + row_bcast<t>(c4[n]) * dyt);
+                    dsum += d;
+                });
+            } else {
+                // The states of the tile again.
+                float b4[S], h0[S], a[kTile][S], h[kTile][S], y4[4];
+                load_cols<S>(&s_b[k][at.t][at.n0], b4);
+                load_cols<S>(&s_h[k][at.cl][at.n0], h0);
+                each_token([&](auto tok) {
+                    constexpr int t = decltype(tok)::v;
+                    const float2 du = s_du[k][t][at.cl];
+                    float y = 0.f;
+#pragma unroll
+                    for (int n = 0; n < S; ++n) {
+                        a[t][n] = exp2_raw(du.x * a2[n]);
+                        h[t][n] = fmaf(a[t][n], t == 0 ? h0[n] : h[t > 0 ? t - 1 : 0][n], row_bcast<t>(b4[n]) * du.y);
+                        y = n == 0 ? row_bcast<t>(c4[n]) * h[t][n] : y + row_bcast<t>(c4[n]) * h[t][n];
+                    }
+                    y4[t % 4] = y;
+                    if constexpr (t % 4 == 3) {
+                        if (gate) {
+                            // rows 0, 1, 2, 3 hold tokens t - 3, t - 1, t - 2, t
+                            const float f = fold_rows(y4[0], y4[1], y4[2], y4[3]);
+                            s_o[k][2][t - 3 + 2 * later + second][col] = f;
+                        }
+                    }
+                });
+                // The adjoint, last token first.
+                float tA[S], sb1 = 0.f, sr1 = 0.f;
+#pragma unroll
+                for (int n = 0; n < S; ++n) tA[n] = 0.f;
+                each_token_back([&](auto tok) {
+                    constexpr int t = decltype(tok)::v;
+                    const float2 du = s_du[k][t][at.cl];
+                    const float dyt = s_dy[k][t][at.cl];
+                    float v[2 * S], sb = 0.f, sr = 0.f;
+#pragma unroll
+                    for (int n = 0; n < S; ++n) {
+                        const float gr = carry[n] + row_bcast<t>(c4[n]) * dyt;
+                        v[n] = gr * du.y;
+                        v[S + n] = dyt * h[t][n];
+                        sb = n == 0 ? row_bcast<t>(b4[n]) * gr : sb + row_bcast<t>(b4[n]) * gr;
+                        carry[n] = a[t][n] * gr;
+                        const float r = carry[n] * (t == 0 ? h0[n] : h[t > 0 ? t - 1 : 0][n]);
+                        sr = n == 0 ? r * A[n] : fmaf(r, A[n], sr);
+                        tA[n] = fmaf(r, du.x, tA[n]);
+                    }
+                    s_red[k][at.cl / 16][t][n_red] = fold_row<S>(v, bit3, bit2, bit1);
+                    if constexpr (t % 2 == 1) {
+                        sb1 = sb;
+                        sr1 = sr;
+                    } else {   // value 0: (sb, t + 1), 1: (sr, t + 1), 2: (sb, t), 3: (sr, t)
+                        s_o[k][second][t + 1 - later][col] = fold_rows(sb1, sr1, sb, sr);
+                    }
+                });
+#pragma unroll
+                for (int n = 0; n < S; ++n) dA[n] += tA[n];
+            }
+        }
+        if (live) {
+            if constexpr (kMap) {
+                store_cols<S>(p.seg_h + (seg - 1) * BDN + chn, carry);
+                if (at.n0 == 0) p.seg_d[(seg - 1) * BD + chn / N] = dsum;
+            } else {
+                store_cols<S>(q.part_a + (((size_t)seg * p.B + b) * p.D + ch) * N + at.n0, dA);
+                if (seg == 0 && q.dh0) store_cols<S>(q.dh0 + chn, carry);
+            }
+        }
+        if constexpr (!kMap) __syncthreads();
+        return;
+    }
+
+    // ---- staging waves: the i-th tile from the end in interval i, the gradients of
+    // ---- the (i - 2)-th ---------------------------------------------------------------
+    const int tid = threadIdx.x - kStepThreads;
+    const int len = row_length(p.lengths, b, p.T);
+    const int pt = tid / 16, pl = (tid % 16) * EPT;
     const int be = tid * BC, bt = be / N, bn = be % N;
-    const bool has_bc = bt < kTile;
-    const T* const X = static_cast<const T*>(p.x);
-    const T* const DT = static_cast<const T*>(p.dt);
-    const T* const Z = static_cast<const T*>(p.z);
-    const T* const DY = static_cast<const T*>(q.dy);
-    const T* const Bm = static_cast<const T*>(p.Bm);
-    const T* const Cm = static_cast<const T*>(p.Cm);
+    const int hc = tid * S / N, hn = tid * S % N;     // the thread's entry states
+    const int valid = cend - c0 - pl, here = cend - c0 < CH ? cend - c0 : CH;
     float bias[EPT], skip[EPT], sum_skip[EPT], sum_bias[EPT];
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
-        const int c = pc + i < cend ? pc + i : cend - 1;
+        const int c = c0 + pl + i < cend ? c0 + pl + i : cend - 1;
         bias[i] = p.dt_bias ? p.dt_bias[c] : 0.f;
         skip[i] = p.dskip ? p.dskip[c] : 0.f;
         sum_skip[i] = sum_bias[i] = 0.f;
     }
-
-    const int cl = tid / P, piece = tid % P, n0 = piece * kSsmStates, ch = c0 + cl;
-    const bool live = ch < cend;
-    const int chc = live ? ch : cend - 1;
-    const size_t chn = ((size_t)b * p.D + chc) * N + n0;
-    const size_t BDN = (size_t)p.B * p.D * N, BD = (size_t)p.B * p.D;
+    // Buffers as in the forward: no memory access in the loop is conditional.
+    const uint32_t at = (uint32_t)(((size_t)pt * p.D + pl) * sizeof(T));
+    const uint32_t at_bc = bt < kTile ? (uint32_t)(((size_t)bt * p.G * N + bn) * sizeof(T)) : kNowhere;
+    const int row = p.D * (int)sizeof(T), tail = (cend - c0) * (int)sizeof(T);
+    const int row_bc = p.G * N * (int)sizeof(T), tail_bc = N * (int)sizeof(T);
+    const int last = t_begin + (tiles - 1) * kTile;   // the first tile's first token
+    const int64_t first = (((int64_t)b * p.T + last) * p.D + c0) * (int)sizeof(T);
+    const int64_t first_bc = (((int64_t)b * p.T + last) * p.G + g) * N * (int)sizeof(T);
     const int nck = (p.T + kTile - 1) / kTile;
-    float A[4], a2[4], dA[4] = {0.f, 0.f, 0.f, 0.f}, carry[4] = {0.f, 0.f, 0.f, 0.f}, dsum = 0.f;
-    load_cols<4>(p.A + (size_t)chc * N + n0, A);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) a2[i] = A[i] * kLog2e;
-    if constexpr (!kMap) {
-        if (q.dhT) load_cols<4>(q.dhT + chn, carry);
-        for (int s = p.nseg - 1; s > seg; --s) {
-            float e[4];
-            load_cols<4>(p.seg_h + (s - 1) * BDN + chn, e);
-            const float d = p.seg_d[(s - 1) * BD + chn / N];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) carry[i] = fmaf(exp2_raw(d * a2[i]), carry[i], e[i]);
-        }
-    }
-
-    auto load = [&](Loaded<T, N, kVec>& r, int t0) {
-        const int t = t0 + pt < p.T ? t0 + pt : p.T - 1;
-        const size_t row = ((size_t)b * p.T + t) * p.D;
-        if (!kMap) r.x.load(X + row, pc, cend);
-        r.dt.load(DT + row, pc, cend);
-        r.dy.load(DY + row, pc, cend);
-        if (Z) r.z.load(Z + row, pc, cend);
-        if (has_bc) {
-            const int tb = t0 + bt < p.T ? t0 + bt : p.T - 1;
-            const size_t off = (((size_t)b * p.T + tb) * p.G + g) * N;
-            if (!kMap) r.b.load(Bm + off, bn, N);
-            r.c.load(Cm + off, bn, N);
-        }
+    const bool wide = p.ckpt_bits == 32;
+    const char* const ck = static_cast<const char*>(p.ckpt);
+    const size_t scales = wide ? 0 : ckpt_scale_offset((size_t)p.B * nck * p.D * N);
+    // Byte offset of the i-th tile from the end, and rows of it in the segment.
+    auto rows_of = [&](int i) {
+        const int t0 = last - i * kTile, left = t_end - t0;
+        return i >= tiles || i < 0 ? 0 : left < kTile ? left : kTile;
     };
-
-    // The state entering the tile at t0.
-    auto entry = [&](int t0, float (&h)[4]) {
-        const size_t at = (((size_t)b * nck + t0 / kTile) * p.D + chc) * N + n0;
-        if (p.ckpt_bits == 32) {
-            load_cols<4>(static_cast<const float*>(p.ckpt) + at, h);
-        } else {
-            const char* const base = static_cast<const char*>(p.ckpt);
-            decode8(*reinterpret_cast<const uint32_t*>(base + at),
-                    reinterpret_cast<const float*>(base + ckpt_scale_offset((size_t)p.B * nck * p.D * N))[at / N], h);
-        }
-    };
-
-    Loaded<T, N, kVec> cur;
-    // The last tile (none when there are no tokens).
-    const int t_last = t_begin < t_end ? t_begin + (t_end - t_begin - 1) / kTile * kTile : t_begin - kTile;
-    if (t_begin < t_end) load(cur, t_last);
-    for (int t0 = t_last; t0 >= t_begin; t0 -= kTile) {
-        // ---- stage the tile -------------------------------------------------
-        const bool in = t0 + pt < len && t0 + pt < t_end;
-        float x[EPT], d[EPT], v[EPT], dy[EPT], dout[EPT], zz[EPT];
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) {
-            const bool on = in && pc + i < cend;
-            x[i] = on ? cur.x.get(i) : 0.f;
-            v[i] = cur.dt.get(i) + bias[i];
-            d[i] = on ? (p.softplus ? softplus(v[i]) : v[i]) : 0.f;
-            dout[i] = on ? cur.dy.get(i) : 0.f;
-            zz[i] = Z && on ? cur.z.get(i) : 0.f;
-            dy[i] = Z ? dout[i] * zz[i] * sigmoid(zz[i]) : dout[i];
-            s_du[pt][pl + i] = make_float2(d[i], kMap ? 0.f : d[i] * x[i]);
-            s_dy[pt][pl + i] = dy[i];
-        }
-        if (has_bc) {
-            const bool inb = t0 + bt < len && t0 + bt < t_end;
-#pragma unroll
-            for (int i = 0; i < BC; ++i) {
-                if (!kMap) s_b[bt][bn + i] = inb ? cur.b.get(i) : 0.f;
-                s_c[bt][bn + i] = inb ? cur.c.get(i) : 0.f;
-            }
-        }
-        __syncthreads();
-        if (t0 > t_begin) load(cur, t0 - kTile);
-        if constexpr (kMap) {
-#pragma unroll
-            for (int t = kTile - 1; t >= 0; --t) {
-                const float dt = s_du[t][cl].x, dyt = s_dy[t][cl];
-                const float4 c4 = *reinterpret_cast<const float4*>(&s_c[t][n0]);
-                const float cc[4] = {c4.x, c4.y, c4.z, c4.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) carry[i] = exp2_raw(dt * a2[i]) * fmaf(dyt, cc[i], carry[i]);
-                dsum += dt;
-            }
-        } else {
-            // ---- the states of the tile again -------------------------------
-            float h0[4], a[kTile][4], h[kTile][4];
-            entry(t0, h0);
-            float keep = 0.f;
-#pragma unroll
-            for (int t = 0; t < kTile; ++t) {
-                const float2 du = s_du[t][cl];
-                const float4 b4 = *reinterpret_cast<const float4*>(&s_b[t][n0]);
-                const float bb[4] = {b4.x, b4.y, b4.z, b4.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    a[t][i] = exp2_raw(du.x * a2[i]);
-                    h[t][i] = fmaf(a[t][i], t == 0 ? h0[i] : h[t - 1][i], du.y * bb[i]);
-                }
-                if (Z) {
-                    const float4 c4 = *reinterpret_cast<const float4*>(&s_c[t][n0]);
-                    const float y = group_sum<P>(dot4(make_float4(h[t][0], h[t][1], h[t][2], h[t][3]), c4));
-                    keep = t % P == piece ? y : keep;
-                    if (t % P == P - 1) s_o[2][t - (P - 1) + piece][cl] = keep;
-                }
-            }
-            // ---- the adjoint, last token first ------------------------------
-            float tA[4] = {0.f, 0.f, 0.f, 0.f}, keep0 = 0.f, keep1 = 0.f;
-#pragma unroll
-            for (int t = kTile - 1; t >= 0; --t) {
-                const float2 du = s_du[t][cl];
-                const float dyt = s_dy[t][cl];
-                const float4 b4 = *reinterpret_cast<const float4*>(&s_b[t][n0]);
-                const float4 c4 = *reinterpret_cast<const float4*>(&s_c[t][n0]);
-                const float bb[4] = {b4.x, b4.y, b4.z, b4.w}, cc[4] = {c4.x, c4.y, c4.z, c4.w};
-                float bc[8], sb = 0.f, sr = 0.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float gr = fmaf(dyt, cc[i], carry[i]);
-                    bc[i] = gr * du.y;
-                    bc[4 + i] = dyt * h[t][i];
-                    sb = fmaf(gr, bb[i], sb);
-                    carry[i] = a[t][i] * gr;
-                    const float r = carry[i] * (t == 0 ? h0[i] : h[t - 1][i]);
-                    sr = fmaf(r, A[i], sr);
-                    tA[i] = fmaf(r, du.x, tA[i]);
-                }
-                sb = group_sum<P>(sb);
-                sr = group_sum<P>(sr);
-                keep0 = t % P == piece ? sb : keep0;
-                keep1 = t % P == piece ? sr : keep1;
-                if (t % P == 0) {
-                    s_o[0][t + piece][cl] = keep0;
-                    s_o[1][t + piece][cl] = keep1;
-                }
-                float f[2];
-                fold8<P>(bc, f);
-                // Lanes whose low channel bits are 0 hold the sums of their states.
-                if ((lane & 15) / P == 0) {
-                    const int n = n0 + 2 * ((lane >> 4) & 1) + (lane >> 5);
-                    s_red[wave][t][n] = f[0];
-                    s_red[wave][t][N + n] = f[1];
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dA[i] += tA[i];
-        }
-        __syncthreads();
+    auto load = [&](Loaded<T, N, kVec>& r, int i) {
+        const int n = rows_of(i);
+        const int bytes = n > 0 ? (n - 1) * row + tail : 0, bytes_bc = n > 0 ? (n - 1) * row_bc + tail_bc : 0;
+        const int64_t back = first - (int64_t)i * kTile * row, back_bc = first_bc - (int64_t)i * kTile * row_bc;
+        r.dt.load(buffer_of(static_cast<const char*>(p.dt) + back, bytes), at);
+        r.dy.load(buffer_of(static_cast<const char*>(q.dy) + back, bytes), at);
+        r.z.load(buffer_of(static_cast<const char*>(gate ? p.z : p.x) + back, gate ? bytes : 0), at);
+        r.c.load(buffer_of(static_cast<const char*>(p.Cm) + back_bc, bytes_bc), at_bc);
         if constexpr (!kMap) {
-            // ---- dB, dC of the tile -----------------------------------------
-            for (int e = tid; e < kTile * 2 * N; e += kSsmThreads) {
-                const int t = e / (2 * N), n = e % (2 * N);
-                if (t0 + t < t_end) {
-                    float s = 0.f;
+            r.x.load(buffer_of(static_cast<const char*>(p.x) + back, bytes), at);
+            r.b.load(buffer_of(static_cast<const char*>(p.Bm) + back_bc, bytes_bc), at_bc);
+            const int64_t crow = ((int64_t)b * nck + (last / kTile - i)) * p.D + c0;
+            const int states = n > 0 ? here * N : 0;
+            r.h.load(buffer_of(ck + crow * N * 4, wide ? states * 4 : 0), 4u * (hc * N + hn));
+            const __amdgpu_buffer_rsrc_t codes = buffer_of(ck + crow * N, wide ? 0 : states);
+            if constexpr (S == 2) r.codes = __builtin_amdgcn_raw_buffer_load_b16(codes, hc * N + hn, 0, 0);
+            else r.codes = __builtin_amdgcn_raw_buffer_load_b32(codes, hc * N + hn, 0, 0);
+            r.scale = __builtin_amdgcn_raw_buffer_load_b32(
+                buffer_of(ck + scales + crow * 4, wide || n == 0 ? 0 : 4 * here), 4u * hc, 0, 0);
+        }
+    };
+    auto stage = [&](const Loaded<T, N, kVec>& r, Kept<EPT>& o, int i) {
+        const int t0 = last - i * kTile, k = i & 1;
+        const int end = len < t_end ? len : t_end;
+        const bool in = t0 + pt < end;
+        float u[EPT];
 #pragma unroll
-                    for (int w = 0; w < kWaves; ++w) s += s_red[w][t][n];
-                    const size_t row = ((size_t)b * p.T + t0 + t) * p.G + g;
-                    if (q.part_bc) {
-                        q.part_bc[((size_t)j * p.B * p.T * p.G + row) * (2 * N) + n] = s;
-                    } else if (n < N) {
-                        Elem<T>::store1(static_cast<T*>(q.dBm) + row * N + n, s);
-                    } else {
-                        Elem<T>::store1(static_cast<T*>(q.dCm) + row * N + n - N, s);
-                    }
-                }
+        for (int e = 0; e < EPT; ++e) {
+            const bool on = in && e < valid;
+            const float v = r.dt.get(e) + bias[e];
+            // softplus and its slope 1 / (1 + exp(-v)) from one exponential
+            const float ex = exp_raw(-fabsf(v)), w = 1.f + ex, inv = __builtin_amdgcn_rcpf(w);
+            const float sp = fmaxf(v, 0.f) + fmaf(__builtin_amdgcn_logf(w), kLn2, ex - (w - 1.f));
+            const float d = p.softplus ? sp : v, slope = p.softplus ? (v >= 0.f ? inv : ex * inv) : 1.f;
+            const float dout = on ? r.dy.get(e) : 0.f;
+            o.d[e] = on ? d : 0.f;
+            if constexpr (!kMap) {
+                o.x[e] = on ? r.x.get(e) : 0.f;
+                o.slope[e] = on ? slope : 0.f;
             }
-            // ---- per token and channel --------------------------------------
-            if (t0 + pt < t_end) {
-                float dx[EPT], ddt[EPT], dz[EPT];
+            if (gate) {
+                const float z = on ? r.z.get(e) : 0.f, s = sigmoid(z);
+                o.dy[e] = dout * z * s;
+                if constexpr (!kMap) o.w[e] = dout * (s * fmaf(z, 1.f - s, 1.f));
+            } else {
+                o.dy[e] = dout;
+            }
+            u[e] = kMap ? 0.f : o.d[e] * o.x[e];
+        }
 #pragma unroll
-                for (int i = 0; i < EPT; ++i) {
-                    const float du = s_o[0][pt][pl + i], sr = s_o[1][pt][pl + i];
-                    dx[i] = fmaf(du, d[i], dy[i] * skip[i]);
-                    const float dd = fmaf(du, x[i], sr);
-                    ddt[i] = in ? (p.softplus ? dd * sigmoid(v[i]) : dd) : 0.f;
-                    if (Z) {
-                        const float y = fmaf(skip[i], x[i], s_o[2][pt][pl + i]), s = sigmoid(zz[i]);
-                        dz[i] = dout[i] * y * (s * fmaf(zz[i], 1.f - s, 1.f));
-                    }
-                    sum_skip[i] = fmaf(dy[i], x[i], sum_skip[i]);
-                    sum_bias[i] += ddt[i];
-                }
-                const size_t row = ((size_t)b * p.T + t0 + pt) * p.D;
-                store_piece<kVec>(static_cast<T*>(q.dx) + row, pc, cend, dx);
-                store_piece<kVec>(static_cast<T*>(q.ddt) + row, pc, cend, ddt);
-                if (Z) store_piece<kVec>(static_cast<T*>(q.dz) + row, pc, cend, dz);
+        for (int e = 0; e < EPT; ++e) {
+            s_du[k][pt][pl + e] = make_float2(o.d[e], u[e]);
+            s_dy[k][pt][pl + e] = o.dy[e];
+        }
+        if (bt < kTile) {
+            const bool inb = t0 + bt < end;
+#pragma unroll
+            for (int e = 0; e < BC; ++e) {
+                if constexpr (!kMap) s_b[k][bt][bn + e] = inb ? r.b.get(e) : 0.f;
+                s_c[k][bt][bn + e] = inb ? r.c.get(e) : 0.f;
             }
         }
+        if constexpr (!kMap) {
+            const float sc = __uint_as_float(r.scale);
+            float h[S];
+#pragma unroll
+            for (int n = 0; n < S; ++n)
+                h[n] = wide ? r.h.get(n) : (float)(int8_t)(r.codes >> (8 * n)) * sc;
+            store_cols<S>(&s_h[k][hc][hn], h);
+        }
+    };
+    auto write_out = [&](const Kept<EPT>& o, int i) {
+        const int k = i & 1, n = rows_of(i);
+        const int bytes = n > 0 ? (n - 1) * row + tail : 0;
+        const int64_t back = first - (int64_t)i * kTile * row;
+        float dx[EPT], ddt[EPT], dz[EPT];
+#pragma unroll
+        for (int e = 0; e < EPT; ++e) {
+            const int c = pl + e, base = c / 16 * PW * 16 + c % 16;
+            float du = s_o[k][0][pt][base], sr = s_o[k][1][pt][base];
+#pragma unroll
+            for (int w = 1; w < PW; ++w) {
+                du += s_o[k][0][pt][base + 16 * w];
+                sr += s_o[k][1][pt][base + 16 * w];
+            }
+            dx[e] = fmaf(du, o.d[e], o.dy[e] * skip[e]);
+            ddt[e] = fmaf(du, o.x[e], sr) * o.slope[e];
+            // before the first tile and behind the last, what is kept is stale
+            sum_skip[e] = n > 0 ? fmaf(o.dy[e], o.x[e], sum_skip[e]) : sum_skip[e];
+            sum_bias[e] = n > 0 ? sum_bias[e] + ddt[e] : sum_bias[e];
+        }
+        if (gate) {
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) {
+                const int c = pl + e, base = c / 16 * PW * 16 + c % 16;
+                float y = s_o[k][2][pt][base];
+#pragma unroll
+                for (int w = 1; w < PW; ++w) y += s_o[k][2][pt][base + 16 * w];
+                dz[e] = o.w[e] * fmaf(skip[e], o.x[e], y);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) dz[e] = 0.f;
+        }
+        store_piece<T, kVec>(buffer_of(static_cast<char*>(q.dx) + back, bytes), at, valid, dx);
+        store_piece<T, kVec>(buffer_of(static_cast<char*>(q.ddt) + back, bytes), at, valid, ddt);
+        store_piece<T, kVec>(buffer_of(static_cast<char*>(gate ? q.dz : q.dx) + back, gate ? bytes : 0), at, valid, dz);
+        // dB and dC: 2 N values per token, E neighbouring ones per thread.
+        constexpr int E = kTile * 2 * N / kStepThreads;
+        const int rt = tid * E / (2 * N), rn = tid * E % (2 * N);
+        float s[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            s[e] = s_red[k][0][rt][rn + e];
+#pragma unroll
+            for (int c = 1; c < CG; ++c) s[e] += s_red[k][c][rt][rn + e];
+        }
+        const bool part = q.part_bc != nullptr;
+        const int64_t r0 = (int64_t)b * p.T + last - (int64_t)i * kTile;   // the tile's first token
+        const int64_t prow = (((int64_t)j * p.B * p.T + r0) * p.G + g) * (2 * N);
+        const int pbytes = n > 0 ? ((n - 1) * p.G * 2 * N + 2 * N) * 4 : 0;
+        store_piece<float, true>(buffer_of(q.part_bc + prow, part ? pbytes : 0), 4u * (rt * p.G * 2 * N + rn), 1, s);
+        const int64_t orow = (r0 * p.G + g) * N;
+        const int obytes = n > 0 && !part ? (n - 1) * row_bc + tail_bc : 0;
+        const uint32_t oat = (uint32_t)((rt * p.G * N + rn % N) * (int)sizeof(T));
+        store_piece<T, true>(buffer_of(static_cast<T*>(q.dBm) + orow, obytes), oat, rn < N, s);
+        store_piece<T, true>(buffer_of(static_cast<T*>(q.dCm) + orow, obytes), oat, rn >= N, s);
+    };
+
+    Loaded<T, N, kVec> r0, r1;
+    Kept<EPT> k0 = {}, k1 = {};
+    load(r0, 0);
+    load(r1, 1);
+    auto interval = [&](int i, Loaded<T, N, kVec>& r, Kept<EPT>& o) {
+        if constexpr (!kMap) write_out(o, i - 2);
+        stage(r, o, i);
+        load(r, i + 2);
+        __syncthreads();
+    };
+    for (int i = 0; i < intervals; i += 2) {
+        interval(i, r0, k0);
+        interval(i + 1, r1, k1);
     }
-    if constexpr (kMap) {
-        if (live) {
-            store_cols<4>(p.seg_h + (seg - 1) * BDN + chn, carry);
-            if (n0 == 0) p.seg_d[(seg - 1) * BD + chn / N] = dsum;
-        }
-    } else {
-        if (live) {
-            store_cols<4>(q.part_a + (((size_t)seg * p.B + b) * p.D + ch) * N + n0, dA);
-            if (seg == 0 && q.dh0) store_cols<4>(q.dh0 + chn, carry);
-        }
-        // The per-channel vectors: the sixteen threads of a row piece's channels
-        // hold every sixteenth token each.
-        __syncthreads();
+    if constexpr (!kMap) {
+        // The per-channel vectors: sixteen threads hold a channel's tokens.
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) {
-            s_o[0][pt][pl + i] = sum_skip[i];
-            s_o[1][pt][pl + i] = sum_bias[i];
+        for (int e = 0; e < EPT; ++e) {
+            s_o[0][0][pt][pl + e] = sum_skip[e];
+            s_o[0][1][pt][pl + e] = sum_bias[e];
         }
         __syncthreads();
-        for (int c = tid; c < CH; c += kSsmThreads) {
-            if (c0 + c < cend) {
-                float s0 = 0.f, s1 = 0.f;
-                for (int t = 0; t < kTile; ++t) {
-                    s0 += s_o[0][t][c];
-                    s1 += s_o[1][t][c];
-                }
-                *reinterpret_cast<float2*>(q.part_v + (((size_t)seg * p.B + b) * p.D + c0 + c) * 2) =
-                    make_float2(s0, s1);
+        if (tid < CH && c0 + tid < cend) {
+            float s0 = 0.f, s1 = 0.f;
+            for (int t = 0; t < kTile; ++t) {
+                s0 += s_o[0][0][t][tid];
+                s1 += s_o[0][1][t][tid];
             }
+            *reinterpret_cast<float2*>(q.part_v + (((size_t)seg * p.B + b) * p.D + c0 + tid) * 2) = make_float2(s0, s1);
         }
     }
 }
@@ -383,7 +473,7 @@ __global__ __launch_bounds__(256) void ssm_params_kernel(const float* __restrict
 
 template <typename T, int N>
 hipError_t launch_bwd(const SsmBwdArgs& q, hipStream_t stream) {
-    using S = Shape<N>;
+    using S = Shape<N, kStates<N>>;
     const SsmArgs& p = q.f;
     const int Dg = p.D / p.G, blocks = (Dg + S::CH - 1) / S::CH;
     const unsigned per = (unsigned)p.B * p.G * blocks;
@@ -391,14 +481,14 @@ hipError_t launch_bwd(const SsmBwdArgs& q, hipStream_t stream) {
     hipError_t e;
     if (p.nseg > 1 && per > 0) {
         const dim3 grid(per * (p.nseg - 1));
-        if (vec) ssm_bwd_kernel<T, N, true, true><<<grid, kSsmThreads, 0, stream>>>(q, blocks);
-        else ssm_bwd_kernel<T, N, false, true><<<grid, kSsmThreads, 0, stream>>>(q, blocks);
+        if (vec) ssm_bwd_kernel<T, N, true, true><<<grid, 2 * kStepThreads, 0, stream>>>(q, blocks);
+        else ssm_bwd_kernel<T, N, false, true><<<grid, 2 * kStepThreads, 0, stream>>>(q, blocks);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (per > 0) {
         const dim3 grid(per * p.nseg);
-        if (vec) ssm_bwd_kernel<T, N, true, false><<<grid, kSsmThreads, 0, stream>>>(q, blocks);
-        else ssm_bwd_kernel<T, N, false, false><<<grid, kSsmThreads, 0, stream>>>(q, blocks);
+        if (vec) ssm_bwd_kernel<T, N, true, false><<<grid, 2 * kStepThreads, 0, stream>>>(q, blocks);
+        else ssm_bwd_kernel<T, N, false, false><<<grid, 2 * kStepThreads, 0, stream>>>(q, blocks);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     const size_t rows = (size_t)p.B * p.T * p.G;

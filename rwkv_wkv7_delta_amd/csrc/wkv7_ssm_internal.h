@@ -10,10 +10,12 @@ namespace wkv7 {
 
 constexpr int kSsmChunk = 16;      // tokens per state checkpoint and per kernel tile
 constexpr int kSsmThreads = 256;   // lanes that hold a scan workgroup's states
-constexpr int kSsmStates = 4;      // states of a channel per lane
+constexpr int kSsmStates = 4;      // states of a channel per lane (forward)
 
-// Channels that one scan workgroup takes: N / 4 lanes per channel.
+// Channels that one workgroup takes: of the forward (four states per lane) and of
+// the backward (two, at N = 64 four).
 inline int ssm_channels(int N) { return kSsmThreads * kSsmStates / N; }
+inline int ssm_bwd_channels(int N) { return kSsmThreads * (N == 64 ? 4 : 2) / N; }
 
 struct SsmArgs {
     int B, T, D, N, G;

@@ -1,17 +1,17 @@
 // wkv7_ssm_tile.h -- how the selective scan's kernels lay their work over a
 // workgroup.
 //
-// A workgroup takes CH = 1024 / N channels of one group and one batch row and
+// A workgroup takes CH = 256 S / N channels of one group and one batch row and
 // walks the tokens in tiles of 16.  Four step waves own the states: each of
-// their sixteen 16-lane rows takes 16 channels (one per lane) and four of their
-// N states, so a channel's states lie over P = N / 4 rows.  Four staging waves
+// their sixteen 16-lane rows takes 16 channels (one per lane) and S of their N
+// states, so a channel's states lie over P = N / S rows.  Four staging waves
 // move everything else: they load the token rows two tiles ahead, form what
 // depends on token and channel only, once, and leave it in LDS as fp32, read
 // the partial sums that the step waves leave there, and store whole row pieces.
 // One barrier per tile; both sides of every hand-over are double-buffered.
 //
 // With 16 channels on a row and 16 tokens in a tile, lane t of a row holds the
-// row's four values of B and C for token t, and the products broadcast them by
+// row's S values of B and C for token t, and the products broadcast them by
 // DPP (row_newbcast:t) as an operand: no LDS read per token for B and C, which
 // otherwise (16 bytes per lane and token each) took more LDS time than the
 // products themselves take on the vector ALU.
@@ -25,10 +25,10 @@ namespace wkv7 {
 constexpr int kTile = kSsmChunk;
 constexpr int kStepThreads = 256;    // four step waves, then four staging waves
 
-template <int N>
+template <int N, int S>
 struct Shape {
-    static constexpr int P = N / kSsmStates;               // rows of 16 lanes per channel
-    static constexpr int CH = kStepThreads * kSsmStates / N;   // channels per workgroup
+    static constexpr int P = N / S;                        // rows of 16 lanes per channel
+    static constexpr int CH = kStepThreads * S / N;        // channels per workgroup
     static constexpr int EPT = CH / 16;                    // channels of a staging thread's piece
     static constexpr int BC = kTile * N / kStepThreads > 0 ? kTile * N / kStepThreads : 1;
     static constexpr int YS = CH + 16;                     // row stride of the partial sums
@@ -37,15 +37,34 @@ struct Shape {
 
 // Where a step lane stands: its channel in the workgroup, its first state, and
 // the index of its group of states.
-template <int N>
+template <int N, int S>
 struct StepLane {
     int cl, part, n0, t;   // t: the token whose B and C the lane holds
     __device__ __forceinline__ explicit StepLane(int tid) {
         const int row = tid / 16;
         t = tid % 16;
-        cl = row / Shape<N>::P * 16 + t;
-        part = row % Shape<N>::P;
-        n0 = part * kSsmStates;
+        cl = row / Shape<N, S>::P * 16 + t;
+        part = row % Shape<N, S>::P;
+        n0 = part * S;
+    }
+};
+
+// The workgroup's place in the problem.  The device hands workgroups to its
+// eight XCDs in turn; giving each XCD a run of consecutive places keeps
+// neighbouring channel blocks, which share cache lines of the token rows and
+// the rows of B and C, behind one L2.
+struct Place {
+    int j, g, b, seg;
+    __device__ __forceinline__ Place(int blocks, int G, int B) {
+        unsigned u = blockIdx.x;
+        const unsigned n = gridDim.x, per = n / 8;
+        if (u < per * 8) u = u % 8 * per + u / 8;
+        j = u % blocks;
+        u /= blocks;
+        g = u % G;
+        u /= G;
+        b = u % B;
+        seg = u / B;
     }
 };
 
@@ -60,7 +79,8 @@ __device__ __forceinline__ float row_bcast(float x) {
 // would spend a move on each).  What the hardware leaves to the code here: an
 // exponential's result may not be read by the very next vector instruction (the
 // s_nop), and a DPP operand not have been written by the two vector instructions
-// before (the four updates in front).
+// before (the two updates in front).  Updates and read-out alternate: a DPP sum
+// that waits for the one before it takes 8 clocks instead of 4.
 template <int t>
 __device__ __forceinline__ float step_read(float (&h)[4], const float (&a)[4], const float (&x)[4],
                                            const float (&c)[4]) {
@@ -68,10 +88,10 @@ __device__ __forceinline__ float step_read(float (&h)[4], const float (&a)[4], c
     asm("s_nop 0\n\t"
         "v_fma_f32 %0, %5, %0, %9\n\t"
         "v_fma_f32 %1, %6, %1, %10\n\t"
-        "v_fma_f32 %2, %7, %2, %11\n\t"
-        "v_fma_f32 %3, %8, %3, %12\n\t"
         "v_mul_f32_dpp %4, %13, %0 row_newbcast:%17 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fma_f32 %2, %7, %2, %11\n\t"
         "v_fmac_f32_dpp %4, %14, %1 row_newbcast:%17 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fma_f32 %3, %8, %3, %12\n\t"
         "v_fmac_f32_dpp %4, %15, %2 row_newbcast:%17 row_mask:0xf bank_mask:0xf\n\t"
         "v_fmac_f32_dpp %4, %16, %3 row_newbcast:%17 row_mask:0xf bank_mask:0xf"
         : "+&v"(h[0]), "+&v"(h[1]), "+&v"(h[2]), "+&v"(h[3]), "=&v"(y)
