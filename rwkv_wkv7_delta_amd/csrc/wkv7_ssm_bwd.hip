@@ -53,34 +53,59 @@ struct Kept {
     float x[EPT], d[EPT], slope[EPT], dy[EPT], w[EPT];   // w: dz per read-out
 };
 
-template <int kCtrl>
-__device__ __forceinline__ float dpp(float x) {
-    return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), kCtrl, 0xF, 0xF, true));
+// Two folds of four values each over the sixteen lanes of every row: a step adds
+// a lane's partner (row_ror:8, row_half_mirror, quad_perm) and, while there are
+// several values, keeps one by a bit of the lane, which the bank masks of the DPP
+// writes select.  Lane l returns the sum of value 2 bit2(l) + bit3(l) of each.
+// Two folds at once, so that each fills the two instructions that must lie
+// between writing a register and reading it through DPP in the other.
+__device__ __forceinline__ void fold_row(const float (&v)[4], const float (&w)[4], float& y, float& z) {
+    float x0, x1, u0, u1;
+    asm("s_nop 1\n\t"
+        "v_add_f32_dpp %0, %7, %7 row_ror:8 row_mask:0xf bank_mask:0xf\n\t"
+        "v_add_f32_dpp %1, %9, %9 row_ror:8 row_mask:0xf bank_mask:0xf\n\t"
+        "v_add_f32_dpp %2, %11, %11 row_ror:8 row_mask:0xf bank_mask:0xf\n\t"
+        "v_add_f32_dpp %3, %13, %13 row_ror:8 row_mask:0xf bank_mask:0xf\n\t"
+        "v_add_f32_dpp %0, %6, %6 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+        "v_add_f32_dpp %1, %8, %8 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+        "v_add_f32_dpp %2, %10, %10 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+        "v_add_f32_dpp %3, %12, %12 row_ror:8 row_mask:0xf bank_mask:0x3\n\t"
+        "v_add_f32_dpp %4, %0, %0 row_half_mirror row_mask:0xf bank_mask:0xf\n\t"
+        "v_add_f32_dpp %5, %2, %2 row_half_mirror row_mask:0xf bank_mask:0xf\n\t"
+        "v_add_f32_dpp %4, %1, %1 row_half_mirror row_mask:0xf bank_mask:0xa\n\t"
+        "v_add_f32_dpp %5, %3, %3 row_half_mirror row_mask:0xf bank_mask:0xa\n\t"
+        "s_nop 0\n\t"
+        "v_add_f32_dpp %4, %4, %4 quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+        "v_add_f32_dpp %5, %5, %5 quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 0\n\t"
+        "v_add_f32_dpp %4, %4, %4 quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+        "v_add_f32_dpp %5, %5, %5 quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
+        "s_nop 0"
+        : "=&v"(x0), "=&v"(x1), "=&v"(u0), "=&v"(u1), "=&v"(y), "=&v"(z)
+        : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(w[0]), "v"(w[1]), "v"(w[2]), "v"(w[3]));
 }
 
-// Sums of 2 S values over the sixteen lanes of every row, folded: each step adds
-// a lane's partner (row_ror:8, row_half_mirror, quad_perm) and, while there are
-// two values, keeps one of them by a bit of the lane.  Lane l returns the sum of
-// value 2 bit2 + bit3 (S = 2), 4 bit1 + 2 bit2 + bit3 (S = 4).
-template <int S>
-__device__ __forceinline__ float fold_row(const float (&v)[2 * S], bool bit3, bool bit2, bool bit1) {
-    float x[S], y[S / 2];
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-        const float p = v[2 * i] + dpp<0x128>(v[2 * i]), q = v[2 * i + 1] + dpp<0x128>(v[2 * i + 1]);
-        x[i] = bit3 ? q : p;
-    }
-#pragma unroll
-    for (int i = 0; i < S / 2; ++i) {
-        const float p = x[2 * i] + dpp<0x141>(x[2 * i]), q = x[2 * i + 1] + dpp<0x141>(x[2 * i + 1]);
-        y[i] = bit2 ? q : p;
-    }
-    float z = y[0] + dpp<0x4E>(y[0]);
-    if constexpr (S == 4) {
-        const float q = y[1] + dpp<0x4E>(y[1]);
-        z = bit1 ? q : z;
-    }
-    return z + dpp<0xB1>(z);
+// One step of the adjoint for two states: g <- g + c dy (c broadcast from lane t of
+// the row), v = (g u, dy h), the sum of (b broadcast) g, and g <- a g.  The two
+// products in front keep the DPP operands c two instructions from whatever wrote
+// them.
+template <int t>
+__device__ __forceinline__ float adjoint_step(float& g0, float& g1, float (&v)[4], float c0, float c1, float b0,
+                                              float b1, float dy, float u, float h0, float h1, float a0, float a1) {
+    float sb;
+    asm("v_mul_f32 %4, %11, %13\n\t"
+        "v_mul_f32 %5, %11, %14\n\t"
+        "v_fmac_f32_dpp %0, %7, %11 row_newbcast:%17 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %1, %8, %11 row_newbcast:%17 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32 %2, %0, %12\n\t"
+        "v_mul_f32_dpp %6, %9, %0 row_newbcast:%17 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32 %3, %1, %12\n\t"
+        "v_mul_f32 %0, %15, %0\n\t"
+        "v_fmac_f32_dpp %6, %10, %1 row_newbcast:%17 row_mask:0xf bank_mask:0xf\n\t"
+        "v_mul_f32 %1, %16, %1"
+        : "+&v"(g0), "+&v"(g1), "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(sb)
+        : "v"(c0), "v"(c1), "v"(b0), "v"(b1), "v"(dy), "v"(u), "v"(h0), "v"(h1), "v"(a0), "v"(a1), "n"(t));
+    return sb;
 }
 
 // Sums of four values over the wave's four rows: row r returns the sum of value
@@ -93,7 +118,7 @@ __device__ __forceinline__ float fold_rows(float v0, float v1, float v2, float v
     return __uint_as_float(c[0]) + __uint_as_float(c[1]);
 }
 
-template <typename T, int N, bool kVec, bool kMap>
+template <typename T, int N, bool kVec, bool kMap, bool kGate>
 __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmBwdArgs q, int blocks) {
     constexpr int S = kStates<N>;
     using Sh = Shape<N, S>;
@@ -120,13 +145,11 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
     const int tiles = (t_end - t_begin + kTile - 1) / kTile;
     const int intervals = (tiles + 5) / 4 * 4;   // tiles + 2, to a multiple of 4
     const size_t BDN = (size_t)p.B * p.D * N, BD = (size_t)p.B * p.D;
-    const bool gate = p.z != nullptr;
 
     if (threadIdx.x < kStepThreads) {
         // ---- step waves: the i-th tile from the end in interval i + 1 ---------------
         const StepLane<N, S> at(threadIdx.x);
         const int wave = threadIdx.x / 64, l = threadIdx.x % 16, row = threadIdx.x / 16 % 4;
-        const bool bit3 = l & 8, bit2 = l & 4, bit1 = l & 2;
         const bool live = c0 + at.cl < cend;
         const int ch = live ? c0 + at.cl : cend - 1;
         const size_t chn = ((size_t)b * p.D + ch) * N + at.n0;
@@ -148,12 +171,11 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
             }
         }
         // Where the lane leaves its folded sums: row r of the wave holds value 0,
-        // 2, 1, 3 of a fold over the rows; a lane of a row the state (and dB or
-        // dC) that fold_row names.
+        // 2, 1, 3 of a fold over the rows; a lane of a row the state and dB or dC
+        // (the values are (g u, dy h) of two states) that fold_row names.
         const int col = wave * 16 + l;
         const int second = row >> 1, later = row & 1;   // of (sb, sr), (t, t - 1)
-        const int n_red = S == 2 ? at.n0 + (bit3 ? 1 : 0) + (bit2 ? N : 0)
-                                 : at.n0 + (bit3 ? 1 : 0) + (bit2 ? 2 : 0) + (bit1 ? N : 0);
+        const int n_red = at.n0 + (l >> 3) + (l >> 2 & 1) * N;
         for (int i = 0; i < intervals; ++i) {
             __syncthreads();
             if (i >= tiles) continue;
@@ -182,11 +204,12 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
                     for (int n = 0; n < S; ++n) {
                         a[t][n] = exp2_raw(du.x * a2[n]);
                         h[t][n] = fmaf(a[t][n], t == 0 ? h0[n] : h[t > 0 ? t - 1 : 0][n], row_bcast<t>(b4[n]) * du.y);
-                        y = n == 0 ? row_bcast<t>(c4[n]) * h[t][n] : y + row_bcast<t>(c4[n]) * h[t][n];
+                        if constexpr (kGate)
+                            y = n == 0 ? row_bcast<t>(c4[n]) * h[t][n] : y + row_bcast<t>(c4[n]) * h[t][n];
                     }
                     y4[t % 4] = y;
                     if constexpr (t % 4 == 3) {
-                        if (gate) {
+                        if constexpr (kGate) {
                             // rows 0, 1, 2, 3 hold tokens t - 3, t - 1, t - 2, t
                             const float f = fold_rows(y4[0], y4[1], y4[2], y4[3]);
                             s_o[k][2][t - 3 + 2 * later + second][col] = f;
@@ -197,28 +220,42 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
                 float tA[S], sb1 = 0.f, sr1 = 0.f;
 #pragma unroll
                 for (int n = 0; n < S; ++n) tA[n] = 0.f;
+                float v1[4];
                 each_token_back([&](auto tok) {
                     constexpr int t = decltype(tok)::v;
                     const float2 du = s_du[k][t][at.cl];
                     const float dyt = s_dy[k][t][at.cl];
-                    float v[2 * S], sb = 0.f, sr = 0.f;
+                    float v[S / 2][4], sb = 0.f, sr = 0.f;
+#pragma unroll
+                    for (int n = 0; n < S; n += 2) {
+                        const float s = adjoint_step<t>(carry[n], carry[n + 1], v[n / 2], c4[n], c4[n + 1], b4[n],
+                                                        b4[n + 1], dyt, du.y, h[t][n], h[t][n + 1], a[t][n], a[t][n + 1]);
+                        sb = n == 0 ? s : sb + s;
+                    }
 #pragma unroll
                     for (int n = 0; n < S; ++n) {
-                        const float gr = carry[n] + row_bcast<t>(c4[n]) * dyt;
-                        v[n] = gr * du.y;
-                        v[S + n] = dyt * h[t][n];
-                        sb = n == 0 ? row_bcast<t>(b4[n]) * gr : sb + row_bcast<t>(b4[n]) * gr;
-                        carry[n] = a[t][n] * gr;
                         const float r = carry[n] * (t == 0 ? h0[n] : h[t > 0 ? t - 1 : 0][n]);
                         sr = n == 0 ? r * A[n] : fmaf(r, A[n], sr);
                         tA[n] = fmaf(r, du.x, tA[n]);
                     }
-                    s_red[k][at.cl / 16][t][n_red] = fold_row<S>(v, bit3, bit2, bit1);
+                    float f0, f1;
+                    if constexpr (S == 4) {
+                        fold_row(v[0], v[1], f0, f1);
+                        s_red[k][at.cl / 16][t][n_red] = f0;
+                        s_red[k][at.cl / 16][t][n_red + 2] = f1;
+                    }
                     if constexpr (t % 2 == 1) {
                         sb1 = sb;
                         sr1 = sr;
+#pragma unroll
+                        for (int n = 0; n < 4; ++n) v1[n] = v[0][n];
                     } else {   // value 0: (sb, t + 1), 1: (sr, t + 1), 2: (sb, t), 3: (sr, t)
                         s_o[k][second][t + 1 - later][col] = fold_rows(sb1, sr1, sb, sr);
+                        if constexpr (S == 2) {
+                            fold_row(v1, v[0], f0, f1);
+                            s_red[k][at.cl / 16][t + 1][n_red] = f0;
+                            s_red[k][at.cl / 16][t][n_red] = f1;
+                        }
                     }
                 });
 #pragma unroll
@@ -264,33 +301,55 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
     const int64_t first_bc = (((int64_t)b * p.T + last) * p.G + g) * N * (int)sizeof(T);
     const int nck = (p.T + kTile - 1) / kTile;
     const bool wide = p.ckpt_bits == 32;
-    const char* const ck = static_cast<const char*>(p.ckpt);
-    const size_t scales = wide ? 0 : ckpt_scale_offset((size_t)p.B * nck * p.D * N);
-    // Byte offset of the i-th tile from the end, and rows of it in the segment.
+    // Where the next tile is read, and where the next gradients go (two tiles
+    // behind); every pointer moves back by a tile at a time.
+    auto from = [&](const void* base, int64_t off) { return static_cast<const char*>(base) + off; };
+    const char *x_at = from(p.x, first), *dt_at = from(p.dt, first), *z_at = from(p.z, first),
+               *dy_at = from(q.dy, first), *b_at = from(p.Bm, first_bc), *c_at = from(p.Cm, first_bc);
+    const int64_t crow = ((int64_t)b * nck + last / kTile) * p.D + c0;   // the first tile's entry states
+    const char* ck_at = from(p.ckpt, crow * N * (wide ? 4 : 1));
+    const char* scale_at = from(p.ckpt, wide ? 0 : (int64_t)ckpt_scale_offset((size_t)p.B * nck * p.D * N) + crow * 4);
+    const int64_t step = (int64_t)kTile * row, step_bc = (int64_t)kTile * row_bc;
+    const int64_t step_ck = (int64_t)p.D * N * (wide ? 4 : 1), step_scale = wide ? 0 : (int64_t)p.D * 4;
+    char *dx_at = const_cast<char*>(from(q.dx, first + 2 * step)), *ddt_at = const_cast<char*>(from(q.ddt, first + 2 * step)),
+         *dz_at = const_cast<char*>(from(q.dz, first + 2 * step));
+    // dB and dC, or their partial sums [2N].
+    const bool part = q.part_bc != nullptr;
+    const int row_out = part ? p.G * 2 * N * 4 : row_bc, tail_out = part ? 2 * N * 4 : tail_bc;
+    const int64_t first_out =
+        part ? (((int64_t)j * p.B * p.T + (int64_t)b * p.T + last) * p.G + g) * (2 * N * 4) : first_bc;
+    const int64_t step_out = (int64_t)kTile * row_out;
+    char *db_at = const_cast<char*>(from(part ? (void*)q.part_bc : q.dBm, first_out + 2 * step_out)),
+         *dc_at = const_cast<char*>(from(part ? (void*)q.part_bc : q.dCm, first_out + 2 * step_out));
+    // Rows of the i-th tile from the end.
     auto rows_of = [&](int i) {
-        const int t0 = last - i * kTile, left = t_end - t0;
+        const int left = t_end - last + i * kTile;
         return i >= tiles || i < 0 ? 0 : left < kTile ? left : kTile;
     };
     auto load = [&](Loaded<T, N, kVec>& r, int i) {
         const int n = rows_of(i);
         const int bytes = n > 0 ? (n - 1) * row + tail : 0, bytes_bc = n > 0 ? (n - 1) * row_bc + tail_bc : 0;
-        const int64_t back = first - (int64_t)i * kTile * row, back_bc = first_bc - (int64_t)i * kTile * row_bc;
-        r.dt.load(buffer_of(static_cast<const char*>(p.dt) + back, bytes), at);
-        r.dy.load(buffer_of(static_cast<const char*>(q.dy) + back, bytes), at);
-        r.z.load(buffer_of(static_cast<const char*>(gate ? p.z : p.x) + back, gate ? bytes : 0), at);
-        r.c.load(buffer_of(static_cast<const char*>(p.Cm) + back_bc, bytes_bc), at_bc);
+        r.dt.load(buffer_of(dt_at, bytes), at);
+        r.dy.load(buffer_of(dy_at, bytes), at);
+        if constexpr (kGate) r.z.load(buffer_of(z_at, bytes), at);
+        r.c.load(buffer_of(c_at, bytes_bc), at_bc);
         if constexpr (!kMap) {
-            r.x.load(buffer_of(static_cast<const char*>(p.x) + back, bytes), at);
-            r.b.load(buffer_of(static_cast<const char*>(p.Bm) + back_bc, bytes_bc), at_bc);
-            const int64_t crow = ((int64_t)b * nck + (last / kTile - i)) * p.D + c0;
+            r.x.load(buffer_of(x_at, bytes), at);
+            r.b.load(buffer_of(b_at, bytes_bc), at_bc);
             const int states = n > 0 ? here * N : 0;
-            r.h.load(buffer_of(ck + crow * N * 4, wide ? states * 4 : 0), 4u * (hc * N + hn));
-            const __amdgpu_buffer_rsrc_t codes = buffer_of(ck + crow * N, wide ? 0 : states);
-            if constexpr (S == 2) r.codes = __builtin_amdgcn_raw_buffer_load_b16(codes, hc * N + hn, 0, 0);
-            else r.codes = __builtin_amdgcn_raw_buffer_load_b32(codes, hc * N + hn, 0, 0);
-            r.scale = __builtin_amdgcn_raw_buffer_load_b32(
-                buffer_of(ck + scales + crow * 4, wide || n == 0 ? 0 : 4 * here), 4u * hc, 0, 0);
+            r.h.load(buffer_of(ck_at, wide ? states * 4 : 0), 4u * (hc * N + hn));
+            if constexpr (S == 2) r.codes = __builtin_amdgcn_raw_buffer_load_b16(buffer_of(ck_at, wide ? 0 : states), hc * N + hn, 0, 0);
+            else r.codes = __builtin_amdgcn_raw_buffer_load_b32(buffer_of(ck_at, wide ? 0 : states), hc * N + hn, 0, 0);
+            r.scale = __builtin_amdgcn_raw_buffer_load_b32(buffer_of(scale_at, wide || n == 0 ? 0 : 4 * here), 4u * hc, 0, 0);
         }
+        dt_at -= step;
+        dy_at -= step;
+        z_at -= step;
+        x_at -= step;
+        b_at -= step_bc;
+        c_at -= step_bc;
+        ck_at -= step_ck;
+        scale_at -= step_scale;
     };
     auto stage = [&](const Loaded<T, N, kVec>& r, Kept<EPT>& o, int i) {
         const int t0 = last - i * kTile, k = i & 1;
@@ -304,21 +363,20 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
             // softplus and its slope 1 / (1 + exp(-v)) from one exponential
             const float ex = exp_raw(-fabsf(v)), w = 1.f + ex, inv = __builtin_amdgcn_rcpf(w);
             const float sp = fmaxf(v, 0.f) + fmaf(__builtin_amdgcn_logf(w), kLn2, ex - (w - 1.f));
-            const float d = p.softplus ? sp : v, slope = p.softplus ? (v >= 0.f ? inv : ex * inv) : 1.f;
-            const float dout = on ? r.dy.get(e) : 0.f;
-            o.d[e] = on ? d : 0.f;
-            if constexpr (!kMap) {
-                o.x[e] = on ? r.x.get(e) : 0.f;
-                o.slope[e] = on ? slope : 0.f;
-            }
-            if (gate) {
+            const float sl = inv * (v >= 0.f ? 1.f : ex);
+            const float d = p.softplus ? sp : v, slope = p.softplus ? sl : 1.f;
+            const float dout = on ? r.dy.get(e) : 0.f, x = kMap || !on ? 0.f : r.x.get(e);
+            float dy = dout;
+            if constexpr (kGate) {
                 const float z = on ? r.z.get(e) : 0.f, s = sigmoid(z);
-                o.dy[e] = dout * z * s;
-                if constexpr (!kMap) o.w[e] = dout * (s * fmaf(z, 1.f - s, 1.f));
-            } else {
-                o.dy[e] = dout;
+                dy = dout * (z * s);
+                o.w[e] = dout * (s * fmaf(z, 1.f - s, 1.f));
             }
-            u[e] = kMap ? 0.f : o.d[e] * o.x[e];
+            o.dy[e] = dy;
+            o.x[e] = x;
+            o.d[e] = on ? d : 0.f;
+            o.slope[e] = on ? slope : 0.f;
+            u[e] = o.d[e] * x;
         }
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
@@ -337,15 +395,16 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
             const float sc = __uint_as_float(r.scale);
             float h[S];
 #pragma unroll
-            for (int n = 0; n < S; ++n)
-                h[n] = wide ? r.h.get(n) : (float)(int8_t)(r.codes >> (8 * n)) * sc;
+            for (int n = 0; n < S; ++n) {
+                const float code = (float)(int8_t)(r.codes >> (8 * n)) * sc, full = r.h.get(n);
+                h[n] = wide ? full : code;
+            }
             store_cols<S>(&s_h[k][hc][hn], h);
         }
     };
     auto write_out = [&](const Kept<EPT>& o, int i) {
         const int k = i & 1, n = rows_of(i);
         const int bytes = n > 0 ? (n - 1) * row + tail : 0;
-        const int64_t back = first - (int64_t)i * kTile * row;
         float dx[EPT], ddt[EPT], dz[EPT];
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
@@ -362,7 +421,7 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
             sum_skip[e] = n > 0 ? fmaf(o.dy[e], o.x[e], sum_skip[e]) : sum_skip[e];
             sum_bias[e] = n > 0 ? sum_bias[e] + ddt[e] : sum_bias[e];
         }
-        if (gate) {
+        if constexpr (kGate) {
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
                 const int c = pl + e, base = c / 16 * PW * 16 + c % 16;
@@ -371,13 +430,10 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
                 for (int w = 1; w < PW; ++w) y += s_o[k][2][pt][base + 16 * w];
                 dz[e] = o.w[e] * fmaf(skip[e], o.x[e], y);
             }
-        } else {
-#pragma unroll
-            for (int e = 0; e < EPT; ++e) dz[e] = 0.f;
         }
-        store_piece<T, kVec>(buffer_of(static_cast<char*>(q.dx) + back, bytes), at, valid, dx);
-        store_piece<T, kVec>(buffer_of(static_cast<char*>(q.ddt) + back, bytes), at, valid, ddt);
-        store_piece<T, kVec>(buffer_of(static_cast<char*>(gate ? q.dz : q.dx) + back, gate ? bytes : 0), at, valid, dz);
+        store_piece<T, kVec>(buffer_of(dx_at, bytes), at, valid, dx);
+        store_piece<T, kVec>(buffer_of(ddt_at, bytes), at, valid, ddt);
+        if constexpr (kGate) store_piece<T, kVec>(buffer_of(dz_at, bytes), at, valid, dz);
         // dB and dC: 2 N values per token, E neighbouring ones per thread.
         constexpr int E = kTile * 2 * N / kStepThreads;
         const int rt = tid * E / (2 * N), rn = tid * E % (2 * N);
@@ -388,16 +444,16 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
 #pragma unroll
             for (int c = 1; c < CG; ++c) s[e] += s_red[k][c][rt][rn + e];
         }
-        const bool part = q.part_bc != nullptr;
-        const int64_t r0 = (int64_t)b * p.T + last - (int64_t)i * kTile;   // the tile's first token
-        const int64_t prow = (((int64_t)j * p.B * p.T + r0) * p.G + g) * (2 * N);
-        const int pbytes = n > 0 ? ((n - 1) * p.G * 2 * N + 2 * N) * 4 : 0;
-        store_piece<float, true>(buffer_of(q.part_bc + prow, part ? pbytes : 0), 4u * (rt * p.G * 2 * N + rn), 1, s);
-        const int64_t orow = (r0 * p.G + g) * N;
-        const int obytes = n > 0 && !part ? (n - 1) * row_bc + tail_bc : 0;
+        const int obytes = n > 0 ? (n - 1) * row_out + tail_out : 0;
         const uint32_t oat = (uint32_t)((rt * p.G * N + rn % N) * (int)sizeof(T));
-        store_piece<T, true>(buffer_of(static_cast<T*>(q.dBm) + orow, obytes), oat, rn < N, s);
-        store_piece<T, true>(buffer_of(static_cast<T*>(q.dCm) + orow, obytes), oat, rn >= N, s);
+        store_piece<float, true>(buffer_of(db_at, part ? obytes : 0), 4u * (rt * p.G * 2 * N + rn), 1, s);
+        store_piece<T, true>(buffer_of(db_at, part ? 0 : obytes), oat, rn < N, s);
+        store_piece<T, true>(buffer_of(dc_at, part ? 0 : obytes), oat, rn >= N, s);
+        dx_at -= step;
+        ddt_at -= step;
+        dz_at -= step;
+        db_at -= step_out;
+        dc_at -= step_out;
     };
 
     Loaded<T, N, kVec> r0, r1;
@@ -471,26 +527,32 @@ __global__ __launch_bounds__(256) void ssm_params_kernel(const float* __restrict
     }
 }
 
+template <typename T, int N, bool kVec, bool kGate>
+hipError_t launch_bwd_v(const SsmBwdArgs& q, int blocks, hipStream_t stream) {
+    constexpr int threads = 2 * kStepThreads;
+    const SsmArgs& p = q.f;
+    const unsigned per = (unsigned)p.B * p.G * blocks;
+    if (per == 0) return hipSuccess;
+    if (p.nseg > 1) {
+        ssm_bwd_kernel<T, N, kVec, true, kGate><<<dim3(per * (p.nseg - 1)), threads, 0, stream>>>(q, blocks);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    ssm_bwd_kernel<T, N, kVec, false, kGate><<<dim3(per * p.nseg), threads, 0, stream>>>(q, blocks);
+    return hipGetLastError();
+}
+
 template <typename T, int N>
 hipError_t launch_bwd(const SsmBwdArgs& q, hipStream_t stream) {
     using S = Shape<N, kStates<N>>;
     const SsmArgs& p = q.f;
     const int Dg = p.D / p.G, blocks = (Dg + S::CH - 1) / S::CH;
-    const unsigned per = (unsigned)p.B * p.G * blocks;
     const bool vec = Dg % S::EPT == 0;
-    hipError_t e;
-    if (p.nseg > 1 && per > 0) {
-        const dim3 grid(per * (p.nseg - 1));
-        if (vec) ssm_bwd_kernel<T, N, true, true><<<grid, 2 * kStepThreads, 0, stream>>>(q, blocks);
-        else ssm_bwd_kernel<T, N, false, true><<<grid, 2 * kStepThreads, 0, stream>>>(q, blocks);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    if (per > 0) {
-        const dim3 grid(per * p.nseg);
-        if (vec) ssm_bwd_kernel<T, N, true, false><<<grid, 2 * kStepThreads, 0, stream>>>(q, blocks);
-        else ssm_bwd_kernel<T, N, false, false><<<grid, 2 * kStepThreads, 0, stream>>>(q, blocks);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
+    hipError_t e = p.z ? (vec ? launch_bwd_v<T, N, true, true>(q, blocks, stream)
+                              : launch_bwd_v<T, N, false, true>(q, blocks, stream))
+                       : (vec ? launch_bwd_v<T, N, true, false>(q, blocks, stream)
+                              : launch_bwd_v<T, N, false, false>(q, blocks, stream));
+    if (e != hipSuccess) return e;
     const size_t rows = (size_t)p.B * p.T * p.G;
     if (q.part_bc && rows > 0) {
         const size_t n = (rows * 2 * N / 4 + 255) / 256;

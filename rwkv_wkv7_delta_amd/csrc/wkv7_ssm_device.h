@@ -174,8 +174,14 @@ __device__ __forceinline__ void store_piece(__amdgpu_buffer_rsrc_t r, uint32_t a
 }
 
 // `bytes` at p as a buffer (0: every access lies outside, nothing is touched).
+// Both are the same in every lane; said so, or the compiler may keep them per
+// lane and loop over the lanes at each access.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* p, int bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), (short)0, bytes, 0x00020000);
+    const uint64_t u = reinterpret_cast<uint64_t>(p);
+    const uint64_t v = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(u >> 32)) << 32 |
+                       (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)u);
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(v), (short)0,
+                                             __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
 }
 
 // Sum and maximum over each aligned group of P = 2, 4, 8 or 16 lanes, in every lane.
