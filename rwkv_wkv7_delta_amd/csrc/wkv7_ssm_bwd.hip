@@ -126,13 +126,16 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
     constexpr int PW = P / 4;                  // waves that share a channel
     constexpr int CG = CH / 16;                // groups of 16 channels
     constexpr int OS = 64 + 16;                // row stride of the sums over states
-    __shared__ __attribute__((aligned(16))) float2 s_du[2][kTile][CH];
-    __shared__ __attribute__((aligned(16))) float s_dy[2][kTile][CH];
-    __shared__ __attribute__((aligned(16))) float s_b[2][kMap ? 1 : kTile][N], s_c[2][kTile][N];
+    // A tile's inputs and its read-outs are live through four intervals (staged;
+    // its states; its adjoint; its gradients), the rest through two.
+    __shared__ __attribute__((aligned(16))) float2 s_du[4][kTile][CH];
+    __shared__ __attribute__((aligned(16))) float s_dy[4][kTile][CH];
+    __shared__ __attribute__((aligned(16))) float s_b[4][kMap ? 1 : kTile][N], s_c[4][kTile][N];
     __shared__ __attribute__((aligned(16))) float s_h[2][kMap ? 1 : CH][HS];
-    // Per token: sums over a wave's states of du, of r A, and the read-out; and
+    // Per token: the read-out, the sums over a wave's states of du and of r A; and
     // the sums over 16 channels of dB and dC.
-    __shared__ __attribute__((aligned(16))) float s_o[2][kMap ? 1 : 3][kMap ? 1 : kTile][OS];
+    __shared__ __attribute__((aligned(16))) float s_y[kGate && !kMap ? 4 : 1][kMap ? 1 : kTile][OS];
+    __shared__ __attribute__((aligned(16))) float s_o[2][kMap ? 1 : 2][kMap ? 1 : kTile][OS];
     __shared__ __attribute__((aligned(16))) float s_red[2][kMap ? 1 : CG][kMap ? 1 : kTile][2 * N];
 
     const SsmArgs& p = q.f;
@@ -143,11 +146,12 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
     const int t_begin = seg * p.seg_len;
     const int t_end = seg == p.nseg - 1 ? p.T : t_begin + p.seg_len;
     const int tiles = (t_end - t_begin + kTile - 1) / kTile;
-    const int intervals = (tiles + 5) / 4 * 4;   // tiles + 2, to a multiple of 4
+    const int intervals = (tiles + 6) / 4 * 4;   // tiles + 3, to a multiple of 4
     const size_t BDN = (size_t)p.B * p.D * N, BD = (size_t)p.B * p.D;
 
     if (threadIdx.x < kStepThreads) {
-        // ---- step waves: the i-th tile from the end in interval i + 1 ---------------
+        // ---- step waves, tiles counted from the end: in interval i + 1 the states of
+        // ---- tile i and, interleaved with them, the adjoint of tile i - 1 ----------------
         const StepLane<N, S> at(threadIdx.x);
         const int wave = threadIdx.x / 64, l = threadIdx.x % 16, row = threadIdx.x / 16 % 4;
         const bool live = c0 + at.cl < cend;
@@ -176,13 +180,13 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
         const int col = wave * 16 + l;
         const int second = row >> 1, later = row & 1;   // of (sb, sr), (t, t - 1)
         const int n_red = at.n0 + (l >> 3) + (l >> 2 & 1) * N;
-        for (int i = 0; i < intervals; ++i) {
-            __syncthreads();
-            if (i >= tiles) continue;
-            const int k = i & 1;
-            float c4[S];
-            load_cols<S>(&s_c[k][at.t][at.n0], c4);
-            if constexpr (kMap) {
+        if constexpr (kMap) {
+            for (int i = 0; i < intervals; ++i) {
+                __syncthreads();
+                if (i >= tiles) continue;
+                const int k = i & 3;
+                float c4[S];
+                load_cols<S>(&s_c[k][at.t][at.n0], c4);
                 each_token_back([&](auto tok) {
                     constexpr int t = decltype(tok)::v;
                     const float d = s_du[k][t][at.cl].x, dyt = s_dy[k][t][at.cl];
@@ -191,76 +195,101 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
                         carry[n] = exp2_raw(d * a2[n]) * (carry[n] + row_bcast<t>(c4[n]) * dyt);
                     dsum += d;
                 });
-            } else {
-                // The states of the tile again.
-                float b4[S], h0[S], a[kTile][S], h[kTile][S], y4[4];
-                load_cols<S>(&s_b[k][at.t][at.n0], b4);
-                load_cols<S>(&s_h[k][at.cl][at.n0], h0);
+            }
+        } else {
+            // A tile's transitions and states, from the state entering it.
+            struct Tile {
+                float a[kTile][S], h[kTile][S], h0[S], b[S], c[S];
+            };
+            float y4[4], v1[4], tA[S], sb1, sr1;
+            auto begin = [&](Tile& w, int i) {
+                load_cols<S>(&s_b[i & 3][at.t][at.n0], w.b);
+                load_cols<S>(&s_c[i & 3][at.t][at.n0], w.c);
+                load_cols<S>(&s_h[i & 1][at.cl][at.n0], w.h0);
+            };
+            auto states = [&](auto tok, Tile& w, int i) {
+                constexpr int t = decltype(tok)::v;
+                const float2 du = s_du[i & 3][t][at.cl];
+                float y = 0.f;
+#pragma unroll
+                for (int n = 0; n < S; ++n) {
+                    w.a[t][n] = exp2_raw(du.x * a2[n]);
+                    w.h[t][n] = fmaf(w.a[t][n], t == 0 ? w.h0[n] : w.h[t > 0 ? t - 1 : 0][n], row_bcast<t>(w.b[n]) * du.y);
+                    if constexpr (kGate)
+                        y = n == 0 ? row_bcast<t>(w.c[n]) * w.h[t][n] : y + row_bcast<t>(w.c[n]) * w.h[t][n];
+                }
+                if constexpr (kGate) {
+                    y4[t % 4] = y;
+                    // rows 0, 1, 2, 3 hold tokens t - 3, t - 1, t - 2, t
+                    if constexpr (t % 4 == 3)
+                        s_y[i & 3][t - 3 + 2 * later + second][col] = fold_rows(y4[0], y4[1], y4[2], y4[3]);
+                }
+            };
+            auto adjoint = [&](auto tok, const Tile& w, int i) {
+                constexpr int t = decltype(tok)::v;
+                const int k = i & 1;
+                const float2 du = s_du[i & 3][t][at.cl];
+                const float dyt = s_dy[i & 3][t][at.cl];
+                float v[S / 2][4], sb = 0.f, sr = 0.f;
+#pragma unroll
+                for (int n = 0; n < S; n += 2) {
+                    const float s = adjoint_step<t>(carry[n], carry[n + 1], v[n / 2], w.c[n], w.c[n + 1], w.b[n], w.b[n + 1],
+                                                    dyt, du.y, w.h[t][n], w.h[t][n + 1], w.a[t][n], w.a[t][n + 1]);
+                    sb = n == 0 ? s : sb + s;
+                }
+#pragma unroll
+                for (int n = 0; n < S; ++n) {
+                    const float r = carry[n] * (t == 0 ? w.h0[n] : w.h[t > 0 ? t - 1 : 0][n]);
+                    sr = n == 0 ? r * A[n] : fmaf(r, A[n], sr);
+                    tA[n] = t == kTile - 1 ? r * du.x : fmaf(r, du.x, tA[n]);
+                }
+                float f0, f1;
+                if constexpr (S == 4) {
+                    fold_row(v[0], v[1], f0, f1);
+                    s_red[k][at.cl / 16][t][n_red] = f0;
+                    s_red[k][at.cl / 16][t][n_red + 2] = f1;
+                }
+                if constexpr (t % 2 == 1) {
+                    sb1 = sb;
+                    sr1 = sr;
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) v1[n] = v[0][n];
+                } else {   // value 0: (sb, t + 1), 1: (sr, t + 1), 2: (sb, t), 3: (sr, t)
+                    s_o[k][second][t + 1 - later][col] = fold_rows(sb1, sr1, sb, sr);
+                    if constexpr (S == 2) {
+                        fold_row(v1, v[0], f0, f1);
+                        s_red[k][at.cl / 16][t + 1][n_red] = f0;
+                        s_red[k][at.cl / 16][t][n_red] = f1;
+                    }
+                }
+            };
+            // Two chains that do not depend on each other, a token of each in turn
+            // (one wave to a SIMD beside a staging wave leaves a single chain's
+            // latencies bare); as many states die on one side as are born on the
+            // other.  The states behind the last tile are formed and not used.
+            auto both = [&](const Tile& w, Tile& next, int i) {
+                begin(next, i);
                 each_token([&](auto tok) {
                     constexpr int t = decltype(tok)::v;
-                    const float2 du = s_du[k][t][at.cl];
-                    float y = 0.f;
-#pragma unroll
-                    for (int n = 0; n < S; ++n) {
-                        a[t][n] = exp2_raw(du.x * a2[n]);
-                        h[t][n] = fmaf(a[t][n], t == 0 ? h0[n] : h[t > 0 ? t - 1 : 0][n], row_bcast<t>(b4[n]) * du.y);
-                        if constexpr (kGate)
-                            y = n == 0 ? row_bcast<t>(c4[n]) * h[t][n] : y + row_bcast<t>(c4[n]) * h[t][n];
-                    }
-                    y4[t % 4] = y;
-                    if constexpr (t % 4 == 3) {
-                        if constexpr (kGate) {
-                            // rows 0, 1, 2, 3 hold tokens t - 3, t - 1, t - 2, t
-                            const float f = fold_rows(y4[0], y4[1], y4[2], y4[3]);
-                            s_o[k][2][t - 3 + 2 * later + second][col] = f;
-                        }
-                    }
-                });
-                // The adjoint, last token first.
-                float tA[S], sb1 = 0.f, sr1 = 0.f;
-#pragma unroll
-                for (int n = 0; n < S; ++n) tA[n] = 0.f;
-                float v1[4];
-                each_token_back([&](auto tok) {
-                    constexpr int t = decltype(tok)::v;
-                    const float2 du = s_du[k][t][at.cl];
-                    const float dyt = s_dy[k][t][at.cl];
-                    float v[S / 2][4], sb = 0.f, sr = 0.f;
-#pragma unroll
-                    for (int n = 0; n < S; n += 2) {
-                        const float s = adjoint_step<t>(carry[n], carry[n + 1], v[n / 2], c4[n], c4[n + 1], b4[n],
-                                                        b4[n + 1], dyt, du.y, h[t][n], h[t][n + 1], a[t][n], a[t][n + 1]);
-                        sb = n == 0 ? s : sb + s;
-                    }
-#pragma unroll
-                    for (int n = 0; n < S; ++n) {
-                        const float r = carry[n] * (t == 0 ? h0[n] : h[t > 0 ? t - 1 : 0][n]);
-                        sr = n == 0 ? r * A[n] : fmaf(r, A[n], sr);
-                        tA[n] = fmaf(r, du.x, tA[n]);
-                    }
-                    float f0, f1;
-                    if constexpr (S == 4) {
-                        fold_row(v[0], v[1], f0, f1);
-                        s_red[k][at.cl / 16][t][n_red] = f0;
-                        s_red[k][at.cl / 16][t][n_red + 2] = f1;
-                    }
-                    if constexpr (t % 2 == 1) {
-                        sb1 = sb;
-                        sr1 = sr;
-#pragma unroll
-                        for (int n = 0; n < 4; ++n) v1[n] = v[0][n];
-                    } else {   // value 0: (sb, t + 1), 1: (sr, t + 1), 2: (sb, t), 3: (sr, t)
-                        s_o[k][second][t + 1 - later][col] = fold_rows(sb1, sr1, sb, sr);
-                        if constexpr (S == 2) {
-                            fold_row(v1, v[0], f0, f1);
-                            s_red[k][at.cl / 16][t + 1][n_red] = f0;
-                            s_red[k][at.cl / 16][t][n_red] = f1;
-                        }
-                    }
+                    states(tok, next, i);
+                    adjoint(Tok<kTile - 1 - t>(), w, i - 1);
                 });
 #pragma unroll
                 for (int n = 0; n < S; ++n) dA[n] += tA[n];
+            };
+            Tile w0, w1;
+            __syncthreads();
+            begin(w0, 0);
+            each_token([&](auto tok) { states(tok, w0, 0); });
+            int i = 1;
+            while (i <= tiles) {
+                __syncthreads();
+                both(w0, w1, i++);
+                if (i > tiles) break;
+                __syncthreads();
+                both(w1, w0, i++);
             }
+            for (; i < intervals; ++i) __syncthreads();
         }
         if (live) {
             if constexpr (kMap) {
@@ -276,7 +305,7 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
     }
 
     // ---- staging waves: the i-th tile from the end in interval i, the gradients of
-    // ---- the (i - 2)-th ---------------------------------------------------------------
+    // ---- the (i - 3)-th ---------------------------------------------------------------
     const int tid = threadIdx.x - kStepThreads;
     const int len = row_length(p.lengths, b, p.T);
     const int pt = tid / 16, pl = (tid % 16) * EPT;
@@ -301,7 +330,7 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
     const int64_t first_bc = (((int64_t)b * p.T + last) * p.G + g) * N * (int)sizeof(T);
     const int nck = (p.T + kTile - 1) / kTile;
     const bool wide = p.ckpt_bits == 32;
-    // Where the next tile is read, and where the next gradients go (two tiles
+    // Where the next tile is read, and where the next gradients go (three tiles
     // behind); every pointer moves back by a tile at a time.
     auto from = [&](const void* base, int64_t off) { return static_cast<const char*>(base) + off; };
     const char *x_at = from(p.x, first), *dt_at = from(p.dt, first), *z_at = from(p.z, first),
@@ -311,16 +340,16 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
     const char* scale_at = from(p.ckpt, wide ? 0 : (int64_t)ckpt_scale_offset((size_t)p.B * nck * p.D * N) + crow * 4);
     const int64_t step = (int64_t)kTile * row, step_bc = (int64_t)kTile * row_bc;
     const int64_t step_ck = (int64_t)p.D * N * (wide ? 4 : 1), step_scale = wide ? 0 : (int64_t)p.D * 4;
-    char *dx_at = const_cast<char*>(from(q.dx, first + 2 * step)), *ddt_at = const_cast<char*>(from(q.ddt, first + 2 * step)),
-         *dz_at = const_cast<char*>(from(q.dz, first + 2 * step));
+    char *dx_at = const_cast<char*>(from(q.dx, first + 3 * step)), *ddt_at = const_cast<char*>(from(q.ddt, first + 3 * step)),
+         *dz_at = const_cast<char*>(from(q.dz, first + 3 * step));
     // dB and dC, or their partial sums [2N].
     const bool part = q.part_bc != nullptr;
     const int row_out = part ? p.G * 2 * N * 4 : row_bc, tail_out = part ? 2 * N * 4 : tail_bc;
     const int64_t first_out =
         part ? (((int64_t)j * p.B * p.T + (int64_t)b * p.T + last) * p.G + g) * (2 * N * 4) : first_bc;
     const int64_t step_out = (int64_t)kTile * row_out;
-    char *db_at = const_cast<char*>(from(part ? (void*)q.part_bc : q.dBm, first_out + 2 * step_out)),
-         *dc_at = const_cast<char*>(from(part ? (void*)q.part_bc : q.dCm, first_out + 2 * step_out));
+    char *db_at = const_cast<char*>(from(part ? (void*)q.part_bc : q.dBm, first_out + 3 * step_out)),
+         *dc_at = const_cast<char*>(from(part ? (void*)q.part_bc : q.dCm, first_out + 3 * step_out));
     // Rows of the i-th tile from the end.
     auto rows_of = [&](int i) {
         const int left = t_end - last + i * kTile;
@@ -352,7 +381,7 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
         scale_at -= step_scale;
     };
     auto stage = [&](const Loaded<T, N, kVec>& r, Kept<EPT>& o, int i) {
-        const int t0 = last - i * kTile, k = i & 1;
+        const int t0 = last - i * kTile, k = i & 3;
         const int end = len < t_end ? len : t_end;
         const bool in = t0 + pt < end;
         float u[EPT];
@@ -399,7 +428,7 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
                 const float code = (float)(int8_t)(r.codes >> (8 * n)) * sc, full = r.h.get(n);
                 h[n] = wide ? full : code;
             }
-            store_cols<S>(&s_h[k][hc][hn], h);
+            store_cols<S>(&s_h[i & 1][hc][hn], h);
         }
     };
     auto write_out = [&](const Kept<EPT>& o, int i) {
@@ -425,9 +454,9 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
                 const int c = pl + e, base = c / 16 * PW * 16 + c % 16;
-                float y = s_o[k][2][pt][base];
+                float y = s_y[i & 3][pt][base];
 #pragma unroll
-                for (int w = 1; w < PW; ++w) y += s_o[k][2][pt][base + 16 * w];
+                for (int w = 1; w < PW; ++w) y += s_y[i & 3][pt][base + 16 * w];
                 dz[e] = o.w[e] * fmaf(skip[e], o.x[e], y);
             }
         }
@@ -457,18 +486,20 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
     };
 
     Loaded<T, N, kVec> r0, r1;
-    Kept<EPT> k0 = {}, k1 = {};
+    Kept<EPT> k0 = {}, k1 = {}, k2 = {}, k3 = {};
     load(r0, 0);
     load(r1, 1);
-    auto interval = [&](int i, Loaded<T, N, kVec>& r, Kept<EPT>& o) {
-        if constexpr (!kMap) write_out(o, i - 2);
+    auto interval = [&](int i, Loaded<T, N, kVec>& r, Kept<EPT>& o, const Kept<EPT>& done) {
+        if constexpr (!kMap) write_out(done, i - 3);
         stage(r, o, i);
         load(r, i + 2);
         __syncthreads();
     };
-    for (int i = 0; i < intervals; i += 2) {
-        interval(i, r0, k0);
-        interval(i + 1, r1, k1);
+    for (int i = 0; i < intervals; i += 4) {
+        interval(i, r0, k0, k1);
+        interval(i + 1, r1, k1, k2);
+        interval(i + 2, r0, k2, k3);
+        interval(i + 3, r1, k3, k0);
     }
     if constexpr (!kMap) {
         // The per-channel vectors: sixteen threads hold a channel's tokens.
