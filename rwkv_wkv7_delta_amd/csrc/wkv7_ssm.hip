@@ -134,36 +134,59 @@ __global__ __launch_bounds__(2 * kStepThreads) void ssm_fwd_kernel(const SsmArgs
     }
     const int nck = (p.T + kTile - 1) / kTile;
     const bool gate = p.z != nullptr;
-
-    // A tile's rows of a token tensor as a buffer: the workgroup's channels of
-    // its first row to those of its last; rows behind the segment read as 0 and
-    // are not written.  So nothing that touches memory in the loop below is
-    // conditional, and each wait covers exactly the loads it needs.
-    const uint32_t at = (uint32_t)(((size_t)pt * p.D + pl) * sizeof(T));
-    const uint32_t at_bc = bt < kTile ? (uint32_t)(((size_t)bt * p.G * N + bn) * sizeof(T)) : kNowhere;
-    const int valid = cend - c0 - pl, here = cend - c0 < CH ? cend - c0 : CH;
-    const int row = p.D * (int)sizeof(T), tail = (cend - c0) * (int)sizeof(T);
-    const int row_bc = p.G * N * (int)sizeof(T), tail_bc = N * (int)sizeof(T);
-    const size_t first = (((size_t)b * p.T + t_begin) * p.D + c0) * sizeof(T);
-    const size_t first_bc = (((size_t)b * p.T + t_begin) * p.G + g) * N * sizeof(T);
-    const char *x_at = static_cast<const char*>(p.x) + first, *dt_at = static_cast<const char*>(p.dt) + first,
-               *z_at = static_cast<const char*>(gate ? p.z : p.x) + first,
-               *b_at = static_cast<const char*>(p.Bm) + first_bc, *c_at = static_cast<const char*>(p.Cm) + first_bc;
-    char* y_at = static_cast<char*>(p.y) + (int64_t)first - 2 * (int64_t)kTile * row;   // written two tiles later
-    auto load = [&](Loaded<T, N, kVec>& r, int left) {   // left: rows from the tile's first to the segment's end
-        const int n = left < kTile ? left : kTile;
-        const int bytes = n > 0 ? (n - 1) * row + tail : 0, bytes_bc = n > 0 ? (n - 1) * row_bc + tail_bc : 0;
-        r.x.load(buffer_of(x_at, bytes), at);
-        r.dt.load(buffer_of(dt_at, bytes), at);
-        if constexpr (!kMap) r.z.load(buffer_of(z_at, gate ? bytes : 0), at);
-        r.b.load(buffer_of(b_at, bytes_bc), at_bc);
-        if constexpr (!kMap) r.c.load(buffer_of(c_at, bytes_bc), at_bc);
-        x_at += kTile * (int64_t)row;
-        dt_at += kTile * (int64_t)row;
-        z_at += kTile * (int64_t)row;
-        b_at += kTile * (int64_t)row_bc;
-        c_at += kTile * (int64_t)row_bc;
+    // The segment's tokens of a tensor as one buffer, from the workgroup's first
+    // channel to the end of its group in the last row: one offset per thread moves
+    // along all of them, rows behind the segment and pieces behind the group read
+    // as 0 and are not written.  So nothing that touches memory in the loop below
+    // is conditional, and each wait covers exactly the loads it needs.
+    const bool full = kVec || EPT == 1;   // a piece lies inside its group or behind it
+    const bool dead = c0 + pl >= cend;
+    const int valid = full ? 1 : cend - c0 - pl, here = cend - c0 < CH ? cend - c0 : CH;
+    const uint32_t row = p.D * (uint32_t)sizeof(T), row_bc = p.G * N * (uint32_t)sizeof(T);
+    const int tokens = t_end - t_begin;
+    auto rows_of = [&](const void* base, bool on) {
+        return buffer_of(static_cast<const char*>(base) + (((int64_t)b * p.T + t_begin) * p.D + c0) * (int)sizeof(T),
+                         on && tokens > 0 ? (int)((tokens - 1) * row + (cend - c0) * (uint32_t)sizeof(T)) : 0);
     };
+    auto rows_of_bc = [&](const void* base) {
+        return buffer_of(static_cast<const char*>(base) + (((int64_t)b * p.T + t_begin) * p.G + g) * N * (int)sizeof(T),
+                         tokens > 0 ? (int)((tokens - 1) * row_bc + N * (uint32_t)sizeof(T)) : 0);
+    };
+    const __amdgpu_buffer_rsrc_t x_rows = rows_of(p.x, true), dt_rows = rows_of(p.dt, true),
+                                 z_rows = rows_of(gate ? p.z : p.x, gate), y_rows = rows_of(p.y, !kMap),
+                                 b_rows = rows_of_bc(p.Bm), c_rows = rows_of_bc(p.Cm);
+    const uint32_t step = dead ? 0 : kTile * row, step_bc = bt < kTile ? kTile * row_bc : 0;
+    uint32_t at = dead ? kNowhere : pt * row + pl * (uint32_t)sizeof(T);
+    uint32_t at_bc = bt < kTile ? bt * row_bc + bn * (uint32_t)sizeof(T) : kNowhere;
+    uint32_t out_at = dead ? kNowhere : at - 2 * step;   // written two tiles later; before that, outside
+    auto load = [&](Loaded<T, N, kVec>& r) {
+        r.x.load(x_rows, at);
+        r.dt.load(dt_rows, at);
+        if constexpr (!kMap) r.z.load(z_rows, at);
+        r.b.load(b_rows, at_bc);
+        if constexpr (!kMap) r.c.load(c_rows, at_bc);
+        at += step;
+        at_bc += step_bc;
+    };
+    // The checkpoints of the segment: the thread's four states of channel hc, two
+    // tiles behind.
+    const int hc = tid / P, hn = (tid % P) * kSsmStates;
+    const int blocks_here = (tokens + kTile - 1) / kTile;
+    const bool wide = p.ckpt_bits == 32;
+    __amdgpu_buffer_rsrc_t h_rows, code_rows, scale_rows;
+    uint32_t code_at = 0, scale_at = 0;
+    const uint32_t code_step = hc < here ? (uint32_t)p.D * N : 0, scale_step = hc < here && hn == 0 ? 4u * p.D : 0;
+    if constexpr (kCkpt) {
+        const int64_t crow = ((int64_t)b * nck + t_begin / kTile) * p.D + c0;   // the first tile's first channel
+        const int size = blocks_here > 0 ? ((blocks_here - 1) * p.D + here) * N : 0;
+        char* const base = static_cast<char*>(p.ckpt);
+        h_rows = buffer_of(base + crow * N * 4, wide ? size * 4 : 0);
+        code_rows = buffer_of(base + (wide ? 0 : crow * N), wide ? 0 : size);
+        scale_rows = buffer_of(base + (wide ? 0 : ckpt_scale_offset((size_t)p.B * nck * p.D * N) + crow * 4),
+                               wide || blocks_here == 0 ? 0 : ((blocks_here - 1) * p.D + here) * 4);
+        code_at = hc < here ? (uint32_t)(hc * N + hn) - 2 * code_step : kNowhere / 4;
+        scale_at = hc < here && hn == 0 ? 4u * hc - 2 * scale_step : kNowhere;
+    }
     auto stage = [&](const Loaded<T, N, kVec>& r, int tile) {
         const int t0 = t_begin + tile * kTile, k = tile & 1;
         float d[EPT];
@@ -220,40 +243,33 @@ __global__ __launch_bounds__(2 * kStepThreads) void ssm_fwd_kernel(const SsmArgs
 #pragma unroll
             for (int i = 0; i < EPT; ++i) out[i] = t0 + pt < len ? out[i] : 0.f;
         }
-        const int left = tile >= 0 ? t_end - t0 : 0, n = left < kTile ? left : kTile;
-        store_piece<T, kVec>(buffer_of(y_at, n > 0 ? (n - 1) * row + tail : 0), at, valid, out);
-        y_at += kTile * (int64_t)row;
+        store_piece<T, kVec>(y_rows, out_at, valid, out);
+        out_at += step;
         if constexpr (kCkpt) {
-            const int hc = tid / P, n0 = (tid % P) * kSsmStates;
             float h[4], scale;
-            load_cols<4>(&s_h[k][hc][n0], h);
+            load_cols<4>(&s_h[k][hc][hn], h);
             const uint32_t w = encode8<P>(h, scale);
-            const bool wide = p.ckpt_bits == 32;
-            const int bytes = n > 0 ? here * N : 0;
-            const size_t crow = ((size_t)b * nck + (tile >= 0 ? t0 / kTile : 0)) * p.D + c0;   // the first channel's
-            char* const base = static_cast<char*>(p.ckpt);
-            const size_t scales = ckpt_scale_offset((size_t)p.B * nck * p.D * N);
-            store_piece<float, true>(buffer_of(base + crow * N * 4, wide ? 4 * bytes : 0), 4u * (hc * N + n0), 1, h);
-            __builtin_amdgcn_raw_buffer_store_b32(w, buffer_of(base + crow * N, wide ? 0 : bytes), hc * N + n0, 0, 0);
-            __builtin_amdgcn_raw_buffer_store_b32(
-                __float_as_uint(scale), buffer_of(base + scales + crow * 4, wide || n <= 0 ? 0 : 4 * here),
-                n0 == 0 ? 4u * hc : kNowhere, 0, 0);
+            store_piece<float, true>(h_rows, code_at * 4, 1, h);
+            __builtin_amdgcn_raw_buffer_store_b32(w, code_rows, code_at, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(scale), scale_rows, scale_at, 0, 0);
+            code_at += code_step;
+            scale_at += scale_step;
         }
     };
 
     // Two tiles of loads in flight, and the x and z of the two tiles whose
     // read-outs are still to come: four sets of registers in turn (moving a set
     // that is still being loaded would wait for it).  Behind the last tile and
-    // before the first the loads and stores meet empty buffers, and what is
+    // before the first the loads and stores lie outside their buffers, and what is
     // staged is not read.
     Loaded<T, N, kVec> r0, r1, r2, r3;
-    load(r0, t_end - t_begin);
-    load(r1, t_end - t_begin - kTile);
+    load(r0);
+    load(r1);
     r2 = r0, r3 = r0;
     auto interval = [&](int i, const Loaded<T, N, kVec>& r, Loaded<T, N, kVec>& old) {
         stage(r, i);
         if constexpr (!kMap) write_out(old.x, old.z, i - 2);
-        load(old, t_end - t_begin - (i + 2) * kTile);
+        load(old);
         __syncthreads();
     };
     for (int i = 0; i < intervals; i += 4) {

@@ -72,8 +72,9 @@ int check_ssm(const wkv7_ssm_desc* d) {
     if (d->N != 8 && d->N != 16 && d->N != 32 && d->N != 64) return WKV7_ERR_UNSUPPORTED;
     if (d->dtype != WKV7_F32 && d->dtype != WKV7_BF16) return WKV7_ERR_UNSUPPORTED;
     if (d->ckpt_bits != 0 && d->ckpt_bits != 8 && d->ckpt_bits != 32) return WKV7_ERR_UNSUPPORTED;
-    // A tile of sixteen rows is addressed with 32-bit byte offsets.
-    if (d->T > INT32_MAX - 64 || d->D > (1 << 24) || (int64_t)d->G * d->N > (1 << 22)) return WKV7_ERR_UNSUPPORTED;
+    // A segment's rows are addressed with 32-bit byte offsets (token_bytes): a tile
+    // of sixteen tokens has to fit.
+    if (d->T > INT32_MAX - 64 || d->D > (1 << 22) || (int64_t)d->G * d->N > (1 << 22)) return WKV7_ERR_UNSUPPORTED;
     const int64_t blocks = ((int64_t)d->T + 15) / 16, most = (int64_t)1 << 40;
     // A launch has at most B G ceil(D / G / channels) workgroups per segment.
     if (!product_fits(d->B, d->T, d->D, 1, most) || !product_fits(d->B, blocks, d->D, d->N, most) ||
@@ -86,6 +87,13 @@ int check_ssm(const wkv7_ssm_desc* d) {
 int64_t channel_blocks(const wkv7_ssm_desc* d, bool backward) {
     const int ch = backward ? wkv7::ssm_bwd_channels(d->N) : wkv7::ssm_channels(d->N);
     return ((int64_t)d->D / d->G + ch - 1) / ch;
+}
+
+// Bytes by which a token moves the widest of the buffers that a segment's
+// workgroup walks: fp32 tokens, fp32 checkpoints (every 16 tokens), partial sums.
+int64_t token_bytes(const wkv7_ssm_desc* d) {
+    const int64_t tok = (int64_t)d->D * (d->N / 4 > 4 ? d->N / 4 : 4), bc = (int64_t)d->G * d->N * 8;
+    return tok > bc ? tok : bc;
 }
 
 // Time segments: a launch without them has one workgroup per batch row, group
@@ -105,7 +113,12 @@ SsmPlan plan_ssm(const wkv7_ssm_desc* d, bool backward) {
     int64_t n = 2 * kUnits / wgs;
     if (n > d->T / kMinSegmentTokens) n = d->T / kMinSegmentTokens;
     if (n > kMaxSegments) n = kMaxSegments;
-    if (n < 3) return none;
+    if (n < 3) n = 1;
+    // No buffer of a segment reaches 2^31 bytes (with a few tiles to spare).
+    const int64_t most = ((int64_t)INT32_MAX / token_bytes(d) - 128) / 16 * 16;
+    const int64_t least = most >= 16 ? (d->T + most - 1) / most : d->T;
+    if (n < least) n = least;
+    if (n < 2) return none;
     const int64_t len = (((int64_t)d->T + n - 1) / n + 15) / 16 * 16;
     n = ((int64_t)d->T + len - 1) / len;
     return SsmPlan{(int)n, (int)len};

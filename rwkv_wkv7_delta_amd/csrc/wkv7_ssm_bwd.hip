@@ -311,7 +311,6 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
     const int pt = tid / 16, pl = (tid % 16) * EPT;
     const int be = tid * BC, bt = be / N, bn = be % N;
     const int hc = tid * S / N, hn = tid * S % N;     // the thread's entry states
-    const int valid = cend - c0 - pl, here = cend - c0 < CH ? cend - c0 : CH;
     float bias[EPT], skip[EPT], sum_skip[EPT], sum_bias[EPT];
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
@@ -320,100 +319,122 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
         skip[i] = p.dskip ? p.dskip[c] : 0.f;
         sum_skip[i] = sum_bias[i] = 0.f;
     }
-    // Buffers as in the forward: no memory access in the loop is conditional.
-    const uint32_t at = (uint32_t)(((size_t)pt * p.D + pl) * sizeof(T));
-    const uint32_t at_bc = bt < kTile ? (uint32_t)(((size_t)bt * p.G * N + bn) * sizeof(T)) : kNowhere;
-    const int row = p.D * (int)sizeof(T), tail = (cend - c0) * (int)sizeof(T);
-    const int row_bc = p.G * N * (int)sizeof(T), tail_bc = N * (int)sizeof(T);
-    const int last = t_begin + (tiles - 1) * kTile;   // the first tile's first token
-    const int64_t first = (((int64_t)b * p.T + last) * p.D + c0) * (int)sizeof(T);
-    const int64_t first_bc = (((int64_t)b * p.T + last) * p.G + g) * N * (int)sizeof(T);
+    // Buffers over the segment as in the forward, walked backwards: no memory access
+    // in the loop is conditional.  Tiles before the first token lie below the
+    // buffers' start, which as an unsigned offset is behind their end.
+    const bool full = kVec || EPT == 1;
+    const bool dead = c0 + pl >= cend;
+    const int valid = full ? 1 : cend - c0 - pl, here = cend - c0 < CH ? cend - c0 : CH;
+    const uint32_t row = p.D * (uint32_t)sizeof(T), row_bc = p.G * N * (uint32_t)sizeof(T);
+    const int tokens = t_end - t_begin;
+    auto rows_of = [&](const void* base) {
+        return buffer_of(static_cast<const char*>(base) + (((int64_t)b * p.T + t_begin) * p.D + c0) * (int)sizeof(T),
+                         tokens > 0 ? (int)((tokens - 1) * row + (cend - c0) * (uint32_t)sizeof(T)) : 0);
+    };
+    auto rows_of_bc = [&](const void* base, bool on) {
+        return buffer_of(static_cast<const char*>(base) + (((int64_t)b * p.T + t_begin) * p.G + g) * N * (int)sizeof(T),
+                         on && tokens > 0 ? (int)((tokens - 1) * row_bc + N * (uint32_t)sizeof(T)) : 0);
+    };
+    const int last = (tiles - 1) * kTile;   // the first tile's first token in the segment
+    const uint32_t step = dead ? 0 : kTile * row, step_bc = bt < kTile ? kTile * row_bc : 0;
+    uint32_t at = dead ? kNowhere : (last + pt) * row + pl * (uint32_t)sizeof(T);
+    uint32_t at_bc = bt < kTile ? (last + bt) * row_bc + bn * (uint32_t)sizeof(T) : kNowhere;
+    const __amdgpu_buffer_rsrc_t dt_rows = rows_of(p.dt), dy_rows = rows_of(q.dy), c_rows = rows_of_bc(p.Cm, true);
+    __amdgpu_buffer_rsrc_t x_rows, z_rows, b_rows, h_rows, code_rows, scale_rows, dx_rows, ddt_rows, dz_rows, part_rows,
+        db_rows, dc_rows;
+    // Entry states: fp32, or codes and scales, of the thread's S states of channel hc.
     const int nck = (p.T + kTile - 1) / kTile;
     const bool wide = p.ckpt_bits == 32;
-    // Where the next tile is read, and where the next gradients go (three tiles
-    // behind); every pointer moves back by a tile at a time.
-    auto from = [&](const void* base, int64_t off) { return static_cast<const char*>(base) + off; };
-    const char *x_at = from(p.x, first), *dt_at = from(p.dt, first), *z_at = from(p.z, first),
-               *dy_at = from(q.dy, first), *b_at = from(p.Bm, first_bc), *c_at = from(p.Cm, first_bc);
-    const int64_t crow = ((int64_t)b * nck + last / kTile) * p.D + c0;   // the first tile's entry states
-    const char* ck_at = from(p.ckpt, crow * N * (wide ? 4 : 1));
-    const char* scale_at = from(p.ckpt, wide ? 0 : (int64_t)ckpt_scale_offset((size_t)p.B * nck * p.D * N) + crow * 4);
-    const int64_t step = (int64_t)kTile * row, step_bc = (int64_t)kTile * row_bc;
-    const int64_t step_ck = (int64_t)p.D * N * (wide ? 4 : 1), step_scale = wide ? 0 : (int64_t)p.D * 4;
-    char *dx_at = const_cast<char*>(from(q.dx, first + 3 * step)), *ddt_at = const_cast<char*>(from(q.ddt, first + 3 * step)),
-         *dz_at = const_cast<char*>(from(q.dz, first + 3 * step));
-    // dB and dC, or their partial sums [2N].
-    const bool part = q.part_bc != nullptr;
-    const int row_out = part ? p.G * 2 * N * 4 : row_bc, tail_out = part ? 2 * N * 4 : tail_bc;
-    const int64_t first_out =
-        part ? (((int64_t)j * p.B * p.T + (int64_t)b * p.T + last) * p.G + g) * (2 * N * 4) : first_bc;
-    const int64_t step_out = (int64_t)kTile * row_out;
-    char *db_at = const_cast<char*>(from(part ? (void*)q.part_bc : q.dBm, first_out + 3 * step_out)),
-         *dc_at = const_cast<char*>(from(part ? (void*)q.part_bc : q.dCm, first_out + 3 * step_out));
-    // Rows of the i-th tile from the end.
-    auto rows_of = [&](int i) {
-        const int left = t_end - last + i * kTile;
-        return i >= tiles || i < 0 ? 0 : left < kTile ? left : kTile;
-    };
-    auto load = [&](Loaded<T, N, kVec>& r, int i) {
-        const int n = rows_of(i);
-        const int bytes = n > 0 ? (n - 1) * row + tail : 0, bytes_bc = n > 0 ? (n - 1) * row_bc + tail_bc : 0;
-        r.dt.load(buffer_of(dt_at, bytes), at);
-        r.dy.load(buffer_of(dy_at, bytes), at);
-        if constexpr (kGate) r.z.load(buffer_of(z_at, bytes), at);
-        r.c.load(buffer_of(c_at, bytes_bc), at_bc);
+    const uint32_t code_step = hc < here ? (uint32_t)p.D * N : 0, scale_step = hc < here ? 4u * p.D : 0;
+    uint32_t code_at = hc < here ? (tiles - 1) * code_step + hc * N + hn : kNowhere / 4;
+    uint32_t scale_at = hc < here ? (tiles - 1) * scale_step + 4u * hc : kNowhere;
+    // Gradients go out three tiles behind.  dB and dC: E neighbouring ones of the 2 N
+    // values of a token per thread, or their partial sums [2 N].
+    constexpr int E = kTile * 2 * N / kStepThreads;
+    const int rt = tid * E / (2 * N), rn = tid * E % (2 * N);
+    const uint32_t row_part = p.G * 2 * N * 4u, step_part = kTile * row_part, step_o = kTile * row_bc;
+    uint32_t out_at = dead ? kNowhere : at + 3 * step;
+    uint32_t part_at = (last + 3 * kTile + rt) * row_part + rn * 4u;
+    uint32_t o_at = (last + 3 * kTile + rt) * row_bc + rn % N * (uint32_t)sizeof(T);
+    if constexpr (kGate) z_rows = rows_of(p.z);
+    if constexpr (!kMap) {
+        const bool part = q.part_bc != nullptr;
+        x_rows = rows_of(p.x);
+        b_rows = rows_of_bc(p.Bm, true);
+        dx_rows = rows_of(q.dx);
+        ddt_rows = rows_of(q.ddt);
+        if constexpr (kGate) dz_rows = rows_of(q.dz);
+        const int64_t crow = ((int64_t)b * nck + t_begin / kTile) * p.D + c0;
+        const int size = tiles > 0 ? ((tiles - 1) * p.D + here) * N : 0;
+        const char* const base = static_cast<const char*>(p.ckpt);
+        h_rows = buffer_of(base + crow * N * 4, wide ? size * 4 : 0);
+        code_rows = buffer_of(base + (wide ? 0 : crow * N), wide ? 0 : size);
+        scale_rows = buffer_of(base + (wide ? 0 : ckpt_scale_offset((size_t)p.B * nck * p.D * N) + crow * 4),
+                               wide || tiles == 0 ? 0 : ((tiles - 1) * p.D + here) * 4);
+        part_rows = buffer_of(q.part_bc + (((int64_t)j * p.B * p.T + (int64_t)b * p.T + t_begin) * p.G + g) * (2 * N),
+                              part && tokens > 0 ? (int)((tokens - 1) * row_part + 2 * N * 4) : 0);
+        db_rows = rows_of_bc(q.dBm, !part);
+        dc_rows = rows_of_bc(q.dCm, !part);
+    }
+    auto load = [&](Loaded<T, N, kVec>& r) {
+        r.dt.load(dt_rows, at);
+        r.dy.load(dy_rows, at);
+        if constexpr (kGate) r.z.load(z_rows, at);
+        r.c.load(c_rows, at_bc);
         if constexpr (!kMap) {
-            r.x.load(buffer_of(x_at, bytes), at);
-            r.b.load(buffer_of(b_at, bytes_bc), at_bc);
-            const int states = n > 0 ? here * N : 0;
-            r.h.load(buffer_of(ck_at, wide ? states * 4 : 0), 4u * (hc * N + hn));
-            if constexpr (S == 2) r.codes = __builtin_amdgcn_raw_buffer_load_b16(buffer_of(ck_at, wide ? 0 : states), hc * N + hn, 0, 0);
-            else r.codes = __builtin_amdgcn_raw_buffer_load_b32(buffer_of(ck_at, wide ? 0 : states), hc * N + hn, 0, 0);
-            r.scale = __builtin_amdgcn_raw_buffer_load_b32(buffer_of(scale_at, wide || n == 0 ? 0 : 4 * here), 4u * hc, 0, 0);
+            r.x.load(x_rows, at);
+            r.b.load(b_rows, at_bc);
+            r.h.load(h_rows, code_at * 4);
+            if constexpr (S == 2) r.codes = __builtin_amdgcn_raw_buffer_load_b16(code_rows, code_at, 0, 0);
+            else r.codes = __builtin_amdgcn_raw_buffer_load_b32(code_rows, code_at, 0, 0);
+            r.scale = __builtin_amdgcn_raw_buffer_load_b32(scale_rows, scale_at, 0, 0);
         }
-        dt_at -= step;
-        dy_at -= step;
-        z_at -= step;
-        x_at -= step;
-        b_at -= step_bc;
-        c_at -= step_bc;
-        ck_at -= step_ck;
-        scale_at -= step_scale;
+        at -= step;
+        at_bc -= step_bc;
+        code_at -= code_step;
+        scale_at -= scale_step;
     };
     auto stage = [&](const Loaded<T, N, kVec>& r, Kept<EPT>& o, int i) {
-        const int t0 = last - i * kTile, k = i & 3;
+        const int t0 = t_begin + last - i * kTile, k = i & 3;
         const int end = len < t_end ? len : t_end;
-        const bool in = t0 + pt < end;
-        float u[EPT];
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
-            const bool on = in && e < valid;
             const float v = r.dt.get(e) + bias[e];
             // softplus and its slope 1 / (1 + exp(-v)) from one exponential
             const float ex = exp_raw(-fabsf(v)), w = 1.f + ex, inv = __builtin_amdgcn_rcpf(w);
             const float sp = fmaxf(v, 0.f) + fmaf(__builtin_amdgcn_logf(w), kLn2, ex - (w - 1.f));
             const float sl = inv * (v >= 0.f ? 1.f : ex);
-            const float d = p.softplus ? sp : v, slope = p.softplus ? sl : 1.f;
-            const float dout = on ? r.dy.get(e) : 0.f, x = kMap || !on ? 0.f : r.x.get(e);
-            float dy = dout;
+            o.d[e] = p.softplus ? sp : v;
+            o.slope[e] = p.softplus ? sl : 1.f;
+            const float dout = r.dy.get(e);
+            o.x[e] = kMap ? 0.f : r.x.get(e);
             if constexpr (kGate) {
-                const float z = on ? r.z.get(e) : 0.f, s = sigmoid(z);
-                dy = dout * (z * s);
+                const float z = r.z.get(e), s = sigmoid(z);
+                o.dy[e] = dout * (z * s);
                 o.w[e] = dout * (s * fmaf(z, 1.f - s, 1.f));
+            } else {
+                o.dy[e] = dout;
             }
-            o.dy[e] = dy;
-            o.x[e] = x;
-            o.d[e] = on ? d : 0.f;
-            o.slope[e] = on ? slope : 0.f;
-            u[e] = o.d[e] * x;
+        }
+        const bool partial = t0 + kTile > end;
+        if (partial || !full) {   // tokens behind the row's length, channels behind the group
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) {
+                const bool on = t0 + pt < end && (full || e < valid);
+                o.d[e] = on ? o.d[e] : 0.f;
+                o.slope[e] = on ? o.slope[e] : 0.f;
+                o.x[e] = on ? o.x[e] : 0.f;
+                o.dy[e] = on ? o.dy[e] : 0.f;
+                if constexpr (kGate) o.w[e] = on ? o.w[e] : 0.f;
+            }
         }
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
-            s_du[k][pt][pl + e] = make_float2(o.d[e], u[e]);
+            s_du[k][pt][pl + e] = make_float2(o.d[e], o.d[e] * o.x[e]);
             s_dy[k][pt][pl + e] = o.dy[e];
         }
         if (bt < kTile) {
-            const bool inb = t0 + bt < end;
+            const bool inb = !partial || t0 + bt < end;
 #pragma unroll
             for (int e = 0; e < BC; ++e) {
                 if constexpr (!kMap) s_b[k][bt][bn + e] = inb ? r.b.get(e) : 0.f;
@@ -425,15 +446,14 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
             float h[S];
 #pragma unroll
             for (int n = 0; n < S; ++n) {
-                const float code = (float)(int8_t)(r.codes >> (8 * n)) * sc, full = r.h.get(n);
-                h[n] = wide ? full : code;
+                const float code = (float)(int8_t)(r.codes >> (8 * n)) * sc, wide_h = r.h.get(n);
+                h[n] = wide ? wide_h : code;
             }
             store_cols<S>(&s_h[i & 1][hc][hn], h);
         }
     };
     auto write_out = [&](const Kept<EPT>& o, int i) {
-        const int k = i & 1, n = rows_of(i);
-        const int bytes = n > 0 ? (n - 1) * row + tail : 0;
+        const int k = i & 1;
         float dx[EPT], ddt[EPT], dz[EPT];
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
@@ -446,10 +466,16 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
             }
             dx[e] = fmaf(du, o.d[e], o.dy[e] * skip[e]);
             ddt[e] = fmaf(du, o.x[e], sr) * o.slope[e];
-            // before the first tile and behind the last, what is kept is stale
-            sum_skip[e] = n > 0 ? fmaf(o.dy[e], o.x[e], sum_skip[e]) : sum_skip[e];
-            sum_bias[e] = n > 0 ? sum_bias[e] + ddt[e] : sum_bias[e];
         }
+        if (i >= 0 && i < tiles) {
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) {
+                sum_skip[e] = fmaf(o.dy[e], o.x[e], sum_skip[e]);
+                sum_bias[e] += ddt[e];
+            }
+        }
+        store_piece<T, kVec>(dx_rows, out_at, valid, dx);
+        store_piece<T, kVec>(ddt_rows, out_at, valid, ddt);
         if constexpr (kGate) {
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
@@ -459,13 +485,8 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
                 for (int w = 1; w < PW; ++w) y += s_y[i & 3][pt][base + 16 * w];
                 dz[e] = o.w[e] * fmaf(skip[e], o.x[e], y);
             }
+            store_piece<T, kVec>(dz_rows, out_at, valid, dz);
         }
-        store_piece<T, kVec>(buffer_of(dx_at, bytes), at, valid, dx);
-        store_piece<T, kVec>(buffer_of(ddt_at, bytes), at, valid, ddt);
-        if constexpr (kGate) store_piece<T, kVec>(buffer_of(dz_at, bytes), at, valid, dz);
-        // dB and dC: 2 N values per token, E neighbouring ones per thread.
-        constexpr int E = kTile * 2 * N / kStepThreads;
-        const int rt = tid * E / (2 * N), rn = tid * E % (2 * N);
         float s[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -473,26 +494,22 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
 #pragma unroll
             for (int c = 1; c < CG; ++c) s[e] += s_red[k][c][rt][rn + e];
         }
-        const int obytes = n > 0 ? (n - 1) * row_out + tail_out : 0;
-        const uint32_t oat = (uint32_t)((rt * p.G * N + rn % N) * (int)sizeof(T));
-        store_piece<float, true>(buffer_of(db_at, part ? obytes : 0), 4u * (rt * p.G * 2 * N + rn), 1, s);
-        store_piece<T, true>(buffer_of(db_at, part ? 0 : obytes), oat, rn < N, s);
-        store_piece<T, true>(buffer_of(dc_at, part ? 0 : obytes), oat, rn >= N, s);
-        dx_at -= step;
-        ddt_at -= step;
-        dz_at -= step;
-        db_at -= step_out;
-        dc_at -= step_out;
+        store_piece<float, true>(part_rows, part_at, 1, s);
+        store_piece<T, true>(db_rows, o_at, rn < N, s);
+        store_piece<T, true>(dc_rows, o_at, rn >= N, s);
+        out_at -= step;
+        part_at -= step_part;
+        o_at -= step_o;
     };
 
     Loaded<T, N, kVec> r0, r1;
     Kept<EPT> k0 = {}, k1 = {}, k2 = {}, k3 = {};
-    load(r0, 0);
-    load(r1, 1);
+    load(r0);
+    load(r1);
     auto interval = [&](int i, Loaded<T, N, kVec>& r, Kept<EPT>& o, const Kept<EPT>& done) {
         if constexpr (!kMap) write_out(done, i - 3);
         stage(r, o, i);
-        load(r, i + 2);
+        load(r);
         __syncthreads();
     };
     for (int i = 0; i < intervals; i += 4) {

@@ -1,6 +1,7 @@
 """The short convolution and the selective scan without a GPU: the 64-bit
-definition's gradients against differences, sizes, and every refusal (no call
-here reaches a kernel: it fails validation or the problem is empty)."""
+definition's gradients against differences, sizes, and every refusal.  The
+pointers are made up, so only calls that fail validation or have nothing to do
+are made: each refusal names the entry points it is made on."""
 
 import ctypes
 import os
@@ -112,16 +113,25 @@ def test_sizes(L):
 CONV_OK = dict(B=1, T=8, D=16, W=4, dtype=wk.WKV7_BF16, silu=1)
 
 
-def conv_all(L, d, **over):
-    """Status of the three convolution entry points with valid pointers but for `over`."""
+FORWARD, BACKWARD, STEP = 0, 1, 2
+ALL = (FORWARD, BACKWARD, STEP)
+
+
+def refusals(calls, which):
+    return [calls[k]() for k in which]
+
+
+def conv(L, d, which, **over):
+    """Statuses of the named convolution entry points, with valid pointers but for `over`."""
     a = dict(weight=FAKE, bias=FAKE, lengths=None, x=FAKE, s0=None, y=FAKE, sT=None, dy=FAKE, dsT=None, dx=FAKE,
              dweight=FAKE, dbias=FAKE, ds0=None, ws=FAKE, wsb=1 << 30, state=FAKE)
     a.update(over)
     d = d if d is None else C(d)
-    return (L.wkv7_conv_forward(d, a["weight"], a["bias"], a["lengths"], a["x"], a["s0"], a["y"], a["sT"], None),
-            L.wkv7_conv_backward(d, a["weight"], a["bias"], a["lengths"], a["x"], a["s0"], a["dy"], a["dsT"],
-                                 a["dx"], a["dweight"], a["dbias"], a["ds0"], a["ws"], a["wsb"], None),
-            L.wkv7_conv_step(d, a["weight"], a["bias"], a["x"], a["state"], a["y"], None))
+    return refusals((
+        lambda: L.wkv7_conv_forward(d, a["weight"], a["bias"], a["lengths"], a["x"], a["s0"], a["y"], a["sT"], None),
+        lambda: L.wkv7_conv_backward(d, a["weight"], a["bias"], a["lengths"], a["x"], a["s0"], a["dy"], a["dsT"],
+                                     a["dx"], a["dweight"], a["dbias"], a["ds0"], a["ws"], a["wsb"], None),
+        lambda: L.wkv7_conv_step(d, a["weight"], a["bias"], a["x"], a["state"], a["y"], None)), which)
 
 
 @pytest.mark.parametrize("field,value,status", [
@@ -129,101 +139,110 @@ def conv_all(L, d, **over):
     ("T", 2 ** 31 - 1, 2), ("D", 2 ** 31 - 1, 2)])
 def test_conv_descriptor(L, field, value, status):
     d = wk.ConvDesc(**dict(CONV_OK, **{field: value}))
-    assert conv_all(L, d) == (status,) * 3
+    assert conv(L, d, ALL) == [status] * 3
     assert L.wkv7_conv_backward_workspace_bytes(C(d)) == 0
 
 
 def test_conv_sizes_that_would_wrap(L):
     for over in (dict(B=1 << 20, T=1 << 20, D=1 << 20), dict(B=2 ** 31 - 1, T=2 ** 31 - 100, D=1 << 20),
                  dict(B=1 << 28, T=1, D=8)):
-        assert conv_all(L, wk.ConvDesc(**dict(CONV_OK, **over))) == (wk.WKV7_ERR_UNSUPPORTED,) * 3
+        assert conv(L, wk.ConvDesc(**dict(CONV_OK, **over)), ALL) == [wk.WKV7_ERR_UNSUPPORTED] * 3
 
 
 def test_conv_pointers(L):
     ok, bad = wk.ConvDesc(**CONV_OK), wk.WKV7_ERR_INVALID_ARG
-    assert conv_all(L, None) == (bad,) * 3
+    assert conv(L, None, ALL) == [bad] * 3
     for name in ("weight", "x", "bias"):
-        assert conv_all(L, ok, **{name: FAKE + 8}) == (bad,) * 3
+        assert conv(L, ok, ALL, **{name: FAKE + 8}) == [bad] * 3
     for name in ("weight", "x"):
-        assert conv_all(L, ok, **{name: None}) == (bad,) * 3
-    for name, which in (("y", 0), ("s0", 0), ("sT", 0), ("dy", 1), ("dx", 1), ("dweight", 1), ("dbias", 1),
-                        ("ds0", 1), ("dsT", 1), ("s0", 1), ("ws", 1), ("state", 2), ("y", 2)):
-        assert conv_all(L, ok, **{name: FAKE + 4})[which] == bad, name
-    for name, which in (("y", 0), ("dy", 1), ("dx", 1), ("dweight", 1), ("dbias", 1), ("state", 2), ("y", 2)):
-        assert conv_all(L, ok, **{name: None})[which] == bad, name
-    assert conv_all(L, ok, lengths=FAKE + 2)[:2] == (bad,) * 2
-    assert conv_all(L, ok, bias=None)[1] == bad   # a gradient for a bias that is not there
-    assert conv_all(L, ok, ws=None)[1] == wk.WKV7_ERR_WORKSPACE
+        assert conv(L, ok, ALL, **{name: None}) == [bad] * 3
+    for name, which in (("y", FORWARD), ("s0", FORWARD), ("sT", FORWARD), ("dy", BACKWARD), ("dx", BACKWARD),
+                        ("dweight", BACKWARD), ("dbias", BACKWARD), ("ds0", BACKWARD), ("dsT", BACKWARD),
+                        ("s0", BACKWARD), ("ws", BACKWARD), ("state", STEP), ("y", STEP)):
+        assert conv(L, ok, (which,), **{name: FAKE + 4}) == [bad], name
+    for name, which in (("y", FORWARD), ("dy", BACKWARD), ("dx", BACKWARD), ("dweight", BACKWARD),
+                        ("dbias", BACKWARD), ("state", STEP), ("y", STEP)):
+        assert conv(L, ok, (which,), **{name: None}) == [bad], name
+    assert conv(L, ok, (FORWARD, BACKWARD), lengths=FAKE + 2) == [bad] * 2
+    assert conv(L, ok, (BACKWARD,), bias=None) == [bad]   # a gradient for a bias that is not there
+    assert conv(L, ok, (BACKWARD,), ws=None) == [wk.WKV7_ERR_WORKSPACE]
     need = L.wkv7_conv_backward_workspace_bytes(C(ok))
-    assert need > 0 and conv_all(L, ok, wsb=need - 1)[1] == wk.WKV7_ERR_WORKSPACE
+    assert need > 0 and conv(L, ok, (BACKWARD,), wsb=need - 1) == [wk.WKV7_ERR_WORKSPACE]
     # nothing to do
-    assert conv_all(L, wk.ConvDesc(**dict(CONV_OK, D=0))) == (wk.WKV7_OK,) * 3
-    e = conv_all(L, wk.ConvDesc(**dict(CONV_OK, B=0)))
-    assert e[0] == wk.WKV7_OK and e[2] == wk.WKV7_OK
+    assert conv(L, wk.ConvDesc(**dict(CONV_OK, D=0)), ALL) == [wk.WKV7_OK] * 3
+    assert conv(L, wk.ConvDesc(**dict(CONV_OK, B=0)), (FORWARD, STEP)) == [wk.WKV7_OK] * 2
 
 
 SSM_OK = dict(B=1, T=8, D=16, N=16, G=2, dtype=wk.WKV7_BF16, ckpt_bits=32)
 
 
-def ssm_all(L, d, **over):
+def ssm(L, d, which, **over):
+    """Statuses of the named scan entry points, with valid pointers but for `over`."""
     a = dict(A=FAKE, dskip=FAKE, dt_bias=FAKE, lengths=None, softplus=1, x=FAKE, dt=FAKE, Bm=FAKE, Cm=FAKE, z=FAKE,
              h0=None, y=FAKE, hT=None, ckpt=FAKE, ws=FAKE, wsb=1 << 40, dy=FAKE, dhT=None, state=FAKE, dx=FAKE,
-             ddt=FAKE, dBm=FAKE, dCm=FAKE, dz=FAKE, dA=FAKE, ddskip=FAKE, ddt_bias=FAKE, dh0=None)
+             ddt=FAKE, dBm=FAKE, dCm=FAKE, dz=FAKE, dA=FAKE, ddskip=FAKE, ddt_bias=FAKE, dh0=None, params=True)
     a.update(over)
-    p = C(wk.SsmParams(a["A"], a["dskip"], a["dt_bias"], a["lengths"], a["softplus"])) if a["A"] != "none" else None
+    p = C(wk.SsmParams(a["A"], a["dskip"], a["dt_bias"], a["lengths"], a["softplus"])) if a["params"] else None
     g = wk.SsmGradPointers(*(a[k] for k in ("dx", "ddt", "dBm", "dCm", "dz", "dA", "ddskip", "ddt_bias", "dh0")))
     d = d if d is None else C(d)
     ins = [a[k] for k in ("x", "dt", "Bm", "Cm", "z")]
-    return (L.wkv7_ssm_forward(d, p, *ins, a["h0"], a["y"], a["hT"], a["ckpt"], a["ws"], a["wsb"], None),
-            L.wkv7_ssm_backward(d, p, *ins, a["dy"], a["dhT"], a["ckpt"], C(g), a["ws"], a["wsb"], None),
-            L.wkv7_ssm_step(d, p, *ins, a["state"], a["y"], None))
+    return refusals((
+        lambda: L.wkv7_ssm_forward(d, p, *ins, a["h0"], a["y"], a["hT"], a["ckpt"], a["ws"], a["wsb"], None),
+        lambda: L.wkv7_ssm_backward(d, p, *ins, a["dy"], a["dhT"], a["ckpt"], C(g), a["ws"], a["wsb"], None),
+        lambda: L.wkv7_ssm_step(d, p, *ins, a["state"], a["y"], None)), which)
 
 
 @pytest.mark.parametrize("field,value,status", [
     ("B", -1, 1), ("T", -1, 1), ("D", -16, 1), ("G", 0, 1), ("G", -1, 1), ("G", 3, 1), ("N", 4, 2), ("N", 24, 2),
-    ("N", 128, 2), ("N", 0, 2), ("dtype", 5, 2), ("ckpt_bits", 16, 2), ("ckpt_bits", -8, 2), ("T", 2 ** 31 - 1, 2)])
+    ("N", 128, 2), ("N", 0, 2), ("dtype", 5, 2), ("ckpt_bits", 16, 2), ("ckpt_bits", -8, 2), ("T", 2 ** 31 - 1, 2),
+    ("D", 1 << 23, 2)])
 def test_ssm_descriptor(L, field, value, status):
     d = wk.SsmDesc(**dict(SSM_OK, **{field: value}))
-    assert ssm_all(L, d) == (status,) * 3
+    assert ssm(L, d, ALL) == [status] * 3
     assert wk.ssm_ckpt_bytes(d) == 0 and L.wkv7_ssm_backward_workspace_bytes(C(d)) == 0
     assert L.wkv7_ssm_forward_workspace_bytes(C(d)) == 0
 
 
 def test_ssm_sizes_that_would_wrap(L):
-    for over in (dict(B=1 << 20, T=1 << 20, D=1 << 20), dict(B=2 ** 31 - 1, T=2 ** 31 - 100, D=1 << 28),
-                 dict(B=1 << 14, T=1, D=1 << 16), dict(B=1 << 10, T=1 << 25, D=1 << 10, G=1 << 10)):
-        assert ssm_all(L, wk.SsmDesc(**dict(SSM_OK, **over))) == (wk.WKV7_ERR_UNSUPPORTED,) * 3
+    for over in (dict(B=1 << 20, T=1 << 20, D=1 << 20), dict(B=2 ** 31 - 1, T=2 ** 31 - 100, D=1 << 22),
+                 dict(B=1 << 14, T=1, D=1 << 16), dict(B=1 << 10, T=1 << 25, D=1 << 10, G=1 << 10),
+                 dict(D=1 << 20, G=1 << 19)):
+        assert ssm(L, wk.SsmDesc(**dict(SSM_OK, **over)), ALL) == [wk.WKV7_ERR_UNSUPPORTED] * 3
 
 
 def test_ssm_pointers(L):
     ok, bad = wk.SsmDesc(**SSM_OK), wk.WKV7_ERR_INVALID_ARG
-    assert ssm_all(L, None) == (bad,) * 3 and ssm_all(L, ok, A="none") == (bad,) * 3
+    assert ssm(L, None, ALL) == [bad] * 3 and ssm(L, ok, ALL, params=False) == [bad] * 3
     for name in ("A", "x", "dt", "Bm", "Cm"):
-        assert ssm_all(L, ok, **{name: None}) == (bad,) * 3, name
+        assert ssm(L, ok, ALL, **{name: None}) == [bad] * 3, name
     for name in ("A", "x", "dt", "Bm", "Cm", "z", "dskip", "dt_bias"):
-        assert ssm_all(L, ok, **{name: FAKE + 8}) == (bad,) * 3, name
-    assert ssm_all(L, ok, softplus=2) == (bad,) * 3 and ssm_all(L, ok, lengths=FAKE + 1) == (bad,) * 3
-    assert ssm_all(L, ok, lengths=FAKE)[2] == bad   # a step has no lengths
-    for name, which in (("y", 0), ("h0", 0), ("hT", 0), ("ckpt", 0), ("ws", 0), ("dy", 1), ("dhT", 1), ("ckpt", 1),
-                        ("dx", 1), ("ddt", 1), ("dBm", 1), ("dCm", 1), ("dz", 1), ("dA", 1), ("ddskip", 1),
-                        ("ddt_bias", 1), ("dh0", 1), ("ws", 1), ("state", 2), ("y", 2)):
-        assert ssm_all(L, ok, **{name: FAKE + 4})[which] == bad, name
-    for name, which in (("y", 0), ("ckpt", 0), ("dy", 1), ("ckpt", 1), ("dx", 1), ("ddt", 1), ("dBm", 1), ("dCm", 1),
-                        ("dz", 1), ("dA", 1), ("ddskip", 1), ("ddt_bias", 1), ("state", 2), ("y", 2)):
-        assert ssm_all(L, ok, **{name: None})[which] == bad, name
+        assert ssm(L, ok, ALL, **{name: FAKE + 8}) == [bad] * 3, name
+    assert ssm(L, ok, ALL, softplus=2) == [bad] * 3 and ssm(L, ok, ALL, lengths=FAKE + 1) == [bad] * 3
+    assert ssm(L, ok, (STEP,), lengths=FAKE) == [bad]   # a step has no lengths
+    for name, which in (("y", FORWARD), ("h0", FORWARD), ("hT", FORWARD), ("ckpt", FORWARD), ("ws", FORWARD),
+                        ("dy", BACKWARD), ("dhT", BACKWARD), ("ckpt", BACKWARD), ("dx", BACKWARD),
+                        ("ddt", BACKWARD), ("dBm", BACKWARD), ("dCm", BACKWARD), ("dz", BACKWARD),
+                        ("dA", BACKWARD), ("ddskip", BACKWARD), ("ddt_bias", BACKWARD), ("dh0", BACKWARD),
+                        ("ws", BACKWARD), ("state", STEP), ("y", STEP)):
+        assert ssm(L, ok, (which,), **{name: FAKE + 4}) == [bad], name
+    for name, which in (("y", FORWARD), ("ckpt", FORWARD), ("dy", BACKWARD), ("ckpt", BACKWARD), ("dx", BACKWARD),
+                        ("ddt", BACKWARD), ("dBm", BACKWARD), ("dCm", BACKWARD), ("dz", BACKWARD),
+                        ("dA", BACKWARD), ("ddskip", BACKWARD), ("ddt_bias", BACKWARD), ("state", STEP),
+                        ("y", STEP)):
+        assert ssm(L, ok, (which,), **{name: None}) == [bad], name
     # a gradient for what is not there, a checkpoint that was not asked for
     for name in ("z", "dskip", "dt_bias"):
-        assert ssm_all(L, ok, **{name: None})[1] == bad, name
+        assert ssm(L, ok, (BACKWARD,), **{name: None}) == [bad], name
     none = wk.SsmDesc(**dict(SSM_OK, ckpt_bits=0))
-    assert ssm_all(L, none)[:2] == (bad, wk.WKV7_ERR_UNSUPPORTED)
-    assert ssm_all(L, ok, ws=None)[1] == wk.WKV7_ERR_WORKSPACE
-    assert ssm_all(L, ok, wsb=L.wkv7_ssm_backward_workspace_bytes(C(ok)) - 1)[1] == wk.WKV7_ERR_WORKSPACE
+    assert ssm(L, none, (FORWARD, BACKWARD)) == [bad, wk.WKV7_ERR_UNSUPPORTED]
+    assert ssm(L, ok, (BACKWARD,), ws=None) == [wk.WKV7_ERR_WORKSPACE]
+    need = L.wkv7_ssm_backward_workspace_bytes(C(ok))
+    assert need > 0 and ssm(L, ok, (BACKWARD,), wsb=need - 1) == [wk.WKV7_ERR_WORKSPACE]
     long = wk.SsmDesc(**dict(SSM_OK, T=4096))
     need = L.wkv7_ssm_forward_workspace_bytes(C(long))
-    assert need > 0 and ssm_all(L, long, wsb=need - 1)[0] == wk.WKV7_ERR_WORKSPACE
-    assert ssm_all(L, wk.SsmDesc(**dict(SSM_OK, D=0))) == (wk.WKV7_OK,) * 3
-    e = ssm_all(L, wk.SsmDesc(**dict(SSM_OK, B=0)))
-    assert e[0] == wk.WKV7_OK and e[2] == wk.WKV7_OK
+    assert need > 0 and ssm(L, long, (FORWARD,), wsb=need - 1) == [wk.WKV7_ERR_WORKSPACE]
+    assert ssm(L, wk.SsmDesc(**dict(SSM_OK, D=0)), ALL) == [wk.WKV7_OK] * 3
+    assert ssm(L, wk.SsmDesc(**dict(SSM_OK, B=0)), (FORWARD, STEP)) == [wk.WKV7_OK] * 2
 
 
 # ---- refusals in the binding --------------------------------------------------------------------
