@@ -23,6 +23,13 @@ namespace {
 
 constexpr int kConvThreads = 256;
 
+struct Yes {
+    static constexpr bool value = true;
+};
+struct No {
+    static constexpr bool value = false;
+};
+
 // Weights of the thread's channels, transposed to taps; zero behind the width.
 template <int W, int V>
 __device__ __forceinline__ void load_weights(const ConvArgs& p, int c, float (&w)[W][V], float (&bias)[V]) {
@@ -154,19 +161,20 @@ __global__ __launch_bounds__(kConvThreads) void conv_step_kernel(const ConvArgs 
 //   dweight[k] = sum_t e_t x_{t-(W-1)+k},   dbias = sum_t e_t
 // A wave takes 64 column pieces of one run of tokens, a workgroup four runs; a
 // run steps W - 1 tokens past its end for the e that its last dx need, and the
-// first run of a row W - 1 tokens before the first for ds0.  The sums over a
-// run stay in registers; the workgroup's four meet in LDS, the workgroups in a
-// second kernel, in a fixed order.
-template <typename T, int W, int V, bool kVec>
+// first run of a row gives ds0.  x and dy are read through buffers that end
+// with the row's length (what is behind reads as 0, so e and dx there come out
+// as 0), dx is written through one that holds the run's tokens: the loop has no
+// condition per token.  The sums over a run stay in registers; the workgroup's
+// four meet in LDS, the workgroups in a second kernel, in a fixed order.
+template <typename T, int W, int V, bool kVec, bool kSilu>
 __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvBwdArgs q, unsigned cblocks, int runs) {
-    constexpr int R = kConvThreads / 64, M = W + 1;
+    constexpr int R = kConvThreads / 64, M = W + 1, H = W - 1, U = 4;
     __shared__ float s_part[R][M][64 * V];
     const ConvArgs& p = q.f;
-    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const unsigned cb = blockIdx.x % cblocks, part = blockIdx.x / cblocks;
     const int c = (int)(cb * 64 + lane) * V;
     const int64_t r0 = (int64_t)part * R + wave;
-    const bool some = c < p.D && r0 < (int64_t)p.B * runs;
     float w[W][V], bias[V], dw[W][V], db[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -174,100 +182,101 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvBwdArg
 #pragma unroll
         for (int k = 0; k < W; ++k) dw[k][i] = 0.f;
     }
-    if (some) {
+    if (r0 < (int64_t)p.B * runs) {
         const int b = (int)(r0 / runs), rr = (int)(r0 % runs);
         const int t0 = rr * q.run, t1 = t0 + q.run < p.T ? t0 + q.run : p.T;
         const int len = row_length(p.lengths, b, p.T);
-        const T* const X = static_cast<const T*>(p.x) + (size_t)b * p.T * p.D;
-        const T* const DY = static_cast<const T*>(q.dy) + (size_t)b * p.T * p.D;
         load_weights<W, V>(p, c, w, bias);
-        float hist[W - 1][V];   // x of the W - 1 tokens before t
-        float eh[W - 1][V];     // e of the W - 1 tokens before t
+        const int64_t row = (int64_t)p.D * (int)sizeof(T), base = ((int64_t)b * p.T + t0) * row;
+        const int ahead = t1 + H < len ? t1 + H : len;   // the last input that is needed
+        const int bytes = ahead > t0 ? (int)((ahead - t0) * row) : 0;
+        const __amdgpu_buffer_rsrc_t x_rows = buffer_of(static_cast<const char*>(p.x) + base, bytes),
+                                     dy_rows = buffer_of(static_cast<const char*>(q.dy) + base, bytes),
+                                     dx_rows = buffer_of(static_cast<char*>(q.dx) + base, (int)((t1 - t0) * row));
+        const bool dead = c >= p.D;
+        const uint32_t step = dead ? 0 : (uint32_t)row;
+        uint32_t at = dead ? kNowhere : c * (uint32_t)sizeof(T);
+        // x and e of the W - 1 tokens before the group's, then the group's.
+        float xw[H + U][V], ew[H + U][V];
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) {
+        for (int k = 0; k < H; ++k) {
             Piece<T, V, kVec> r;
             bool zero;
-            load_input<T, W, V, kVec>(p, b, t0 - (W - 1) + k, c, r, zero);
-            const bool keep = !zero && t0 - (W - 1) + k < len;
+            load_input<T, W, V, kVec>(p, b, t0 - H + k, c, r, zero);
+            const bool keep = !zero && t0 - H + k < len;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                hist[k][i] = keep ? r.get(i) : 0.f;
-                eh[k][i] = 0.f;
+                xw[k][i] = keep ? r.get(i) : 0.f;
+                ew[k][i] = 0.f;
             }
         }
-        // Token t gives dx of input t - (W - 1): inputs before t0 belong to the
-        // run before (or, in a row's first run, to the state).
-        const int stop = t1 + W - 1;
-        constexpr int U = 4;
-        for (int t = t0; t < stop; t += U) {
+        // A group of U tokens from t on; edge: some lie outside the run, or give
+        // gradients of a state.
+        auto group = [&](int t, auto edge_) {
+            constexpr bool kEdge = decltype(edge_)::value;
             Piece<T, V, kVec> rx[U], ry[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const size_t row = (size_t)(t + u < p.T ? t + u : p.T - 1) * p.D;
-                rx[u].load(X + row, c, p.D);
-                ry[u].load(DY + row, c, p.D);
+                rx[u].load(x_rows, at + u * step);
+                ry[u].load(dy_rows, at + u * step);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int tt = t + u;
-                if (tt < stop) {
-                    const bool in = tt < len, own = in && tt < t1;
-                    const int src = tt - (W - 1);
-                    float g[V];
+                float g[V];
 #pragma unroll
-                    for (int i = 0; i < V; ++i) {
-                        const float x = in ? rx[u].get(i) : 0.f;
-                        float e = in ? ry[u].get(i) : 0.f;
-                        if (p.silu) {
-                            float pre = bias[i];
+                for (int i = 0; i < V; ++i) {
+                    const float x = rx[u].get(i);
+                    float e = ry[u].get(i);
+                    xw[H + u][i] = x;
+                    if constexpr (kSilu) {
+                        float pre = bias[i];
 #pragma unroll
-                            for (int k = 0; k < W - 1; ++k) pre = fmaf(w[k][i], hist[k][i], pre);
-                            pre = fmaf(w[W - 1][i], x, pre);
-                            const float s = sigmoid(pre);
-                            e = in ? e * (s * fmaf(pre, 1.f - s, 1.f)) : 0.f;
-                        }
-                        const float eo = own ? e : 0.f;
-#pragma unroll
-                        for (int k = 0; k < W - 1; ++k) dw[k][i] = fmaf(eo, hist[k][i], dw[k][i]);
-                        dw[W - 1][i] = fmaf(eo, x, dw[W - 1][i]);
-                        db[i] += eo;
-                        // x_{tt-(W-1)} meets tap W-1 at its own token, tap 0 at tt.
-                        float s = w[0][i] * e;
-#pragma unroll
-                        for (int k = 0; k < W - 1; ++k) s = fmaf(w[W - 1 - k][i], eh[k][i], s);
-                        g[i] = s;
-#pragma unroll
-                        for (int k = 0; k + 1 < W - 1; ++k) {
-                            hist[k][i] = hist[k + 1][i];
-                            eh[k][i] = eh[k + 1][i];
-                        }
-                        hist[W - 2][i] = x;
-                        eh[W - 2][i] = e;
+                        for (int k = 0; k < W; ++k) pre = fmaf(w[k][i], xw[u + k][i], pre);
+                        const float s = sigmoid(pre);
+                        e *= s * fmaf(pre, 1.f - s, 1.f);
                     }
-                    const bool past = src < 0;   // an input of the state
-                    if (src >= t0 || (past && rr == 0)) {
-                        // Inputs len - (W-1) .. len - 1 are the last state's.
-                        const int k = src - (len - (W - 1));
-                        if (q.dsT && k >= 0 && src < len) {
-                            Piece<T, V, kVec> r;
-                            r.load(static_cast<const T*>(q.dsT) + ((size_t)b * (W - 1) + k) * p.D, c, p.D);
+                    ew[H + u][i] = e;
+                    const float own = !kEdge || t + u < t1 ? e : 0.f;
 #pragma unroll
-                            for (int i = 0; i < V; ++i) g[i] += r.get(i);
-                        }
-                        if (!past) {
-                            if (src >= len) {
+                    for (int k = 0; k < W; ++k) dw[k][i] = fmaf(own, xw[u + k][i], dw[k][i]);
+                    db[i] += own;
+                    // input t + u - (W-1) meets tap W-1 at its own token, tap 0 here
+                    g[i] = w[0][i] * e;
 #pragma unroll
-                                for (int i = 0; i < V; ++i) g[i] = 0.f;
-                            }
-                            store_piece<kVec>(static_cast<T*>(q.dx) + ((size_t)b * p.T + src) * p.D, c, p.D, g);
-                        } else if (q.ds0) {
-                            store_piece<kVec>(static_cast<T*>(q.ds0) + ((size_t)b * (W - 1) + src + W - 1) * p.D, c,
-                                              p.D, g);
-                        }
-                    }
+                    for (int k = 0; k < H; ++k) g[i] = fmaf(w[H - k][i], ew[u + k][i], g[i]);
                 }
+                const int src = t + u - H;
+                if constexpr (kEdge) {
+                    const int k = src - (len - H);   // in the last state
+                    if (q.dsT && k >= 0 && src < len && !dead) {
+                        Piece<T, V, kVec> r;
+                        r.load(static_cast<const T*>(q.dsT) + ((size_t)b * H + k) * p.D, c, p.D);
+#pragma unroll
+                        for (int i = 0; i < V; ++i) g[i] += r.get(i);
+                    }
+                    if (src < 0 && q.ds0)
+                        store_piece<kVec>(static_cast<T*>(q.ds0) + ((size_t)b * H + src + H) * p.D, c, p.D, g);
+                }
+                // inputs before the run's lie below the buffer's start: dropped
+                store_piece<T, kVec>(dx_rows, at + u * step - H * step, kVec ? 1 : p.D - c, g);
             }
+#pragma unroll
+            for (int k = 0; k < H; ++k)
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    xw[k][i] = xw[U + k][i];
+                    ew[k][i] = ew[U + k][i];
+                }
+            at += U * step;
+        };
+        const int inner = t1 < len ? t1 : len;
+        int t = t0;
+        if (rr == 0) {
+            group(t, Yes());
+            t += U;
         }
+        for (; t + U <= inner; t += U) group(t, No());
+        for (; t < t1 + H; t += U) group(t, Yes());
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -340,7 +349,9 @@ hipError_t bwd_v(const ConvBwdArgs& q, hipStream_t stream) {
     const unsigned cblocks = (unsigned)((p.D + 64 * V - 1) / (64 * V));
     const int runs = (p.T + q.run - 1) / q.run;
     if ((uint64_t)cblocks * q.parts > (1ull << 30)) return hipErrorInvalidValue;
-    conv_bwd_kernel<T, W, V, kVec><<<dim3(cblocks * q.parts), kConvThreads, 0, stream>>>(q, cblocks, runs);
+    const dim3 grid(cblocks * q.parts);
+    if (p.silu) conv_bwd_kernel<T, W, V, kVec, true><<<grid, kConvThreads, 0, stream>>>(q, cblocks, runs);
+    else conv_bwd_kernel<T, W, V, kVec, false><<<grid, kConvThreads, 0, stream>>>(q, cblocks, runs);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const size_t total = (size_t)p.D * (W + 1);
@@ -356,19 +367,27 @@ __global__ __launch_bounds__(kConvThreads) void conv_pass_kernel(const T* __rest
     if (id < n) to[id] = from ? from[id] : (T)0;
 }
 
+// Channels per thread: the widest piece, up to 16 bytes, that the rows are made of.
 template <typename T, int W>
 hipError_t fwd_w(const ConvArgs& p, hipStream_t stream) {
     constexpr int V = 16 / sizeof(T);
-    hipError_t e = p.D % V == 0 ? fwd_v<T, W, V, true>(p, stream) : fwd_v<T, W, 1, true>(p, stream);
+    hipError_t e = p.D % V == 0         ? fwd_v<T, W, V, true>(p, stream)
+                   : p.D % (V / 2) == 0 ? fwd_v<T, W, V / 2, true>(p, stream)
+                   : p.D % 2 == 0       ? fwd_v<T, W, 2, true>(p, stream)
+                                        : fwd_v<T, W, 1, true>(p, stream);
     if (e != hipSuccess || !p.sT) return e;
     const uint64_t n = (uint64_t)p.B * (W - 1) * p.D;
+    if (n == 0) return hipSuccess;
     conv_state_kernel<T, W><<<dim3((unsigned)((n + kConvThreads - 1) / kConvThreads)), kConvThreads, 0, stream>>>(p);
     return hipGetLastError();
 }
 template <typename T, int W>
 hipError_t step_w(const ConvArgs& p, hipStream_t stream) {
     constexpr int V = 16 / sizeof(T);
-    return p.D % V == 0 ? step_v<T, W, V, true>(p, stream) : step_v<T, W, 1, true>(p, stream);
+    return p.D % V == 0         ? step_v<T, W, V, true>(p, stream)
+           : p.D % (V / 2) == 0 ? step_v<T, W, V / 2, true>(p, stream)
+           : p.D % 2 == 0       ? step_v<T, W, 2, true>(p, stream)
+                                : step_v<T, W, 1, true>(p, stream);
 }
 template <typename T, int W>
 hipError_t bwd_w(const ConvBwdArgs& q, hipStream_t stream) {

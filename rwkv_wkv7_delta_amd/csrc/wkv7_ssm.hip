@@ -67,13 +67,7 @@ __global__ __launch_bounds__(2 * kStepThreads) void ssm_fwd_kernel(const SsmArgs
         if constexpr (!kMap) {
             if (p.h0) load_cols<4>(p.h0 + chn, h);
             const size_t BDN = (size_t)p.B * p.D * N, BD = (size_t)p.B * p.D;
-            for (int s = 0; s < seg; ++s) {
-                float e[4];
-                load_cols<4>(p.seg_h + s * BDN + chn, e);
-                const float d = p.seg_d[s * BD + chn / N];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) h[i] = fmaf(exp2_raw(d * a2[i]), h[i], e[i]);
-            }
+            through_segments<4>(h, a2, p.seg_h + chn, (int64_t)BDN, p.seg_d + chn / N, (int64_t)BD, seg);
         }
         for (int i = 0; i < intervals; ++i) {
             __syncthreads();
@@ -281,39 +275,49 @@ __global__ __launch_bounds__(2 * kStepThreads) void ssm_fwd_kernel(const SsmArgs
 }
 
 // One token on resident states, in place: bound by the states' bytes (read and
-// written once, 16 bytes per lane).
-template <typename T, int N>
+// written once, 16 bytes per lane).  A lane takes four states of one channel in
+// R batch rows, whose loads go out together and share A and the vectors.
+constexpr int kStepRows = 4;
+
+template <typename T, int N, int R>
 __global__ __launch_bounds__(kSsmThreads) void ssm_step_kernel(const SsmArgs p) {
     constexpr int P = N / kSsmStates, CH = kSsmThreads / P;
-    const int64_t ch = (int64_t)blockIdx.x * CH + threadIdx.x / P;   // over B * D
-    if (ch >= (int64_t)p.B * p.D) return;
-    const int n0 = (threadIdx.x % P) * kSsmStates;
-    const int d = (int)(ch % p.D);
-    const int64_t b = ch / p.D;
-    const size_t bc = ((size_t)b * p.G + d / (p.D / p.G)) * N + n0;
-    float a[4], h[4], bb[4], cc[4];
-    load_cols<4>(p.A + (size_t)d * N + n0, a);
-    load_cols<4>(p.hT + (size_t)ch * N + n0, h);
-    load_cols<4>(static_cast<const T*>(p.Bm) + bc, bb);
-    load_cols<4>(static_cast<const T*>(p.Cm) + bc, cc);
-    const float x = Elem<T>::load1(static_cast<const T*>(p.x) + ch);
-    const float v = Elem<T>::load1(static_cast<const T*>(p.dt) + ch) + (p.dt_bias ? p.dt_bias[d] : 0.f);
-    const float rate = p.softplus ? softplus(v) : v, u = rate * x;
-    float y = 0.f;
+    const unsigned cblocks = (unsigned)((p.D + CH - 1) / CH);
+    const int d = (int)(blockIdx.x % cblocks) * CH + threadIdx.x / P;
+    const int b0 = (int)(blockIdx.x / cblocks) * R;
+    if (d >= p.D) return;
+    const int n0 = (threadIdx.x % P) * kSsmStates, g = d / (p.D / p.G);
+    float a2[4], h[R][4], bb[R][4], cc[R][4], x[R], v[R], z[R];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        h[i] = fmaf(exp2_raw(rate * (a[i] * kLog2e)), h[i], u * bb[i]);
-        y = fmaf(cc[i], h[i], y);
+    for (int r = 0; r < R; ++r) {   // rows behind the last are read as the last, and not written
+        const size_t b = b0 + r < p.B ? b0 + r : p.B - 1;
+        const size_t bd = b * p.D + d, bc = (b * p.G + g) * N + n0;
+        load_cols<4>(p.hT + bd * N + n0, h[r]);
+        load_cols<4>(static_cast<const T*>(p.Bm) + bc, bb[r]);
+        load_cols<4>(static_cast<const T*>(p.Cm) + bc, cc[r]);
+        x[r] = Elem<T>::load1(static_cast<const T*>(p.x) + bd);
+        v[r] = Elem<T>::load1(static_cast<const T*>(p.dt) + bd);
+        z[r] = p.z ? Elem<T>::load1(static_cast<const T*>(p.z) + bd) : 0.f;
     }
-    store_cols<4>(p.hT + (size_t)ch * N + n0, h);
-    y = group_sum<P>(y);
-    if (n0 == 0) {
-        if (p.dskip) y = fmaf(p.dskip[d], x, y);
-        if (p.z) {
-            const float z = Elem<T>::load1(static_cast<const T*>(p.z) + ch);
-            y *= z * sigmoid(z);
+    load_cols<4>(p.A + (size_t)d * N + n0, a2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a2[i] *= kLog2e;
+    const float bias = p.dt_bias ? p.dt_bias[d] : 0.f, skip = p.dskip ? p.dskip[d] : 0.f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        if (b0 + r >= p.B) break;
+        const size_t bd = (size_t)(b0 + r) * p.D + d;
+        const float rate = p.softplus ? softplus(v[r] + bias) : v[r] + bias, u = rate * x[r];
+        float y = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[r][i] = fmaf(exp2_raw(rate * a2[i]), h[r][i], u * bb[r][i]);
+            y = fmaf(cc[r][i], h[r][i], y);
         }
-        Elem<T>::store1(static_cast<T*>(p.y) + ch, y);
+        store_cols<4>(p.hT + bd * N + n0, h[r]);
+        y = fmaf(skip, x[r], group_sum<P>(y));
+        if (p.z) y *= z[r] * sigmoid(z[r]);
+        if (n0 == 0) Elem<T>::store1(static_cast<T*>(p.y) + bd, y);
     }
 }
 
@@ -344,8 +348,13 @@ hipError_t launch_fwd(const SsmArgs& p, hipStream_t stream) {
 template <typename T, int N>
 hipError_t launch_step(const SsmArgs& p, hipStream_t stream) {
     constexpr int CH = kSsmThreads * kSsmStates / N;
-    const int64_t n = (int64_t)p.B * p.D;
-    ssm_step_kernel<T, N><<<dim3((unsigned)((n + CH - 1) / CH)), kSsmThreads, 0, stream>>>(p);
+    const unsigned cblocks = (unsigned)((p.D + CH - 1) / CH);
+    // One row per lane until the device is full: few rows are latency alone.
+    if ((int64_t)cblocks * p.B < 2048)
+        ssm_step_kernel<T, N, 1><<<dim3(cblocks * p.B), kSsmThreads, 0, stream>>>(p);
+    else
+        ssm_step_kernel<T, N, kStepRows>
+            <<<dim3(cblocks * ((p.B + kStepRows - 1) / kStepRows)), kSsmThreads, 0, stream>>>(p);
     return hipGetLastError();
 }
 

@@ -33,7 +33,7 @@ int check_conv(const wkv7_conv_desc* d) {
     if (d->silu != 0 && d->silu != 1) return WKV7_ERR_INVALID_ARG;
     if (d->W < 2 || d->W > 4) return WKV7_ERR_UNSUPPORTED;
     if (d->dtype != WKV7_F32 && d->dtype != WKV7_BF16) return WKV7_ERR_UNSUPPORTED;
-    if (d->T > INT32_MAX - 64 || d->D > INT32_MAX - 4096) return WKV7_ERR_UNSUPPORTED;
+    if (d->T > INT32_MAX - 1024 || d->D > (1 << 19)) return WKV7_ERR_UNSUPPORTED;   // 520 fp32 rows below 2^31 bytes
     if (!product_fits(d->B, (int64_t)d->T + 64, d->D, 1, (int64_t)1 << 35) ||
         !product_fits(d->B, d->D, 4, 1, (int64_t)1 << 31))
         return WKV7_ERR_UNSUPPORTED;
@@ -41,17 +41,23 @@ int check_conv(const wkv7_conv_desc* d) {
 }
 
 // Runs of the gradient: the sums over a run's tokens stay in registers and
-// leave as one partial row, so runs are as long as still leaves about 4096
-// waves of four channels a lane; at least 32 tokens, at most 512.
+// leave as one partial row, and a run steps W - 1 tokens past its end, so runs
+// are as long as still leaves about kConvWaves waves of 64 column pieces; a
+// multiple of 4 from 16 to 512 tokens.  A run is addressed with 32-bit byte
+// offsets (D is limited for that).
+constexpr int kConvWaves = 2048;
+constexpr int kConvPiece = 4;   // channels of a gradient lane
+
 struct ConvPlan {
     int run, parts;
 };
 ConvPlan plan_conv(const wkv7_conv_desc* d) {
-    const int64_t waves = ((int64_t)d->D + 255) / 256 * d->B;   // per run
-    int64_t runs = waves > 0 ? 4096 / waves : 1;
+    const int64_t piece = 64 * (d->D % kConvPiece == 0 ? kConvPiece : 1);
+    const int64_t waves = ((int64_t)d->D + piece - 1) / piece * d->B;   // per run
+    int64_t runs = waves > 0 ? kConvWaves / waves : 1;
     if (runs < 1) runs = 1;
-    int64_t run = ((int64_t)d->T + runs - 1) / runs;
-    run = run < 32 ? 32 : run > 512 ? 512 : run;
+    int64_t run = (((int64_t)d->T + runs - 1) / runs + 3) / 4 * 4;
+    run = run < 16 ? 16 : run > 512 ? 512 : run;
     const int64_t all = ((int64_t)d->T + run - 1) / run * d->B;
     int64_t parts = (all + 3) / 4;
     if (parts < 1) parts = 1;
@@ -98,13 +104,17 @@ int64_t token_bytes(const wkv7_ssm_desc* d) {
 
 // Time segments: a launch without them has one workgroup per batch row, group
 // and channel block.  The first of the two launches repeats most of the
-// exponentials, so a split only pays when it shortens the chain enough.
+// exponentials, so a split only pays when it shortens the chain enough: three
+// segments at least, as many as make two workgroups per compute unit (forward at
+// B = 1, T = 16384, D = 768, N = 16: 64 segments at most 95 us, 32 116 us; four
+// workgroups per unit 102 us; forward and backward at B = 4, T = 1024, D = 768:
+// one, two, four per unit 170, 128, 153 us), of 64 tokens at least.
 struct SsmPlan {
     int nseg, seg_len;
 };
 constexpr int kUnits = 256;          // compute units of the device
-constexpr int kMaxSegments = 32;
-constexpr int kMinSegmentTokens = 128;
+constexpr int kMaxSegments = 64;
+constexpr int kMinSegmentTokens = 64;
 
 SsmPlan plan_ssm(const wkv7_ssm_desc* d, bool backward) {
     const SsmPlan none{1, d->T};

@@ -166,13 +166,9 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
         }
         if constexpr (!kMap) {
             if (q.dhT) load_cols<S>(q.dhT + chn, carry);
-            for (int s = p.nseg - 1; s > seg; --s) {
-                float e[S];
-                load_cols<S>(p.seg_h + (s - 1) * BDN + chn, e);
-                const float d = p.seg_d[(s - 1) * BD + chn / N];
-#pragma unroll
-                for (int n = 0; n < S; ++n) carry[n] = fmaf(exp2_raw(d * a2[n]), carry[n], e[n]);
-            }
+            // segments nseg - 1 down to seg + 1, kept at one less
+            through_segments<S>(carry, a2, p.seg_h + (p.nseg - 2) * (int64_t)BDN + chn, -(int64_t)BDN,
+                                p.seg_d + (p.nseg - 2) * (int64_t)BD + chn / N, -(int64_t)BD, p.nseg - 1 - seg);
         }
         // Where the lane leaves its folded sums: row r of the wave holds value 0,
         // 2, 1, 3 of a fold over the rows; a lane of a row the state and dB or dC
@@ -545,11 +541,17 @@ __global__ __launch_bounds__(256) void ssm_bc_kernel(const float* __restrict__ p
     const size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4, total = rows * 2 * N;
     if (at >= total) return;
     float s[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < blocks; ++k) {
-        float v[4];
-        load_cols<4>(part + k * total + at, v);
+    for (int k = 0; k < blocks; k += 8) {
+        float v[8][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[i] += v[i];
+        for (int u = 0; u < 8; ++u) load_cols<4>(part + (k + u < blocks ? k + u : blocks - 1) * total + at, v[u]);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            if (k + u < blocks) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[i] += v[u][i];
+            }
+        }
     }
     const size_t row = at / (2 * N), n = at % (2 * N);
     Elem<T>::store4(n < (size_t)N ? dB + row * N + n : dC + row * N + n - N, make_float4(s[0], s[1], s[2], s[3]));

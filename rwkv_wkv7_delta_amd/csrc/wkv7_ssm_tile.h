@@ -68,6 +68,30 @@ struct Place {
     }
 };
 
+// The state h (S of a channel's) taken through `count` segments: h <- exp(A sum D) h
+// + e each, e at e0 + k stride_e, sum D at d0 + k stride_d.  Eight segments' loads go
+// out together: one by one their latencies add up.
+template <int S>
+__device__ __forceinline__ void through_segments(float (&h)[S], const float (&a2)[S], const float* e0, int64_t stride_e,
+                                                 const float* d0, int64_t stride_d, int count) {
+    for (int s = 0; s < count; s += 8) {
+        float e[8][S], d[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int at = s + k < count ? s + k : count - 1;
+            load_cols<S>(e0 + at * stride_e, e[k]);
+            d[k] = d0[at * stride_d];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (s + k < count) {
+#pragma unroll
+                for (int n = 0; n < S; ++n) h[n] = fmaf(exp2_raw(d[k] * a2[n]), h[n], e[k][n]);
+            }
+        }
+    }
+}
+
 // The value of lane `t` of the row in every lane of the row; folded into the
 // multiply that uses it.
 template <int t>
