@@ -79,16 +79,37 @@ __device__ __forceinline__ void fold_row(const float (&v)[4], const float (&w)[4
         "v_add_f32_dpp %5, %5, %5 quad_perm:[2,3,0,1] row_mask:0xf bank_mask:0xf\n\t"
         "s_nop 0\n\t"
         "v_add_f32_dpp %4, %4, %4 quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
-        "v_add_f32_dpp %5, %5, %5 quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf\n\t"
-        "s_nop 0"
+        "v_add_f32_dpp %5, %5, %5 quad_perm:[1,0,3,2] row_mask:0xf bank_mask:0xf"
         : "=&v"(x0), "=&v"(x1), "=&v"(u0), "=&v"(u1), "=&v"(y), "=&v"(z)
         : "v"(v[0]), "v"(v[1]), "v"(v[2]), "v"(v[3]), "v"(w[0]), "v"(w[1]), "v"(w[2]), "v"(w[3]));
+}
+
+// h = a g + x for two states, and the sum of (c broadcast from lane t of the row) h.
+// As in the forward's step_read: the s_nop for a, which an exponential may just have
+// written, the two updates in front of the products that read c through DPP.  Every
+// fourth token's sum goes straight into a lane swap (fold_rows), which may not read
+// what one of the two vector instructions before it wrote; the compiler keeps that
+// distance for its own instructions, not for those in here.
+template <int t>
+__device__ __forceinline__ float state_step(float& h0, float& h1, float g0, float g1, float a0, float a1, float x0,
+                                            float x1, float c0, float c1) {
+    float y;
+    asm("s_nop 0\n\t"
+        "v_fma_f32 %0, %5, %3, %7\n\t"
+        "v_fma_f32 %1, %6, %4, %8\n\t"
+        "v_mul_f32_dpp %2, %9, %0 row_newbcast:%11 row_mask:0xf bank_mask:0xf\n\t"
+        "v_fmac_f32_dpp %2, %10, %1 row_newbcast:%11 row_mask:0xf bank_mask:0xf"
+        : "=&v"(h0), "=&v"(h1), "=&v"(y)
+        : "v"(g0), "v"(g1), "v"(a0), "v"(a1), "v"(x0), "v"(x1), "v"(c0), "v"(c1), "n"(t));
+    if constexpr (t % 4 == 3) asm("s_nop 1" : "+v"(y));
+    return y;
 }
 
 // One step of the adjoint for two states: g <- g + c dy (c broadcast from lane t of
 // the row), v = (g u, dy h), the sum of (b broadcast) g, and g <- a g.  The two
 // products in front keep the DPP operands c two instructions from whatever wrote
-// them.
+// them.  The sum meets a lane swap only together with the sum of r A, whose three
+// products follow this.
 template <int t>
 __device__ __forceinline__ float adjoint_step(float& g0, float& g1, float (&v)[4], float c0, float c1, float b0,
                                               float b1, float dy, float u, float h0, float h1, float a0, float a1) {
@@ -206,13 +227,23 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
             auto states = [&](auto tok, Tile& w, int i) {
                 constexpr int t = decltype(tok)::v;
                 const float2 du = s_du[i & 3][t][at.cl];
-                float y = 0.f;
+                float y = 0.f, x[S];
+                const float(&before)[S] = t == 0 ? w.h0 : w.h[t > 0 ? t - 1 : 0];
 #pragma unroll
                 for (int n = 0; n < S; ++n) {
                     w.a[t][n] = exp2_raw(du.x * a2[n]);
-                    w.h[t][n] = fmaf(w.a[t][n], t == 0 ? w.h0[n] : w.h[t > 0 ? t - 1 : 0][n], row_bcast<t>(w.b[n]) * du.y);
-                    if constexpr (kGate)
-                        y = n == 0 ? row_bcast<t>(w.c[n]) * w.h[t][n] : y + row_bcast<t>(w.c[n]) * w.h[t][n];
+                    x[n] = row_bcast<t>(w.b[n]) * du.y;
+                }
+#pragma unroll
+                for (int n = 0; n < S; n += 2) {
+                    if constexpr (kGate) {
+                        const float q = state_step<t>(w.h[t][n], w.h[t][n + 1], before[n], before[n + 1], w.a[t][n],
+                                                      w.a[t][n + 1], x[n], x[n + 1], w.c[n], w.c[n + 1]);
+                        y = n == 0 ? q : y + q;
+                    } else {
+                        w.h[t][n] = fmaf(w.a[t][n], before[n], x[n]);
+                        w.h[t][n + 1] = fmaf(w.a[t][n + 1], before[n + 1], x[n + 1]);
+                    }
                 }
                 if constexpr (kGate) {
                     y4[t % 4] = y;
@@ -533,48 +564,53 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
     }
 }
 
-// dB and dC: the sum of `blocks` partials per element, in order.  Four elements
-// per thread (N is a multiple of 8).
+// The partial sums, each element's in order.  Workgroups below bc_blocks: dB and
+// dC, the sum over the channel blocks, four elements per thread (N is a multiple
+// of 8).  The rest: dA, ddskip and ddt_bias, the sum over `parts` batch rows and
+// segments; element e of D N + 2 D is dA's, then the two vectors' interleaved.
 template <typename T>
-__global__ __launch_bounds__(256) void ssm_bc_kernel(const float* __restrict__ part, int blocks,
-                                                     size_t rows, int N, T* dB, T* dC) {
-    const size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4, total = rows * 2 * N;
-    if (at >= total) return;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int k = 0; k < blocks; k += 8) {
-        float v[8][4];
+__global__ __launch_bounds__(256) void ssm_sums_kernel(const SsmBwdArgs q, int blocks, size_t rows, unsigned bc_blocks,
+                                                       int parts) {
+    const int N = q.f.N, D = q.f.D;
+    if (blockIdx.x < bc_blocks) {
+        const size_t at = ((size_t)blockIdx.x * 256 + threadIdx.x) * 4, total = rows * 2 * N;
+        if (at >= total) return;
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < blocks; k += 8) {   // eight loads in flight
+            float v[8][4];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) load_cols<4>(part + (k + u < blocks ? k + u : blocks - 1) * total + at, v[u]);
+            for (int u = 0; u < 8; ++u) load_cols<4>(q.part_bc + (k + u < blocks ? k + u : blocks - 1) * total + at, v[u]);
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-            if (k + u < blocks) {
+            for (int u = 0; u < 8; ++u) {
+                if (k + u < blocks) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) s[i] += v[u][i];
+                    for (int i = 0; i < 4; ++i) s[i] += v[u][i];
+                }
             }
         }
+        const size_t row = at / (2 * N), n = at % (2 * N);
+        T* const to = n < (size_t)N ? static_cast<T*>(q.dBm) + row * N + n : static_cast<T*>(q.dCm) + row * N + n - N;
+        Elem<T>::store4(to, make_float4(s[0], s[1], s[2], s[3]));
+        return;
     }
-    const size_t row = at / (2 * N), n = at % (2 * N);
-    Elem<T>::store4(n < (size_t)N ? dB + row * N + n : dC + row * N + n - N, make_float4(s[0], s[1], s[2], s[3]));
-}
-
-// dA, ddskip and ddt_bias: the sum over `parts` batch rows and segments.
-// Element e of D N + 2 D: dA, then the two vectors interleaved.
-__global__ __launch_bounds__(256) void ssm_params_kernel(const float* __restrict__ part_a,
-                                                         const float* __restrict__ part_v, int parts, int D,
-                                                         int N, float* dA, float* ddskip, float* ddt_bias) {
-    const size_t e = (size_t)blockIdx.x * 256 + threadIdx.x, DN = (size_t)D * N;
-    if (e < DN) {
-        float s = 0.f;
-        for (int k = 0; k < parts; ++k) s += part_a[k * DN + e];
-        dA[e] = s;
-    } else if (e < DN + 2 * (size_t)D) {
-        const size_t i = e - DN;
-        float* const out = i % 2 == 0 ? ddskip : ddt_bias;
-        if (!out) return;
-        float s = 0.f;
-        for (int k = 0; k < parts; ++k) s += part_v[k * 2 * (size_t)D + i];
-        out[i / 2] = s;
+    const size_t e = (size_t)(blockIdx.x - bc_blocks) * 256 + threadIdx.x, DN = (size_t)D * N;
+    const bool vec = e >= DN;
+    if (e >= DN + 2 * (size_t)D) return;
+    const size_t i = e - DN;
+    float* const out = !vec ? q.dA + e : i % 2 == 0 ? (q.ddskip ? q.ddskip + i / 2 : nullptr)
+                                                    : (q.ddt_bias ? q.ddt_bias + i / 2 : nullptr);
+    if (!out) return;
+    const float* const from = vec ? q.part_v + i : q.part_a + e;
+    const size_t stride = vec ? 2 * (size_t)D : DN;
+    float s = 0.f;
+    for (int k = 0; k < parts; k += 8) {
+        float v[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) v[u] = from[(k + u < parts ? k + u : parts - 1) * stride];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s += k + u < parts ? v[u] : 0.f;
     }
+    *out = s;
 }
 
 template <typename T, int N, bool kVec, bool kGate>
@@ -604,15 +640,8 @@ hipError_t launch_bwd(const SsmBwdArgs& q, hipStream_t stream) {
                               : launch_bwd_v<T, N, false, false>(q, blocks, stream));
     if (e != hipSuccess) return e;
     const size_t rows = (size_t)p.B * p.T * p.G;
-    if (q.part_bc && rows > 0) {
-        const size_t n = (rows * 2 * N / 4 + 255) / 256;
-        ssm_bc_kernel<T><<<dim3((unsigned)n), 256, 0, stream>>>(q.part_bc, blocks, rows, N,
-                                                                static_cast<T*>(q.dBm), static_cast<T*>(q.dCm));
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    const size_t n = ((size_t)p.D * (N + 2) + 255) / 256;
-    ssm_params_kernel<<<dim3((unsigned)n), 256, 0, stream>>>(q.part_a, q.part_v, p.B * p.nseg, p.D, N, q.dA,
-                                                             q.ddskip, q.ddt_bias);
+    const size_t bc = q.part_bc ? (rows * 2 * N / 4 + 255) / 256 : 0, rest = ((size_t)p.D * (N + 2) + 255) / 256;
+    ssm_sums_kernel<T><<<dim3((unsigned)(bc + rest)), 256, 0, stream>>>(q, blocks, rows, (unsigned)bc, p.B * p.nseg);
     return hipGetLastError();
 }
 
