@@ -457,9 +457,16 @@ int wkv7_forward_epilogue(const wkv7_desc *desc, const void *r, const void *w, c
  * alignment, row-major layouts without gaps, fp32 states and learned vectors,
  * asynchronous work on `stream`, synchronous validation that launches nothing
  * on error), with channels in place of heads: token tensors are [B][T][D].
- * Work goes to the current device: make the tensors' device current first.
+ * Outputs may share memory with no input and no other output, but for the
+ * states of the single-token calls.  Work goes to the current device: make the tensors' device current first.
  * D is any width; widths whose rows hold whole 16-byte (convolution) pieces run
- * fastest.  Calls share no scratch; a workspace may be used again by a later
+ * fastest.  Sizes beyond these limits are refused (WKV7_ERR_UNSUPPORTED):
+ *   convolution  T <= 2^31 - 1025, D <= 2^19, B (T + 64) max(D, 64) <= 2^35,
+ *                B D <= 2^29;
+ *   scan         T <= 2^31 - 65, D <= 2^22, D N <= 2^26, G N <= 2^21, B T D and
+ *                B ceil(T / 16) D N <= 2^40, B T G N <= 2^32, B D <= 2^25, and as
+ *                many workgroups (one per batch row, group, 256 S / N of the
+ *                group's channels, S = 2 or 4, and time segment) as 2^22.  Calls share no scratch; a workspace may be used again by a later
  * call on the same stream, not by two calls that can overlap (two captured
  * graphs replayed on different streams need one each).
  *

@@ -34,7 +34,9 @@ int check_conv(const wkv7_conv_desc* d) {
     if (d->W < 2 || d->W > 4) return WKV7_ERR_UNSUPPORTED;
     if (d->dtype != WKV7_F32 && d->dtype != WKV7_BF16) return WKV7_ERR_UNSUPPORTED;
     if (d->T > INT32_MAX - 1024 || d->D > (1 << 19)) return WKV7_ERR_UNSUPPORTED;   // 520 fp32 rows below 2^31 bytes
-    if (!product_fits(d->B, (int64_t)d->T + 64, d->D, 1, (int64_t)1 << 35) ||
+    // Below that no launch has more than 2^31 threads (a row of few channels takes a
+    // wave all the same).
+    if (!product_fits(d->B, (int64_t)d->T + 64, d->D < 64 ? 64 : d->D, 1, (int64_t)1 << 35) ||
         !product_fits(d->B, d->D, 4, 1, (int64_t)1 << 31))
         return WKV7_ERR_UNSUPPORTED;
     return WKV7_OK;
@@ -72,24 +74,6 @@ wkv7::ConvArgs conv_args(const wkv7_conv_desc* d, const float* weight, const flo
 
 // ---- the scan ------------------------------------------------------------------
 
-int check_ssm(const wkv7_ssm_desc* d) {
-    if (!d) return WKV7_ERR_INVALID_ARG;
-    if (d->B < 0 || d->T < 0 || d->D < 0 || d->G < 1 || d->D % d->G != 0) return WKV7_ERR_INVALID_ARG;
-    if (d->N != 8 && d->N != 16 && d->N != 32 && d->N != 64) return WKV7_ERR_UNSUPPORTED;
-    if (d->dtype != WKV7_F32 && d->dtype != WKV7_BF16) return WKV7_ERR_UNSUPPORTED;
-    if (d->ckpt_bits != 0 && d->ckpt_bits != 8 && d->ckpt_bits != 32) return WKV7_ERR_UNSUPPORTED;
-    // A segment's rows are addressed with 32-bit byte offsets (token_bytes): a tile
-    // of sixteen tokens has to fit.
-    if (d->T > INT32_MAX - 64 || d->D > (1 << 22) || (int64_t)d->G * d->N > (1 << 22)) return WKV7_ERR_UNSUPPORTED;
-    const int64_t blocks = ((int64_t)d->T + 15) / 16, most = (int64_t)1 << 40;
-    // A launch has at most B G ceil(D / G / channels) workgroups per segment.
-    if (!product_fits(d->B, d->T, d->D, 1, most) || !product_fits(d->B, blocks, d->D, d->N, most) ||
-        !product_fits(d->B, d->T, d->G, d->N, (int64_t)1 << 38) ||
-        !product_fits(d->B, d->D, 64, 1, (int64_t)1 << 31))
-        return WKV7_ERR_UNSUPPORTED;
-    return WKV7_OK;
-}
-
 int64_t channel_blocks(const wkv7_ssm_desc* d, bool backward) {
     const int ch = backward ? wkv7::ssm_bwd_channels(d->N) : wkv7::ssm_channels(d->N);
     return ((int64_t)d->D / d->G + ch - 1) / ch;
@@ -124,7 +108,7 @@ SsmPlan plan_ssm(const wkv7_ssm_desc* d, bool backward) {
     if (n > d->T / kMinSegmentTokens) n = d->T / kMinSegmentTokens;
     if (n > kMaxSegments) n = kMaxSegments;
     if (n < 3) n = 1;
-    // No buffer of a segment reaches 2^31 bytes (with a few tiles to spare).
+    // No buffer of a segment, nor the eight tiles behind it, reaches 2^31 bytes.
     const int64_t most = ((int64_t)INT32_MAX / token_bytes(d) - 128) / 16 * 16;
     const int64_t least = most >= 16 ? (d->T + most - 1) / most : d->T;
     if (n < least) n = least;
@@ -132,6 +116,29 @@ SsmPlan plan_ssm(const wkv7_ssm_desc* d, bool backward) {
     const int64_t len = (((int64_t)d->T + n - 1) / n + 15) / 16 * 16;
     n = ((int64_t)d->T + len - 1) / len;
     return SsmPlan{(int)n, (int)len};
+}
+
+int check_ssm(const wkv7_ssm_desc* d) {
+    if (!d) return WKV7_ERR_INVALID_ARG;
+    if (d->B < 0 || d->T < 0 || d->D < 0 || d->G < 1 || d->D % d->G != 0) return WKV7_ERR_INVALID_ARG;
+    if (d->N != 8 && d->N != 16 && d->N != 32 && d->N != 64) return WKV7_ERR_UNSUPPORTED;
+    if (d->dtype != WKV7_F32 && d->dtype != WKV7_BF16) return WKV7_ERR_UNSUPPORTED;
+    if (d->ckpt_bits != 0 && d->ckpt_bits != 8 && d->ckpt_bits != 32) return WKV7_ERR_UNSUPPORTED;
+    // A segment's rows are addressed with 32-bit byte offsets that move up to six
+    // tiles past its end (token_bytes): no tile of 16 tokens has more than 2^28 bytes.
+    if (d->T > INT32_MAX - 64 || d->D > (1 << 22) || (int64_t)d->D * d->N > (1 << 26) ||
+        (int64_t)d->G * d->N > (1 << 21))
+        return WKV7_ERR_UNSUPPORTED;
+    const int64_t blocks = ((int64_t)d->T + 15) / 16, most = (int64_t)1 << 40;
+    if (!product_fits(d->B, d->T, d->D, 1, most) || !product_fits(d->B, blocks, d->D, d->N, most) ||
+        !product_fits(d->B, d->T, d->G, d->N, (int64_t)1 << 32) ||
+        !product_fits(d->B, d->D, 64, 1, (int64_t)1 << 31))
+        return WKV7_ERR_UNSUPPORTED;
+    // A launch of 512 threads per workgroup stays at or below 2^31.
+    for (const bool backward : {false, true})
+        if (!product_fits(d->B, d->G, channel_blocks(d, backward), plan_ssm(d, backward).nseg, 1 << 22))
+            return WKV7_ERR_UNSUPPORTED;
+    return WKV7_OK;
 }
 
 size_t pad4(size_t floats) { return (floats + 3) / 4 * 4; }

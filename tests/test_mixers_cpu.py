@@ -270,3 +270,13 @@ def test_binding_takes_device_tensors_only():
         wk.conv_forward(x.half(), torch.zeros(16, 4))
     with pytest.raises(ValueError):
         wk.conv_forward(x[0], torch.zeros(16, 4))
+
+
+def test_launches_of_too_many_threads_are_refused():
+    """Rows of few channels: small tensors, but a workgroup (512 threads) or a wave each."""
+    L = wk.lib()
+    for over in (dict(B=1 << 24, D=1, T=1), dict(B=1 << 27, D=1, T=1), dict(B=64, D=1, T=1 << 25)):
+        assert conv(L, wk.ConvDesc(**dict(CONV_OK, **over)), ALL) == [wk.WKV7_ERR_UNSUPPORTED] * 3
+    for over in (dict(B=1 << 23, D=1, G=1, T=1), dict(B=1 << 12, D=1 << 12, G=1 << 12, T=1),
+                 dict(B=1 << 12, D=64, G=1, N=16, T=1 << 17)):   # the last: B T G N of 2^33
+        assert ssm(L, wk.SsmDesc(**dict(SSM_OK, **over)), ALL) == [wk.WKV7_ERR_UNSUPPORTED] * 3
