@@ -57,9 +57,29 @@ __device__ __forceinline__ void load_input(const ConvArgs& p, int b, int t, int 
     }
 }
 
+// The state behind each row: its last W - 1 inputs, copied, element `id` of
+// [B][W - 1][D].
+template <typename T, int W>
+__device__ __forceinline__ void copy_state(const ConvArgs& p, int64_t id) {
+    if (id >= (int64_t)p.B * (W - 1) * p.D) return;
+    const int c = (int)(id % p.D);
+    const int k = (int)(id / p.D % (W - 1)), b = (int)(id / p.D / (W - 1));
+    const int t = row_length(p.lengths, b, p.T) - (W - 1) + k;
+    T v = 0;
+    if (t >= 0) v = static_cast<const T*>(p.x)[((size_t)b * p.T + t) * p.D + c];
+    else if (p.s0) v = static_cast<const T*>(p.s0)[((size_t)b * (W - 1) + t + W - 1) * p.D + c];
+    static_cast<T*>(p.sT)[id] = v;
+}
+
+// Workgroups from `runs_end` on copy the state: a launch of its own for that took
+// 4 us more.
 template <typename T, int W, int V, bool kVec>
 __global__ __launch_bounds__(kConvThreads) void conv_fwd_kernel(const ConvArgs p, unsigned cols, unsigned runs,
-                                                               int run, unsigned items) {
+                                                               int run, unsigned items, unsigned runs_end) {
+    if (blockIdx.x >= runs_end) {
+        copy_state<T, W>(p, (int64_t)(blockIdx.x - runs_end) * kConvThreads + threadIdx.x);
+        return;
+    }
     const unsigned id = blockIdx.x * kConvThreads + threadIdx.x;
     if (id >= items) return;
     const unsigned rr = id / cols;
@@ -110,21 +130,6 @@ __global__ __launch_bounds__(kConvThreads) void conv_fwd_kernel(const ConvArgs p
         xp += (size_t)U * p.D;
         yp += (size_t)U * p.D;
     }
-}
-
-// The state behind each row: its last W - 1 inputs, copied (one thread per
-// channel; also the whole answer when there are no tokens).
-template <typename T, int W>
-__global__ __launch_bounds__(kConvThreads) void conv_state_kernel(const ConvArgs p) {
-    const int64_t id = (int64_t)blockIdx.x * kConvThreads + threadIdx.x;
-    if (id >= (int64_t)p.B * (W - 1) * p.D) return;
-    const int c = (int)(id % p.D);
-    const int k = (int)(id / p.D % (W - 1)), b = (int)(id / p.D / (W - 1));
-    const int t = row_length(p.lengths, b, p.T) - (W - 1) + k;
-    T v = 0;
-    if (t >= 0) v = static_cast<const T*>(p.x)[((size_t)b * p.T + t) * p.D + c];
-    else if (p.s0) v = static_cast<const T*>(p.s0)[((size_t)b * (W - 1) + t + W - 1) * p.D + c];
-    static_cast<T*>(p.sT)[id] = v;
 }
 
 // One token: y from the state and the input, the state moved on in place.
@@ -326,10 +331,12 @@ template <typename T, int W, int V, bool kVec>
 hipError_t fwd_v(const ConvArgs& p, hipStream_t stream) {
     const unsigned cols = (unsigned)((p.D + V - 1) / V), runs = (unsigned)((p.T + kRun - 1) / kRun);
     const uint64_t items = (uint64_t)cols * runs * p.B;
-    if (items == 0) return hipSuccess;
-    if (items > (1ull << 31)) return hipErrorInvalidValue;
-    const unsigned grid = (unsigned)((items + kConvThreads - 1) / kConvThreads);
-    conv_fwd_kernel<T, W, V, kVec><<<grid, kConvThreads, 0, stream>>>(p, cols, runs, kRun, (unsigned)items);
+    const uint64_t states = p.sT ? (uint64_t)p.B * (W - 1) * p.D : 0;
+    if (items > (1ull << 31) || states > (1ull << 31)) return hipErrorInvalidValue;
+    const unsigned runs_end = (unsigned)((items + kConvThreads - 1) / kConvThreads);
+    const unsigned grid = runs_end + (unsigned)((states + kConvThreads - 1) / kConvThreads);
+    if (grid == 0) return hipSuccess;
+    conv_fwd_kernel<T, W, V, kVec><<<grid, kConvThreads, 0, stream>>>(p, cols, runs, kRun, (unsigned)items, runs_end);
     return hipGetLastError();
 }
 
@@ -371,15 +378,10 @@ __global__ __launch_bounds__(kConvThreads) void conv_pass_kernel(const T* __rest
 template <typename T, int W>
 hipError_t fwd_w(const ConvArgs& p, hipStream_t stream) {
     constexpr int V = 16 / sizeof(T);
-    hipError_t e = p.D % V == 0         ? fwd_v<T, W, V, true>(p, stream)
-                   : p.D % (V / 2) == 0 ? fwd_v<T, W, V / 2, true>(p, stream)
-                   : p.D % 2 == 0       ? fwd_v<T, W, 2, true>(p, stream)
-                                        : fwd_v<T, W, 1, true>(p, stream);
-    if (e != hipSuccess || !p.sT) return e;
-    const uint64_t n = (uint64_t)p.B * (W - 1) * p.D;
-    if (n == 0) return hipSuccess;
-    conv_state_kernel<T, W><<<dim3((unsigned)((n + kConvThreads - 1) / kConvThreads)), kConvThreads, 0, stream>>>(p);
-    return hipGetLastError();
+    return p.D % V == 0         ? fwd_v<T, W, V, true>(p, stream)
+           : p.D % (V / 2) == 0 ? fwd_v<T, W, V / 2, true>(p, stream)
+           : p.D % 2 == 0       ? fwd_v<T, W, 2, true>(p, stream)
+                                : fwd_v<T, W, 1, true>(p, stream);
 }
 template <typename T, int W>
 hipError_t step_w(const ConvArgs& p, hipStream_t stream) {
