@@ -52,7 +52,7 @@ __global__ __launch_bounds__(2 * kStepThreads) void ssm_fwd_kernel(const SsmArgs
     const int t_begin = seg * p.seg_len;
     const int t_end = seg == p.nseg - 1 ? p.T : t_begin + p.seg_len;
     const int tiles = (t_end - t_begin + kTile - 1) / kTile;
-    const int intervals = (tiles + 5) / 4 * 4;   // tiles + 2, to a multiple of 4
+    const int intervals = tiles + (kMap ? 0 : 2);
 
     if (threadIdx.x < kStepThreads) {
         // ---- step waves: tile i - 1 in interval i --------------------------------
@@ -268,8 +268,11 @@ __global__ __launch_bounds__(2 * kStepThreads) void ssm_fwd_kernel(const SsmArgs
     };
     for (int i = 0; i < intervals; i += 4) {
         interval(i, r0, r2);
+        if (i + 1 == intervals) break;
         interval(i + 1, r1, r3);
+        if (i + 2 == intervals) break;
         interval(i + 2, r2, r0);
+        if (i + 3 == intervals) break;
         interval(i + 3, r3, r1);
     }
 }

@@ -167,7 +167,7 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
     const int t_begin = seg * p.seg_len;
     const int t_end = seg == p.nseg - 1 ? p.T : t_begin + p.seg_len;
     const int tiles = (t_end - t_begin + kTile - 1) / kTile;
-    const int intervals = (tiles + 6) / 4 * 4;   // tiles + 3, to a multiple of 4
+    const int intervals = tiles + (kMap ? 0 : 3);
     const size_t BDN = (size_t)p.B * p.D * N, BD = (size_t)p.B * p.D;
 
     if (threadIdx.x < kStepThreads) {
@@ -541,8 +541,11 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
     };
     for (int i = 0; i < intervals; i += 4) {
         interval(i, r0, k0, k1);
+        if (i + 1 == intervals) break;
         interval(i + 1, r1, k1, k2);
+        if (i + 2 == intervals) break;
         interval(i + 2, r0, k2, k3);
+        if (i + 3 == intervals) break;
         interval(i + 3, r1, k3, k0);
     }
     if constexpr (!kMap) {
