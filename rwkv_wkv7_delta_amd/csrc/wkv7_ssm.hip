@@ -117,12 +117,14 @@ __global__ __launch_bounds__(2 * kStepThreads) void ssm_fwd_kernel(const SsmArgs
     // ---- staging waves: tile i in interval i, the outputs of tile i - 2 -------------
     const int tid = threadIdx.x - kStepThreads;
     const int len = row_length(p.lengths, b, p.T);
-    const int pt = tid / 16, pl = (tid % 16) * EPT;   // the thread's row piece
+    // The thread's row piece: EPT neighbouring channels, or every sixteenth.
+    constexpr int ES = kVec ? 1 : kApart;
+    const int pt = tid / 16, pl = tid % 16 * (kVec ? EPT : 1);
     const int be = tid * BC, bt = be / N, bn = be % N;              // and its elements of B and C
     float bias[EPT], skip[EPT];
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
-        const int c = c0 + pl + i < cend ? c0 + pl + i : cend - 1;
+        const int c = c0 + pl + ES * i < cend ? c0 + pl + ES * i : cend - 1;
         bias[i] = p.dt_bias ? p.dt_bias[c] : 0.f;
         skip[i] = p.dskip ? p.dskip[c] : 0.f;
     }
@@ -135,7 +137,7 @@ __global__ __launch_bounds__(2 * kStepThreads) void ssm_fwd_kernel(const SsmArgs
     // is conditional, and each wait covers exactly the loads it needs.
     const bool full = kVec || EPT == 1;   // a piece lies inside its group or behind it
     const bool dead = c0 + pl >= cend;
-    const int valid = full ? 1 : cend - c0 - pl, here = cend - c0 < CH ? cend - c0 : CH;
+    const int valid = full ? 1 : (cend - c0 - pl + ES - 1) / ES, here = cend - c0 < CH ? cend - c0 : CH;
     const uint32_t row = p.D * (uint32_t)sizeof(T), row_bc = p.G * N * (uint32_t)sizeof(T);
     const int tokens = t_end - t_begin;
     auto rows_of = [&](const void* base, bool on) {
@@ -193,7 +195,7 @@ __global__ __launch_bounds__(2 * kStepThreads) void ssm_fwd_kernel(const SsmArgs
         const int end = len < t_end ? len : t_end;
         if (t0 + kTile <= end) {
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) s_du[k][pt][pl + i] = make_float2(d[i], d[i] * r.x.get(i));
+            for (int i = 0; i < EPT; ++i) s_du[k][pt][pl + ES * i] = make_float2(d[i], d[i] * r.x.get(i));
             if (bt < kTile) {
 #pragma unroll
                 for (int i = 0; i < BC; ++i) {
@@ -206,7 +208,7 @@ __global__ __launch_bounds__(2 * kStepThreads) void ssm_fwd_kernel(const SsmArgs
 #pragma unroll
             for (int i = 0; i < EPT; ++i) {
                 const float u = d[i] * r.x.get(i);
-                s_du[k][pt][pl + i] = make_float2(in ? d[i] : 0.f, in ? u : 0.f);
+                s_du[k][pt][pl + ES * i] = make_float2(in ? d[i] : 0.f, in ? u : 0.f);
             }
             if (bt < kTile) {
 #pragma unroll
@@ -222,11 +224,11 @@ __global__ __launch_bounds__(2 * kStepThreads) void ssm_fwd_kernel(const SsmArgs
         const int t0 = t_begin + tile * kTile, k = tile & 1;
         float out[EPT];
 #pragma unroll
-        for (int i = 0; i < EPT; ++i) out[i] = s_y[k][pt][0][pl + i];
+        for (int i = 0; i < EPT; ++i) out[i] = s_y[k][pt][0][pl + ES * i];
 #pragma unroll
         for (int q = 1; q < P; ++q)
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) out[i] += s_y[k][pt][q][pl + i];
+            for (int i = 0; i < EPT; ++i) out[i] += s_y[k][pt][q][pl + ES * i];
 #pragma unroll
         for (int i = 0; i < EPT; ++i) out[i] = fmaf(skip[i], xr.get(i), out[i]);
         if (gate) {

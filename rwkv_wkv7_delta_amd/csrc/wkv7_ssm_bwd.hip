@@ -335,13 +335,14 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
     // ---- the (i - 3)-th ---------------------------------------------------------------
     const int tid = threadIdx.x - kStepThreads;
     const int len = row_length(p.lengths, b, p.T);
-    const int pt = tid / 16, pl = (tid % 16) * EPT;
+    constexpr int ES = kVec ? 1 : kApart;
+    const int pt = tid / 16, pl = tid % 16 * (kVec ? EPT : 1);
     const int be = tid * BC, bt = be / N, bn = be % N;
     const int hc = tid * S / N, hn = tid * S % N;     // the thread's entry states
     float bias[EPT], skip[EPT], sum_skip[EPT], sum_bias[EPT];
 #pragma unroll
     for (int i = 0; i < EPT; ++i) {
-        const int c = c0 + pl + i < cend ? c0 + pl + i : cend - 1;
+        const int c = c0 + pl + ES * i < cend ? c0 + pl + ES * i : cend - 1;
         bias[i] = p.dt_bias ? p.dt_bias[c] : 0.f;
         skip[i] = p.dskip ? p.dskip[c] : 0.f;
         sum_skip[i] = sum_bias[i] = 0.f;
@@ -351,7 +352,7 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
     // buffers' start, which as an unsigned offset is behind their end.
     const bool full = kVec || EPT == 1;
     const bool dead = c0 + pl >= cend;
-    const int valid = full ? 1 : cend - c0 - pl, here = cend - c0 < CH ? cend - c0 : CH;
+    const int valid = full ? 1 : (cend - c0 - pl + ES - 1) / ES, here = cend - c0 < CH ? cend - c0 : CH;
     const uint32_t row = p.D * (uint32_t)sizeof(T), row_bc = p.G * N * (uint32_t)sizeof(T);
     const int tokens = t_end - t_begin;
     auto rows_of = [&](const void* base) {
@@ -457,8 +458,8 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
         }
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
-            s_du[k][pt][pl + e] = make_float2(o.d[e], o.d[e] * o.x[e]);
-            s_dy[k][pt][pl + e] = o.dy[e];
+            s_du[k][pt][pl + ES * e] = make_float2(o.d[e], o.d[e] * o.x[e]);
+            s_dy[k][pt][pl + ES * e] = o.dy[e];
         }
         if (bt < kTile) {
             const bool inb = !partial || t0 + bt < end;
@@ -484,7 +485,7 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
         float dx[EPT], ddt[EPT], dz[EPT];
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
-            const int c = pl + e, base = c / 16 * PW * 16 + c % 16;
+            const int c = pl + ES * e, base = c / 16 * PW * 16 + c % 16;
             float du = s_o[k][0][pt][base], sr = s_o[k][1][pt][base];
 #pragma unroll
             for (int w = 1; w < PW; ++w) {
@@ -506,7 +507,7 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
         if constexpr (kGate) {
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
-                const int c = pl + e, base = c / 16 * PW * 16 + c % 16;
+                const int c = pl + ES * e, base = c / 16 * PW * 16 + c % 16;
                 float y = s_y[i & 3][pt][base];
 #pragma unroll
                 for (int w = 1; w < PW; ++w) y += s_y[i & 3][pt][base + 16 * w];
@@ -552,8 +553,8 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
         // The per-channel vectors: sixteen threads hold a channel's tokens.
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
-            s_o[0][0][pt][pl + e] = sum_skip[e];
-            s_o[0][1][pt][pl + e] = sum_bias[e];
+            s_o[0][0][pt][pl + ES * e] = sum_skip[e];
+            s_o[0][1][pt][pl + ES * e] = sum_bias[e];
         }
         __syncthreads();
         if (tid < CH && c0 + tid < cend) {

@@ -33,6 +33,8 @@ __device__ __forceinline__ float softplus(float x) {
 typedef uint32_t vu2 __attribute__((ext_vector_type(2)));
 typedef uint32_t vu4 __attribute__((ext_vector_type(4)));
 
+constexpr int kApart = 16;
+
 template <typename T, int V, bool kVec>
 struct Piece {
     static constexpr int kBytes = V * (int)sizeof(T);
@@ -67,13 +69,14 @@ struct Piece {
             }
         }
     }
-    // At byte `at` of a buffer; what lies outside it reads as 0.
+    // At byte `at` of a buffer; what lies outside it reads as 0.  Without kVec the
+    // elements are kApart elements apart: sixteen lanes' loads lie side by side.
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t at) {
         if constexpr (!kVec) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                if constexpr (sizeof(T) == 4) w[i] = __builtin_amdgcn_raw_buffer_load_b32(r, at + 4 * i, 0, 0);
-                else w[i] = __builtin_amdgcn_raw_buffer_load_b16(r, at + 2 * i, 0, 0);
+                if constexpr (sizeof(T) == 4) w[i] = __builtin_amdgcn_raw_buffer_load_b32(r, at + 4 * kApart * i, 0, 0);
+                else w[i] = __builtin_amdgcn_raw_buffer_load_b16(r, at + 2 * kApart * i, 0, 0);
             }
         } else if constexpr (kBytes == 2) {
             w[0] = __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0);
@@ -141,7 +144,7 @@ __device__ __forceinline__ void store_piece(__amdgpu_buffer_rsrc_t r, uint32_t a
     if constexpr (!kVec) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const uint32_t o = i < valid ? at + i * (uint32_t)sizeof(T) : kNowhere;
+            const uint32_t o = i < valid ? at + i * kApart * (uint32_t)sizeof(T) : kNowhere;
             if constexpr (sizeof(T) == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x[i]), r, o, 0, 0);
             else __builtin_amdgcn_raw_buffer_store_b16(f2bf(x[i]), r, o, 0, 0);
         }
