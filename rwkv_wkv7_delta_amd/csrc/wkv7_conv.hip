@@ -13,6 +13,10 @@
 // along a run of tokens with the last W - 1 inputs in registers, so that a
 // token row is read by one run only, but for the W - 1 rows before a run.
 // fp32 arithmetic, outputs rounded once.
+//
+// (8, 4096) tokens of 2560 channels, bf16, two taps: 74 us, 4.5 TB/s (a copy of
+// 1 GiB reaches 5.1); (5, 1021) tokens of 1001 channels, fp32, four taps, one
+// channel per lane: 12 us.
 
 #include "wkv7_ssm_device.h"
 #include "wkv7_ssm_internal.h"
@@ -169,7 +173,9 @@ __global__ __launch_bounds__(kConvThreads) void conv_step_kernel(const ConvArgs 
 // first run of a row gives ds0.  x and dy are read through buffers that end
 // with the row's length (what is behind reads as 0, so e and dx there come out
 // as 0), dx is written through one that holds the run's tokens: the loop has no
-// condition per token.  The sums over a run stay in registers; the workgroup's
+// condition per token.  (4, 4096) tokens of 2048 channels, bf16, four taps: 48 us,
+// 4.2 TB/s, with four channels a lane and about 2048 waves (4096: 50 us; two
+// channels a lane: 51 to 55 us).  The sums over a run stay in registers; the workgroup's
 // four meet in LDS, the workgroups in a second kernel, in a fixed order.
 template <typename T, int W, int V, bool kVec, bool kSilu>
 __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvBwdArgs q, unsigned cblocks, int runs) {
@@ -325,7 +331,9 @@ __global__ __launch_bounds__(256) void conv_params_kernel(const float* __restric
     }
 }
 
-constexpr int kRun = 16;   // tokens of a forward run
+// Tokens of a forward run.  8, 16 and 32 for the two shapes named at the top: 74.5,
+// 73.9, 72.3 us and 11.8, 12.0, 15.1 us.
+constexpr int kRun = 16;
 
 template <typename T, int W, int V, bool kVec>
 hipError_t fwd_v(const ConvArgs& p, hipStream_t stream) {

@@ -90,9 +90,9 @@ int64_t token_bytes(const wkv7_ssm_desc* d) {
 // and channel block.  The first of the two launches repeats most of the
 // exponentials, so a split only pays when it shortens the chain enough: three
 // segments at least, as many as make two workgroups per compute unit (forward at
-// B = 1, T = 16384, D = 768, N = 16: 64 segments at most 95 us, 32 116 us; four
-// workgroups per unit 102 us; forward and backward at B = 4, T = 1024, D = 768:
-// one, two, four per unit 170, 128, 153 us), of 64 tokens at least.
+// B = 1, T = 16384, D = 768, N = 16: 64 segments at most 95 us, 32 116 us; one, two,
+// four workgroups per unit 96, 95, 102 us; forward and backward at B = 4, T = 1024,
+// D = 768: 170, 128, 153 us), of 64 tokens at least.
 struct SsmPlan {
     int nseg, seg_len;
 };
