@@ -81,7 +81,13 @@ __global__ __launch_bounds__(2 * kStepThreads) void ssm_fwd_kernel(const SsmArgs
             const size_t BDN = (size_t)p.B * p.D * N, BD = (size_t)p.B * p.D;
             through_segments<4>(h, a2, p.seg_h + chn, (int64_t)BDN, p.seg_d + chn / N, (int64_t)BD, seg);
         }
-        for (int i = 0; i < intervals; ++i) {
+        // A wave whose channels all lie behind the group only keeps the barriers: what
+        // is read of its sums is not stored.
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+        int i = 0;
+        if (c0 + wave * 4 / P * 16 >= cend)
+            for (; i < intervals; ++i) __syncthreads();
+        for (; i < intervals; ++i) {
             __syncthreads();
             if (i >= tiles) continue;
             const int k = i & 1;
