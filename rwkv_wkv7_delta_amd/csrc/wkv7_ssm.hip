@@ -15,7 +15,7 @@
 // fp32; only the stored outputs are rounded.
 //
 // Bound by the vector ALU.  (8, 4096) tokens of 2048 channels, 16 states, bf16,
-// with a gate: 250 us, against 105 us for its 0.54 GB at the rate of a large copy
+// with a gate: 259 us, against 105 us for its 0.54 GB at the rate of a large copy
 // (5.1 TB/s).  A token of four states per lane takes 20 vector instructions, four
 // of them exponentials, and a SIMD 41 ns at any occupancy: 168 us for the whole,
 // and the staging waves' softplus and gate take most of the rest.  Measured
