@@ -96,7 +96,6 @@ int64_t token_bytes(const wkv7_ssm_desc* d) {
 struct SsmPlan {
     int nseg, seg_len;
 };
-constexpr int kUnits = 256;          // compute units of the device
 constexpr int kMaxSegments = 64;
 constexpr int kMinSegmentTokens = 64;
 
@@ -104,7 +103,7 @@ SsmPlan plan_ssm(const wkv7_ssm_desc* d, bool backward) {
     const SsmPlan none{1, d->T};
     const int64_t wgs = (int64_t)d->B * d->G * channel_blocks(d, backward);
     if (wgs == 0 || d->T == 0) return none;
-    int64_t n = 2 * kUnits / wgs;
+    int64_t n = 2 * wkv7::kUnits / wgs;
     if (n > d->T / kMinSegmentTokens) n = d->T / kMinSegmentTokens;
     if (n > kMaxSegments) n = kMaxSegments;
     if (n < 3) n = 1;

@@ -150,14 +150,20 @@ __device__ __forceinline__ float fold_rows(float v0, float v1, float v2, float v
     return __uint_as_float(c[0]) + __uint_as_float(c[1]);
 }
 
-template <typename T, int N, bool kVec, bool kMap, bool kGate>
-__global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmBwdArgs q, int blocks) {
+// A row of 64 sums, turned by 16 per token: neighbouring tokens' rows then lie on
+// different banks.
+__device__ __forceinline__ int turned(int t, int col) { return (col + 16 * t) & 63; }
+
+// kDense: registers for two workgroups per compute unit (LDS holds two at N = 16
+// and 32).
+template <typename T, int N, bool kVec, bool kMap, bool kGate, bool kDense>
+__global__ __launch_bounds__(2 * kStepThreads, (kDense ? 4 : 2)) void ssm_bwd_kernel(const SsmBwdArgs q, int blocks) {
     constexpr int S = kStates<N>;
     using Sh = Shape<N, S>;
     constexpr int EPT = Sh::EPT, BC = Sh::BC, P = Sh::P, CH = Sh::CH, HS = Sh::HS;
     constexpr int PW = P / 4;                  // waves that share a channel
     constexpr int CG = CH / 16;                // groups of 16 channels
-    constexpr int OS = 64 + 16;                // row stride of the sums over states
+    constexpr int OS = 64;                     // row stride of the sums over states
     // A tile's inputs and its read-outs are live through four intervals (staged;
     // its states; its adjoint; its gradients), the rest through two.
     __shared__ __attribute__((aligned(16))) float2 s_du[4][kTile][CH];
@@ -260,7 +266,7 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
                     y4[t % 4] = y;
                     // rows 0, 1, 2, 3 hold tokens t - 3, t - 1, t - 2, t
                     if constexpr (t % 4 == 3)
-                        s_y[i & 3][t - 3 + 2 * later + second][col] = fold_rows(y4[0], y4[1], y4[2], y4[3]);
+                        s_y[i & 3][t - 3 + 2 * later + second][turned(t - 3 + 2 * later + second, col)] = fold_rows(y4[0], y4[1], y4[2], y4[3]);
                 }
             };
             auto adjoint = [&](auto tok, const Tile& w, int i) {
@@ -293,7 +299,7 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
 #pragma unroll
                     for (int n = 0; n < 4; ++n) v1[n] = v[0][n];
                 } else {   // value 0: (sb, t + 1), 1: (sr, t + 1), 2: (sb, t), 3: (sr, t)
-                    s_o[k][second][t + 1 - later][col] = fold_rows(sb1, sr1, sb, sr);
+                    s_o[k][second][t + 1 - later][turned(t + 1 - later, col)] = fold_rows(sb1, sr1, sb, sr);
                     if constexpr (S == 2) {
                         fold_row(v1, v[0], f0, f1);
                         s_red[k][at.cl / 16][t + 1][n_red] = f0;
@@ -497,11 +503,11 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
             const int c = pl + ES * e, base = c / 16 * PW * 16 + c % 16;
-            float du = s_o[k][0][pt][base], sr = s_o[k][1][pt][base];
+            float du = s_o[k][0][pt][turned(pt, base)], sr = s_o[k][1][pt][turned(pt, base)];
 #pragma unroll
             for (int w = 1; w < PW; ++w) {
-                du += s_o[k][0][pt][base + 16 * w];
-                sr += s_o[k][1][pt][base + 16 * w];
+                du += s_o[k][0][pt][turned(pt, base + 16 * w)];
+                sr += s_o[k][1][pt][turned(pt, base + 16 * w)];
             }
             dx[e] = fmaf(du, o.d[e], o.dy[e] * skip[e]);
             ddt[e] = fmaf(du, o.x[e], sr) * o.slope[e];
@@ -519,9 +525,9 @@ __global__ __launch_bounds__(2 * kStepThreads, 2) void ssm_bwd_kernel(const SsmB
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
                 const int c = pl + ES * e, base = c / 16 * PW * 16 + c % 16;
-                float y = s_y[i & 3][pt][base];
+                float y = s_y[i & 3][pt][turned(pt, base)];
 #pragma unroll
-                for (int w = 1; w < PW; ++w) y += s_y[i & 3][pt][base + 16 * w];
+                for (int w = 1; w < PW; ++w) y += s_y[i & 3][pt][turned(pt, base + 16 * w)];
                 dz[e] = o.w[e] * fmaf(skip[e], o.x[e], y);
             }
             store_piece<T, kVec>(dz_rows, out_at, valid, dz);
@@ -635,11 +641,17 @@ hipError_t launch_bwd_v(const SsmBwdArgs& q, int blocks, hipStream_t stream) {
     const unsigned per = (unsigned)p.B * p.G * blocks;
     if (per == 0) return hipSuccess;
     if (p.nseg > 1) {
-        ssm_bwd_kernel<T, N, kVec, true, kGate><<<dim3(per * (p.nseg - 1)), threads, 0, stream>>>(q, blocks);
+        ssm_bwd_kernel<T, N, kVec, true, kGate, false><<<dim3(per * (p.nseg - 1)), threads, 0, stream>>>(q, blocks);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    ssm_bwd_kernel<T, N, kVec, false, kGate><<<dim3(per * p.nseg), threads, 0, stream>>>(q, blocks);
+    if constexpr (N == 16 || N == 32) {
+        if (per * p.nseg > kUnits) {
+            ssm_bwd_kernel<T, N, kVec, false, kGate, true><<<dim3(per * p.nseg), threads, 0, stream>>>(q, blocks);
+            return hipGetLastError();
+        }
+    }
+    ssm_bwd_kernel<T, N, kVec, false, kGate, false><<<dim3(per * p.nseg), threads, 0, stream>>>(q, blocks);
     return hipGetLastError();
 }
 

@@ -8,6 +8,7 @@
 
 namespace wkv7 {
 
+constexpr int kUnits = 256;        // compute units of the device
 constexpr int kSsmChunk = 16;      // tokens per state checkpoint and per kernel tile
 constexpr int kSsmThreads = 256;   // lanes that hold a scan workgroup's states
 constexpr int kSsmStates = 4;      // states of a channel per lane (forward)
