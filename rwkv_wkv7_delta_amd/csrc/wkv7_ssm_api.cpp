@@ -89,10 +89,15 @@ int64_t token_bytes(const wkv7_ssm_desc* d) {
 // Time segments: a launch without them has one workgroup per batch row, group
 // and channel block.  The first of the two launches repeats most of the
 // exponentials, so a split only pays when it shortens the chain enough: three
-// segments at least, as many as make two workgroups per compute unit (forward at
-// B = 1, T = 16384, D = 768, N = 16: 64 segments at most 95 us, 32 116 us; one, two,
-// four workgroups per unit 96, 95, 102 us; forward and backward at B = 4, T = 1024,
-// D = 768: 170, 128, 153 us), of 64 tokens at least.
+// segments at least, of 64 tokens at least, as many as make one or two workgroups
+// per compute unit.  Two at N = 16, and in the backward at N = 32, whose workgroups
+// run two at a time (forward and backward at B = 4, T = 1024, D = 768, N = 16: one,
+// two, four per unit 159, 104, 111 us; forward at B = 1, T = 16384, D = 768 95, 93,
+// 98 us; backward at B = 2, T = 1024, D = 512, N = 32 53, 49, 52 us); one elsewhere,
+// where more only add first launches' work (B = 3, T = 1024, D = 1024, N = 8: forward
+// 25, 30, 30 us, backward 44, 50, 53; B = 1, T = 2048, D = 512, N = 64: 37, 42, 64 and
+// 83, 87, 110; forward at N = 32 21.5, 24, 24).  At most 64: B = 1, T = 16384, D = 768
+// with 32 at most took 116 us where 64 took 95.
 struct SsmPlan {
     int nseg, seg_len;
 };
@@ -103,7 +108,7 @@ SsmPlan plan_ssm(const wkv7_ssm_desc* d, bool backward) {
     const SsmPlan none{1, d->T};
     const int64_t wgs = (int64_t)d->B * d->G * channel_blocks(d, backward);
     if (wgs == 0 || d->T == 0) return none;
-    int64_t n = 2 * wkv7::kUnits / wgs;
+    int64_t n = (d->N == 16 || (backward && d->N == 32) ? 2 : 1) * wkv7::kUnits / wgs;
     if (n > d->T / kMinSegmentTokens) n = d->T / kMinSegmentTokens;
     if (n > kMaxSegments) n = kMaxSegments;
     if (n < 3) n = 1;
