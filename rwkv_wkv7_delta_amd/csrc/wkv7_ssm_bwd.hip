@@ -22,7 +22,7 @@
 // tiles in registers, over batch rows and segments by the second kernel.
 //
 // Bound by the vector ALU and the one step wave per SIMD that feeds it.  (4, 4096)
-// tokens of 2048 channels, 16 states, bf16, gate, 8-bit checkpoints: 480 us and 25
+// tokens of 2048 channels, 16 states, bf16, gate, 8-bit checkpoints: 472 us and 25
 // for the sums of the partial dB and dC (134 MB), against 144 us for all bytes.  A
 // step wave takes 630 vector instructions per tile (two states and sixteen tokens
 // per lane: 128 of them folds over channels, 48 swaps and adds over states), a
@@ -30,7 +30,7 @@
 // this split: one state per lane on eight step waves 543 us where this took 521;
 // the sums over states on v_mfma_f32_16x16x4 974 us; states and adjoint on four
 // waves each, the states handed over in LDS and the exponentials taken twice, 540
-// where this took 504.
+// where this took 505.
 //
 // Time segments (few channels): the adjoint is affine too, carry_left =
 // exp(A sum D) carry_right + e; a first launch finds e and sum D of every
@@ -155,7 +155,10 @@ __device__ __forceinline__ float fold_rows(float v0, float v1, float v2, float v
 __device__ __forceinline__ int turned(int t, int col) { return (col + 16 * t) & 63; }
 
 // kDense: registers for two workgroups per compute unit (LDS holds two at N = 16
-// and 32).
+// and 32).  That fills each one's waits, but ties the schedule: with more than
+// one workgroup per unit, (4, 1024) tokens of 768 channels, forward and
+// backward, take 104 us with it and 112 without; one workgroup per unit, (4, 4096)
+// of 2048 channels, 568 with it and 497 without.
 template <typename T, int N, bool kVec, bool kMap, bool kGate, bool kDense>
 __global__ __launch_bounds__(2 * kStepThreads, (kDense ? 4 : 2)) void ssm_bwd_kernel(const SsmBwdArgs q, int blocks) {
     constexpr int S = kStates<N>;
