@@ -168,3 +168,16 @@ def test_repeats_agree_and_other_stream(wk):
         second = wk.conv_backward(*args, silu=True)
     torch.cuda.current_stream().wait_stream(side)
     assert all(torch.equal(a, b) for a, b in zip(first, second))
+
+
+@pytest.mark.parametrize("B,T,D", [(700, 530, 5), (600, 40, 4)])   # gradient runs of 268 and 16 tokens
+def test_gradients_of_many_rows(wk, B, T, D):
+    import torch
+    p, more = make(13, B, T, D, 3, "bf16", lengths=[(7 * b) % (T + 9) for b in range(B)])
+    dx, dw, db, ds0 = wk.conv_backward(p["x"], p["weight"], more["dy"], p["bias"], s0=p["s0"], dsT=more["dsT"],
+                                       lengths=p["lengths"], silu=True)
+    grads = ref.conv_grads(dy=host(more["dy"]), dsT=host(more["dsT"]), silu=True, **{k: host(v) for k, v in p.items()})
+    ref.assert_within(dx, grads["dx"], p["x"].dtype, 32, "dx")
+    ref.assert_within(ds0, grads["ds0"], p["x"].dtype, 32, "ds0")
+    ref.assert_within(dw, grads["dweight"], torch.float32, 32 + B * T, "dweight")
+    ref.assert_within(db, grads["dbias"], torch.float32, 32 + B * T, "dbias")

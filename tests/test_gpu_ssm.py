@@ -309,3 +309,36 @@ def test_repeats_agree_and_other_stream(wk):
         second = once()
     torch.cuda.current_stream().wait_stream(side)
     assert all(torch.equal(a, b) for a, b in zip(first, second))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("N,D,G,gate,lengths", [(16, 32, 16, True, None), (16, 48, 16, False, "some"),
+                                                (32, 32, 16, True, "some"), (32, 64, 16, False, None)])
+def test_gradients_of_many_workgroups(wk, N, D, G, gate, lengths, dtype):
+    """More workgroups than the device has compute units (20 rows of 16 groups): the
+    backward's variant for two of them on one unit."""
+    B, T = 20, 21
+    lengths = [t % 24 for t in range(B)] if lengths else None
+    p, h0, more = make(59, B, T, D, N, G, dtype, gate=gate, lengths=lengths)
+    args, kw = call(p)
+    _, _, ck = wk.ssm_forward(*args, h0=h0, ckpt_bits=32, **kw)
+    got = wk.ssm_backward(*args, more["dy"], ck, dhT=more["dhT"], **kw)
+    check_grads(got, ref.Scan(h0=host(h0), **hosts(p)), more, p)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("N", [8, 64])
+def test_single_tokens_of_many_rows(wk, N, dtype):
+    """Several rows per lane (4096 workgroups and more of one row each); the last lanes
+    have fewer."""
+    import torch
+    B, D = 4099, 6
+    p, h0, _ = make(63, B, 1, D, N, 1, dtype)
+    at = lambda v: v[:, 0].contiguous()   # noqa: E731
+    state = h0.clone()
+    y = wk.ssm_step(at(p["x"]), at(p["dt"]), p["A"], at(p["Bm"]), at(p["Cm"]), state, z=at(p["z"]),
+                    dskip=p["dskip"], dt_bias=p["dt_bias"])
+    s = ref.Scan(h0=host(h0), **hosts(p))
+    want = s.outputs()
+    ref.assert_within(y[:, None], want["y"], p["x"].dtype, s.roundings() + N, "y")
+    ref.assert_within(state, want["hT"], torch.float32, s.roundings(), "state")
