@@ -22,7 +22,7 @@
 // tiles in registers, over batch rows and segments by the second kernel.
 //
 // Bound by the vector ALU and the one step wave per SIMD that feeds it.  (4, 4096)
-// tokens of 2048 channels, 16 states, bf16, gate, 8-bit checkpoints: 472 us and 25
+// tokens of 2048 channels, 16 states, bf16, gate, 8-bit checkpoints: 466 us and 25
 // for the sums of the partial dB and dC (134 MB), against 144 us for all bytes.  A
 // step wave takes 630 vector instructions per tile (two states and sixteen tokens
 // per lane: 128 of them folds over channels, 48 swaps and adds over states), a
@@ -97,10 +97,8 @@ __device__ __forceinline__ void fold_row(const float (&v)[4], const float (&w)[4
 
 // h = a g + x for two states, and the sum of (c broadcast from lane t of the row) h.
 // As in the forward's step_read: the s_nop for a, which an exponential may just have
-// written, the two updates in front of the products that read c through DPP.  Every
-// fourth token's sum goes straight into a lane swap (fold_rows), which may not read
-// what one of the two vector instructions before it wrote; the compiler keeps that
-// distance for its own instructions, not for those in here.
+// written, the two updates in front of the products that read c through DPP.  The
+// sums go into lane swaps (fold_rows): settled() first.
 template <int t>
 __device__ __forceinline__ float state_step(float& h0, float& h1, float g0, float g1, float a0, float a1, float x0,
                                             float x1, float c0, float c1) {
@@ -112,9 +110,13 @@ __device__ __forceinline__ float state_step(float& h0, float& h1, float g0, floa
         "v_fmac_f32_dpp %2, %10, %1 row_newbcast:%11 row_mask:0xf bank_mask:0xf"
         : "=&v"(h0), "=&v"(h1), "=&v"(y)
         : "v"(g0), "v"(g1), "v"(a0), "v"(a1), "v"(x0), "v"(x1), "v"(c0), "v"(c1), "n"(t));
-    if constexpr (t % 4 == 3) asm("s_nop 1" : "+v"(y));
     return y;
 }
+
+// A swap may not read what one of the two instructions before it wrote; the compiler
+// keeps that distance for its own instructions, not for state_step's sums.  Of each
+// pair that is swapped the later one counts: the other was written a token earlier.
+__device__ __forceinline__ void settled(float& y1, float& y3) { asm("s_nop 1" : "+v"(y1), "+v"(y3)); }
 
 // One step of the adjoint for two states: g <- g + c dy (c broadcast from lane t of
 // the row), v = (g u, dy h), the sum of (b broadcast) g, and g <- a g.  The two
@@ -158,7 +160,7 @@ __device__ __forceinline__ int turned(int t, int col) { return (col + 16 * t) & 
 // and 32).  That fills each one's waits, but ties the schedule: with more than
 // one workgroup per unit, (4, 1024) tokens of 768 channels, forward and
 // backward, take 104 us with it and 112 without; one workgroup per unit, (4, 4096)
-// of 2048 channels, 568 with it and 497 without.
+// of 2048 channels, 568 with it and 497 without (491 now).
 template <typename T, int N, bool kVec, bool kMap, bool kGate, bool kDense>
 __global__ __launch_bounds__(2 * kStepThreads, (kDense ? 4 : 2)) void ssm_bwd_kernel(const SsmBwdArgs q, int blocks) {
     constexpr int S = kStates<N>;
@@ -268,8 +270,11 @@ __global__ __launch_bounds__(2 * kStepThreads, (kDense ? 4 : 2)) void ssm_bwd_ke
                 if constexpr (kGate) {
                     y4[t % 4] = y;
                     // rows 0, 1, 2, 3 hold tokens t - 3, t - 1, t - 2, t
-                    if constexpr (t % 4 == 3)
-                        s_y[i & 3][t - 3 + 2 * later + second][turned(t - 3 + 2 * later + second, col)] = fold_rows(y4[0], y4[1], y4[2], y4[3]);
+                    if constexpr (t % 4 == 3) {
+                        settled(y4[1], y4[3]);
+                        const int tok = t - 3 + 2 * later + second;
+                        s_y[i & 3][tok][turned(tok, col)] = fold_rows(y4[0], y4[1], y4[2], y4[3]);
+                    }
                 }
             };
             auto adjoint = [&](auto tok, const Tile& w, int i) {
