@@ -26,7 +26,7 @@
 // for the sums of the partial dB and dC (134 MB), against 144 us for all bytes.  A
 // step wave takes 630 vector instructions per tile (two states and sixteen tokens
 // per lane: 128 of them folds over channels, 48 swaps and adds over states), a
-// staging wave 130; the vector ALU is busy for 77 % of the time.  Measured against
+// staging wave 130; the vector ALU is busy for 78 % of the time.  Measured against
 // this split: one state per lane on eight step waves 543 us where this took 521;
 // the sums over states on v_mfma_f32_16x16x4 974 us; states and adjoint on four
 // waves each, the states handed over in LDS and the exponentials taken twice, 540
