@@ -212,6 +212,10 @@ __global__ __launch_bounds__(2 * kStepThreads, (kDense ? 4 : 2)) void ssm_bwd_ke
             // segments nseg - 1 down to seg + 1, kept at one less
             through_segments<S>(carry, a2, p.seg_h + (p.nseg - 2) * (int64_t)BDN + chn, -(int64_t)BDN,
                                 p.seg_d + (p.nseg - 2) * (int64_t)BD + chn / N, -(int64_t)BD, p.nseg - 1 - seg);
+            // A lane behind the group read its last channel's; it adds to the row's dB and dC,
+            // and with D = u = dy = 0 from the staging waves every term of it is 0.
+#pragma unroll
+            for (int n = 0; n < S; ++n) carry[n] = live ? carry[n] : 0.f;
         }
         // Where the lane leaves its folded sums: row r of the wave holds value 0,
         // 2, 1, 3 of a fold over the rows; a lane of a row the state and dB or dC
@@ -378,6 +382,7 @@ __global__ __launch_bounds__(2 * kStepThreads, (kDense ? 4 : 2)) void ssm_bwd_ke
     const bool full = kVec || EPT == 1;
     const bool dead = c0 + pl >= cend;
     const int valid = full ? 1 : (cend - c0 - pl + ES - 1) / ES, here = cend - c0 < CH ? cend - c0 : CH;
+    const int held = full ? (dead ? 0 : EPT) : valid;   // the thread's channels in the group
     const uint32_t row = p.D * (uint32_t)sizeof(T), row_bc = p.G * N * (uint32_t)sizeof(T);
     const int tokens = t_end - t_begin;
     auto rows_of = [&](const void* base) {
@@ -470,10 +475,12 @@ __global__ __launch_bounds__(2 * kStepThreads, (kDense ? 4 : 2)) void ssm_bwd_ke
             }
         }
         const bool partial = t0 + kTile > end;
-        if (partial || !full) {   // tokens behind the row's length, channels behind the group
+        // Tokens behind the row's length; channels behind the group, whose rate would be
+        // that of the last channel's bias alone, and their states could grow without limit.
+        if (partial || here < CH) {
 #pragma unroll
             for (int e = 0; e < EPT; ++e) {
-                const bool on = t0 + pt < end && (full || e < valid);
+                const bool on = t0 + pt < end && e < held;
                 o.d[e] = on ? o.d[e] : 0.f;
                 o.slope[e] = on ? o.slope[e] : 0.f;
                 o.x[e] = on ? o.x[e] : 0.f;
