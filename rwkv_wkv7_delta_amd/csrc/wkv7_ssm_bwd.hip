@@ -514,7 +514,7 @@ __global__ __launch_bounds__(2 * kStepThreads, (kDense ? 4 : 2)) void ssm_bwd_ke
     };
     auto write_out = [&](const Kept<EPT>& o, int i) {
         const int k = i & 1;
-        float dx[EPT], ddt[EPT], dz[EPT];
+        float dx[EPT], ddt[EPT], dz[EPT], s[E];
 #pragma unroll
         for (int e = 0; e < EPT; ++e) {
             const int c = pl + ES * e, base = c / 16 * PW * 16 + c % 16;
@@ -526,6 +526,32 @@ __global__ __launch_bounds__(2 * kStepThreads, (kDense ? 4 : 2)) void ssm_bwd_ke
             }
             dx[e] = fmaf(du, o.d[e], o.dy[e] * skip[e]);
             ddt[e] = fmaf(du, o.x[e], sr) * o.slope[e];
+            if constexpr (kGate) {
+                float y = s_y[i & 3][pt][turned(pt, base)];
+#pragma unroll
+                for (int w = 1; w < PW; ++w) y += s_y[i & 3][pt][turned(pt, base + 16 * w)];
+                dz[e] = o.w[e] * fmaf(skip[e], o.x[e], y);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            s[e] = s_red[k][0][rt][rn + e];
+#pragma unroll
+            for (int c = 1; c < CG; ++c) s[e] += s_red[k][c][rt][rn + e];
+        }
+        // Tokens behind the row's length: their products are 0 unless the channel's state or
+        // gradient is not finite, their outputs 0 all the same.
+        const int end = len < t_end ? len : t_end, t0 = t_begin + last - i * kTile;
+        if (t0 + kTile > end) {
+            const bool in = t0 + pt < end, inb = t0 + rt < end;
+#pragma unroll
+            for (int e = 0; e < EPT; ++e) {
+                dx[e] = in ? dx[e] : 0.f;
+                ddt[e] = in ? ddt[e] : 0.f;
+                if constexpr (kGate) dz[e] = in ? dz[e] : 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) s[e] = inb ? s[e] : 0.f;
         }
         if (i >= 0 && i < tiles) {
 #pragma unroll
@@ -536,24 +562,7 @@ __global__ __launch_bounds__(2 * kStepThreads, (kDense ? 4 : 2)) void ssm_bwd_ke
         }
         store_piece<T, kVec>(dx_rows, out_at, valid, dx);
         store_piece<T, kVec>(ddt_rows, out_at, valid, ddt);
-        if constexpr (kGate) {
-#pragma unroll
-            for (int e = 0; e < EPT; ++e) {
-                const int c = pl + ES * e, base = c / 16 * PW * 16 + c % 16;
-                float y = s_y[i & 3][pt][turned(pt, base)];
-#pragma unroll
-                for (int w = 1; w < PW; ++w) y += s_y[i & 3][pt][turned(pt, base + 16 * w)];
-                dz[e] = o.w[e] * fmaf(skip[e], o.x[e], y);
-            }
-            store_piece<T, kVec>(dz_rows, out_at, valid, dz);
-        }
-        float s[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            s[e] = s_red[k][0][rt][rn + e];
-#pragma unroll
-            for (int c = 1; c < CG; ++c) s[e] += s_red[k][c][rt][rn + e];
-        }
+        if constexpr (kGate) store_piece<T, kVec>(dz_rows, out_at, valid, dz);
         store_piece<float, true>(part_rows, part_at, 1, s);
         store_piece<T, true>(db_rows, o_at, rn < N, s);
         store_piece<T, true>(dc_rows, o_at, rn >= N, s);
