@@ -221,6 +221,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvBwdArg
                 ew[k][i] = 0.f;
             }
         }
+        const int inner = t1 < len ? t1 : len;   // the run's own tokens end here
         // A group of U tokens from t on; edge: some lie outside the run, or give
         // gradients of a state.
         auto group = [&](int t, auto edge_) {
@@ -245,12 +246,14 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvBwdArg
                         for (int k = 0; k < W; ++k) pre = fmaf(w[k][i], xw[u + k][i], pre);
                         const float s = sigmoid(pre);
                         e *= s * fmaf(pre, 1.f - s, 1.f);
+                        // 0 behind the row's last token, whatever the taps make of its last inputs
+                        if constexpr (kEdge) e = t + u < len ? e : 0.f;
                     }
                     ew[H + u][i] = e;
-                    const float own = !kEdge || t + u < t1 ? e : 0.f;
+                    const bool own = !kEdge || t + u < inner;
 #pragma unroll
-                    for (int k = 0; k < W; ++k) dw[k][i] = fmaf(own, xw[u + k][i], dw[k][i]);
-                    db[i] += own;
+                    for (int k = 0; k < W; ++k) dw[k][i] = own ? fmaf(e, xw[u + k][i], dw[k][i]) : dw[k][i];
+                    db[i] += own ? e : 0.f;
                     // input t + u - (W-1) meets tap W-1 at its own token, tap 0 here
                     g[i] = w[0][i] * e;
 #pragma unroll
@@ -280,7 +283,6 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvBwdArg
                 }
             at += U * step;
         };
-        const int inner = t1 < len ? t1 : len;
         int t = t0;
         if (rr == 0) {
             group(t, Yes());
