@@ -584,7 +584,8 @@ int wkv7_ssm_forward(const wkv7_ssm_desc *desc, const wkv7_ssm_params *params, c
  * states inside a block of 16 tokens are formed again from the block's
  * checkpoint; with 8 bits the gradients are those of states rounded there, and
  * dh0 is taken through the rounding unchanged.  Sums run in a fixed order:
- * repeated calls agree bit for bit.
+ * repeated calls agree bit for bit.  With D = 0 nothing is written, dBm and dCm
+ * included.
  */
 int wkv7_ssm_backward(const wkv7_ssm_desc *desc, const wkv7_ssm_params *params, const void *x,
                       const void *dt, const void *Bm, const void *Cm, const void *z,

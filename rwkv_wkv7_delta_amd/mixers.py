@@ -248,8 +248,10 @@ def ssm_backward(x, dt, A, Bm, Cm, dy, ckpt, *, z=None, dskip=None, dt_bias=None
         _same(ckpt, "ckpt", (d.B, (d.T + 15) // 16, d.D, d.N), f32, dev)
     else:
         _same(ckpt, "ckpt", (ssm_ckpt_bytes(d),), torch.uint8, dev)
-    g = SsmGrads(torch.empty_like(x), torch.empty_like(x), torch.empty_like(A), torch.empty_like(Bm),
-                 torch.empty_like(Cm), None if z is None else torch.empty_like(x),
+    # Without channels the entry point writes nothing, and B and C have gradients all the same.
+    shared = torch.empty_like if d.D else torch.zeros_like
+    g = SsmGrads(torch.empty_like(x), torch.empty_like(x), torch.empty_like(A), shared(Bm), shared(Cm),
+                 None if z is None else torch.empty_like(x),
                  None if dskip is None else torch.empty_like(dskip),
                  None if dt_bias is None else torch.empty_like(dt_bias),
                  torch.empty(state, device=dev, dtype=f32) if want_dh0 else None)

@@ -71,3 +71,17 @@ def test_growing_states_at_small_rates(wk, N, D):   # noqa: F811
     got = wk.ssm_backward(*args, more["dy"], ck, dhT=more["dhT"], **kw)
     want = _bounds.scan(h0=host(h0), dy=host(more["dy"]), dhT=host(more["dhT"]), segment=128, **hosts(p))
     _bounds.assert_grads(got, want, p["x"].dtype)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_no_channels(wk, bits):   # noqa: F811
+    """D = 0: nothing depends on B and C, their gradients are 0."""
+    import torch
+    p, h0, more = make(77, 2, 20, 0, 16, 1, "fp32")
+    args, kw = call(p)
+    y, hT, ck = wk.ssm_forward(*args, h0=h0, ckpt_bits=bits, **kw)
+    assert y.shape == (2, 20, 0) and hT.shape == (2, 0, 16) and ck.numel() == 0
+    dirty = [torch.full_like(p["Bm"], float("nan")) for _ in range(8)]   # what the allocator hands out next
+    del dirty
+    g = wk.ssm_backward(*args, more["dy"], ck, dhT=more["dhT"], ckpt_bits=bits, **kw)
+    assert bool((g.dB == 0).all()) and bool((g.dC == 0).all()) and g.dA.shape == (0, 16)
