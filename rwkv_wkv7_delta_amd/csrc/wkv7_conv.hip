@@ -49,8 +49,8 @@ __device__ __forceinline__ void load_weights(const ConvArgs& p, int c, float (&w
 
 // Input number t of batch row b (t in [1 - W, T)): the state before the first
 // token.  The loaded piece holds valid memory's values for any t in that range.
-template <typename T, int W, int V, bool kVec>
-__device__ __forceinline__ void load_input(const ConvArgs& p, int b, int t, int c, Piece<T, V, kVec>& r, bool& zero) {
+template <typename T, int W, int V>
+__device__ __forceinline__ void load_input(const ConvArgs& p, int b, int t, int c, Piece<T, V, true>& r, bool& zero) {
     const T* const X = static_cast<const T*>(p.x);
     const T* const S0 = static_cast<const T*>(p.s0);
     zero = t < 0 && !S0;
@@ -77,7 +77,7 @@ __device__ __forceinline__ void copy_state(const ConvArgs& p, int64_t id) {
 
 // Workgroups from `runs_end` on copy the state: a launch of its own for that took
 // 4 us more.
-template <typename T, int W, int V, bool kVec>
+template <typename T, int W, int V>
 __global__ __launch_bounds__(kConvThreads) void conv_fwd_kernel(const ConvArgs p, unsigned cols, unsigned runs,
                                                                int run, unsigned items, unsigned runs_end) {
     if (blockIdx.x >= runs_end) {
@@ -95,9 +95,9 @@ __global__ __launch_bounds__(kConvThreads) void conv_fwd_kernel(const ConvArgs p
     load_weights<W, V>(p, c, w, bias);
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) {
-        Piece<T, V, kVec> r;
+        Piece<T, V, true> r;
         bool zero;
-        load_input<T, W, V, kVec>(p, b, t0 - (W - 1) + k, c, r, zero);
+        load_input<T, W, V>(p, b, t0 - (W - 1) + k, c, r, zero);
         const bool keep = !zero && t0 - (W - 1) + k < len;
 #pragma unroll
         for (int i = 0; i < V; ++i) hist[k][i] = keep ? r.get(i) : 0.f;
@@ -106,7 +106,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_fwd_kernel(const ConvArgs p
     T* yp = static_cast<T*>(p.y) + ((size_t)b * p.T + t0) * p.D;
     constexpr int U = 4;   // rows loaded together
     for (int t = t0; t < t1; t += U) {
-        Piece<T, V, kVec> r[U];
+        Piece<T, V, true> r[U];
 #pragma unroll
         for (int u = 0; u < U; ++u)
             r[u].load(xp + (size_t)(t + u < t1 ? u : t1 - 1 - t) * p.D, c, p.D);
@@ -128,7 +128,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_fwd_kernel(const ConvArgs p
                     if (p.silu) pre *= sigmoid(pre);
                     out[i] = in ? pre : 0.f;
                 }
-                store_piece<kVec>(yp + (size_t)u * p.D, c, p.D, out);
+                store_piece(yp + (size_t)u * p.D, c, p.D, out);
             }
         }
         xp += (size_t)U * p.D;
@@ -137,14 +137,14 @@ __global__ __launch_bounds__(kConvThreads) void conv_fwd_kernel(const ConvArgs p
 }
 
 // One token: y from the state and the input, the state moved on in place.
-template <typename T, int W, int V, bool kVec>
+template <typename T, int W, int V>
 __global__ __launch_bounds__(kConvThreads) void conv_step_kernel(const ConvArgs p, unsigned cols, unsigned items) {
     const unsigned id = blockIdx.x * kConvThreads + threadIdx.x;
     if (id >= items) return;
     const int c = (int)(id % cols) * V;
     const size_t b = id / cols;
     float w[W][V], bias[V], in[W][V], out[V];
-    Piece<T, V, kVec> r[W];
+    Piece<T, V, true> r[W];
     T* const S = static_cast<T*>(p.sT) + b * (W - 1) * p.D;
 #pragma unroll
     for (int k = 0; k < W - 1; ++k) r[k].load(S + (size_t)k * p.D, c, p.D);
@@ -161,8 +161,8 @@ __global__ __launch_bounds__(kConvThreads) void conv_step_kernel(const ConvArgs 
         out[i] = p.silu ? pre * sigmoid(pre) : pre;
     }
 #pragma unroll
-    for (int k = 0; k < W - 1; ++k) store_piece<kVec>(S + (size_t)k * p.D, c, p.D, in[k + 1]);
-    store_piece<kVec>(static_cast<T*>(p.y) + b * p.D, c, p.D, out);
+    for (int k = 0; k < W - 1; ++k) store_piece(S + (size_t)k * p.D, c, p.D, in[k + 1]);
+    store_piece(static_cast<T*>(p.y) + b * p.D, c, p.D, out);
 }
 
 // Gradients.  e_t = dy_t, times the activation's slope at pre_t:
@@ -177,7 +177,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_step_kernel(const ConvArgs 
 // 4.2 TB/s, with four channels a lane and about 2048 waves (4096: 50 us; two
 // channels a lane: 51 to 55 us).  The sums over a run stay in registers; the workgroup's
 // four meet in LDS, the workgroups in a second kernel, in a fixed order.
-template <typename T, int W, int V, bool kVec, bool kSilu>
+template <typename T, int W, int V, bool kSilu>
 __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvBwdArgs q, unsigned cblocks, int runs) {
     constexpr int R = kConvThreads / 64, M = W + 1, H = W - 1, U = 4;
     __shared__ float s_part[R][M][64 * V];
@@ -211,9 +211,9 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvBwdArg
         float xw[H + U][V], ew[H + U][V];
 #pragma unroll
         for (int k = 0; k < H; ++k) {
-            Piece<T, V, kVec> r;
+            Piece<T, V, true> r;
             bool zero;
-            load_input<T, W, V, kVec>(p, b, t0 - H + k, c, r, zero);
+            load_input<T, W, V>(p, b, t0 - H + k, c, r, zero);
             const bool keep = !zero && t0 - H + k < len;
 #pragma unroll
             for (int i = 0; i < V; ++i) {
@@ -226,7 +226,7 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvBwdArg
         // gradients of a state.
         auto group = [&](int t, auto edge_) {
             constexpr bool kEdge = decltype(edge_)::value;
-            Piece<T, V, kVec> rx[U], ry[U];
+            Piece<T, V, true> rx[U], ry[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 rx[u].load(x_rows, at + u * step);
@@ -263,16 +263,16 @@ __global__ __launch_bounds__(kConvThreads) void conv_bwd_kernel(const ConvBwdArg
                 if constexpr (kEdge) {
                     const int k = src - (len - H);   // in the last state
                     if (q.dsT && k >= 0 && src < len && !dead) {
-                        Piece<T, V, kVec> r;
+                        Piece<T, V, true> r;
                         r.load(static_cast<const T*>(q.dsT) + ((size_t)b * H + k) * p.D, c, p.D);
 #pragma unroll
                         for (int i = 0; i < V; ++i) g[i] += r.get(i);
                     }
                     if (src < 0 && q.ds0)
-                        store_piece<kVec>(static_cast<T*>(q.ds0) + ((size_t)b * H + src + H) * p.D, c, p.D, g);
+                        store_piece(static_cast<T*>(q.ds0) + ((size_t)b * H + src + H) * p.D, c, p.D, g);
                 }
                 // inputs before the run's lie below the buffer's start: dropped
-                store_piece<T, kVec>(dx_rows, at + u * step - H * step, kVec ? 1 : p.D - c, g);
+                store_piece<T, true>(dx_rows, at + u * step - H * step, 1, g);
             }
 #pragma unroll
             for (int k = 0; k < H; ++k)
@@ -337,7 +337,7 @@ __global__ __launch_bounds__(256) void conv_params_kernel(const float* __restric
 // 73.9, 72.3 us and 11.8, 12.0, 15.1 us.
 constexpr int kRun = 16;
 
-template <typename T, int W, int V, bool kVec>
+template <typename T, int W, int V>
 hipError_t fwd_v(const ConvArgs& p, hipStream_t stream) {
     const unsigned cols = (unsigned)((p.D + V - 1) / V), runs = (unsigned)((p.T + kRun - 1) / kRun);
     const uint64_t items = (uint64_t)cols * runs * p.B;
@@ -346,29 +346,29 @@ hipError_t fwd_v(const ConvArgs& p, hipStream_t stream) {
     const unsigned runs_end = (unsigned)((items + kConvThreads - 1) / kConvThreads);
     const unsigned grid = runs_end + (unsigned)((states + kConvThreads - 1) / kConvThreads);
     if (grid == 0) return hipSuccess;
-    conv_fwd_kernel<T, W, V, kVec><<<grid, kConvThreads, 0, stream>>>(p, cols, runs, kRun, (unsigned)items, runs_end);
+    conv_fwd_kernel<T, W, V><<<grid, kConvThreads, 0, stream>>>(p, cols, runs, kRun, (unsigned)items, runs_end);
     return hipGetLastError();
 }
 
-template <typename T, int W, int V, bool kVec>
+template <typename T, int W, int V>
 hipError_t step_v(const ConvArgs& p, hipStream_t stream) {
     const unsigned cols = (unsigned)((p.D + V - 1) / V);
     const uint64_t items = (uint64_t)cols * p.B;
     if (items > (1ull << 31)) return hipErrorInvalidValue;
     const unsigned grid = (unsigned)((items + kConvThreads - 1) / kConvThreads);
-    conv_step_kernel<T, W, V, kVec><<<grid, kConvThreads, 0, stream>>>(p, cols, (unsigned)items);
+    conv_step_kernel<T, W, V><<<grid, kConvThreads, 0, stream>>>(p, cols, (unsigned)items);
     return hipGetLastError();
 }
 
-template <typename T, int W, int V, bool kVec>
+template <typename T, int W, int V>
 hipError_t bwd_v(const ConvBwdArgs& q, hipStream_t stream) {
     const ConvArgs& p = q.f;
     const unsigned cblocks = (unsigned)((p.D + 64 * V - 1) / (64 * V));
     const int runs = (p.T + q.run - 1) / q.run;
     if ((uint64_t)cblocks * q.parts > (1ull << 30)) return hipErrorInvalidValue;
     const dim3 grid(cblocks * q.parts);
-    if (p.silu) conv_bwd_kernel<T, W, V, kVec, true><<<grid, kConvThreads, 0, stream>>>(q, cblocks, runs);
-    else conv_bwd_kernel<T, W, V, kVec, false><<<grid, kConvThreads, 0, stream>>>(q, cblocks, runs);
+    if (p.silu) conv_bwd_kernel<T, W, V, true><<<grid, kConvThreads, 0, stream>>>(q, cblocks, runs);
+    else conv_bwd_kernel<T, W, V, false><<<grid, kConvThreads, 0, stream>>>(q, cblocks, runs);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const size_t total = (size_t)p.D * (W + 1);
@@ -388,18 +388,18 @@ __global__ __launch_bounds__(kConvThreads) void conv_pass_kernel(const T* __rest
 template <typename T, int W>
 hipError_t fwd_w(const ConvArgs& p, hipStream_t stream) {
     constexpr int V = 16 / sizeof(T);
-    return p.D % V == 0         ? fwd_v<T, W, V, true>(p, stream)
-           : p.D % (V / 2) == 0 ? fwd_v<T, W, V / 2, true>(p, stream)
-           : p.D % 2 == 0       ? fwd_v<T, W, 2, true>(p, stream)
-                                : fwd_v<T, W, 1, true>(p, stream);
+    return p.D % V == 0         ? fwd_v<T, W, V>(p, stream)
+           : p.D % (V / 2) == 0 ? fwd_v<T, W, V / 2>(p, stream)
+           : p.D % 2 == 0       ? fwd_v<T, W, 2>(p, stream)
+                                : fwd_v<T, W, 1>(p, stream);
 }
 template <typename T, int W>
 hipError_t step_w(const ConvArgs& p, hipStream_t stream) {
     constexpr int V = 16 / sizeof(T);
-    return p.D % V == 0         ? step_v<T, W, V, true>(p, stream)
-           : p.D % (V / 2) == 0 ? step_v<T, W, V / 2, true>(p, stream)
-           : p.D % 2 == 0       ? step_v<T, W, 2, true>(p, stream)
-                                : step_v<T, W, 1, true>(p, stream);
+    return p.D % V == 0         ? step_v<T, W, V>(p, stream)
+           : p.D % (V / 2) == 0 ? step_v<T, W, V / 2>(p, stream)
+           : p.D % 2 == 0       ? step_v<T, W, 2>(p, stream)
+                                : step_v<T, W, 1>(p, stream);
 }
 template <typename T, int W>
 hipError_t bwd_w(const ConvBwdArgs& q, hipStream_t stream) {
@@ -411,7 +411,7 @@ hipError_t bwd_w(const ConvBwdArgs& q, hipStream_t stream) {
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
-    return q.f.D % V == 0 ? bwd_v<T, W, V, true>(q, stream) : bwd_v<T, W, 1, true>(q, stream);
+    return q.f.D % V == 0 ? bwd_v<T, W, V>(q, stream) : bwd_v<T, W, 1>(q, stream);
 }
 
 }  // namespace

@@ -41,31 +41,23 @@ struct Piece {
     static constexpr int kWords = kVec ? (kBytes + 3) / 4 : V;
     uint32_t w[kWords];
 
-    // From a row in memory; c is a multiple of V with kVec.  Addresses at or
+    // From a row in memory (whole pieces only); c is a multiple of V.  Addresses at or
     // behind `lim` are clamped into the row.
     __device__ __forceinline__ void load(const T* row, int c, int lim) {
-        if constexpr (kVec) {
-            const T* p = row + (c < lim ? c : lim - V);
-            if constexpr (kBytes == 2) {
-                w[0] = *reinterpret_cast<const uint16_t*>(p);
-            } else if constexpr (kBytes == 4) {
-                w[0] = *reinterpret_cast<const uint32_t*>(p);
-            } else if constexpr (kBytes == 8) {
-                const uint2 u = *reinterpret_cast<const uint2*>(p);
-                w[0] = u.x; w[1] = u.y;
-            } else {
-#pragma unroll
-                for (int i = 0; i < kWords; i += 4) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
-                    w[i] = u.x; w[i + 1] = u.y; w[i + 2] = u.z; w[i + 3] = u.w;
-                }
-            }
+        static_assert(kVec, "element by element from buffers only");
+        const T* p = row + (c < lim ? c : lim - V);
+        if constexpr (kBytes == 2) {
+            w[0] = *reinterpret_cast<const uint16_t*>(p);
+        } else if constexpr (kBytes == 4) {
+            w[0] = *reinterpret_cast<const uint32_t*>(p);
+        } else if constexpr (kBytes == 8) {
+            const uint2 u = *reinterpret_cast<const uint2*>(p);
+            w[0] = u.x; w[1] = u.y;
         } else {
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int k = c + i < lim ? c + i : lim - 1;
-                if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(row[k]);
-                else w[i] = row[k];
+            for (int i = 0; i < kWords; i += 4) {
+                const uint4 u = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
+                w[i] = u.x; w[i + 1] = u.y; w[i + 2] = u.z; w[i + 3] = u.w;
             }
         }
     }
@@ -100,39 +92,32 @@ struct Piece {
     }
 };
 
-template <bool kVec, int V>
+// Stored in a row unless c lies at or behind `lim`.
+template <int V>
 __device__ __forceinline__ void store_piece(float* row, int c, int lim, const float (&x)[V]) {
-    if constexpr (kVec && V % 4 == 0) {
-        if (c < lim) {
-#pragma unroll
-            for (int i = 0; i < V; i += 4)
-                *reinterpret_cast<float4*>(row + c + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-        }
-    } else if constexpr (kVec && V == 2) {
-        if (c < lim) *reinterpret_cast<float2*>(row + c) = make_float2(x[0], x[1]);
+    if (c >= lim) return;
+    if constexpr (V == 1) {
+        row[c] = x[0];
+    } else if constexpr (V == 2) {
+        *reinterpret_cast<float2*>(row + c) = make_float2(x[0], x[1]);
     } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (c + i < lim) row[c + i] = x[i];
+        for (int i = 0; i < V; i += 4)
+            *reinterpret_cast<float4*>(row + c + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
     }
 }
-template <bool kVec, int V>
+template <int V>
 __device__ __forceinline__ void store_piece(bf16_t* row, int c, int lim, const float (&x)[V]) {
-    if constexpr (kVec && V == 8) {
-        if (c < lim)
-            *reinterpret_cast<uint4*>(row + c) =
-                make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                           pack_bf16x2(x[6], x[7]));
-    } else if constexpr (kVec && V == 4) {
-        if (c < lim)
-            *reinterpret_cast<uint2*>(row + c) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
-    } else if constexpr (kVec && V == 2) {
-        if (c < lim) *reinterpret_cast<uint32_t*>(row + c) = pack_bf16x2(x[0], x[1]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (c + i < lim) row[c + i] = f2bf(x[i]);
-    }
+    if (c >= lim) return;
+    if constexpr (V == 1)
+        row[c] = f2bf(x[0]);
+    else if constexpr (V == 2)
+        *reinterpret_cast<uint32_t*>(row + c) = pack_bf16x2(x[0], x[1]);
+    else if constexpr (V == 4)
+        *reinterpret_cast<uint2*>(row + c) = make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
+    else
+        *reinterpret_cast<uint4*>(row + c) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                                                        pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
 }
 
 // The same into a buffer, of the first `valid` elements (kVec: all or none);
@@ -240,10 +225,6 @@ __device__ __forceinline__ uint32_t encode8(const float (&h)[4], float& scale) {
         w |= (uint32_t)(q & 0xff) << (8 * i);
     }
     return w;
-}
-__device__ __forceinline__ void decode8(uint32_t w, float scale, float (&h)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = (float)(int8_t)(w >> (8 * i)) * scale;
 }
 
 }  // namespace wkv7
