@@ -458,22 +458,26 @@ int wkv7_forward_epilogue(const wkv7_desc *desc, const void *r, const void *w, c
  * asynchronous work on `stream`, synchronous validation that launches nothing
  * on error), with channels in place of heads: token tensors are [B][T][D].
  * Outputs may share memory with no input and no other output, but for the
- * states of the single-token calls.  Work goes to the current device: make the tensors' device current first.
- * D is any width; widths whose rows hold whole 16-byte (convolution) pieces run
- * fastest.  Sizes beyond these limits are refused (WKV7_ERR_UNSUPPORTED):
+ * states of the single-token calls.  Work goes to the current device: make the
+ * tensors' device current first.  D is any width; widths whose rows hold whole
+ * 16-byte (convolution) pieces run fastest.  Sizes beyond these limits are refused (WKV7_ERR_UNSUPPORTED):
  *   convolution  T <= 2^31 - 1025, D <= 2^19, B (T + 64) max(D, 64) <= 2^35,
  *                B D <= 2^29;
  *   scan         T <= 2^31 - 65, D <= 2^22, D N <= 2^26, G N <= 2^21, B T D and
  *                B ceil(T / 16) D N <= 2^40, B T G N <= 2^32, B D <= 2^25, and as
  *                many workgroups (one per batch row, group, 256 S / N of the
- *                group's channels, S = 2 or 4, and time segment) as 2^22.  Calls share no scratch; a workspace may be used again by a later
- * call on the same stream, not by two calls that can overlap (two captured
- * graphs replayed on different streams need one each).
+ *                group's channels, S = 2 or 4, and time segment) as 2^22.
+ * Calls share no scratch; a workspace may be used again by a later call on the
+ * same stream, not by two calls that can overlap (two captured graphs replayed
+ * on different streams need one each).
  *
  * `lengths` (int32 [B], 4-byte aligned, or NULL = T each) gives the valid
  * tokens of every batch row, clamped to [0, T]: what the inputs hold at and
  * behind a row's length (NaN included) is not used, outputs there are 0, and
  * the state behind the sequence is the one after the row's last valid token.
+ * An infinity or a NaN in a valid token, a state or a gradient goes where the
+ * formulas take it and to its channel's dA, but not to other channels' outputs
+ * (dBm and dCm sum over a group's) nor to other rows' or padded tokens'.
  */
 
 /* W: 2, 3 or 4 taps.  silu: 0 or 1. */
@@ -511,8 +515,10 @@ int wkv7_conv_backward(const wkv7_conv_desc *desc, const float *weight, const fl
                        const void *dsT, void *dx, float *dweight, float *dbias, void *ds0,
                        void *workspace, size_t workspace_bytes, void *stream);
 
-/* One token: x, y [B][D]; state [B][W-1][D] is read and moved on in place
-   (desc->T is ignored).  y may not overlap x or state. */
+/* One token: x, y [B][D]; state [B][W-1][D] is read and moved on in place.  The
+   descriptor is checked as for wkv7_conv_forward, T and its limits included, and
+   T has no other effect: the prompt's descriptor serves, or T = 1.  y may not
+   overlap x or state. */
 int wkv7_conv_step(const wkv7_conv_desc *desc, const float *weight, const float *bias,
                    const void *x, void *state, void *y, void *stream);
 
@@ -557,7 +563,12 @@ typedef struct {
 size_t wkv7_ssm_ckpt_bytes(const wkv7_ssm_desc *desc);
 
 /* Device scratch of wkv7_ssm_forward (0: none needed) and wkv7_ssm_backward;
-   0 on an invalid descriptor. */
+   0 on an invalid descriptor.  The forward's holds the states of its time
+   segments, if there are any.  The backward's is mostly the partial sums of dBm
+   and dCm, one per token and block of a group's channels when there is more than
+   one block: blocks x B T G x 2 N x 4 bytes with blocks = ceil(D / G / c), c =
+   64, 32, 16, 16 channels for N = 8, 16, 32, 64.  At B = 4, T = 4096, D = 2048,
+   G = 1 that is 34 MB, 134 MB, 537 MB and 1.07 GB. */
 size_t wkv7_ssm_forward_workspace_bytes(const wkv7_ssm_desc *desc);
 size_t wkv7_ssm_backward_workspace_bytes(const wkv7_ssm_desc *desc);
 
@@ -594,8 +605,10 @@ int wkv7_ssm_backward(const wkv7_ssm_desc *desc, const wkv7_ssm_params *params, 
                       void *stream);
 
 /* One token on resident states: x, dt, z, y [B][D], Bm, Cm [B][G][N], state
-   fp32 [B][D][N] read and overwritten.  desc->T and ckpt_bits are ignored;
-   params->lengths must be NULL. */
+   fp32 [B][D][N] read and overwritten.  The descriptor is checked as for
+   wkv7_ssm_forward, T and ckpt_bits included, which have no other effect: the
+   prompt's descriptor serves, or T = 1 and ckpt_bits = 0.  params->lengths must
+   be NULL. */
 int wkv7_ssm_step(const wkv7_ssm_desc *desc, const wkv7_ssm_params *params, const void *x,
                   const void *dt, const void *Bm, const void *Cm, const void *z, float *state,
                   void *y, void *stream);
