@@ -460,7 +460,8 @@ int wkv7_forward_epilogue(const wkv7_desc *desc, const void *r, const void *w, c
  * Outputs may share memory with no input and no other output, but for the
  * states of the single-token calls.  Work goes to the current device: make the
  * tensors' device current first.  D is any width; widths whose rows hold whole
- * 16-byte (convolution) pieces run fastest.  Sizes beyond these limits are refused (WKV7_ERR_UNSUPPORTED):
+ * 16-byte (convolution) pieces run fastest.  Sizes beyond these limits are
+ * refused (WKV7_ERR_UNSUPPORTED):
  *   convolution  T <= 2^31 - 1025, D <= 2^19, B (T + 64) max(D, 64) <= 2^35,
  *                B D <= 2^29;
  *   scan         T <= 2^31 - 65, D <= 2^22, D N <= 2^26, G N <= 2^21, B T D and

@@ -52,3 +52,29 @@ def test_scan_gradients_behind_a_row_are_zero(wk, N, D, G, T, gate, dtype):   # 
             if name not in ("h0", "dhT"):   # rows without such values
                 assert torch.equal(y[0], y1[0]) and torch.equal(g.dx[:2], g1.dx[:2]) and torch.equal(g.dh0[:2], g1.dh0[:2])
                 assert torch.equal(g.dB[:2], g1.dB[:2]) and torch.equal(g.ddt[:2], g1.ddt[:2])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("N,D,T", [(8, 70, 40), (16, 48, 40), (16, 21, 700), (32, 40, 40), (64, 18, 40)])
+def test_values_that_are_not_finite_stay_in_their_channel(wk, N, D, T, dtype):   # noqa: F811
+    """dB and dC are sums over channels; everything else of the other channels keeps its bits."""
+    import torch
+    p, h0, more = make(89, 2, T, D, N, 1, dtype)
+    args, kw = call(p)
+
+    def grads(x, dy, dhT):
+        y, hT, ck = wk.ssm_forward(x, *args[1:], h0=h0, ckpt_bits=8, **kw)
+        g = wk.ssm_backward(x, *args[1:], dy, ck, dhT=dhT, ckpt_bits=8, **kw)
+        return dict(y=y, hT=hT, dx=g.dx, ddt=g.ddt, dz=g.dz, dA=g.dA[None, None], ddskip=g.ddskip[None, None],
+                    ddt_bias=g.ddt_bias[None, None], dh0=g.dh0)
+
+    sound = grads(args[0], more["dy"], more["dhT"])
+    others = torch.arange(D, device="cuda") != 7
+    for value in (NAN, INF):
+        for name in ("x", "dy", "dhT"):
+            bad = dict(x=args[0].clone(), dy=more["dy"].clone(), dhT=more["dhT"].clone())
+            bad[name][0, 7 if name == "dhT" else 5].flatten()[3 if name == "dhT" else 7] = value
+            for k, v in grads(**bad).items():
+                dim = 1 if k in ("hT", "dh0") else 2
+                pick = lambda t: t.movedim(dim, 0)[others]   # noqa: E731,B023
+                assert torch.equal(pick(v), pick(sound[k])), (name, value, k)
