@@ -22,11 +22,15 @@
 // tiles in registers, over batch rows and segments by the second kernel.
 //
 // Bound by the vector ALU and the one step wave per SIMD that feeds it.  (4, 4096)
-// tokens of 2048 channels, 16 states, bf16, gate, 8-bit checkpoints: 466 us and 25
-// for the sums of the partial dB and dC (134 MB), against 144 us for all bytes.  A
+// tokens of 2048 channels, 16 states, bf16, gate, 8-bit checkpoints: 470 us and 24
+// for the sums of the partial dB and dC (134 MB), against 92 us for the tensors' bytes
+// (144 with those sums') and 163 us for the formulas' products alone, one lane per state.  A
 // step wave takes 630 vector instructions per tile (two states and sixteen tokens
 // per lane: 128 of them folds over channels, 48 swaps and adds over states), a
-// staging wave 130; the vector ALU is busy for 78 % of the time.  Measured against
+// staging wave 140: 370 us for both at their rates; the vector ALU is busy for 79 % of
+// the time.  At 32 and 64 states a workgroup holds 16 channels, and the partial sums
+// (537 MB and 1.07 GB at the same shape) outgrow the tensors: 820 + 130 and 1610 + 235
+// us.  At 8 it holds 64, 128 workgroups for 256 compute units: 483 + 7 us.  Measured against
 // this split: one state per lane on eight step waves 543 us where this took 521;
 // the sums over states on v_mfma_f32_16x16x4 974 us; states and adjoint on four
 // waves each, the states handed over in LDS and the exponentials taken twice, 540
