@@ -89,9 +89,9 @@ int64_t token_bytes(const wkv7_ssm_desc* d) {
 // Time segments: a launch without them has one workgroup per batch row, group
 // and channel block.  The first of the two launches repeats most of the
 // exponentials, so a split only pays when it shortens the chain enough: three
-// segments at least (two leave half the chain to each launch; an estimate, not
-// measured: launches of 86 to 128 workgroups leave units idle), of 64 tokens at least,
-// as many as make one or two workgroups per compute unit.  Two at N = 16, and in the backward at N = 32, whose workgroups
+// segments at least (two leave half the chain to each launch: an estimate, not
+// measured; where one workgroup per unit is the aim, 86 to 128 of them leave units
+// idle), of 64 tokens at least, as many as make one or two workgroups per compute unit.  Two at N = 16, and in the backward at N = 32, whose workgroups
 // run two at a time (forward and backward at B = 4, T = 1024, D = 768, N = 16: one,
 // two, four per unit 159, 104, 111 us; forward at B = 1, T = 16384, D = 768 95, 93,
 // 98 us; backward at B = 2, T = 1024, D = 512, N = 32 53, 49, 52 us); one elsewhere,
