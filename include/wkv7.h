@@ -614,6 +614,88 @@ int wkv7_ssm_step(const wkv7_ssm_desc *desc, const wkv7_ssm_params *params, cons
                   const void *dt, const void *Bm, const void *Cm, const void *z, float *state,
                   void *y, void *stream);
 
+/*
+ * ---- Linear attention with one decay per head ---------------------------------
+ * The recurrence with a scalar in place of w ("Paper Review: RWKV-7 Goose",
+ * Background information on delta rule: linear attention, and Mamba 2's decay):
+ * keys and values of different sizes, heads that share queries and keys, rows of
+ * different lengths padded or one behind the other.  Conventions as above
+ * (device pointers, 16-byte alignment, no gaps, fp32 states, asynchronous work on
+ * `stream`, synchronous validation that launches nothing on error, no overlap of
+ * outputs with anything but the step's state in place, the current device, one
+ * workspace for calls that may run at once each).
+ *
+ * H heads in G groups of H / G neighbouring ones (H a multiple of G); a group
+ * shares its queries and keys.  N: key columns, P: value rows of a state, each 32,
+ * 64 or 128.  Tokens are [B][T] with `rows` = lengths (int32 [B], clamped to
+ * [0, T], or NULL = T each): what inputs hold behind a row's length is not used,
+ * outputs there are 0.  Or, with packed = 1, [tokens], with `rows` = starts (int32
+ * [B + 1], required, not decreasing): row b has the tokens from starts[b] to
+ * starts[b + 1] (both clamped to [0, tokens]); T is about the longest row's length
+ * (the work is laid out for it; longer rows are taken whole all the same); outputs
+ * of tokens that no row has are left as they were.  rows: 4-byte aligned.
+ * Sizes beyond these are refused (WKV7_ERR_UNSUPPORTED): T and tokens <= 2^31 - 65,
+ * H P and G N <= 2^22, B H <= 2^21, B H P N <= 2^32, B ceil(T / 64) G <= 2^23, tokens
+ * H P <= 2^40, and tiles H P N <= 2^40 with tiles = B ceil(T / 64), packed tokens / 64 + B.
+ */
+typedef struct {
+    int32_t B, T, H, G, N, P;
+    int32_t dtype;         /* wkv7_dtype */
+    int32_t fixed_decay;   /* 1: g is fp32 [H], the same for every token */
+    int32_t packed;
+    int32_t tokens;        /* packed: tokens of the tensors; else not used */
+    float scale;           /* finite */
+} wkv7_linattn_desc;
+
+/* Bytes of the states entering every 64 tokens, in dtype [tiles][H][P][N]: tile i of
+   row b is number b ceil(T / 64) + i, packed clamped starts[b] / 64 + b + i.  Entries
+   without tokens are not written.  0 on an invalid descriptor. */
+size_t wkv7_linattn_ckpt_bytes(const wkv7_linattn_desc* desc);
+
+/* Device scratch: the forward's holds the states of its time segments, if there are
+   any; the backward's as many bytes as the checkpoints (the gradient of the state
+   behind every tile), its own segments' states, and where heads share keys and tiles
+   are few, partial sums of dq and dk.  0 where none is needed. */
+size_t wkv7_linattn_forward_workspace_bytes(const wkv7_linattn_desc* desc);
+size_t wkv7_linattn_backward_workspace_bytes(const wkv7_linattn_desc* desc);
+
+/*
+ * Per head h (group h / (H / G)) and token t, from S = s0 (NULL = zeros):
+ *     S   <- exp(g_t) S + v_t k_t^T        y_t = scale S q_t
+ *   q, k     [B][T][G][N];  v, y [B][T][H][P];  g [B][T][H] (dtype), or fp32 [H]
+ *   s0, sT   fp32 [B][H][P][N]; sT, the state behind the row, may be NULL
+ *   ckpt     wkv7_linattn_ckpt_bytes, or NULL
+ * g is a log decay: 0 or below in use; -infinity forgets everything before the
+ * token.  States are fp32 to their last bits (with bf16 tokens too); a read-out's
+ * weights within 64 tokens, and the states it reads, are rounded to dtype.
+ * An infinity or a NaN in a token reaches what the formulas take it to: its own and
+ * later tokens' y of its heads, and their states.  fixed_decay: a NaN for its head.
+ */
+int wkv7_linattn_forward(const wkv7_linattn_desc* desc, const int32_t* rows, const void* q, const void* k,
+                         const void* v, const void* g, const float* s0, void* y, float* sT, void* ckpt,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradients of <dy, y> + <dsT, sT> (dsT NULL = 0) from the inputs and the forward's
+ * checkpoints (the first is s0), whose rounding to dtype they carry: dq, dk, dv, dg
+ * of the inputs' shapes and dtype (dg NULL with fixed_decay), ds0 fp32 or NULL.  dq
+ * and dk are sums over a group's heads.  Sums are fp32 or wider in a fixed order:
+ * repeated calls agree bit for bit.  A value that is not finite reaches what the
+ * formulas take it to, in dg also the other tokens of its 64.
+ */
+int wkv7_linattn_backward(const wkv7_linattn_desc* desc, const int32_t* rows, const void* q, const void* k,
+                          const void* v, const void* g, const void* dy, const float* dsT, const void* ckpt, void* dq,
+                          void* dk, void* dv, void* dg, float* ds0, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/* One token on resident states: q, k [B][G][N], v, y [B][H][P], g [B][H] or fp32 [H];
+   state fp32 [nslots][H][P][N], read and overwritten where row b's slot is
+   slots[b] (int32 [B], 4-byte aligned; NULL: slot b, nslots at least B).  A row whose
+   slot is not in [0, nslots), or is an earlier row's, touches no state and gets y = 0.
+   The descriptor is checked as for a prompt, T has no other effect; packed is refused. */
+int wkv7_linattn_step(const wkv7_linattn_desc* desc, const int32_t* slots, int32_t nslots, const void* q,
+                      const void* k, const void* v, const void* g, float* state, void* y, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

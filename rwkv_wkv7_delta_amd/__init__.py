@@ -52,7 +52,9 @@ EXPORTED = ("wkv7_abi_version", "wkv7_status_string", "wkv7_tape_bytes", "wkv7_c
             "wkv7_forward_epilogue", "wkv7_conv_forward", "wkv7_conv_backward_workspace_bytes",
             "wkv7_conv_backward", "wkv7_conv_step", "wkv7_ssm_ckpt_bytes",
             "wkv7_ssm_forward_workspace_bytes", "wkv7_ssm_backward_workspace_bytes",
-            "wkv7_ssm_forward", "wkv7_ssm_backward", "wkv7_ssm_step")
+            "wkv7_ssm_forward", "wkv7_ssm_backward", "wkv7_ssm_step", "wkv7_linattn_ckpt_bytes",
+            "wkv7_linattn_forward_workspace_bytes", "wkv7_linattn_backward_workspace_bytes",
+            "wkv7_linattn_forward", "wkv7_linattn_backward", "wkv7_linattn_step")
 
 
 class WKV7Error(RuntimeError):
@@ -89,6 +91,11 @@ class SsmDesc(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("T", ctypes.c_int32), ("D", ctypes.c_int32),
                 ("N", ctypes.c_int32), ("G", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("ckpt_bits", ctypes.c_int32)]
+
+
+class LinattnDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "H", "G", "N", "P", "dtype", "fixed_decay",
+                                              "packed", "tokens")] + [("scale", ctypes.c_float)]
 
 
 class SsmParams(ctypes.Structure):
@@ -157,6 +164,7 @@ def lib():
         L.wkv7_forward_epilogue.argtypes = [D] + [P] * 7 + [P, E, P, P, P]
         L.wkv7_forward_epilogue.restype = ctypes.c_int
         CD, SD = ctypes.POINTER(ConvDesc), ctypes.POINTER(SsmDesc)
+        LD = ctypes.POINTER(LinattnDesc)
         SP, SG = ctypes.POINTER(SsmParams), ctypes.POINTER(SsmGradPointers)
         for name, args, res in (
                 ("wkv7_conv_forward", [CD] + [P] * 8, ctypes.c_int),
@@ -168,7 +176,13 @@ def lib():
                 ("wkv7_ssm_backward_workspace_bytes", [SD], Z),
                 ("wkv7_ssm_forward", [SD, SP] + [P] * 9 + [P, Z, P], ctypes.c_int),
                 ("wkv7_ssm_backward", [SD, SP] + [P] * 8 + [SG, P, Z, P], ctypes.c_int),
-                ("wkv7_ssm_step", [SD, SP] + [P] * 8, ctypes.c_int)):
+                ("wkv7_ssm_step", [SD, SP] + [P] * 8, ctypes.c_int),
+                ("wkv7_linattn_ckpt_bytes", [LD], Z),
+                ("wkv7_linattn_forward_workspace_bytes", [LD], Z),
+                ("wkv7_linattn_backward_workspace_bytes", [LD], Z),
+                ("wkv7_linattn_forward", [LD] + [P] * 10 + [Z, P], ctypes.c_int),
+                ("wkv7_linattn_backward", [LD] + [P] * 14 + [Z, P], ctypes.c_int),
+                ("wkv7_linattn_step", [LD, P, I] + [P] * 7, ctypes.c_int)):
             fn = getattr(L, name)
             fn.argtypes, fn.restype = args, res
         _lib = L
@@ -485,3 +499,5 @@ def decode_step(r, w, k, v, a, b, state, out=None):
 
 from .mixers import (SsmGrads, conv_backward, conv_forward, conv_step, ssm_backward,  # noqa: E402,F401
                      ssm_ckpt_bytes, ssm_forward, ssm_split_ckpt, ssm_step)
+from .linattn import (LinattnGrads, linattn_backward, linattn_ckpt_shape, linattn_forward,  # noqa: E402,F401
+                      linattn_step)

@@ -1,0 +1,261 @@
+// wkv7_linattn_device.h -- tiles, operands and decays of the linear attention
+// kernels.
+//
+// A tile is 64 tokens of one head; a workgroup is four waves.  Products go
+// through the matrix cores in 16 x 16 results, 32 deep: for bf16 tokens one
+// 16x16x32 instruction, for fp32 tokens eight 16x16x4 ones.  Which 32 values of
+// the contraction a lane's eight operand elements stand for is the same for
+// both operands of every product here, one of
+//   rows     8 g + j                (read along a row of memory)
+//   columns  4 g + j, 16 + 4 g + j - 4  (j < 4, j >= 4; read down a column)
+// with g = lane / 16: the second is also how the lanes hold two result tiles
+// (row 4 g + q in register q), so a result feeds the next product in place.
+#pragma once
+
+#include "wkv7_linattn_internal.h"
+#include "wkv7_mfma.h"
+#include "wkv7_ssm_device.h"
+
+namespace wkv7 {
+
+constexpr int kLaThreads = 256;
+
+template <typename T> struct LaMat;
+
+template <> struct LaMat<bf16_t> {
+    typedef bf16x8 Frag;
+    typedef bf16x4 Half;
+    static constexpr int kParts = 3;   // bf16 terms that carry a 32-bit operand
+    static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) { return mfma32(a, b, c); }
+    static __device__ __forceinline__ Frag cat(Half a, Half b) { return cat8(a, b); }
+    static __device__ __forceinline__ Half half(f32x4 x) { return cvt4(x); }
+    static __device__ __forceinline__ f32x4 wide(Half x) { return unpack4(x); }
+    static __device__ __forceinline__ Frag rows(const bf16_t* p) {
+        return __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(p));
+    }
+    static __device__ __forceinline__ Half column(const bf16_t* tile, int stride, int g, int l16) {
+        return ld4_tr(tr_addr(tile, stride, g, l16));
+    }
+    static __device__ __forceinline__ Half four(const bf16_t* p) {
+        return __builtin_bit_cast(bf16x4, *reinterpret_cast<const uint2*>(p));
+    }
+    static __device__ __forceinline__ void put(bf16_t* p, f32x4 x) {
+        *reinterpret_cast<uint2*>(p) = __builtin_bit_cast(uint2, cvt4(x));
+    }
+};
+
+template <> struct LaMat<float> {
+    struct Frag {
+        float v[8];
+    };
+    typedef f32x4 Half;
+    static constexpr int kParts = 1;
+    static __device__ __forceinline__ f32x4 mma(const Frag& a, const Frag& b, f32x4 c) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[j], b.v[j], c, 0, 0, 0);
+        return c;
+    }
+    static __device__ __forceinline__ Frag cat(Half a, Half b) {
+        Frag f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f.v[j] = a[j];
+            f.v[4 + j] = b[j];
+        }
+        return f;
+    }
+    static __device__ __forceinline__ Half half(f32x4 x) { return x; }
+    static __device__ __forceinline__ f32x4 wide(Half x) { return x; }
+    static __device__ __forceinline__ Frag rows(const float* p) {
+        return cat(*reinterpret_cast<const f32x4*>(p), *reinterpret_cast<const f32x4*>(p + 4));
+    }
+    static __device__ __forceinline__ Half column(const float* tile, int stride, int g, int l16) {
+        Half h;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) h[q] = tile[(4 * g + q) * stride + l16];
+        return h;
+    }
+    static __device__ __forceinline__ Half four(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+    static __device__ __forceinline__ void put(float* p, f32x4 x) { *reinterpret_cast<f32x4*>(p) = x; }
+};
+
+// Two column halves, rows r0 and r0 + 16 of a tile in LDS.
+template <typename T>
+__device__ __forceinline__ typename LaMat<T>::Frag columns(const T* tile, int stride, int g, int l16) {
+    typedef LaMat<T> M;
+    return M::cat(M::column(tile, stride, g, l16), M::column(tile + 16 * stride, stride, g, l16));
+}
+
+// A 32-bit operand as kParts operands in the tokens' type that sum to it: three
+// bf16 terms hold 24 bits, so that states (fp32) lose nothing to the matrix
+// cores' input type.  A value that is not finite stands alone in the first.
+template <typename T>
+__device__ __forceinline__ void split_parts(const f32x4& lo, const f32x4& hi, typename LaMat<T>::Frag (&f)[LaMat<T>::kParts]) {
+    typedef LaMat<T> M;
+    if constexpr (M::kParts == 1) {
+        f[0] = M::cat(lo, hi);
+    } else {
+        f32x4 x[2] = {lo, hi};
+#pragma unroll
+        for (int i = 0; i < M::kParts; ++i) {
+            const typename M::Half a = M::half(x[0]), b = M::half(x[1]);
+            f[i] = M::cat(a, b);
+            if (i + 1 < M::kParts) {
+                const f32x4 wa = M::wide(a), wb = M::wide(b);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    x[0][j] = fabsf(wa[j]) < INFINITY ? x[0][j] - wa[j] : 0.f;
+                    x[1][j] = fabsf(wb[j]) < INFINITY ? x[1][j] - wb[j] : 0.f;
+                }
+            }
+        }
+    }
+}
+
+// ---- where a row's tokens are ---------------------------------------------------
+struct LaRow {
+    int64_t first;   // its first token among all
+    int64_t ckpt;    // its first checkpoint
+    int len;         // its tokens
+    int stored;      // token places whose outputs are written
+};
+__device__ __forceinline__ LaRow la_row(const int32_t* rows, bool packed, int64_t tokens, int T, int b) {
+    LaRow r;
+    if (packed) {
+        int64_t a = rows[b], e = rows[b + 1];
+        a = a < 0 ? 0 : a > tokens ? tokens : a;
+        e = e < a ? a : e > tokens ? tokens : e;
+        r.first = a;
+        r.len = r.stored = (int)(e - a);
+        r.ckpt = a / kLaChunk + b;
+    } else {
+        r.first = (int64_t)b * T;
+        r.len = row_length(rows, b, T);
+        r.stored = T;
+        r.ckpt = (int64_t)b * ((T + kLaChunk - 1) / kLaChunk);
+    }
+    r.len = __builtin_amdgcn_readfirstlane(r.len);
+    r.stored = __builtin_amdgcn_readfirstlane(r.stored);
+    return r;
+}
+
+// `n` rows of `width` elements, `stride` elements apart, as a buffer: what lies
+// behind the last of them reads as 0 and is not written.  The offsets of 64 rows
+// stay below 2^31 bytes (sizes are limited for that).
+template <typename T>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const T* p, int n, int64_t stride, int width) {
+    return buffer_of(p, n > 0 ? (int)(((n - 1) * stride + width) * (int)sizeof(T)) : 0);
+}
+
+// A tile of up to 64 rows on its way from memory to LDS: 16 bytes per lane and load.
+template <typename T, int W>
+struct LaStage {
+    static constexpr int kPieces = W * (int)sizeof(T) / 16;          // per row
+    static constexpr int kRowsPer = kLaThreads / kPieces;            // rows of one load of the workgroup
+    static constexpr int kLoads = kLaChunk / kRowsPer;
+    static constexpr int kStride = W + 16 / (int)sizeof(T);          // elements of an LDS row: 16 bytes apart in the banks
+    vu4 w[kLoads];
+
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t row_bytes) {
+        const uint32_t at = threadIdx.x / kPieces * row_bytes + threadIdx.x % kPieces * 16;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            w[i] = __builtin_bit_cast(vu4, __builtin_amdgcn_raw_buffer_load_b128(r, at + i * kRowsPer * row_bytes, 0, 0));
+    }
+    __device__ __forceinline__ void store(T* lds) const {
+        T* const p = lds + threadIdx.x / kPieces * kStride + threadIdx.x % kPieces * (16 / (int)sizeof(T));
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) *reinterpret_cast<vu4*>(p + i * kRowsPer * kStride) = w[i];
+    }
+    // Whether any of the lane's values is infinite or NaN.
+    __device__ __forceinline__ bool odd() const {
+        if constexpr (sizeof(T) == 2) {
+            typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+            us2 m = {0, 0};
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    m = __builtin_elementwise_max(m, __builtin_bit_cast(us2, w[i][j] & 0x7fff7fffu));
+            return m[0] >= 0x7f80 || m[1] >= 0x7f80;
+        } else {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t u = w[i][j] & 0x7fffffffu;
+                    m = m > u ? m : u;
+                }
+            return m >= 0x7f800000u;
+        }
+    }
+};
+
+// ---- decays ---------------------------------------------------------------------
+// Running sums of a tile's log decays, in units of log 2.  Summed in 64 bits and
+// kept as two floats: a difference of two of them is then as exact as a float
+// is, however far the sums have run.
+struct LaDecay {
+    float hi[kLaChunk], lo[kLaChunk];
+    float up[kLaChunk];     // 2^(G_t): from the tile's start to behind token t
+    float down[kLaChunk];   // 2^(G_end - G_t): from behind token t to the tile's end
+    float all;              // 2^(G_end)
+    int odd[4];             // waves that found values that are not finite
+    double sum;             // G_end
+};
+
+template <int kCtrl, int kRowMask>
+__device__ __forceinline__ double dpp_double(double x) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, x);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, kCtrl, kRowMask, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), kCtrl, kRowMask, 0xF, false);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Sum over this lane and those before it in the wave: row_shr 1, 2, 4, 8, then
+// each row's last lane to the row behind (rows 1 and 3) and lane 31 to the upper half.
+__device__ __forceinline__ double wave_running_sum(double x) {
+    x += dpp_double<0x111, 0xF>(x);
+    x += dpp_double<0x112, 0xF>(x);
+    x += dpp_double<0x114, 0xF>(x);
+    x += dpp_double<0x118, 0xF>(x);
+    x += dpp_double<0x142, 0xA>(x);
+    x += dpp_double<0x143, 0xC>(x);
+    return x;
+}
+
+// What lane t of a wave reads of token t's log decay.
+template <typename T>
+struct LaLog {
+    float x;
+    __device__ __forceinline__ void load(const LaArgs& p, int64_t token, int h, bool in) {
+        x = 0.f;
+        if (in) {
+            if (p.fixed) x = static_cast<const float*>(p.g)[h];
+            else x = Elem<T>::load1(static_cast<const T*>(p.g) + token * p.H + h);
+        }
+    }
+};
+
+// By one whole wave.  A log decay of -infinity forgets everything: 2^-144270 is 0,
+// and sums that hold it stay exact to 2^-30.
+__device__ __forceinline__ void put_decays(LaDecay& d, float log_decay) {
+    const int t = threadIdx.x % 64;
+    const double g = (double)fmaxf(log_decay, -1e5f) * 1.4426950408889634;
+    // a NaN stays one (fmaxf would drop it)
+    const double c = wave_running_sum(log_decay != log_decay ? (double)log_decay : g);
+    const uint64_t u = __builtin_bit_cast(uint64_t, c);
+    const uint32_t l0 = __builtin_amdgcn_readlane((uint32_t)u, 63), l1 = __builtin_amdgcn_readlane((uint32_t)(u >> 32), 63);
+    const double end = __builtin_bit_cast(double, (uint64_t)l1 << 32 | l0);
+    const float hi = (float)c;
+    d.hi[t] = hi;
+    d.lo[t] = (float)(c - (double)hi);
+    d.up[t] = exp2_raw((float)c);
+    d.down[t] = exp2_raw((float)(end - c));
+    if (t == 0) {
+        d.all = exp2_raw((float)end);
+        d.sum = end;
+    }
+}
+
+}  // namespace wkv7
