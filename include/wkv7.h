@@ -696,6 +696,77 @@ int wkv7_linattn_backward(const wkv7_linattn_desc* desc, const int32_t* rows, co
 int wkv7_linattn_step(const wkv7_linattn_desc* desc, const int32_t* slots, int32_t nslots, const void* q,
                       const void* k, const void* v, const void* g, float* state, void* y, void* stream);
 
+/*
+ * ---- The group norm with an activation, channels last --------------------------
+ * The normalisation of a read-out (per head: G = H groups of a row's H P channels, see
+ * also wkv7_epilogue) or of a whole row, with its gate or activation, and its
+ * gradients.  Per row of D channels, in G groups of D / G neighbouring ones:
+ *     s(z) = z sigmoid(z)
+ *     u    = x, or x s(z) with gate = WKV7_GATE_BEFORE
+ *     n    = (u - mean u) / sqrt(mean (u - mean u)^2 + eps), means over the group,
+ *            or u / sqrt(mean u^2 + eps) with center = 0
+ *     o    = gamma n + beta
+ *     y    = o, or s(o) with silu = 1; then times s(z) with gate = WKV7_GATE_AFTER
+ *   x, z, y, dy, dx, dz  [rows][D] (dtype); z is given with a gate, else NULL
+ *   gamma, beta          fp32 [D] or NULL (1, 0)
+ * Conventions as above (16-byte alignment, no overlap of outputs with inputs).  The
+ * arithmetic is fp32.  A value that is not finite stays in its row and group (and goes
+ * to dgamma and dbeta there).  D <= 2^22, rows D <= 2^40.  Fastest where groups hold
+ * whole 16-byte pieces and at most 8192 channels (fp32: 4096; by single values 1024).
+ */
+typedef enum { WKV7_GATE_NONE = 0, WKV7_GATE_AFTER = 1, WKV7_GATE_BEFORE = 2 } wkv7_gate;
+
+typedef struct {
+    int64_t rows;
+    int32_t D, G;
+    int32_t dtype;    /* wkv7_dtype */
+    int32_t center, silu;
+    int32_t gate;     /* wkv7_gate */
+    float eps;        /* finite, >= 0 */
+} wkv7_gnorm_desc;
+
+int wkv7_gnorm_forward(const wkv7_gnorm_desc* desc, const float* gamma, const float* beta, const void* x,
+                       const void* z, void* y, void* stream);
+
+/* Device scratch of the backward: partial sums of dgamma and dbeta (not needed without
+   either); 0 on an invalid descriptor. */
+size_t wkv7_gnorm_backward_workspace_bytes(const wkv7_gnorm_desc* desc);
+
+/* Gradients of <dy, y>: dx and dz (given with a gate, else NULL) in dtype, dgamma and
+   dbeta fp32 [D] (each given with its parameter, else NULL), whose sums over the rows
+   are fp32 in a fixed order: repeated calls agree bit for bit. */
+int wkv7_gnorm_backward(const wkv7_gnorm_desc* desc, const float* gamma, const float* beta, const void* x,
+                        const void* z, const void* dy, void* dx, void* dz, float* dgamma, float* dbeta,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ---- Slots of a cache of states ------------------------------------------------
+ * A serving batch keeps the states of its sequences in a cache [planes][slots][row]
+ * (planes: layers, or 1), row_bytes each of any type, 16-byte aligned at its start.
+ * Rows of a multiple of 16 bytes move fastest.  slots <= 2^22, planes <= 2^20, and at
+ * most 2^23 workgroups (rows moved x planes x 1024 pieces of a row, of 16, 4, 2 or 1
+ * bytes as row_bytes allows).  Lists lie on the device and are not checked on the host.
+ */
+
+/* In every plane, for i = 0 .. n - 1 in order: slot dst[i] of pool takes what slot src[i]
+   of `from` holds (pool itself, from_slots = slots, or a cache of from_slots slots that
+   does not overlap it), or zeros where src[i] is -1.  A pair with a slot that does not
+   exist is left out.  In order means: a pair reads what the pairs before it wrote, and of
+   two with one target the later stays.  Pairs that do not touch each other are copied at
+   once; else one after the other, which takes longer. */
+int wkv7_slots_copy(int32_t planes, int32_t slots, int64_t row_bytes, int32_t n, const int32_t* src,
+                    const int32_t* dst, const void* from, int32_t from_slots, void* pool, void* stream);
+
+size_t wkv7_slots_compact_workspace_bytes(int32_t slots);
+
+/* The slots whose keep [slots] byte is not 0 come to the front: with count of them, those
+   at or behind place count move to the free places before it, both in order; the others
+   stay.  moved [slots]: a kept slot's new place, -1 for the others; count [1].  What is at
+   or behind place count is left as it was, or 0 with clear = 1. */
+int wkv7_slots_compact(int32_t planes, int32_t slots, int64_t row_bytes, const uint8_t* keep, int32_t* moved,
+                       int32_t* count, int32_t clear, void* pool, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
 #ifdef __cplusplus
 }
 #endif

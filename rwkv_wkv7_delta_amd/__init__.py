@@ -54,7 +54,9 @@ EXPORTED = ("wkv7_abi_version", "wkv7_status_string", "wkv7_tape_bytes", "wkv7_c
             "wkv7_ssm_forward_workspace_bytes", "wkv7_ssm_backward_workspace_bytes",
             "wkv7_ssm_forward", "wkv7_ssm_backward", "wkv7_ssm_step", "wkv7_linattn_ckpt_bytes",
             "wkv7_linattn_forward_workspace_bytes", "wkv7_linattn_backward_workspace_bytes",
-            "wkv7_linattn_forward", "wkv7_linattn_backward", "wkv7_linattn_step")
+            "wkv7_linattn_forward", "wkv7_linattn_backward", "wkv7_linattn_step", "wkv7_gnorm_forward",
+            "wkv7_gnorm_backward_workspace_bytes", "wkv7_gnorm_backward", "wkv7_slots_copy",
+            "wkv7_slots_compact_workspace_bytes", "wkv7_slots_compact")
 
 
 class WKV7Error(RuntimeError):
@@ -96,6 +98,11 @@ class SsmDesc(ctypes.Structure):
 class LinattnDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("B", "T", "H", "G", "N", "P", "dtype", "fixed_decay",
                                               "packed", "tokens")] + [("scale", ctypes.c_float)]
+
+
+class GnormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64)] + [(n, ctypes.c_int32) for n in
+                ("D", "G", "dtype", "center", "silu", "gate")] + [("eps", ctypes.c_float)]
 
 
 class SsmParams(ctypes.Structure):
@@ -164,7 +171,7 @@ def lib():
         L.wkv7_forward_epilogue.argtypes = [D] + [P] * 7 + [P, E, P, P, P]
         L.wkv7_forward_epilogue.restype = ctypes.c_int
         CD, SD = ctypes.POINTER(ConvDesc), ctypes.POINTER(SsmDesc)
-        LD = ctypes.POINTER(LinattnDesc)
+        LD, GD = ctypes.POINTER(LinattnDesc), ctypes.POINTER(GnormDesc)
         SP, SG = ctypes.POINTER(SsmParams), ctypes.POINTER(SsmGradPointers)
         for name, args, res in (
                 ("wkv7_conv_forward", [CD] + [P] * 8, ctypes.c_int),
@@ -182,7 +189,13 @@ def lib():
                 ("wkv7_linattn_backward_workspace_bytes", [LD], Z),
                 ("wkv7_linattn_forward", [LD] + [P] * 10 + [Z, P], ctypes.c_int),
                 ("wkv7_linattn_backward", [LD] + [P] * 14 + [Z, P], ctypes.c_int),
-                ("wkv7_linattn_step", [LD, P, I] + [P] * 7, ctypes.c_int)):
+                ("wkv7_linattn_step", [LD, P, I] + [P] * 7, ctypes.c_int),
+                ("wkv7_gnorm_forward", [GD] + [P] * 6, ctypes.c_int),
+                ("wkv7_gnorm_backward_workspace_bytes", [GD], Z),
+                ("wkv7_gnorm_backward", [GD] + [P] * 10 + [Z, P], ctypes.c_int),
+                ("wkv7_slots_copy", [I, I, ctypes.c_int64, I, P, P, P, I, P, P], ctypes.c_int),
+                ("wkv7_slots_compact_workspace_bytes", [I], Z),
+                ("wkv7_slots_compact", [I, I, ctypes.c_int64, P, P, P, I, P, P, Z, P], ctypes.c_int)):
             fn = getattr(L, name)
             fn.argtypes, fn.restype = args, res
         _lib = L
@@ -501,3 +514,5 @@ from .mixers import (SsmGrads, conv_backward, conv_forward, conv_step, ssm_backw
                      ssm_ckpt_bytes, ssm_forward, ssm_split_ckpt, ssm_step)
 from .linattn import (LinattnGrads, linattn_backward, linattn_ckpt_shape, linattn_forward,  # noqa: E402,F401
                       linattn_step)
+from .norm import GnormGrads, gnorm_backward, gnorm_forward  # noqa: E402,F401
+from .slots import slots_compact, slots_copy  # noqa: E402,F401

@@ -1,0 +1,201 @@
+// wkv7_slots.hip -- copies between the slots of a cache of states, and its compaction.
+//
+// Bytes only: a cache is [planes][slots][row].  Bound by HBM: each moved row is read and
+// written once.  A lane moves 16 bytes at a time (rows of other sizes 4, 2 or 1).
+
+#include "wkv7_device.h"
+#include "wkv7_slots_internal.h"
+
+namespace wkv7 {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kAhead = 4;                  // pieces that a lane has on their way
+constexpr int kPart = kThreads * kAhead;   // pieces of a row that a workgroup takes
+constexpr int kSeen = 8192;                // slots of the map of targets: a bit each, hashed
+
+template <int S> struct Bytes;
+template <> struct Bytes<16> { typedef uint4 T; static __device__ T zero() { return make_uint4(0, 0, 0, 0); } };
+template <> struct Bytes<4> { typedef uint32_t T; static __device__ T zero() { return 0; } };
+template <> struct Bytes<2> { typedef uint16_t T; static __device__ T zero() { return 0; } };
+template <> struct Bytes<1> { typedef uint8_t T; static __device__ T zero() { return 0; } };
+
+// Whether pair i counts: a target that exists, and a source that does or -1 (zeros).
+__device__ __forceinline__ bool pair_ok(const SlotsArgs& p, int src, int dst) {
+    return dst >= 0 && dst < p.slots && src >= -1 && src < p.from_slots;
+}
+
+// Pieces [c0, c0 + kPart) of row `src` of one plane to row `dst`.
+template <int S>
+__device__ __forceinline__ void move_part(const SlotsArgs& p, int plane, int src, int dst, int64_t c0, int64_t pieces) {
+    typedef typename Bytes<S>::T T;
+    const T* const f = static_cast<const T*>(p.from) + ((int64_t)plane * p.from_slots + (src < 0 ? 0 : src)) * pieces;
+    T* const t = static_cast<T*>(p.pool) + ((int64_t)plane * p.slots + dst) * pieces;
+    T x[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        const int64_t c = c0 + i * kThreads + threadIdx.x;
+        x[i] = Bytes<S>::zero();
+        if (src >= 0 && c < pieces) x[i] = f[c];
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+        const int64_t c = c0 + i * kThreads + threadIdx.x;
+        if (c < pieces) t[c] = x[i];
+    }
+}
+
+// Pair by pair, in order, as the contract says: a lane has its bytes of every row to
+// itself, so what it wrote for one pair is there for the next.  That is one row after the
+// other; where no target is named twice and none is a source, the pairs do not touch and
+// each has a workgroup of its own.  Every workgroup looks that up, the same way: it marks
+// the targets in a table of bits (by slot modulo its size: two slots that share a bit only
+// make the order be kept where it need not).
+template <int S>
+__global__ __launch_bounds__(kThreads) void slots_copy_kernel(const SlotsArgs p, unsigned parts) {
+    __shared__ uint32_t s_seen[kSeen / 32];
+    __shared__ int s_met;
+    const int64_t pieces = p.bytes / S;
+    const unsigned part = blockIdx.x % parts, rest = blockIdx.x / parts;
+    const int plane = (int)(rest % p.planes), pair = (int)(rest / p.planes);
+    const int64_t c0 = (int64_t)part * kPart;
+    if (p.n > 1) {
+        for (int i = threadIdx.x; i < kSeen / 32; i += kThreads) s_seen[i] = 0;
+        if (threadIdx.x == 0) s_met = 0;
+        __syncthreads();
+        bool met = false;
+        for (int i = threadIdx.x; i < p.n; i += kThreads) {
+            const int s = p.src[i], d = p.dst[i];
+            if (pair_ok(p, s, d)) {
+                const uint32_t bit = 1u << (d % 32), old = atomicOr(&s_seen[d / 32 % (kSeen / 32)], bit);
+                met |= (old & bit) != 0;
+            }
+        }
+        __syncthreads();
+        if (p.from == p.pool)
+            for (int i = threadIdx.x; i < p.n; i += kThreads) {
+                const int s = p.src[i], d = p.dst[i];
+                if (pair_ok(p, s, d) && s >= 0 && s != d) met |= (s_seen[s / 32 % (kSeen / 32)] >> (s % 32) & 1) != 0;
+            }
+        if (met) s_met = 1;
+        __syncthreads();
+        if (s_met) {
+            if (pair != 0) return;
+            for (int i = 0; i < p.n; ++i) {
+                const int s = p.src[i], d = p.dst[i];
+                if (pair_ok(p, s, d) && (s != d || p.from != p.pool)) move_part<S>(p, plane, s, d, c0, pieces);
+            }
+            return;
+        }
+    }
+    const int s = p.src[pair], d = p.dst[pair];
+    if (pair_ok(p, s, d) && (s != d || p.from != p.pool)) move_part<S>(p, plane, s, d, c0, pieces);
+}
+
+// Which slots move: with `count` kept ones, those behind the first `count` places fill the
+// free ones among these, both in order, so that no slot is moved twice and none that is
+// read is written.  One workgroup; a thread takes a run of slots.
+constexpr int kScan = 1024;
+__device__ __forceinline__ int block_before(int x, int* lds, int& total) {
+    lds[threadIdx.x] = x;
+    __syncthreads();
+    for (int d = 1; d < kScan; d *= 2) {
+        const int y = threadIdx.x >= (unsigned)d ? lds[threadIdx.x - d] : 0;
+        __syncthreads();
+        lds[threadIdx.x] += y;
+        __syncthreads();
+    }
+    total = lds[kScan - 1];
+    const int r = lds[threadIdx.x] - x;
+    __syncthreads();
+    return r;
+}
+__global__ __launch_bounds__(kScan) void slots_plan_kernel(const SlotsArgs p) {
+    __shared__ int s_run[kScan];
+    const int run = (p.slots + kScan - 1) / kScan;
+    const int64_t a64 = (int64_t)threadIdx.x * run;
+    const int a = (int)(a64 < p.slots ? a64 : p.slots), e = a + run < p.slots ? a + run : p.slots;
+    int kept = 0, count, holes = 0, late = 0, all;
+    for (int i = a; i < e; ++i) kept += p.keep[i] != 0;
+    block_before(kept, s_run, count);
+    for (int i = a; i < e; ++i) {
+        const bool k = p.keep[i] != 0;
+        holes += !k && i < count;
+        late += k && i >= count;
+    }
+    int h = block_before(holes, s_run, all), l = block_before(late, s_run, all);
+    for (int i = a; i < e; ++i) {
+        const bool k = p.keep[i] != 0;
+        if (!k && i < count) p.pairs[p.slots + h++] = i;
+        if (k && i >= count) p.pairs[l++] = i;
+        if (!k) p.moved[i] = -1;
+        else if (i < count) p.moved[i] = i;
+    }
+    if (threadIdx.x == 0) {
+        p.pairs[2 * (size_t)p.slots] = all;
+        p.count[0] = count;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < all; i += kScan) p.moved[p.pairs[i]] = p.pairs[p.slots + i];
+}
+
+// The moves, and zeros behind the last kept slot if wanted.  A slot that is moved is read
+// here and cleared only by its own workgroup's part, behind its copy.
+template <int S>
+__global__ __launch_bounds__(kThreads) void slots_move_kernel(const SlotsArgs p, unsigned parts) {
+    const int64_t pieces = p.bytes / S;
+    const unsigned part = blockIdx.x % parts, rest = blockIdx.x / parts;
+    const int plane = (int)(rest % p.planes), i = (int)(rest / p.planes);
+    const int64_t c0 = (int64_t)part * kPart;
+    if (!p.clear) {
+        // workgroup i: move i (at most half of the slots move)
+        if (i < p.pairs[2 * (size_t)p.slots]) move_part<S>(p, plane, p.pairs[i], p.pairs[p.slots + i], c0, pieces);
+        return;
+    }
+    // workgroup i: slot i
+    if (i < p.count[0]) return;
+    const int n = p.pairs[2 * (size_t)p.slots];
+    if (p.keep[i] != 0) {
+        int lo = 0, hi = n - 1;   // its place among the moved ones, which are in order
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (p.pairs[mid] < i) lo = mid + 1;
+            else hi = mid;
+        }
+        move_part<S>(p, plane, i, p.pairs[p.slots + lo], c0, pieces);
+    }
+    move_part<S>(p, plane, -1, i, c0, pieces);
+}
+
+// Bytes of a piece.
+int piece(const SlotsArgs& p) {
+    const uint64_t all = (uint64_t)p.bytes | reinterpret_cast<uintptr_t>(p.from) | reinterpret_cast<uintptr_t>(p.pool);
+    return all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : all % 2 == 0 ? 2 : 1;
+}
+
+}  // namespace
+
+#define WKV7_SLOTS(kernel, rows)                                                              \
+    {                                                                                         \
+        const int s = piece(p);                                                               \
+        const unsigned parts = (unsigned)((p.bytes / s + kPart - 1) / kPart);                 \
+        const unsigned grid = parts * p.planes * (unsigned)(rows);                            \
+        if (s == 16) kernel<16><<<grid, kThreads, 0, stream>>>(p, parts);                     \
+        else if (s == 4) kernel<4><<<grid, kThreads, 0, stream>>>(p, parts);                  \
+        else if (s == 2) kernel<2><<<grid, kThreads, 0, stream>>>(p, parts);                  \
+        else kernel<1><<<grid, kThreads, 0, stream>>>(p, parts);                              \
+        return hipGetLastError();                                                             \
+    }
+
+hipError_t launch_slots_copy(const SlotsArgs& p, hipStream_t stream) WKV7_SLOTS(slots_copy_kernel, p.n)
+
+hipError_t launch_slots_compact(const SlotsArgs& p, hipStream_t stream) {
+    slots_plan_kernel<<<1, kScan, 0, stream>>>(p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.planes == 0 || p.bytes == 0) return e;
+    const int rows = p.clear ? p.slots : (p.slots + 1) / 2;
+    WKV7_SLOTS(slots_move_kernel, rows)
+}
+
+}  // namespace wkv7
