@@ -20,6 +20,13 @@ namespace {
 // G is a multiple of 8).
 __device__ __forceinline__ int head_of(int i, int H, int G) { return i % G * (H / G) + i / G; }
 
+struct Yes {
+    static constexpr bool value = true;
+};
+struct No {
+    static constexpr bool value = false;
+};
+
 struct LaBlock {
     int b, h, p0, r;   // batch row, head, first value row, segment in the order of the sweep
 };
@@ -47,16 +54,22 @@ __device__ __forceinline__ float* state_at(float* base, const LaArgs& p, int b, 
 // dy: D <- e^{G_end} D + scale sum_t (e^{G_t} dy_t) q_t^T.
 // kSegment: what a segment leaves from zero, and its summed decay.  Else (the
 // reverse only) D behind every tile is written, and the gradient of the first state.
+// Four waves, each with 16 value rows (of 32: and half of the key columns).  Two tiles are
+// on their way from memory at any time: the products of one take a third of its loads' time.
+constexpr int kSweepThreads = 256;
+
 template <typename T, int N, int PB, bool kReverse, bool kSegment>
-__global__ __launch_bounds__(kLaThreads) void la_sweep_kernel(const LaArgs p, const T* kk, const T* vv,
-                                                              const float* first, float* last, T* marks) {
+__global__ __launch_bounds__(kSweepThreads) void la_sweep_kernel(const LaArgs p, const T* kk, const T* vv,
+                                                                 const float* first, float* last, T* marks) {
     typedef LaMat<T> M;
-    typedef LaStage<T, N> SK;
-    typedef LaStage<T, PB> SV;
-    constexpr int NT = N / 16;
-    __shared__ __attribute__((aligned(16))) T s_k[kLaChunk * SK::kStride];
-    __shared__ __attribute__((aligned(16))) T s_v[kLaChunk * SV::kStride];
-    __shared__ LaDecay s_d;
+    typedef LaStage<T, N, kSweepThreads> SK;
+    typedef LaStage<T, PB, kSweepThreads> SV;
+    constexpr int PT = PB / 16, NH = 4 / PT, NT = N / 16 / NH;
+    constexpr int kBytes = kLaChunk * (SK::kStride + SV::kStride) * (int)sizeof(T);
+    constexpr int BUF = kBytes <= 32 * 1024 ? 2 : 1;
+    __shared__ __attribute__((aligned(16))) T s_k[BUF][kLaChunk * SK::kStride];
+    __shared__ __attribute__((aligned(16))) T s_v[BUF][kLaChunk * SV::kStride];
+    __shared__ LaDecay s_d[BUF];
     const LaBlock w = la_block<PB>(p);
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int g = lane / 16, l16 = lane % 16;
@@ -65,16 +78,16 @@ __global__ __launch_bounds__(kLaThreads) void la_sweep_kernel(const LaArgs p, co
     const int64_t begin = (int64_t)seg * p.seg_len;
     const int64_t stop = seg == p.nseg - 1 ? row.len : begin + p.seg_len;
     const int end = (int)(stop < row.len ? stop : row.len);
-    const bool mine = wave < PB / 16;
-    const int prow = w.p0 + 16 * wave + l16;
+    const int ptile = wave % PT * 16, n0 = wave / PT * (NT * 16);
+    const int prow = w.p0 + ptile + l16;
     f32x4 st[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) st[n] = zero4();
     const size_t states = (size_t)p.B * p.H * p.P * N;
-    if (mine && !kSegment) {
+    if (!kSegment) {
         const float* from = w.r > 0 ? p.seg_state + (w.r - 1) * states : first;
         if (from) {
-            from = state_at<N>(const_cast<float*>(from), p, w.b, w.h, prow);
+            from = state_at<N>(const_cast<float*>(from), p, w.b, w.h, prow) + n0;
 #pragma unroll
             for (int n = 0; n < NT; ++n) st[n] = *reinterpret_cast<const f32x4*>(from + 16 * n + 4 * g);
         }
@@ -82,60 +95,68 @@ __global__ __launch_bounds__(kLaThreads) void la_sweep_kernel(const LaArgs p, co
     const int kh = w.h / (p.H / p.G);
     const int64_t krow = (int64_t)p.G * N, vrow = (int64_t)p.H * p.P;
     const int tiles = end > begin ? (int)((end - begin + kLaChunk - 1) / kLaChunk) : 0;
-    SK rk;
-    SV rv;
-    LaLog<T> lg;
-    auto load = [&](int c) {
-        const int64_t t0 = begin + (int64_t)c * kLaChunk;
-        const int n = (int)(end - t0 < kLaChunk ? end - t0 : kLaChunk);
-        const int64_t at = row.first + t0;
-        rk.load(rows_of(kk + at * krow + kh * N, n, krow, N), (uint32_t)(krow * sizeof(T)));
-        rv.load(rows_of(vv + at * vrow + (int64_t)w.h * p.P + w.p0, n, vrow, PB), (uint32_t)(vrow * sizeof(T)));
-        if (wave == 0) lg.load(p, at + lane, w.h, lane < n);
-    };
+    struct Ahead {
+        SK k;
+        SV v;
+        LaLog<T> g;
+    } even, odd_;
+    constexpr bool kDeep = SK::kLoads + SV::kLoads <= 12;
     const auto tile_of = [&](int i) { return kReverse ? tiles - 1 - i : i; };
+    // No condition on the loads (tiles that there are not have no bytes): how many are under
+    // way is then known to the code that waits for the older ones.
+    auto load = [&](int i, Ahead& r) {
+        const int64_t t0 = begin + (int64_t)tile_of(i) * kLaChunk;
+        const int n = i >= tiles ? 0 : (int)(end - t0 < kLaChunk ? end - t0 : kLaChunk);
+        const int64_t at = row.first + t0;
+        r.k.load(rows_of(kk + at * krow + kh * N, n, krow, N), (uint32_t)(krow * sizeof(T)));
+        r.v.load(rows_of(vv + at * vrow + (int64_t)w.h * p.P + w.p0, n, vrow, PB), (uint32_t)(vrow * sizeof(T)));
+        r.g.load(p, at, w.h, n);
+    };
+    auto put = [&](int buf, const Ahead& r) {
+        r.k.store(s_k[buf]);
+        r.v.store(s_v[buf]);
+        const bool odd = __builtin_amdgcn_ballot_w64(r.k.odd() || r.v.odd()) != 0;
+        if (lane == 0) s_d[buf].odd[wave] = odd;
+        if (wave == 0) put_decays(s_d[buf], r.g.get());
+    };
     double total = 0;
-    if (tiles > 0) load(tile_of(0));
-    for (int i = 0; i < tiles; ++i) {
+    auto turn = [&](int i, Ahead& r) {
+        const int buf = BUF == 2 ? i & 1 : 0;
         __syncthreads();
-        rk.store(s_k);
-        rv.store(s_v);
-        if (wave == 0) put_decays(s_d, lg.x);
-        __syncthreads();
-        if (i + 1 < tiles) load(tile_of(i + 1));
-        if (mine) {
-            if (!kSegment) {
-                T* const m = marks + (((row.ckpt + begin / kLaChunk + tile_of(i)) * p.H + w.h) * p.P + prow) * N;
+        const LaDecay& d = s_d[buf];
+        if (!kSegment) {
+            // (of a tile that there is not: nothing)
+            const auto m = buffer_of(marks + (((row.ckpt + begin / kLaChunk + tile_of(i)) * p.H + w.h) * p.P + w.p0) * N,
+                                     i < tiles ? PB * N * (int)sizeof(T) : 0);
+            const uint32_t at = ((ptile + l16) * N + n0 + 4 * g) * (uint32_t)sizeof(T);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) M::put(m + 16 * n + 4 * g, st[n]);
-            }
-            if (kSegment) total += s_d.sum;
-            const float all = s_d.all;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) st[n] *= all;
-#pragma unroll
-            for (int t = 0; t < kLaChunk; t += 32) {
-                f32x4 x[2];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int t1 = t + 16 * u;
-                    x[u] = M::wide(M::column(s_v + t1 * SV::kStride + 16 * wave, SV::kStride, g, l16));
-                    const f32x4 e = *reinterpret_cast<const f32x4*>((kReverse ? s_d.up : s_d.down) + t1 + 4 * g);
-                    x[u] *= kReverse ? e * p.scale : e;
-                }
-                typename M::Frag f[M::kParts];
-                split_parts<T>(x[0], x[1], f);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const typename M::Frag a = columns<T>(s_k + t * SK::kStride + 16 * n, SK::kStride, g, l16);
-#pragma unroll
-                    for (int i2 = M::kParts - 1; i2 >= 0; --i2) st[n] = M::mma(a, f[i2], st[n]);
-                }
+            for (int n = 0; n < NT; ++n) {
+                if constexpr (sizeof(T) == 2)
+                    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(vu2, cvt4(st[n])), m, at + 32 * n, 0, 0);
+                else
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, st[n]), m, at + 64 * n, 0, 0);
             }
         }
+        if (kSegment) total += d.sum;
+        move_state<T, NT>(st, s_k[buf] + n0, SK::kStride, s_v[buf] + ptile, SV::kStride, kReverse ? d.up : d.down,
+                          kReverse ? p.scale : 1.f, d.all, any_odd<4>(d.odd), g, l16);
+        if (BUF == 1) __syncthreads();
+        put(BUF == 2 ? buf ^ 1 : 0, r);
+        load(i + (kDeep ? 3 : 2), r);
+    };
+    if (tiles > 0) {
+        load(0, even);
+        if (kDeep) load(1, odd_);
+        put(0, even);
+        load(kDeep ? 2 : 1, even);
+        // Deep: by twos, the last perhaps a tile without tokens, which changes nothing.
+        for (int i = 0; i < tiles; i += kDeep ? 2 : 1) {
+            turn(i, kDeep ? odd_ : even);
+            if (kDeep) turn(i + 1, even);
+        }
     }
-    if (mine && last && (kSegment || w.r == p.nseg - 1)) {
-        float* const to = state_at<N>(last + (kSegment ? w.r * states : 0), p, w.b, w.h, prow);
+    if (last && (kSegment || w.r == p.nseg - 1)) {
+        float* const to = state_at<N>(last + (kSegment ? w.r * states : 0), p, w.b, w.h, prow) + n0;
 #pragma unroll
         for (int n = 0; n < NT; ++n) *reinterpret_cast<f32x4*>(to + 16 * n + 4 * g) = st[n];
     }
@@ -150,29 +171,43 @@ __global__ __launch_bounds__(256) void la_join_kernel(const LaArgs p, const floa
     const size_t head = e / ((size_t)p.P * p.N), heads = (size_t)p.B * p.H;
     f32x4 s = zero4();
     if (first) s = *reinterpret_cast<const f32x4*>(first + e);
-    for (int r = 0; r + 1 < p.nseg; ++r) {
-        float* const at = p.seg_state + r * states + e;
-        const float d = exp2_raw((float)p.seg_decay[r * heads + head]);
-        s = s * d + *reinterpret_cast<const f32x4*>(at);
-        *reinterpret_cast<f32x4*>(at) = s;
+    constexpr int kAtOnce = 8;   // loads on their way while the chain waits for none
+    for (int r0 = 0; r0 + 1 < p.nseg; r0 += kAtOnce) {
+        f32x4 x[kAtOnce];
+        float d[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int r = r0 + i + 1 < p.nseg ? r0 + i : r0;
+            x[i] = *reinterpret_cast<const f32x4*>(p.seg_state + r * states + e);
+            d[i] = exp2_raw((float)p.seg_decay[r * heads + head]);
+        }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            if (r0 + i + 1 < p.nseg) {
+                s = s * d[i] + x[i];
+                *reinterpret_cast<f32x4*>(p.seg_state + (r0 + i) * states + e) = s;
+            }
+        }
     }
 }
 
 // ---- prompts --------------------------------------------------------------------
-// A workgroup takes 64 (or all 32) value rows of a head's state over a segment.
-// Wave w has tokens 16 w .. of the tile for the read-out and value rows 16 w .. of
-// the state.  Results are formed transposed, [s][t], [p][t], [n][p], so that each
-// feeds the next product from registers (wkv7_linattn_device.h).
+// A workgroup takes 64 (or all 32) value rows of a head's state over a segment.  Waves 0
+// to 3 read out: wave w the tokens 16 w .. of the tile.  Waves 4 to 7 hold the state and
+// move it on, 16 value rows each (of 32: and half of the columns), for the next tile while
+// the others read the one before from LDS.  Results are formed transposed, [s][t], [p][t],
+// [n][p], so that each feeds the next product from registers (wkv7_linattn_device.h).
 template <typename T, int N, int PB>
 struct LaFwdShared {
     typedef LaStage<T, N> SK;
     typedef LaStage<T, PB> SV;
-    // Two of everything, and one barrier a tile, where both fit twice into a unit's LDS.
+    // Two of everything, and one barrier a tile, where two workgroups fit a unit's LDS.
     static constexpr int kBytes = (kLaChunk * (SK::kStride + SV::kStride) + PB * SK::kStride) * (int)sizeof(T);
     static constexpr int kBuffers = kBytes <= 28 * 1024 ? 2 : 1;
     T k[kBuffers][kLaChunk * SK::kStride];
     T v[kBuffers][kLaChunk * SV::kStride];
     T s[kBuffers][PB * SK::kStride];   // the state before the tile, [p][n], in the tokens' type
+    T own[4][LaRows16<T, (N > PB ? N : PB)>::kSize];   // a wave's queries, then its results
     LaDecay d[kBuffers];
 };
 
@@ -181,10 +216,10 @@ __global__ __launch_bounds__(kLaThreads) void la_fwd_kernel(const LaArgs p) {
     typedef LaMat<T> M;
     typedef LaStage<T, N> SK;
     typedef LaStage<T, PB> SV;
+    typedef LaRows16<T, N> SQ;
     typedef LaFwdShared<T, N, PB> Shared;
     typedef typename M::Frag Frag;
-    constexpr int NT = N / 16, PT = PB / 16, KS = N / 32, BUF = Shared::kBuffers;
-    constexpr int kQ = KS * (int)sizeof(T) / 2;   // 16-byte loads of a lane's query
+    constexpr int PT = PB / 16, NT = N / 16 * PT / 4, KS = N / 32, BUF = Shared::kBuffers;
     __shared__ __attribute__((aligned(16))) Shared sm;
     const LaBlock w = la_block<PB>(p);
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -195,190 +230,190 @@ __global__ __launch_bounds__(kLaThreads) void la_fwd_kernel(const LaArgs p) {
     const int64_t stop = begin + p.seg_len;
     const int end = (int)(tail || stop > row.len ? row.len : stop);          // tokens
     const int64_t zero_end = tail || stop > row.stored ? row.stored : stop;  // and places that are written
-    const bool mine = wave < PT;
-    const int prow = w.p0 + 16 * wave + l16;
+    // The state's wave: value rows ptile .., columns n0 ..
+    const int ptile = wave % PT * 16, n0 = (wave % 4) / PT * (NT * 16);
+    const int prow = w.p0 + ptile + l16;
     const size_t states = (size_t)p.B * p.H * p.P * N;
-    f32x4 st[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) st[n] = zero4();
-    if (mine) {
-        const float* from = w.r > 0 ? p.seg_state + (w.r - 1) * states : p.s0;
-        if (from) {
-            from = state_at<N>(const_cast<float*>(from), p, w.b, w.h, prow);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) st[n] = *reinterpret_cast<const f32x4*>(from + 16 * n + 4 * g);
-        }
-    }
     const int kh = w.h / (p.H / p.G);
     const int64_t krow = (int64_t)p.G * N, vrow = (int64_t)p.H * p.P;
+    const uint32_t kb = (uint32_t)(krow * sizeof(T)), vb = (uint32_t)(vrow * sizeof(T));
     const int tiles = end > begin ? (int)((end - begin + kLaChunk - 1) / kLaChunk) : 0;
-    const T* const Q = static_cast<const T*>(p.q);
-    const T* const K = static_cast<const T*>(p.k);
-    const T* const V = static_cast<const T*>(p.v);
     T* const Y = static_cast<T*>(p.y);
-    SK rk;
-    SV rv;
-    LaLog<T> lg;
-    vu4 rq[kQ];
-    auto load = [&](int c) {
-        const int64_t t0 = begin + (int64_t)c * kLaChunk;
-        const int n = (int)(end - t0 < kLaChunk ? end - t0 : kLaChunk);
-        const int64_t at = row.first + t0;
-        const uint32_t kb = (uint32_t)(krow * sizeof(T));
-        rk.load(rows_of(K + at * krow + kh * N, n, krow, N), kb);
-        rv.load(rows_of(V + at * vrow + (int64_t)w.h * p.P + w.p0, n, vrow, PB), (uint32_t)(vrow * sizeof(T)));
-        const auto qb = rows_of(Q + at * krow + kh * N, n, krow, N);
-#pragma unroll
-        for (int i = 0; i < KS; ++i)
-#pragma unroll
-            for (int j = 0; j < kQ / KS; ++j)
-                rq[i * (kQ / KS) + j] = __builtin_bit_cast(vu4, __builtin_amdgcn_raw_buffer_load_b128(
-                    qb, (16 * wave + l16) * kb + (32 * i + 8 * g) * (uint32_t)sizeof(T) + 16 * j, 0, 0));
-        if (wave == 0) lg.load(p, at + lane, w.h, lane < n);
+    // Two tiles are on their way from memory at any time (at a copy's rate, what a unit has
+    // in flight has to cover about 2 us); one where the registers hold no more.
+    struct Ahead {
+        SK k;
+        SV v;
+        SQ q;
+        LaLog<T> g;
     };
-    auto put = [&](int buf) {
-        rk.store(sm.k[buf]);
-        rv.store(sm.v[buf]);
-        if (wave == 0) put_decays(sm.d[buf], lg.x);
-        const bool odd = __builtin_amdgcn_ballot_w64(rk.odd() || rv.odd()) != 0;
-        if (lane == 0) sm.d[buf].odd[wave] = odd;
+    constexpr bool kDeep = SK::kLoads + SV::kLoads + SQ::kEach <= 12;
+    const auto tokens_of = [&](int c, int64_t to) {   // of tile c
+        const int64_t n = to - (begin + (int64_t)c * kLaChunk);
+        return (int)(n < 0 ? 0 : n < kLaChunk ? n : kLaChunk);
     };
-    auto put_state = [&](int buf) {
-        if (mine)
+    f32x4 st[NT];
+    // A wave's whole way over the segment, by its role: the code that waits for older loads
+    // has to know how many younger loads and stores there are, so no role's are conditional
+    // for another and tiles that there are not are loaded as nothing.
+    auto run = [&](auto reads_) {
+        constexpr bool kReads = decltype(reads_)::value;
+        const int t = 16 * wave + l16;   // the read-out's token
+        T* const own = sm.own[wave % 4];
+        Frag qf[KS];
+        auto load = [&](int c, Ahead& r) {
+            const int n = tokens_of(c, end);
+            const int64_t at = row.first + begin + (int64_t)c * kLaChunk;
+            r.k.load(rows_of(static_cast<const T*>(p.k) + at * krow + kh * N, n, krow, N), kb);
+            r.v.load(rows_of(static_cast<const T*>(p.v) + at * vrow + (int64_t)w.h * p.P + w.p0, n, vrow, PB), vb);
+            if constexpr (kReads) {
+                r.q.load(rows_of(static_cast<const T*>(p.q) + at * krow + kh * N, n, krow, N), kb, 16 * wave);
+                r.g.load(p, at, w.h, n);
+            }
+        };
+        auto put = [&](int buf, const Ahead& r) {
+            r.k.store(sm.k[buf]);
+            r.v.store(sm.v[buf]);
+            const bool odd = __builtin_amdgcn_ballot_w64(r.k.odd() || r.v.odd()) != 0;
+            if (lane == 0) sm.d[buf].odd[wave] = odd;
+            if constexpr (kReads) {
+                if (wave == 0) put_decays(sm.d[buf], r.g.get());
+                r.q.put(own);
+#pragma unroll
+                for (int i = 0; i < KS; ++i) qf[i] = M::rows(own + l16 * SQ::kStride + 32 * i + 8 * g);
+            }
+        };
+        auto put_state = [&](int buf) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
-                M::put(sm.s[buf] + (16 * wave + l16) * SK::kStride + 16 * n + 4 * g, st[n]);
-    };
-    put_state(0);
-    if (tiles > 0) {
-        load(0);
-        put(0);
-    }
-    for (int c = 0; c < tiles; ++c) {
-        const int buf = BUF == 2 ? c & 1 : 0, nxt = BUF == 2 ? buf ^ 1 : 0;
-        Frag qf[KS];
+                M::put(sm.s[buf] + (ptile + l16) * SK::kStride + n0 + 16 * n + 4 * g, st[n]);
+        };
+        auto turn = [&](int c, Ahead& r) {
+            const int buf = BUF == 2 ? c & 1 : 0, nxt = BUF == 2 ? buf ^ 1 : 0;
+            __syncthreads();
+            const T* const sk = sm.k[buf];
+            const T* const sv = sm.v[buf];
+            const LaDecay& d = sm.d[buf];
+            const int64_t at = row.first + begin + (int64_t)c * kLaChunk;
+            const bool odd = any_odd(d.odd);
+            if constexpr (kReads) {
+                const int n_in = tokens_of(c, end);
+                const float thi = d.hi[t], tlo = d.lo[t], tup = d.up[t];
+                f32x4 o[PT];
 #pragma unroll
-        for (int i = 0; i < KS; ++i) {
-            if constexpr (sizeof(T) == 2) qf[i] = __builtin_bit_cast(Frag, rq[i]);
-            else qf[i] = M::cat(__builtin_bit_cast(f32x4, rq[2 * i]), __builtin_bit_cast(f32x4, rq[2 * i + 1]));
-        }
-        __syncthreads();
-        const int64_t t0 = begin + (int64_t)c * kLaChunk;
-        const int n_in = (int)(end - t0 < kLaChunk ? end - t0 : kLaChunk);
-        const int n_out = (int)(zero_end - t0 < kLaChunk ? zero_end - t0 : kLaChunk);
-        const T* const sk = sm.k[buf];
-        const T* const sv = sm.v[buf];
-        const LaDecay& d = sm.d[buf];
-        const int64_t at = row.first + t0;
-        if (p.ckpt && mine) {
-            T* const m = static_cast<T*>(p.ckpt) +
-                         (((row.ckpt + begin / kLaChunk + c) * p.H + w.h) * p.P + prow) * N;
+                for (int pt = 0; pt < PT; ++pt) {
+                    o[pt] = zero4();
 #pragma unroll
-            for (int n = 0; n < NT; ++n) M::put(m + 16 * n + 4 * g, st[n]);
-        }
-        if (c + 1 < tiles) load(c + 1);
-        const auto yb = rows_of(Y + at * vrow + (int64_t)w.h * p.P + w.p0, n_out, vrow, PB);
-        const uint32_t yrow = (uint32_t)(vrow * sizeof(T));
-        const int odd = __builtin_amdgcn_readfirstlane(d.odd[0] | d.odd[1] | d.odd[2] | d.odd[3]);
-        if (!odd) {
-            // [s][t] of the wave's tokens t against those up to them.
-            const int t = 16 * wave + l16;
-            const float thi = d.hi[t], tlo = d.lo[t], tup = d.up[t];
-            Frag pf[2];
-#pragma unroll
-            for (int j2 = 0; j2 < 2; ++j2) {
-                typename M::Half h2[2];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int j = 2 * j2 + u;
-                    f32x4 a = zero4();
-                    if (j <= wave) {
-#pragma unroll
-                        for (int i = 0; i < KS; ++i)
-                            a = M::mma(M::rows(sk + (16 * j + l16) * SK::kStride + 32 * i + 8 * g), qf[i], a);
-                        const f32x4 shi = *reinterpret_cast<const f32x4*>(d.hi + 16 * j + 4 * g);
-                        const f32x4 slo = *reinterpret_cast<const f32x4*>(d.lo + 16 * j + 4 * g);
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const float e = exp2_raw((thi - shi[q]) + (tlo - slo[q]));
-                            a[q] = 16 * j + 4 * g + q <= t ? a[q] * e : 0.f;
-                        }
-                    }
-                    // Rounded to the tokens' type for the product with v: an error of half a
-                    // step of each weight, as large as y's own rounding.
-                    h2[u] = M::half(a);
+                    for (int i = 0; i < KS; ++i)
+                        o[pt] = M::mma(M::rows(sm.s[buf] + (16 * pt + l16) * SK::kStride + 32 * i + 8 * g), qf[i], o[pt]);
                 }
-                pf[j2] = M::cat(h2[0], h2[1]);
-            }
+                if (!odd) {
+                    // [s][t] of the wave's tokens t against those up to them.
+                    Frag pf[2];
 #pragma unroll
-            for (int pt = 0; pt < PT; ++pt) {
-                f32x4 o = zero4();
+                    for (int j2 = 0; j2 < 2; ++j2) {
+                        typename M::Half h2[2];
 #pragma unroll
-                for (int i = 0; i < KS; ++i)
-                    o = M::mma(M::rows(sm.s[buf] + (16 * pt + l16) * SK::kStride + 32 * i + 8 * g), qf[i], o);
-                o *= tup;
-                o = M::mma(columns<T>(sv + 16 * pt, SV::kStride, g, l16), pf[0], o);
-                if (wave >= 2) o = M::mma(columns<T>(sv + 32 * SV::kStride + 16 * pt, SV::kStride, g, l16), pf[1], o);
+                        for (int u = 0; u < 2; ++u) {
+                            const int j = 2 * j2 + u;
+                            f32x4 a = zero4();
+                            if (j <= wave) {
+#pragma unroll
+                                for (int i = 0; i < KS; ++i)
+                                    a = M::mma(M::rows(sk + (16 * j + l16) * SK::kStride + 32 * i + 8 * g), qf[i], a);
+                                const f32x4 shi = *reinterpret_cast<const f32x4*>(d.hi + 16 * j + 4 * g);
+                                const f32x4 slo = *reinterpret_cast<const f32x4*>(d.lo + 16 * j + 4 * g);
+#pragma unroll
+                                for (int q = 0; q < 4; ++q) a[q] *= exp2_raw((thi - shi[q]) + (tlo - slo[q]));
+                                if (j == wave)   // the triangle's edge
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q) a[q] = 4 * g + q <= l16 ? a[q] : 0.f;
+                            }
+                            // Rounded to the tokens' type for the product with v: an error of half a
+                            // step of each weight, as large as y's own rounding.
+                            h2[u] = M::half(a);
+                        }
+                        pf[j2] = M::cat(h2[0], h2[1]);
+                    }
+#pragma unroll
+                    for (int pt = 0; pt < PT; ++pt) {
+                        o[pt] *= tup;
+                        o[pt] = M::mma(columns<T>(sv + 16 * pt, SV::kStride, g, l16), pf[0], o[pt]);
+                        if (wave >= 2)
+                            o[pt] = M::mma(columns<T>(sv + 32 * SV::kStride + 16 * pt, SV::kStride, g, l16), pf[1], o[pt]);
+                    }
+                } else {
+                    // An infinity or a NaN among the tile's keys and values: pair by pair, each lane its
+                    // token, so that it meets no weight of 0 of a token before its own.
+#pragma unroll
+                    for (int pt = 0; pt < PT; ++pt) o[pt] *= tup;
+                    for (int s = 0; s < n_in; ++s) {
+                        float a = 0.f;
+#pragma unroll 2
+                        for (int n = 0; n < N; ++n)
+                            a = fmaf(Elem<T>::load1(sk + s * SK::kStride + n), Elem<T>::load1(own + l16 * SQ::kStride + n), a);
+                        a *= exp2_raw((thi - d.hi[s]) + (tlo - d.lo[s]));
+                        if (s <= t)
+#pragma unroll
+                            for (int pt = 0; pt < PT; ++pt)
+                                o[pt] += M::wide(M::four(sv + s * SV::kStride + 16 * pt + 4 * g)) * a;
+                    }
+                }
                 // nothing of a state that is not finite behind the row's last token
 #pragma unroll
-                for (int q = 0; q < 4; ++q) o[q] = t < n_in ? o[q] * p.scale : 0.f;
-                const uint32_t off = t * yrow + (16 * pt + 4 * g) * (uint32_t)sizeof(T);
-                if constexpr (sizeof(T) == 2)
-                    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(vu2, cvt4(o)), yb, off, 0, 0);
-                else
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, o), yb, off, 0, 0);
-            }
-            if (mine) {
-                const float all = d.all;
+                for (int pt = 0; pt < PT; ++pt)
 #pragma unroll
-                for (int n = 0; n < NT; ++n) st[n] *= all;
+                    for (int q = 0; q < 4; ++q) o[pt][q] = t < n_in ? o[pt][q] * p.scale : 0.f;
+                LaRows16<T, PB>::store(own, o, rows_of(Y + at * vrow + (int64_t)w.h * p.P + w.p0, tokens_of(c, zero_end), vrow, PB),
+                                       vb, 16 * wave);
+            } else {
+                const auto m = buffer_of(static_cast<T*>(p.ckpt) +
+                                             (((row.ckpt + begin / kLaChunk + c) * p.H + w.h) * p.P + w.p0) * N,
+                                         p.ckpt && c < tiles ? PB * N * (int)sizeof(T) : 0);
+                const uint32_t mark = ((ptile + l16) * N + n0 + 4 * g) * (uint32_t)sizeof(T);
 #pragma unroll
-                for (int t1 = 0; t1 < kLaChunk; t1 += 32) {
-                    f32x4 x[2];
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        x[u] = M::wide(M::column(sv + (t1 + 16 * u) * SV::kStride + 16 * wave, SV::kStride, g, l16));
-                        x[u] *= *reinterpret_cast<const f32x4*>(d.down + t1 + 16 * u + 4 * g);
-                    }
-                    Frag f[M::kParts];
-                    split_parts<T>(x[0], x[1], f);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const Frag a = columns<T>(sk + t1 * SK::kStride + 16 * n, SK::kStride, g, l16);
-#pragma unroll
-                        for (int i = M::kParts - 1; i >= 0; --i) st[n] = M::mma(a, f[i], st[n]);
-                    }
+                for (int n = 0; n < NT; ++n) {
+                    if constexpr (sizeof(T) == 2)
+                        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(vu2, cvt4(st[n])), m, mark + 32 * n, 0, 0);
+                    else
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, st[n]), m, mark + 64 * n, 0, 0);
                 }
+                move_state<T, NT>(st, sk + n0, SK::kStride, sv + ptile, SV::kStride, d.down, 1.f, d.all, odd, g, l16);
             }
-        } else if (mine) {
-            // An infinity or a NaN among the tile's keys and values: token by token, so that it
-            // reaches no token before its own (in a product it would meet their zero weights).
-            for (int i = 0; i < n_out; ++i) {
-                float y = 0.f;
-                if (i < n_in) {
-                    const float e = exp2_raw(d.hi[i] - (i > 0 ? d.hi[i - 1] : 0.f) + (d.lo[i] - (i > 0 ? d.lo[i - 1] : 0.f)));
-                    const float v = Elem<T>::load1(sv + i * SV::kStride + 16 * wave + l16);
+            if (BUF == 1) __syncthreads();
+            if constexpr (!kReads) put_state(nxt);
+            put(nxt, r);
+            load(c + (kDeep ? 3 : 2), r);
+        };
+        if constexpr (!kReads) {
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const float4 k = Elem<T>::load4(sk + i * SK::kStride + 16 * n + 4 * g);
-                        const float4 q = Elem<T>::load4(Q + (at + i) * krow + kh * N + 16 * n + 4 * g);
-                        st[n][0] = fmaf(k.x, v, st[n][0] * e);
-                        st[n][1] = fmaf(k.y, v, st[n][1] * e);
-                        st[n][2] = fmaf(k.z, v, st[n][2] * e);
-                        st[n][3] = fmaf(k.w, v, st[n][3] * e);
-                        y = fmaf(st[n][3], q.w, fmaf(st[n][2], q.z, fmaf(st[n][1], q.y, fmaf(st[n][0], q.x, y))));
-                    }
-                    y = sum_rows4(y) * p.scale;
-                }
-                if (g == 0) Elem<T>::store1(Y + (at + i) * vrow + (int64_t)w.h * p.P + prow, y);
+            for (int n = 0; n < NT; ++n) st[n] = zero4();
+            const float* from = w.r > 0 ? p.seg_state + (w.r - 1) * states : p.s0;
+            if (from) {
+                from = state_at<N>(const_cast<float*>(from), p, w.b, w.h, prow) + n0;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) st[n] = *reinterpret_cast<const f32x4*>(from + 16 * n + 4 * g);
+            }
+            put_state(0);
+        }
+        if (tiles > 0) {
+            Ahead even, odd_;
+            load(0, even);
+            if (kDeep) load(1, odd_);
+            put(0, even);
+            load(kDeep ? 2 : 1, even);
+            // Deep: by twos, the last perhaps a tile without tokens, which changes nothing.
+            for (int c = 0; c < tiles; c += kDeep ? 2 : 1) {
+                turn(c, kDeep ? odd_ : even);
+                if (kDeep) turn(c + 1, even);
             }
         }
-        if (BUF == 1) __syncthreads();
-        put_state(nxt);
-        if (c + 1 < tiles) put(nxt);
-    }
-    if (mine && tail && p.sT) {
-        float* const to = state_at<N>(p.sT, p, w.b, w.h, prow);
+    };
+    const bool reads = wave < 4;
+    if (reads) run(Yes());
+    else run(No());
+    if (!reads && tail && p.sT) {
+        float* const to = state_at<N>(p.sT, p, w.b, w.h, prow) + n0;
 #pragma unroll
         for (int n = 0; n < NT; ++n) *reinterpret_cast<f32x4*>(to + 16 * n + 4 * g) = st[n];
     }
@@ -448,7 +483,7 @@ template <typename T, int N, int PB>
 hipError_t fwd_block(const LaArgs& p, hipStream_t stream) {
     const unsigned blocks = (unsigned)p.B * p.H * (p.P / PB);
     if (p.nseg > 1) {
-        la_sweep_kernel<T, N, PB, false, true><<<blocks * (p.nseg - 1), kLaThreads, 0, stream>>>(
+        la_sweep_kernel<T, N, PB, false, true><<<blocks * (p.nseg - 1), kSweepThreads, 0, stream>>>(
             p, static_cast<const T*>(p.k), static_cast<const T*>(p.v), nullptr, p.seg_state, nullptr);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -466,14 +501,14 @@ hipError_t adjoint_block(const LaBwdArgs& q, hipStream_t stream) {
     const T* const Q = static_cast<const T*>(p.q);
     const T* const dY = static_cast<const T*>(q.dy);
     if (p.nseg > 1) {
-        la_sweep_kernel<T, N, PB, true, true><<<blocks * (p.nseg - 1), kLaThreads, 0, stream>>>(
+        la_sweep_kernel<T, N, PB, true, true><<<blocks * (p.nseg - 1), kSweepThreads, 0, stream>>>(
             p, Q, dY, nullptr, p.seg_state, nullptr);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         la_join_kernel<<<(unsigned)(((size_t)p.B * p.H * p.P * N / 4 + 255) / 256), 256, 0, stream>>>(p, q.dsT);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    la_sweep_kernel<T, N, PB, true, false><<<blocks * p.nseg, kLaThreads, 0, stream>>>(
+    la_sweep_kernel<T, N, PB, true, false><<<blocks * p.nseg, kSweepThreads, 0, stream>>>(
         p, Q, dY, q.dsT, q.ds0, static_cast<T*>(q.adj));
     return hipGetLastError();
 }

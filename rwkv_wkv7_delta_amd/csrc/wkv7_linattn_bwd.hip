@@ -24,11 +24,12 @@ struct LaBwdShared {
     T q[kLaChunk * SK::kStride], k[kLaChunk * SK::kStride];
     T v[kLaChunk * SV::kStride], dy[kLaChunk * SV::kStride];
     T s[PB * SK::kStride], ds[PB * SK::kStride];   // [p][n]
-    LaDecay d;
-    // For dg: sums of M along its rows, by wave; the rest of what counts for all tokens up to
-    // one (a, and M down its columns taken off), for those behind it (b), and for all.
-    float row[4][kLaChunk], a[kLaChunk], b[kLaChunk], c[4];
-    int odd_k[4];
+    // A wave's results on their way to whole rows (fp32 rows go there by themselves).
+    T own[sizeof(T) == 2 ? 8 : 1][sizeof(T) == 2 ? LaRows16<T, (N > PB ? N : PB)>::kSize : 16];
+    LaDecay d[2];                                  // of this head and the next
+    // For dg: sums of M along its rows, by wave; a; M's sums down its columns; b; parts of <S, D>.
+    float row[4][kLaChunk], a[kLaChunk], col[kLaChunk], b[kLaChunk], c[8];
+    int odd[8];
 };
 
 // PB state rows of N on their way to LDS (64 rows of LaStage, or 32).
@@ -38,13 +39,12 @@ struct LaStateStage {
     static constexpr int kLoads = PB * kPieces / kLaThreads;
     static constexpr int kStride = N + 16 / (int)sizeof(T);
     vu4 w[kLoads > 0 ? kLoads : 1];
-    // Rows are one behind the other in memory.
-    __device__ __forceinline__ void load(const T* p) {
+    // Rows are one behind the other in memory; none where there is no tile.
+    __device__ __forceinline__ void load(const T* p, bool some) {
+        const auto r = buffer_of(p, some ? PB * N * (int)sizeof(T) : 0);
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i)
-            w[i] = *reinterpret_cast<const vu4*>(reinterpret_cast<const char*>(p) + (i * kLaThreads + threadIdx.x) * 16);
-        if (kLoads == 0 && threadIdx.x < PB * kPieces)
-            w[0] = *reinterpret_cast<const vu4*>(reinterpret_cast<const char*>(p) + threadIdx.x * 16);
+        for (int i = 0; i < (kLoads > 0 ? kLoads : 1); ++i)
+            w[i] = __builtin_bit_cast(vu4, __builtin_amdgcn_raw_buffer_load_b128(r, (i * kLaThreads + threadIdx.x) * 16, 0, 0));
     }
     __device__ __forceinline__ void store(T* lds) const {
 #pragma unroll
@@ -76,12 +76,42 @@ struct LaStateStage {
 
 __device__ __forceinline__ float wave_sum(float x) { return sum_rows4(row16_sum(x)); }
 
-// One tile of one group of heads (or of a part of them) per workgroup; the sums over
-// the heads that share a key stay in registers.  Wave w has the tokens 16 w .. both as
-// queries (against those before) and as keys (against those behind): as many products
-// for each wave.
+// Weights W of the tile that stands between a wave's tokens and the 16 of tile j, applied to
+// products x (and y): in lane (g, l16) register r, token 16 j + 4 g + r against the lane's own.
+__device__ __forceinline__ f32x4 decays(const LaDecay& d, int j, int g, float hi, float lo, bool later) {
+    const f32x4 ohi = *reinterpret_cast<const f32x4*>(d.hi + 16 * j + 4 * g);
+    const f32x4 olo = *reinterpret_cast<const f32x4*>(d.lo + 16 * j + 4 * g);
+    f32x4 e;
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+        e[r] = exp2_raw(later ? (ohi[r] - hi) + (olo[r] - lo) : (hi - ohi[r]) + (lo - olo[r]));
+    return e;
+}
+
+struct Yes {
+    static constexpr bool value = true;
+};
+struct No {
+    static constexpr bool value = false;
+};
+
+// What a workgroup has before it: a tile of one group of heads (or of a part of them), and of
+// these one head and PB of its value rows.
+struct LaUnit {
+    int b, kh, part, n_in, n_out, step, steps;
+    int64_t c, at;    // the tile's number in its row; its first token among all
+    int64_t ckpt;     // the row's first checkpoint
+    bool valid;
+};
+
+// Tiles of 64 tokens stand alone, so a workgroup goes from one to the next (as many
+// workgroups as the device holds at once, in turn) with the next one's loads on their
+// way while it computes.  Waves 0 to 3 have the tokens 16 w .. as queries (dq, against the
+// keys before), waves 4 to 7 as keys (dk and dv, against the queries behind); on each SIMD
+// one of either, whose triangles make up a square.  The sums over the heads that share a
+// key stay in registers.
 template <typename T, int N, int PB>
-__global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, int blocks) {
+__global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, unsigned units, int blocks) {
     typedef LaMat<T> M;
     typedef LaStage<T, N> SK;
     typedef LaStage<T, PB> SV;
@@ -92,117 +122,264 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, i
     const LaArgs& p = o.f;
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int g = lane / 16, l16 = lane % 16;
-    unsigned i = blockIdx.x;
-    const int kh = (int)(i % p.G);
-    i /= p.G;
-    const int part = (int)(i % o.split);
-    i /= o.split;
-    const int b = (int)(i / blocks), c0 = (int)(i % blocks);
-    const LaRow row = la_row(p.rows, p.packed, p.tokens, p.T, b);
-    const int shared = p.H / p.G, per = (shared + o.split - 1) / o.split;
-    const int h_first = kh * shared + part * per;
-    const int heads = shared - part * per < per ? shared - part * per : per;
-    const int pblocks = p.P / PB, steps = heads * pblocks;
+    const int w = wave % 4;
+    const int shared = p.H / p.G, per = (shared + o.split - 1) / o.split, pblocks = p.P / PB;
     const int64_t krow = (int64_t)p.G * N, vrow = (int64_t)p.H * p.P;
     const T* const V = static_cast<const T*>(p.v);
     const T* const dY = static_cast<const T*>(o.dy);
     const T* const CK = static_cast<const T*>(p.ckpt);
     const T* const AD = static_cast<const T*>(o.adj);
-    // Every tile of the row whose number is c0 modulo `blocks` (more than one only where a
-    // packed row is longer than the call says).
-    for (int64_t c = c0; c * kLaChunk < row.stored; c += blocks) {
-        const int64_t t0 = c * kLaChunk, at = row.first + t0;
-        const int n_in = (int)(row.len - t0 < kLaChunk ? (row.len > t0 ? row.len - t0 : 0) : kLaChunk);
-        const int n_out = (int)(row.stored - t0 < kLaChunk ? row.stored - t0 : kLaChunk);
-        const int t = 16 * wave + l16;
-        const bool in = t < n_in;
-        f32x4 dq[NT], dk[NT];
+    const int t = 16 * w + l16;   // the lane's token
+    constexpr int kPer = 16 / (int)sizeof(T);
+    // Results of the wave's 16 tokens, rows of W, n of the tile's written.
+    const auto store_rows = [&](auto& x, T* to, int n, int64_t stride) {
+        constexpr int W = 16 * (int)(sizeof(x) / sizeof(f32x4));
+        const auto r = rows_of(to, n, stride, W);
+        const uint32_t bytes = (uint32_t)(stride * (int64_t)sizeof(T));
+        if constexpr (sizeof(T) == 2) {
+            LaRows16<T, W>::store(sm.own[wave], x, r, bytes, 16 * w);
+        } else {
 #pragma unroll
-        for (int n = 0; n < NT; ++n) dq[n] = dk[n] = zero4();
-        SV rv, ry;
-        LaStateStage<T, N, PB> rs, rd;
-        LaLog<T> lg;
-        auto load = [&](int step) {
-            const int h = h_first + step / pblocks, p0 = step % pblocks * PB;
-            const int64_t vat = at * vrow + (int64_t)h * p.P + p0;
-            rv.load(rows_of(V + vat, n_in, vrow, PB), (uint32_t)(vrow * sizeof(T)));
-            ry.load(rows_of(dY + vat, n_in, vrow, PB), (uint32_t)(vrow * sizeof(T)));
-            const size_t sat = (((size_t)(row.ckpt + c) * p.H + h) * p.P + p0) * N;
-            rs.load(CK + sat);
-            rd.load(AD + sat);
-            if (wave == 0) lg.load(p, at + lane, h, lane < n_in);
-        };
-        __syncthreads();   // the tile before has been read
-        if (n_in > 0) {
-            SK rq, rk;
-            const uint32_t kb = (uint32_t)(krow * sizeof(T));
-            rq.load(rows_of(static_cast<const T*>(p.q) + at * krow + kh * N, n_in, krow, N), kb);
-            rk.load(rows_of(static_cast<const T*>(p.k) + at * krow + kh * N, n_in, krow, N), kb);
-            load(0);
+            for (int e = 0; e < W / 16; ++e)
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, x[e]), r, t * bytes + (16 * e + 4 * g) * 4, 0, 0);
+        }
+    };
+    const auto head_of_step = [&](const LaUnit& u) { return u.kh * shared + u.part * per + u.step / pblocks; };
+    // A wave's whole way, by its role (so that the code that waits for loads knows how many
+    // stores were issued behind them).
+    auto run = [&](auto queries_) {
+    constexpr bool kQueries = decltype(queries_)::value;
+    unsigned id = blockIdx.x;
+    int64_t tile = -1;   // of unit `id`'s row, the last one taken
+    // The next unit with tokens.  A unit is every tile of a row whose number is c0 modulo
+    // `blocks` (more than one only where a packed row is longer than the call says); tiles of
+    // padding get their zeros here.
+    auto advance = [&]() {
+        LaUnit u;
+        u.valid = false;
+        for (; id < units; id += gridDim.x, tile = -1) {
+            unsigned i = id;
+            u.kh = (int)(i % p.G);
+            i /= p.G;
+            u.part = (int)(i % o.split);
+            i /= o.split;
+            u.b = (int)(i / blocks);
+            const int c0 = (int)(i % blocks);
+            const LaRow row = la_row(p.rows, p.packed, p.tokens, p.T, u.b);
+            tile = tile < 0 ? c0 : tile + blocks;
+            if (tile * kLaChunk >= row.stored) continue;
+            const int64_t t0 = tile * kLaChunk;
+            u.c = tile;
+            u.ckpt = row.ckpt;
+            u.at = row.first + t0;
+            u.n_in = (int)(row.len - t0 < kLaChunk ? (row.len > t0 ? row.len - t0 : 0) : kLaChunk);
+            u.n_out = (int)(row.stored - t0 < kLaChunk ? row.stored - t0 : kLaChunk);
+            u.step = 0;
+            const int heads = shared - u.part * per < per ? shared - u.part * per : per;
+            u.steps = heads * pblocks;
+            if (u.n_in > 0) {
+                u.valid = true;
+                break;
+            }
+            for (; u.step < u.steps; ++u.step) {
+                const int h = head_of_step(u), p0 = u.step % pblocks * PB;
+                T* const dvp = static_cast<T*>(o.dv) + u.at * vrow + (int64_t)h * p.P + p0;
+                for (int e = threadIdx.x; e < u.n_out * (PB / kPer); e += kLaThreads)
+                    *reinterpret_cast<vu4*>(dvp + e / (PB / kPer) * vrow + e % (PB / kPer) * kPer) = vu4{0, 0, 0, 0};
+                if (o.dg && p0 == 0 && (int)threadIdx.x < u.n_out)
+                    Elem<T>::store1(static_cast<T*>(o.dg) + (u.at + threadIdx.x) * p.H + h, 0.f);
+            }
+            const int64_t kat = u.at * krow + u.kh * N;
+            for (int e = threadIdx.x; e < u.n_out * N; e += kLaThreads) {
+                const int64_t k = kat + e / N * krow + e % N;
+                if (o.split > 1) {
+                    const int64_t parts = (p.packed ? p.tokens : (int64_t)p.B * p.T) * krow * u.part;
+                    o.part_q[parts + k] = o.part_k[parts + k] = 0.f;
+                } else {
+                    Elem<T>::store1(static_cast<T*>(o.dq) + k, 0.f);
+                    Elem<T>::store1(static_cast<T*>(o.dk) + k, 0.f);
+                }
+            }
+        }
+        return u;
+    };
+    SK rq, rk;
+    SV rv, ry;
+    LaStateStage<T, N, PB> rs, rd;
+    LaLog<T> lg;
+    auto load = [&](const LaUnit& u) {
+        const int h = head_of_step(u), p0 = u.step % pblocks * PB;
+        const int64_t vat = u.at * vrow + (int64_t)h * p.P + p0;
+        const int n = u.valid ? u.n_in : 0, n_qk = u.step == 0 ? n : 0;
+        const uint32_t kb = (uint32_t)(krow * sizeof(T));
+        rq.load(rows_of(static_cast<const T*>(p.q) + u.at * krow + u.kh * N, n_qk, krow, N), kb);
+        rk.load(rows_of(static_cast<const T*>(p.k) + u.at * krow + u.kh * N, n_qk, krow, N), kb);
+        if constexpr (kQueries) lg.load(p, u.at, h, n);
+        rv.load(rows_of(V + vat, n, vrow, PB), (uint32_t)(vrow * sizeof(T)));
+        ry.load(rows_of(dY + vat, n, vrow, PB), (uint32_t)(vrow * sizeof(T)));
+        const size_t sat = (((size_t)(u.ckpt + u.c) * p.H + h) * p.P + p0) * N;
+        rs.load(CK + sat, u.valid);
+        rd.load(AD + sat, u.valid);
+    };
+    // dg of a head once the sums over its tile are in LDS, by one wave.  Lane l: what counts
+    // for token 63 - l, from behind it; what counts for token l, from before it.  In 64 bits:
+    // the rows and columns of M cancel where both lie on one side.
+    auto finish_dg = [&](int64_t at, int n_in, int n_out, int h, float all) {
+        const int u = 63 - lane;
+        double x = (double)sm.a[u] - sm.col[u];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x += 16 * j <= u ? (double)sm.row[j][u] : 0.0;
+        x = wave_running_sum(x);
+        const double y = wave_running_sum(lane > 0 ? (double)sm.b[lane - 1] : 0.0);
+        double both = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) both += sm.c[j];
+        const float dg = (float)(x + __shfl(y, u) + all * both);
+        if (u < n_out) Elem<T>::store1(static_cast<T*>(o.dg) + (at + u) * p.H + h, u < n_in ? dg : 0.f);
+    };
+    LaUnit u = advance();
+    if (!u.valid) return;
+    load(u);
+    if (kQueries && wave == 0) put_decays(sm.d[0], lg.get());
+    int dbuf = 0, dg_h = -1, dg_in = 0, dg_out = 0;   // the head whose dg is still to be written
+    int64_t dg_at = 0;
+    float dg_all = 0.f;
+    f32x4 dqk[NT];   // dq of the lane's token, or dk
+    f32x4 rsum[4];   // M's rows 16 j + 4 g .., the lane's column
+    float asum = 0.f, bsum = 0.f, cdot = 0.f;
+    bool odd_qk = false;
+    while (u.valid) {
+        const int h = head_of_step(u), p0 = u.step % pblocks * PB;
+        const int64_t at = u.at;
+        const int n_in = u.n_in, n_out = u.n_out;
+        const bool in = t < n_in;
+        const bool head_first = p0 == 0, head_last = p0 + PB == p.P;
+        __syncthreads();   // the tiles before have been read
+        if (u.step == 0) {
             rq.store(sm.q);
             rk.store(sm.k);
-            const bool odd = __builtin_amdgcn_ballot_w64(rq.odd() || rk.odd()) != 0;
-            if (lane == 0) sm.odd_k[wave] = odd;
-        }
-        f32x4 rsum[4];   // M's rows 16 j + 4 g .., the lane's column
-        float asum = 0.f, bsum = 0.f, cdot = 0.f;
-        for (int step = 0; step < (n_in > 0 ? steps : 0); ++step) {
-            const int h = h_first + step / pblocks, p0 = step % pblocks * PB;
-            const bool head_first = step % pblocks == 0, head_last = step % pblocks == pblocks - 1;
-            if (step > 0) __syncthreads();
-            rv.store(sm.v);
-            ry.store(sm.dy);
-            rs.store(sm.s);
-            rd.store(sm.ds);
-            if (head_first) {
-                if (wave == 0) put_decays(sm.d, lg.x);
+            odd_qk = rq.odd() || rk.odd();
 #pragma unroll
-                for (int j = 0; j < 4; ++j) rsum[j] = zero4();
-                asum = bsum = cdot = 0.f;
-            }
-            cdot += rs.dot(rd);
-            const bool odd_v = __builtin_amdgcn_ballot_w64(rv.odd() || ry.odd()) != 0;
-            if (lane == 0) sm.d.odd[wave] = odd_v;
-            __syncthreads();
-            if (step + 1 < steps) load(step + 1);
-            const LaDecay& d = sm.d;
-            const int odd = __builtin_amdgcn_readfirstlane(d.odd[0] | d.odd[1] | d.odd[2] | d.odd[3] | sm.odd_k[0] |
-                                                           sm.odd_k[1] | sm.odd_k[2] | sm.odd_k[3]);
-            const float up = d.up[t] * p.scale, down = d.down[t];
+            for (int n = 0; n < NT; ++n) dqk[n] = zero4();
+        }
+        if (head_first) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) rsum[j] = zero4();
+            asum = bsum = cdot = 0.f;
+        }
+        rv.store(sm.v);
+        ry.store(sm.dy);
+        rs.store(sm.s);
+        rd.store(sm.ds);
+        cdot += rs.dot(rd);
+        const bool odd_lane = __builtin_amdgcn_ballot_w64(odd_qk || rv.odd() || ry.odd()) != 0;
+        if (lane == 0) sm.odd[wave] = odd_lane;
+        LaUnit next = u;
+        if (++next.step == next.steps) next = advance();
+        __syncthreads();
+        load(next);
+        if (kQueries && dg_h >= 0 && wave == 1) finish_dg(dg_at, dg_in, dg_out, dg_h, dg_all);
+        dg_h = -1;
+        {
+            const LaDecay& d = sm.d[dbuf];
+            const bool odd = any_odd(sm.odd);
             const float thi = d.hi[t], tlo = d.lo[t];
-            f32x4 dv[PT];
-            // ---- the states' parts
-            {
-                // dy_t and v_t along the states' columns (the contraction's second order)
-                Frag yc[PS], vc[PS];
+            if constexpr (kQueries) {
+                // ---- dq_t: the state's part
+                const float up = d.up[t] * p.scale;
+                Frag yf[PS];   // dy_t, along the states' columns (the contraction's second order)
 #pragma unroll
                 for (int j = 0; j < PS; ++j) {
                     const T* const y1 = sm.dy + t * SV::kStride + 32 * j + 4 * g;
-                    const T* const v1 = sm.v + t * SV::kStride + 32 * j + 4 * g;
-                    yc[j] = M::cat(M::four(y1), M::four(y1 + 16));
-                    vc[j] = M::cat(M::four(v1), M::four(v1 + 16));
+                    yf[j] = M::cat(M::four(y1), M::four(y1 + 16));
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    f32x4 x = zero4(), y = zero4();
+                    f32x4 x = zero4();
 #pragma unroll
-                    for (int j = 0; j < PS; ++j) {
-                        x = M::mma(columns<T>(sm.s + 32 * j * SK::kStride + 16 * n, SK::kStride, g, l16), yc[j], x);
-                        y = M::mma(columns<T>(sm.ds + 32 * j * SK::kStride + 16 * n, SK::kStride, g, l16), vc[j], y);
-                    }
+                    for (int j = 0; j < PS; ++j)
+                        x = M::mma(columns<T>(sm.s + 32 * j * SK::kStride + 16 * n, SK::kStride, g, l16), yf[j], x);
                     x *= up;
-                    y *= down;
                     const f32x4 qn = M::wide(M::four(sm.q + t * SK::kStride + 16 * n + 4 * g));
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) asum = fmaf(qn[r], x[r], asum);
+                    dqk[n] += x;
+                }
+                if (!odd) {
+                    // ---- and the tile's: [s][t], s up to t
+                    Frag wt[2];
+#pragma unroll
+                    for (int j = 0; j < PS; ++j) yf[j] = M::rows(sm.dy + t * SV::kStride + 32 * j + 8 * g);
+#pragma unroll
+                    for (int j2 = 0; j2 < 2; ++j2) {
+                        Half h2[2];
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const int j = 2 * j2 + u;
+                            f32x4 x = zero4();
+                            if (j <= w) {
+#pragma unroll
+                                for (int e = 0; e < PS; ++e)
+                                    x = M::mma(M::rows(sm.v + (16 * j + l16) * SV::kStride + 32 * e + 8 * g), yf[e], x);
+                                x *= decays(d, j, g, thi, tlo, false) * p.scale;
+                                if (j == w)   // the triangle's edge
+#pragma unroll
+                                    for (int r = 0; r < 4; ++r) x[r] = 4 * g + r <= l16 ? x[r] : 0.f;
+                            }
+                            // Rounded to the tokens' type, as the weights of the forward: half a step of
+                            // each, as large as the gradients' own rounding.
+                            h2[u] = M::half(x);
+                        }
+                        wt[j2] = M::cat(h2[0], h2[1]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        dqk[n] = M::mma(columns<T>(sm.k + 16 * n, SK::kStride, g, l16), wt[0], dqk[n]);
+                        if (w >= 2)
+                            dqk[n] = M::mma(columns<T>(sm.k + 32 * SK::kStride + 16 * n, SK::kStride, g, l16), wt[1], dqk[n]);
+                    }
+                } else {
+                    // An infinity or a NaN in the tile: pair by pair, each lane its token, so that it
+                    // meets no weight of 0 of a pair that does not exist.
+                    for (int s = 0; s < n_in; ++s) {
+                        float qk = 0.f, yv = 0.f;
+#pragma unroll 2
+                        for (int e = 0; e < N; ++e)
+                            qk = fmaf(Elem<T>::load1(sm.q + t * SK::kStride + e), Elem<T>::load1(sm.k + s * SK::kStride + e), qk);
+#pragma unroll 2
+                        for (int e = 0; e < PB; ++e)
+                            yv = fmaf(Elem<T>::load1(sm.dy + t * SV::kStride + e), Elem<T>::load1(sm.v + s * SV::kStride + e), yv);
+                        yv *= exp2_raw((thi - d.hi[s]) + (tlo - d.lo[s])) * p.scale;
+                        if (in && s <= t) {
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+                                dqk[n] += M::wide(M::four(sm.k + s * SK::kStride + 16 * n + 4 * g)) * yv;
+                            if (s < t && g == 0) asum = fmaf(qk, yv, asum);   // M's row
+                        }
+                    }
+                }
+            } else {
+                // ---- dk_s and dv_s: the parts of the state's gradient
+                const float down = d.down[t];
+                f32x4 dv[PT];
+                Frag vf[PS], kf[KS];
+#pragma unroll
+                for (int j = 0; j < PS; ++j) {
+                    const T* const v1 = sm.v + t * SV::kStride + 32 * j + 4 * g;
+                    vf[j] = M::cat(M::four(v1), M::four(v1 + 16));
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    f32x4 x = zero4();
+#pragma unroll
+                    for (int j = 0; j < PS; ++j)
+                        x = M::mma(columns<T>(sm.ds + 32 * j * SK::kStride + 16 * n, SK::kStride, g, l16), vf[j], x);
+                    x *= down;
                     const f32x4 kn = M::wide(M::four(sm.k + t * SK::kStride + 16 * n + 4 * g));
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        asum = fmaf(qn[r], x[r], asum);
-                        bsum = fmaf(kn[r], y[r], bsum);
-                    }
-                    dq[n] += x;
-                    dk[n] += y;
+                    for (int r = 0; r < 4; ++r) bsum = fmaf(kn[r], x[r], bsum);
+                    dqk[n] += x;
                 }
-                Frag kf[KS];
 #pragma unroll
                 for (int j = 0; j < KS; ++j) kf[j] = M::rows(sm.k + t * SK::kStride + 32 * j + 8 * g);
 #pragma unroll
@@ -213,52 +390,11 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, i
                         dv[m] = M::mma(M::rows(sm.ds + (16 * m + l16) * SK::kStride + 32 * j + 8 * g), kf[j], dv[m]);
                     dv[m] *= down;
                 }
-            }
-            if (!odd) {
-                // ---- the wave's tokens as queries: [s][t], s up to t
-                {
-                    Frag yf[PS], w[2];
-#pragma unroll
-                    for (int j = 0; j < PS; ++j) yf[j] = M::rows(sm.dy + t * SV::kStride + 32 * j + 8 * g);
-#pragma unroll
-                    for (int j2 = 0; j2 < 2; ++j2) {
-                        Half h2[2];
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int j = 2 * j2 + u;
-                            f32x4 x = zero4();
-                            if (j <= wave) {
-#pragma unroll
-                                for (int e = 0; e < PS; ++e)
-                                    x = M::mma(M::rows(sm.v + (16 * j + l16) * SV::kStride + 32 * e + 8 * g), yf[e], x);
-                                const f32x4 shi = *reinterpret_cast<const f32x4*>(d.hi + 16 * j + 4 * g);
-                                const f32x4 slo = *reinterpret_cast<const f32x4*>(d.lo + 16 * j + 4 * g);
-#pragma unroll
-                                for (int r = 0; r < 4; ++r) {
-                                    const float e = exp2_raw((thi - shi[r]) + (tlo - slo[r])) * p.scale;
-                                    x[r] = 16 * j + 4 * g + r <= t ? x[r] * e : 0.f;
-                                }
-                            }
-                            // Rounded to the tokens' type, as the weights of the forward: half a step of
-                            // each, as large as the gradients' own rounding.
-                            h2[u] = M::half(x);
-                        }
-                        w[j2] = M::cat(h2[0], h2[1]);
-                    }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        dq[n] = M::mma(columns<T>(sm.k + 16 * n, SK::kStride, g, l16), w[0], dq[n]);
-                        if (wave >= 2)
-                            dq[n] = M::mma(columns<T>(sm.k + 32 * SK::kStride + 16 * n, SK::kStride, g, l16), w[1], dq[n]);
-                    }
-                }
-                // ---- and as keys: [t][s], s the wave's, t from s on
-                {
-                    Frag vf[PS], kf[KS], wb[2], wa[2];
+                if (!odd) {
+                    // ---- and the tile's: [t][s], t from s on
+                    Frag wb[2], wa[2];
 #pragma unroll
                     for (int j = 0; j < PS; ++j) vf[j] = M::rows(sm.v + t * SV::kStride + 32 * j + 8 * g);
-#pragma unroll
-                    for (int j = 0; j < KS; ++j) kf[j] = M::rows(sm.k + t * SK::kStride + 32 * j + 8 * g);
 #pragma unroll
                     for (int j2 = 0; j2 < 2; ++j2) {
                         Half hb[2], ha[2];
@@ -266,25 +402,27 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, i
                         for (int u = 0; u < 2; ++u) {
                             const int j = 2 * j2 + u;
                             f32x4 x = zero4(), y = zero4();
-                            if (j >= wave) {
+                            if (j >= w) {
 #pragma unroll
                                 for (int e = 0; e < PS; ++e)
                                     x = M::mma(M::rows(sm.dy + (16 * j + l16) * SV::kStride + 32 * e + 8 * g), vf[e], x);
 #pragma unroll
                                 for (int e = 0; e < KS; ++e)
                                     y = M::mma(M::rows(sm.q + (16 * j + l16) * SK::kStride + 32 * e + 8 * g), kf[e], y);
-                                const f32x4 qhi = *reinterpret_cast<const f32x4*>(d.hi + 16 * j + 4 * g);
-                                const f32x4 qlo = *reinterpret_cast<const f32x4*>(d.lo + 16 * j + 4 * g);
+                                const f32x4 e = decays(d, j, g, thi, tlo, true) * p.scale;
+                                y *= e;
+                                f32x4 m = y * x;
+                                x *= e;
+                                if (j == w) {
 #pragma unroll
-                                for (int r = 0; r < 4; ++r) {
-                                    const int tt = 16 * j + 4 * g + r;
-                                    const float e = exp2_raw((qhi[r] - thi) + (qlo[r] - tlo)) * p.scale;
-                                    y[r] = tt >= t ? y[r] * e : 0.f;
-                                    const float m = tt > t ? y[r] * x[r] : 0.f;
-                                    x[r] = tt >= t ? x[r] * e : 0.f;
-                                    rsum[j][r] += m;
-                                    asum -= m;
+                                    for (int r = 0; r < 4; ++r) {
+                                        y[r] = 4 * g + r >= l16 ? y[r] : 0.f;
+                                        x[r] = 4 * g + r >= l16 ? x[r] : 0.f;
+                                        m[r] = 4 * g + r > l16 ? m[r] : 0.f;
+                                    }
                                 }
+                                rsum[j] += m;
+                                asum += (m[0] + m[1]) + (m[2] + m[3]);
                             }
                             hb[u] = M::half(x);
                             ha[u] = M::half(y);
@@ -294,135 +432,105 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, i
                     }
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        if (wave < 2) dk[n] = M::mma(columns<T>(sm.q + 16 * n, SK::kStride, g, l16), wb[0], dk[n]);
-                        dk[n] = M::mma(columns<T>(sm.q + 32 * SK::kStride + 16 * n, SK::kStride, g, l16), wb[1], dk[n]);
+                        if (w < 2) dqk[n] = M::mma(columns<T>(sm.q + 16 * n, SK::kStride, g, l16), wb[0], dqk[n]);
+                        dqk[n] = M::mma(columns<T>(sm.q + 32 * SK::kStride + 16 * n, SK::kStride, g, l16), wb[1], dqk[n]);
                     }
 #pragma unroll
                     for (int m = 0; m < PT; ++m) {
-                        if (wave < 2) dv[m] = M::mma(columns<T>(sm.dy + 16 * m, SV::kStride, g, l16), wa[0], dv[m]);
+                        if (w < 2) dv[m] = M::mma(columns<T>(sm.dy + 16 * m, SV::kStride, g, l16), wa[0], dv[m]);
                         dv[m] = M::mma(columns<T>(sm.dy + 32 * SV::kStride + 16 * m, SV::kStride, g, l16), wa[1], dv[m]);
                     }
-                }
-            } else {
-                // An infinity or a NaN in the tile: pair by pair, each lane its token, so that it
-                // meets no weight of 0 of a pair that does not exist.
-                for (int s = 0; s < n_in; ++s) {
-                    float qk = 0.f, yv = 0.f;   // of the later token's query and dy, the earlier's key and value
-                    const int late = s > t ? s : t, early = s > t ? t : s;
-                    for (int e = 0; e < N; ++e)
-                        qk = fmaf(Elem<T>::load1(sm.q + late * SK::kStride + e), Elem<T>::load1(sm.k + early * SK::kStride + e), qk);
-                    for (int e = 0; e < PB; ++e)
-                        yv = fmaf(Elem<T>::load1(sm.dy + late * SV::kStride + e), Elem<T>::load1(sm.v + early * SV::kStride + e), yv);
-                    const float e = exp2_raw((d.hi[late] - d.hi[early]) + (d.lo[late] - d.lo[early])) * p.scale;
-                    const float m = qk * e * yv;
-                    if (in && s <= t) {
+                } else {
+                    for (int s = 0; s < n_in; ++s) {   // the query's token
+                        float qk = 0.f, yv = 0.f;
+#pragma unroll 2
+                        for (int e = 0; e < N; ++e)
+                            qk = fmaf(Elem<T>::load1(sm.q + s * SK::kStride + e), Elem<T>::load1(sm.k + t * SK::kStride + e), qk);
+#pragma unroll 2
+                        for (int e = 0; e < PB; ++e)
+                            yv = fmaf(Elem<T>::load1(sm.dy + s * SV::kStride + e), Elem<T>::load1(sm.v + t * SV::kStride + e), yv);
+                        const float e = exp2_raw((d.hi[s] - thi) + (d.lo[s] - tlo)) * p.scale;
+                        if (in && s >= t) {
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            dq[n] += M::wide(M::four(sm.k + s * SK::kStride + 16 * n + 4 * g)) * (yv * e);
-                        if (s < t && g == 0) asum += m;
-                    }
-                    if (in && s >= t) {
+                            for (int n = 0; n < NT; ++n)
+                                dqk[n] += M::wide(M::four(sm.q + s * SK::kStride + 16 * n + 4 * g)) * (yv * e);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            dk[n] += M::wide(M::four(sm.q + s * SK::kStride + 16 * n + 4 * g)) * (yv * e);
-#pragma unroll
-                        for (int n = 0; n < PT; ++n)
-                            dv[n] += M::wide(M::four(sm.dy + s * SV::kStride + 16 * n + 4 * g)) * (qk * e);
-                        if (s > t && g == 0) asum -= m;
+                            for (int m = 0; m < PT; ++m)
+                                dv[m] += M::wide(M::four(sm.dy + s * SV::kStride + 16 * m + 4 * g)) * (qk * e);
+                            if (s > t && g == 0) asum = fmaf(qk, yv * e, asum);
+                        }
                     }
                 }
-            }
-            // ---- dv, and with the head's last block dg
-            const auto vb = rows_of(static_cast<T*>(o.dv) + at * vrow + (int64_t)h * p.P + p0, n_out, vrow, PB);
 #pragma unroll
-            for (int m = 0; m < PT; ++m) {
-                const uint32_t off = t * (uint32_t)(vrow * sizeof(T)) + (16 * m + 4 * g) * (uint32_t)sizeof(T);
-                f32x4 x = dv[m];
+                for (int m = 0; m < PT; ++m)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) x[r] = in ? x[r] : 0.f;
-                if constexpr (sizeof(T) == 2)
-                    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(vu2, cvt4(x)), vb, off, 0, 0);
-                else
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, x), vb, off, 0, 0);
+                    for (int r = 0; r < 4; ++r) dv[m][r] = in ? dv[m][r] : 0.f;
+                store_rows(dv, static_cast<T*>(o.dv) + at * vrow + (int64_t)h * p.P + p0, n_out, vrow);
             }
             if (o.dg && head_last) {
-                const float a = sum_rows4(in ? asum : 0.f), bs = sum_rows4(in ? bsum : 0.f), cs = wave_sum(cdot);
-                if (g == 0) {
-                    sm.a[t] = a;
-                    sm.b[t] = bs;
-                }
+                // (what finish_dg reads of the head before)
+                __syncthreads();
+                const float a = sum_rows4(in ? asum : 0.f), cs = wave_sum(cdot);
                 if (lane == 0) sm.c[wave] = cs;
+                if constexpr (kQueries) {
+                    if (g == 0) sm.a[t] = a;
+                } else {
+                    const float bs = sum_rows4(in ? bsum : 0.f);
+                    if (g == 0) {
+                        sm.col[t] = a;
+                        sm.b[t] = bs;
+                    }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (j >= wave) {
-                        f32x4 x;
+                    for (int j = 0; j < 4; ++j) {
+                        if (j >= w) {
+                            f32x4 x;
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) x[r] = row16_sum(rsum[j][r]);
-                        if (l16 == 0) *reinterpret_cast<f32x4*>(sm.row[wave] + 16 * j + 4 * g) = x;
+                            for (int r = 0; r < 4; ++r) x[r] = row16_sum(rsum[j][r]);
+                            if (l16 == 0) *reinterpret_cast<f32x4*>(sm.row[w] + 16 * j + 4 * g) = x;
+                        }
                     }
                 }
-                __syncthreads();
-                if (wave == 0) {
-                    // Lane l: what counts for token 63 - l, from behind it; what counts for token l, from
-                    // before it.  In 64 bits: the rows and columns of M cancel where both lie on one side.
-                    const int u = 63 - lane;
-                    double x = sm.a[u];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) x += 16 * j <= u ? (double)sm.row[j][u] : 0.0;
-                    x = wave_running_sum(x);
-                    const double y = wave_running_sum(lane > 0 ? (double)sm.b[lane - 1] : 0.0);
-                    const double all = (double)d.all * (((double)sm.c[0] + sm.c[1]) + ((double)sm.c[2] + sm.c[3]));
-                    const float dg = (float)(x + __shfl(y, u) + all);
-                    if (u < n_out) Elem<T>::store1(static_cast<T*>(o.dg) + (at + u) * p.H + h, u < n_in ? dg : 0.f);
-                }
+                dg_h = h;
+                dg_at = at;
+                dg_in = n_in;
+                dg_out = n_out;
+                dg_all = d.all;
             }
         }
-        if (n_in == 0) {
-            // a padded tile: nothing but zeros
-            for (int step = 0; step < steps; ++step) {
-                const int h = h_first + step / pblocks, p0 = step % pblocks * PB;
-                T* const dvp = static_cast<T*>(o.dv) + at * vrow + (int64_t)h * p.P + p0;
-                constexpr int kPer = 16 / (int)sizeof(T);
-                for (int e = threadIdx.x; e < n_out * (PB / kPer); e += kLaThreads)
-                    *reinterpret_cast<vu4*>(dvp + e / (PB / kPer) * vrow + e % (PB / kPer) * kPer) = vu4{0, 0, 0, 0};
-                if (o.dg && p0 == 0 && (int)threadIdx.x < n_out)
-                    Elem<T>::store1(static_cast<T*>(o.dg) + (at + threadIdx.x) * p.H + h, 0.f);
+        // ---- dq or dk, or this part's sums of them, behind the last step (before: no rows)
+        {
+            const int n = u.step + 1 == u.steps ? n_out : 0;
+            const int64_t kat = at * krow + u.kh * N;
+            f32x4 x[NT];
+#pragma unroll
+            for (int e = 0; e < NT; ++e)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) x[e][r] = in ? dqk[e][r] : 0.f;
+            if (o.split > 1) {
+                const int64_t parts = (p.packed ? p.tokens : (int64_t)p.B * p.T) * krow * u.part;
+                const auto to = rows_of((kQueries ? o.part_q : o.part_k) + parts + kat, n, krow, N);
+#pragma unroll
+                for (int e = 0; e < NT; ++e)
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, x[e]), to,
+                                                           t * (uint32_t)(krow * 4) + (16 * e + 4 * g) * 4, 0, 0);
+            } else {
+                store_rows(x, static_cast<T*>(kQueries ? o.dq : o.dk) + kat, n, krow);
             }
         }
-        // ---- dq and dk, or this part's sums of them
-        const int64_t kat = at * krow + kh * N;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                dq[n][r] = in ? dq[n][r] : 0.f;
-                dk[n][r] = in ? dk[n][r] : 0.f;
-            }
+        // The next head's decays, where the other waves still compute.
+        if (next.valid && next.step % pblocks == 0) {
+            dbuf ^= 1;
+            if (kQueries && wave == 0) put_decays(sm.d[dbuf], lg.get());
         }
-        if (o.split > 1) {
-            const int64_t parts = (p.packed ? p.tokens : (int64_t)p.B * p.T) * krow * part;
-            const auto qb = rows_of(o.part_q + parts + kat, n_out, krow, N), kb = rows_of(o.part_k + parts + kat, n_out, krow, N);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const uint32_t off = t * (uint32_t)(krow * 4) + (16 * n + 4 * g) * 4;
-                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, dq[n]), qb, off, 0, 0);
-                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, dk[n]), kb, off, 0, 0);
-            }
-        } else {
-            const auto qb = rows_of(static_cast<T*>(o.dq) + kat, n_out, krow, N), kb = rows_of(static_cast<T*>(o.dk) + kat, n_out, krow, N);
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const uint32_t off = t * (uint32_t)(krow * sizeof(T)) + (16 * n + 4 * g) * (uint32_t)sizeof(T);
-                if constexpr (sizeof(T) == 2) {
-                    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(vu2, cvt4(dq[n])), qb, off, 0, 0);
-                    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(vu2, cvt4(dk[n])), kb, off, 0, 0);
-                } else {
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, dq[n]), qb, off, 0, 0);
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, dk[n]), kb, off, 0, 0);
-                }
-            }
-        }
+        u = next;
     }
+    if (dg_h >= 0) {
+        __syncthreads();
+        if (kQueries && wave == 1) finish_dg(dg_at, dg_in, dg_out, dg_h, dg_all);
+    }
+    };
+    if (wave < 4) run(Yes());
+    else run(No());
 }
 
 // dq and dk: the sums over the parts of a group's heads, in order.  Four values a thread;
@@ -455,7 +563,10 @@ hipError_t bwd_block(const LaBwdArgs& q, hipStream_t stream) {
     hipError_t e = launch_la_adjoint(q, stream);
     if (e != hipSuccess) return e;
     const int blocks = p.T > 0 ? (int)(((int64_t)p.T + kLaChunk - 1) / kLaChunk) : 1;
-    la_bwd_kernel<T, N, PB><<<(unsigned)p.B * blocks * p.G * q.split, kLaThreads, 0, stream>>>(q, blocks);
+    const unsigned units = (unsigned)p.B * blocks * p.G * q.split;
+    // As many workgroups as run at once: two to a compute unit where LDS holds them.
+    const unsigned most = sizeof(LaBwdShared<T, N, PB>) <= 80 * 1024 ? 512 : 256;
+    la_bwd_kernel<T, N, PB><<<units < most ? units : most, kLaThreads, 0, stream>>>(q, units, blocks);
     if ((e = hipGetLastError()) != hipSuccess || q.split == 1) return e;
     const int64_t values = (p.packed ? p.tokens : (int64_t)p.B * p.T) * p.G * N;
     const unsigned half = (unsigned)((values / 4 + 255) / 256);

@@ -1,7 +1,8 @@
 // wkv7_linattn_device.h -- tiles, operands and decays of the linear attention
 // kernels.
 //
-// A tile is 64 tokens of one head; a workgroup is four waves.  Products go
+// A tile is 64 tokens of one head; a workgroup is eight waves, two per SIMD, so that
+// one computes while the other waits for its operands.  Products go
 // through the matrix cores in 16 x 16 results, 32 deep: for bf16 tokens one
 // 16x16x32 instruction, for fp32 tokens eight 16x16x4 ones.  Which 32 values of
 // the contraction a lane's eight operand elements stand for is the same for
@@ -18,7 +19,7 @@
 
 namespace wkv7 {
 
-constexpr int kLaThreads = 256;
+constexpr int kLaThreads = 512;
 
 template <typename T> struct LaMat;
 
@@ -88,7 +89,8 @@ __device__ __forceinline__ typename LaMat<T>::Frag columns(const T* tile, int st
 
 // A 32-bit operand as kParts operands in the tokens' type that sum to it: three
 // bf16 terms hold 24 bits, so that states (fp32) lose nothing to the matrix
-// cores' input type.  A value that is not finite stands alone in the first.
+// cores' input type.  The first two are cut off, not rounded: the cut value is its
+// own fp32 image, so that the rest is one subtraction away.  Finite values only.
 template <typename T>
 __device__ __forceinline__ void split_parts(const f32x4& lo, const f32x4& hi, typename LaMat<T>::Frag (&f)[LaMat<T>::kParts]) {
     typedef LaMat<T> M;
@@ -97,17 +99,54 @@ __device__ __forceinline__ void split_parts(const f32x4& lo, const f32x4& hi, ty
     } else {
         f32x4 x[2] = {lo, hi};
 #pragma unroll
-        for (int i = 0; i < M::kParts; ++i) {
-            const typename M::Half a = M::half(x[0]), b = M::half(x[1]);
-            f[i] = M::cat(a, b);
-            if (i + 1 < M::kParts) {
-                const f32x4 wa = M::wide(a), wb = M::wide(b);
+        for (int i = 0; i < 2; ++i) {
+            vu4 w;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    x[0][j] = fabsf(wa[j]) < INFINITY ? x[0][j] - wa[j] : 0.f;
-                    x[1][j] = fabsf(wb[j]) < INFINITY ? x[1][j] - wb[j] : 0.f;
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t a = __float_as_uint(x[h][2 * j]), b = __float_as_uint(x[h][2 * j + 1]);
+                    w[2 * h + j] = __builtin_amdgcn_perm(b, a, 0x07060302u);   // the upper halves
+                    x[h][2 * j] -= __uint_as_float(a & 0xffff0000u);
+                    x[h][2 * j + 1] -= __uint_as_float(b & 0xffff0000u);
                 }
+            f[i] = __builtin_bit_cast(typename M::Frag, w);
+        }
+        f[2] = M::cat(M::half(x[0]), M::half(x[1]));
+    }
+}
+
+// State columns [n][p] of 16 value rows, moved on over a tile: decayed by `all`, and each
+// token's value, times its factor and `scale`, with its key.
+template <typename T, int NT>
+__device__ __forceinline__ void move_state(f32x4 (&st)[NT], const T* k, int kstride, const T* v, int vstride,
+                                           const float* factor, float scale, float all, bool odd, int g, int l16) {
+    typedef LaMat<T> M;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) st[n] *= all;
+    if (!odd) {
+#pragma unroll
+        for (int t = 0; t < kLaChunk; t += 32) {
+            f32x4 x[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                x[u] = M::wide(M::column(v + (t + 16 * u) * vstride, vstride, g, l16));
+                x[u] *= *reinterpret_cast<const f32x4*>(factor + t + 16 * u + 4 * g) * scale;
             }
+            typename M::Frag f[M::kParts];
+            split_parts<T>(x[0], x[1], f);
+#pragma unroll
+            for (int i = M::kParts - 1; i >= 0; --i)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    st[n] = M::mma(columns<T>(k + t * kstride + 16 * n, kstride, g, l16), f[i], st[n]);
+        }
+    } else {
+        // Infinities and NaN: without the parts, which would meet them as zeros.
+        for (int t = 0; t < kLaChunk; ++t) {
+            const float x = Elem<T>::load1(v + t * vstride + l16) * (factor[t] * scale);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) st[n] += M::wide(M::four(k + t * kstride + 16 * n + 4 * g)) * x;
         }
     }
 }
@@ -148,11 +187,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const T* p, int n, int
 }
 
 // A tile of up to 64 rows on its way from memory to LDS: 16 bytes per lane and load.
-template <typename T, int W>
+template <typename T, int W, int kThreads = kLaThreads>
 struct LaStage {
     static constexpr int kPieces = W * (int)sizeof(T) / 16;          // per row
-    static constexpr int kRowsPer = kLaThreads / kPieces;            // rows of one load of the workgroup
-    static constexpr int kLoads = kLaChunk / kRowsPer;
+    static constexpr int kRowsPer = kThreads / kPieces;            // rows of one load of the workgroup
+    static constexpr int kLoads = kLaChunk > kRowsPer ? kLaChunk / kRowsPer : 1;
+    static constexpr bool kAll = kRowsPer <= kLaChunk;               // else the last threads have no piece
     static constexpr int kStride = W + 16 / (int)sizeof(T);          // elements of an LDS row: 16 bytes apart in the banks
     vu4 w[kLoads];
 
@@ -164,8 +204,9 @@ struct LaStage {
     }
     __device__ __forceinline__ void store(T* lds) const {
         T* const p = lds + threadIdx.x / kPieces * kStride + threadIdx.x % kPieces * (16 / (int)sizeof(T));
+        if (kAll || threadIdx.x < kLaChunk * kPieces)
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) *reinterpret_cast<vu4*>(p + i * kRowsPer * kStride) = w[i];
+            for (int i = 0; i < kLoads; ++i) *reinterpret_cast<vu4*>(p + i * kRowsPer * kStride) = w[i];
     }
     // Whether any of the lane's values is infinite or NaN.
     __device__ __forceinline__ bool odd() const {
@@ -201,7 +242,7 @@ struct LaDecay {
     float up[kLaChunk];     // 2^(G_t): from the tile's start to behind token t
     float down[kLaChunk];   // 2^(G_end - G_t): from behind token t to the tile's end
     float all;              // 2^(G_end)
-    int odd[4];             // waves that found values that are not finite
+    int odd[8];             // waves that found values that are not finite
     double sum;             // G_end
 };
 
@@ -224,15 +265,84 @@ __device__ __forceinline__ double wave_running_sum(double x) {
     return x;
 }
 
-// What lane t of a wave reads of token t's log decay.
+template <int kWaves = 8>
+__device__ __forceinline__ bool any_odd(const int (&odd)[8]) {
+    int x = odd[0];
+#pragma unroll
+    for (int i = 1; i < kWaves; ++i) x |= odd[i];
+    return __builtin_amdgcn_readfirstlane(x) != 0;
+}
+
+// What lane t of a wave reads of token t's log decay; 0 behind the tile's n tokens.
 template <typename T>
 struct LaLog {
-    float x;
-    __device__ __forceinline__ void load(const LaArgs& p, int64_t token, int h, bool in) {
-        x = 0.f;
-        if (in) {
-            if (p.fixed) x = static_cast<const float*>(p.g)[h];
-            else x = Elem<T>::load1(static_cast<const T*>(p.g) + token * p.H + h);
+    uint32_t w;
+    bool fixed;
+    __device__ __forceinline__ void load(const LaArgs& p, int64_t token, int h, int n) {
+        const uint32_t t = threadIdx.x % 64;
+        fixed = p.fixed;
+        if (p.fixed) {
+            const auto r = buffer_of(static_cast<const float*>(p.g) + h, n > 0 ? 4 : 0);
+            w = __builtin_amdgcn_raw_buffer_load_b32(r, (int)t < n ? 0 : kNowhere, 0, 0);
+        } else {
+            const auto r = rows_of(static_cast<const T*>(p.g) + token * p.H + h, n, p.H, 1);
+            const uint32_t at = t * (uint32_t)(p.H * (int)sizeof(T));
+            if constexpr (sizeof(T) == 2) w = __builtin_amdgcn_raw_buffer_load_b16(r, at, 0, 0);
+            else w = __builtin_amdgcn_raw_buffer_load_b32(r, at, 0, 0);
+        }
+    }
+    __device__ __forceinline__ float get() const {
+        return sizeof(T) == 4 || fixed ? __uint_as_float(w) : bf16_lo(w);
+    }
+};
+
+// ---- a wave's 16 rows between memory and operands ---------------------------------
+// Sixteen rows of W elements pass through LDS that only this wave touches, so that
+// memory sees whole rows, 16 bytes a lane.
+template <typename T, int W>
+struct LaRows16 {
+    static constexpr int kPieces = W * (int)sizeof(T) / 16, kEach = 16 * kPieces / 64;
+    static constexpr int kStride = W + 16 / (int)sizeof(T);
+    static constexpr int kSize = 16 * kStride;   // elements of LDS
+    vu4 w[kEach];
+
+    // What the wave's lanes wrote is there for its lanes to read, and the reverse.
+    static __device__ __forceinline__ void settle() {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    }
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t row_bytes, int row0) {
+        const int lane = threadIdx.x % 64;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int at = i * 64 + lane;
+            w[i] = __builtin_bit_cast(vu4, __builtin_amdgcn_raw_buffer_load_b128(
+                r, (row0 + at / kPieces) * row_bytes + at % kPieces * 16, 0, 0));
+        }
+    }
+    __device__ __forceinline__ void put(T* lds) const {
+        const int lane = threadIdx.x % 64;
+        settle();
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int at = i * 64 + lane;
+            *reinterpret_cast<vu4*>(lds + at / kPieces * kStride + at % kPieces * (16 / (int)sizeof(T))) = w[i];
+        }
+        settle();
+    }
+    // Results [w][row] (row l16, columns 16 i + 4 g ..) of the rows row0 .. to memory.
+    static __device__ __forceinline__ void store(T* lds, const f32x4 (&x)[W / 16], __amdgpu_buffer_rsrc_t r,
+                                                 uint32_t row_bytes, int row0) {
+        const int lane = threadIdx.x % 64, g = lane / 16, l16 = lane % 16;
+        settle();
+#pragma unroll
+        for (int i = 0; i < W / 16; ++i) LaMat<T>::put(lds + l16 * kStride + 16 * i + 4 * g, x[i]);
+        settle();
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            const int at = i * 64 + lane;
+            const vu4 v = *reinterpret_cast<const vu4*>(lds + at / kPieces * kStride + at % kPieces * (16 / (int)sizeof(T)));
+            __builtin_amdgcn_raw_buffer_store_b128(v, r, (row0 + at / kPieces) * row_bytes + at % kPieces * 16, 0, 0);
         }
     }
 };
