@@ -2,12 +2,13 @@
 // gate, forward (formulas and layout in wkv7_gnorm_device.h).
 
 #include "wkv7_gnorm_device.h"
+#include "wkv7_gnorm_dispatch.h"
 
 namespace wkv7 {
 
 namespace {
 
-template <typename T, int V, int P, int K>
+template <typename T, int V, int P, int K, int kGate, bool kSilu>
 __global__ __launch_bounds__(512) void gn_fwd_kernel(const GnArgs p) {
     __shared__ float s_sum[8];
     const GnPlace<P> at(p);
@@ -24,14 +25,14 @@ __global__ __launch_bounds__(512) void gn_fwd_kernel(const GnArgs p) {
         for (int k = 0; k < K; ++k) {
             const int c = (k * P + at.lane) * V;
             x[k].load(static_cast<const T*>(p.x) + base + c, live && c < p.W);
-            z[k].load(static_cast<const T*>(p.z) + base + c, p.gate != 0 && live && c < p.W);
+            z[k].load(static_cast<const T*>(p.z) + base + c, kGate != 0 && live && c < p.W);
         }
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 u[k][i] = x[k].get(i);
-                if (p.gate == 2) u[k][i] *= silu(z[k].get(i));
+                if constexpr (kGate == 2) u[k][i] *= silu(z[k].get(i));
                 sum += u[k][i];
             }
         const float mean = p.center ? gn_sum<P>(sum, s_sum) * inv : 0.f;
@@ -55,8 +56,8 @@ __global__ __launch_bounds__(512) void gn_fwd_kernel(const GnArgs p) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 y[i] = fmaf(u[k][i] * rstd, g[i], b[i]);
-                if (p.silu) y[i] = silu(y[i]);
-                if (p.gate == 1) y[i] *= silu(z[k].get(i));
+                if constexpr (kSilu) y[i] = silu(y[i]);
+                if constexpr (kGate == 1) y[i] *= silu(z[k].get(i));
             }
             store_piece<V>(static_cast<T*>(p.y) + base, c, p.W, y);
         }
@@ -64,7 +65,7 @@ __global__ __launch_bounds__(512) void gn_fwd_kernel(const GnArgs p) {
 }
 
 // Groups too wide for registers: a workgroup reads one again for each of its sums.
-template <typename T, int V>
+template <typename T, int V, int kGate, bool kSilu>
 __global__ __launch_bounds__(256) void gn_fwd_wide_kernel(const GnArgs p) {
     constexpr int P = 256;
     __shared__ float s_sum[8];
@@ -77,9 +78,9 @@ __global__ __launch_bounds__(256) void gn_fwd_wide_kernel(const GnArgs p) {
         auto value = [&](int c, float (&u)[V], GnPiece<T, V>& z) {
             GnPiece<T, V> x;
             x.load(X + c, true);
-            z.load(Z + c, p.gate != 0);
+            z.load(Z + c, kGate != 0);
 #pragma unroll
-            for (int i = 0; i < V; ++i) u[i] = p.gate == 2 ? x.get(i) * silu(z.get(i)) : x.get(i);
+            for (int i = 0; i < V; ++i) u[i] = kGate == 2 ? x.get(i) * silu(z.get(i)) : x.get(i);
         };
         float u[V], sum = 0.f;
         GnPiece<T, V> z;
@@ -104,26 +105,35 @@ __global__ __launch_bounds__(256) void gn_fwd_wide_kernel(const GnArgs p) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 y[i] = fmaf((u[i] - mean) * rstd, g[i], b[i]);
-                if (p.silu) y[i] = silu(y[i]);
-                if (p.gate == 1) y[i] *= silu(z.get(i));
+                if constexpr (kSilu) y[i] = silu(y[i]);
+                if constexpr (kGate == 1) y[i] *= silu(z.get(i));
             }
             store_piece<V>(static_cast<T*>(p.y) + base, c, p.W, y);
         }
     }
 }
 
-template <typename T, int V, int P, int K>
+template <typename T, int V, int P, int K, int kGate, bool kSilu>
 hipError_t run(const GnArgs& p, hipStream_t stream) {
     const unsigned grid = p.plan.blocks * p.plan.parts;
-    if constexpr (K == 0) gn_fwd_wide_kernel<T, V><<<grid, 256, 0, stream>>>(p);
-    else gn_fwd_kernel<T, V, P, K><<<grid, p.plan.threads, 0, stream>>>(p);
+    if constexpr (K == 0) gn_fwd_wide_kernel<T, V, kGate, kSilu><<<grid, 256, 0, stream>>>(p);
+    else gn_fwd_kernel<T, V, P, K, kGate, kSilu><<<grid, p.plan.threads, 0, stream>>>(p);
     return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_gnorm_forward(const GnArgs& p, hipStream_t stream) {
-#include "wkv7_gnorm_dispatch.h"
+    if (p.bf16) {
+        WKV7_GN_BF16
+    } else {
+        WKV7_GN_F32
+    }
+    return hipErrorInvalidValue;
+}
+
+hipError_t launch_gnorm_backward(const GnArgs& p, hipStream_t stream) {
+    return p.bf16 ? launch_gnorm_backward_bf16(p, stream) : launch_gnorm_backward_f32(p, stream);
 }
 
 }  // namespace wkv7

@@ -30,8 +30,10 @@ int check(const wkv7_gnorm_desc* d) {
 // Channels per access: 16 bytes where a group is made of them, for bf16 also pairs.
 // Lanes: as few (4 to 64) as hold a group in one piece each, then 64 to 512 with two
 // (four took more registers than there are in the backward).  As many groups side by side as 512 threads hold, of
-// several rows if a row has fewer; about 2048 workgroups, each going over as many rows as
-// that leaves, so that the sums for gamma and beta leave few partial rows.
+// several rows if a row has fewer.  Forward about 8192 workgroups; backward 512, each going
+// over as many rows as that leaves: each leaves a partial row of the sums for gamma and
+// beta (2048, a partial row for each row side by side: 318 us where 512 take @@, (16384, 2048)
+// in bf16).
 wkv7::GnPlan plan(const wkv7_gnorm_desc* d, bool backward) {
     wkv7::GnPlan p;
     const int W = d->D / d->G, widest = d->dtype == WKV7_BF16 ? 8 : 4;
@@ -51,9 +53,8 @@ wkv7::GnPlan plan(const wkv7_gnorm_desc* d, bool backward) {
     // a few rows: no more side by side than there are
     if (p.rows > d->rows) p.rows = d->rows > 0 ? (int)d->rows : 1;
     p.threads = (p.groups * p.rows * p.lanes + 63) / 64 * 64;
-    int64_t parts = (2048 + p.blocks - 1) / p.blocks;
+    int64_t parts = ((backward ? 512 : 8192) + p.blocks - 1) / p.blocks;
     const int64_t most = (d->rows + p.rows - 1) / p.rows;
-    if (!backward) parts *= 4;
     if (parts > most) parts = most;
     p.parts = (unsigned)(parts < 1 ? 1 : parts);
     return p;
@@ -98,7 +99,7 @@ int wkv7_gnorm_forward(const wkv7_gnorm_desc* desc, const float* gamma, const fl
 size_t wkv7_gnorm_backward_workspace_bytes(const wkv7_gnorm_desc* desc) {
     if (check(desc) != WKV7_OK || desc->rows == 0 || desc->D == 0) return 0;
     const wkv7::GnPlan p = plan(desc, true);
-    return (size_t)p.parts * p.rows * 2 * desc->D * sizeof(float);
+    return (size_t)p.parts * 2 * desc->D * sizeof(float);
 }
 
 int wkv7_gnorm_backward(const wkv7_gnorm_desc* desc, const float* gamma, const float* beta, const void* x,

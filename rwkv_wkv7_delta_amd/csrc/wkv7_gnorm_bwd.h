@@ -1,5 +1,5 @@
-// wkv7_gnorm_bwd.hip -- gradients of the group norm (formulas and layout in
-// wkv7_gnorm_device.h).
+// wkv7_gnorm_bwd.h -- gradients of the group norm (formulas and layout in
+// wkv7_gnorm_device.h), for the translation unit of each token type.
 //
 // With e the gradient of o (dy through the gate and the activation):
 //   dgamma = sum e n,  dbeta = sum e (over the rows)
@@ -9,38 +9,42 @@
 // The moments are formed again from x: a second tensor of them would cost more bytes
 // than the sums do time.
 
+#pragma once
+
 #include "wkv7_gnorm_device.h"
+#include "wkv7_gnorm_dispatch.h"
 
 namespace wkv7 {
 
 namespace {
 
 // What one channel needs once n is known: e, and its product with gamma.
+// (q: sigmoid(z)).
+template <int kGate, bool kSilu>
 struct GnBack {
     float e, dgate;
-    __device__ __forceinline__ GnBack(const GnArgs& p, float n, float gamma, float beta, float z, float dy) {
+    __device__ __forceinline__ GnBack(float n, float gamma, float beta, float z, float q, float dy) {
         e = dy;
         dgate = 0.f;
-        if (p.gate == 1 || p.silu) {
+        if constexpr (kGate == 1 || kSilu) {
             const float o = fmaf(n, gamma, beta);
-            const float q = p.silu ? sigmoid(o) : 1.f;
-            if (p.gate == 1) {
-                dgate = dy * (o * q);
-                e *= silu(z);
+            const float a = kSilu ? sigmoid(o) : 1.f;
+            if constexpr (kGate == 1) {
+                dgate = dy * (o * a);
+                e *= z * q;
             }
-            if (p.silu) e *= q * fmaf(o, 1.f - q, 1.f);
+            if constexpr (kSilu) e *= a * fmaf(o, 1.f - a, 1.f);
         }
     }
 };
-// The gradient of z from that of z sigmoid(z).
-__device__ __forceinline__ float gn_dz(float dgate, float z) {
-    const float q = sigmoid(z);
-    return dgate * q * fmaf(z, 1.f - q, 1.f);
-}
+// The gradient of z from that of z sigmoid(z), q = sigmoid(z).
+__device__ __forceinline__ float gn_dz(float dgate, float z, float q) { return dgate * q * fmaf(z, 1.f - q, 1.f); }
 
-template <typename T, int V, int P, int K>
+template <typename T, int V, int P, int K, int kGate, bool kSilu>
 __global__ __launch_bounds__(512) void gn_bwd_kernel(const GnArgs p) {
+    constexpr int kBatch = 8;   // sums of a lane that meet in LDS at a time
     __shared__ float s_sum[8];
+    __shared__ float s_part[kBatch][512];
     const GnPlace<P> at(p);
     const float inv = 1.f / p.W;
     const int64_t stride = (int64_t)p.plan.parts * p.plan.rows;
@@ -50,25 +54,41 @@ __global__ __launch_bounds__(512) void gn_bwd_kernel(const GnArgs p) {
     for (int k = 0; k < K; ++k)
 #pragma unroll
         for (int i = 0; i < V; ++i) dg[k][i] = db[k][i] = 0.f;
+    // The next row is on its way while one is worked on.
+    GnPiece<T, V> x1[K], z1[K], y1[K];
+    auto load = [&](int64_t l) {
+        const int64_t row = l * stride + at.side;
+        const bool live = at.live && row < p.rows;
+        const int64_t base = (live ? row : 0) * p.D + (int64_t)at.group * p.W;
+#pragma unroll
+        for (int k = 0; k < K; ++k) {
+            const int c = (k * P + at.lane) * V;
+            x1[k].load(static_cast<const T*>(p.x) + base + c, live && c < p.W);
+            if constexpr (kGate != 0) z1[k].load(static_cast<const T*>(p.z) + base + c, live && c < p.W);
+            y1[k].load(static_cast<const T*>(p.dy) + base + c, live && c < p.W);
+        }
+    };
+    load(0);
     for (int64_t l = 0; l < loops; ++l) {
         const int64_t row = l * stride + at.side;
         const bool live = at.live && row < p.rows;
         const int64_t base = (live ? row : 0) * p.D + (int64_t)at.group * p.W;
         GnPiece<T, V> x[K], z[K], dy[K];
-        float n[K][V], f[K][V], dgate[K][V], sum = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k) {
-            const int c = (k * P + at.lane) * V;
-            x[k].load(static_cast<const T*>(p.x) + base + c, live && c < p.W);
-            z[k].load(static_cast<const T*>(p.z) + base + c, p.gate != 0 && live && c < p.W);
-            dy[k].load(static_cast<const T*>(p.dy) + base + c, live && c < p.W);
+            x[k] = x1[k];
+            if constexpr (kGate != 0) z[k] = z1[k];
+            dy[k] = y1[k];
         }
+        load(l + 1);
+        float n[K][V], f[K][V], q[K][V], dgate[K][V], sum = 0.f;
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 n[k][i] = x[k].get(i);
-                if (p.gate == 2) n[k][i] *= silu(z[k].get(i));
+                if constexpr (kGate != 0) q[k][i] = sigmoid(z[k].get(i));
+                if constexpr (kGate == 2) n[k][i] *= z[k].get(i) * q[k][i];
                 sum += n[k][i];
             }
         const float mean = p.center ? gn_sum<P>(sum, s_sum) * inv : 0.f;
@@ -87,11 +107,13 @@ __global__ __launch_bounds__(512) void gn_bwd_kernel(const GnArgs p) {
             const int c = (k * P + at.lane) * V;
             float g[V], b[V];
             gn_vector<V>(p.gamma ? p.gamma + at.group * p.W + c : nullptr, c < p.W, 1.f, g);
-            gn_vector<V>(p.beta ? p.beta + at.group * p.W + c : nullptr, c < p.W, 0.f, b);
+            if constexpr (kGate == 1 || kSilu)
+                gn_vector<V>(p.beta ? p.beta + at.group * p.W + c : nullptr, c < p.W, 0.f, b);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 n[k][i] *= rstd;
-                const GnBack r(p, n[k][i], g[i], b[i], z[k].get(i), dy[k].get(i));
+                const GnBack<kGate, kSilu> r(n[k][i], g[i], kGate == 1 || kSilu ? b[i] : 0.f, kGate ? z[k].get(i) : 0.f,
+                                             kGate ? q[k][i] : 0.f, dy[k].get(i));
                 dgate[k][i] = r.dgate;
                 dg[k][i] = live ? fmaf(r.e, n[k][i], dg[k][i]) : dg[k][i];
                 db[k][i] = live ? db[k][i] + r.e : db[k][i];
@@ -110,32 +132,41 @@ __global__ __launch_bounds__(512) void gn_bwd_kernel(const GnArgs p) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 dx[i] = rstd * (f[k][i] - fmaf(n[k][i], sfn, sf));
-                if (p.gate != 0) {
+                if constexpr (kGate != 0) {
                     const float zz = z[k].get(i);
-                    dz[i] = gn_dz(p.gate == 2 ? dx[i] * x[k].get(i) : dgate[k][i], zz);
-                    if (p.gate == 2) dx[i] *= silu(zz);
+                    dz[i] = gn_dz(kGate == 2 ? dx[i] * x[k].get(i) : dgate[k][i], zz, q[k][i]);
+                    if constexpr (kGate == 2) dx[i] *= zz * q[k][i];
                 }
             }
             store_piece<V>(static_cast<T*>(p.dx) + base, c, p.W, dx);
-            if (p.gate != 0) store_piece<V>(static_cast<T*>(p.dz) + base, c, p.W, dz);
+            if constexpr (kGate != 0) store_piece<V>(static_cast<T*>(p.dz) + base, c, p.W, dz);
         }
     }
-    if (p.part && at.live) {
-        float* const to = p.part + (size_t)at.side * 2 * p.D + at.group * p.W;
+    if (!p.part) return;
+    // The rows side by side meet in LDS, in order; the workgroup leaves one partial row.
+    const int ring = p.plan.groups * P;   // lanes of one of these rows
+    float* const to = p.part + (size_t)(blockIdx.x / p.plan.blocks) * 2 * p.D + at.group * p.W;
+    constexpr int kSums = 2 * K * V;
 #pragma unroll
-        for (int k = 0; k < K; ++k) {
-            const int c = (k * P + at.lane) * V;
-            if (c < p.W)
+    for (int s0 = 0; s0 < kSums; s0 += kBatch) {
+        __syncthreads();
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    to[c + i] = dg[k][i];
-                    to[p.D + c + i] = db[k][i];
-                }
+        for (int s = s0; s < kSums && s < s0 + kBatch; ++s)
+            s_part[s - s0][threadIdx.x] = s < K * V ? dg[s / V % K][s % V] : db[s / V % K][s % V];
+        __syncthreads();
+        if (at.live && at.row == 0) {
+#pragma unroll
+            for (int s = s0; s < kSums && s < s0 + kBatch; ++s) {
+                const int c = (s / V % K * P + at.lane) * V + s % V;
+                float sum = 0.f;
+                for (int r = 0; r < p.plan.rows; ++r) sum += s_part[s - s0][threadIdx.x + r * ring];
+                if (c < p.W) to[(s < K * V ? 0 : p.D) + c] = sum;
+            }
         }
     }
 }
 
-template <typename T, int V>
+template <typename T, int V, int kGate, bool kSilu>
 __global__ __launch_bounds__(256) void gn_bwd_wide_kernel(const GnArgs p) {
     constexpr int P = 256;
     __shared__ float s_sum[8];
@@ -146,9 +177,9 @@ __global__ __launch_bounds__(256) void gn_bwd_wide_kernel(const GnArgs p) {
         const int64_t base = row * p.D + (int64_t)at.group * p.W;
         auto value = [&](int c, float (&u)[V], GnPiece<T, V>& x, GnPiece<T, V>& z) {
             x.load(static_cast<const T*>(p.x) + base + c, true);
-            z.load(static_cast<const T*>(p.z) + base + c, p.gate != 0);
+            z.load(static_cast<const T*>(p.z) + base + c, kGate != 0);
 #pragma unroll
-            for (int i = 0; i < V; ++i) u[i] = p.gate == 2 ? x.get(i) * silu(z.get(i)) : x.get(i);
+            for (int i = 0; i < V; ++i) u[i] = kGate == 2 ? x.get(i) * silu(z.get(i)) : x.get(i);
         };
         float u[V], sum = 0.f;
         GnPiece<T, V> x, z, dy;
@@ -176,7 +207,7 @@ __global__ __launch_bounds__(256) void gn_bwd_wide_kernel(const GnArgs p) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float n = (u[i] - mean) * rstd;
-                const GnBack r(p, n, g[i], b[i], z.get(i), dy.get(i));
+                const GnBack<kGate, kSilu> r(n, g[i], b[i], z.get(i), sigmoid(z.get(i)), dy.get(i));
                 if (to) {   // this thread's channels in every row
                     to[i] = first ? r.e * n : fmaf(r.e, n, to[i]);
                     to[p.D + i] = first ? r.e : to[p.D + i] + r.e;
@@ -196,15 +227,15 @@ __global__ __launch_bounds__(256) void gn_bwd_wide_kernel(const GnArgs p) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 const float n = (u[i] - mean) * rstd;
-                const GnBack r(p, n, g[i], b[i], z.get(i), dy.get(i));
+                const GnBack<kGate, kSilu> r(n, g[i], b[i], z.get(i), sigmoid(z.get(i)), dy.get(i));
                 dx[i] = rstd * (r.e * g[i] - fmaf(n, sfn, sf));
-                if (p.gate != 0) {
-                    dz[i] = gn_dz(p.gate == 2 ? dx[i] * x.get(i) : r.dgate, z.get(i));
-                    if (p.gate == 2) dx[i] *= silu(z.get(i));
+                if constexpr (kGate != 0) {
+                    dz[i] = gn_dz(kGate == 2 ? dx[i] * x.get(i) : r.dgate, z.get(i), sigmoid(z.get(i)));
+                    if constexpr (kGate == 2) dx[i] *= silu(z.get(i));
                 }
             }
             store_piece<V>(static_cast<T*>(p.dx) + base, c, p.W, dx);
-            if (p.gate != 0) store_piece<V>(static_cast<T*>(p.dz) + base, c, p.W, dz);
+            if constexpr (kGate != 0) store_piece<V>(static_cast<T*>(p.dz) + base, c, p.W, dz);
         }
     }
 }
@@ -227,25 +258,20 @@ __global__ __launch_bounds__(256) void gn_params_kernel(const GnArgs p, int64_t 
     }
 }
 
-template <typename T, int V, int P, int K>
+template <typename T, int V, int P, int K, int kGate, bool kSilu>
 hipError_t run(const GnArgs& p, hipStream_t stream) {
     const unsigned grid = p.plan.blocks * p.plan.parts;
     if (p.rows > 0) {
-        if constexpr (K == 0) gn_bwd_wide_kernel<T, V><<<grid, 256, 0, stream>>>(p);
-        else gn_bwd_kernel<T, V, P, K><<<grid, p.plan.threads, 0, stream>>>(p);
+        if constexpr (K == 0) gn_bwd_wide_kernel<T, V, kGate, kSilu><<<grid, 256, 0, stream>>>(p);
+        else gn_bwd_kernel<T, V, P, K, kGate, kSilu><<<grid, p.plan.threads, 0, stream>>>(p);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     }
     if (!p.part) return hipSuccess;
-    gn_params_kernel<<<(unsigned)((2 * (int64_t)p.D + 15) / 16), 256, 0, stream>>>(
-        p, p.rows > 0 ? (int64_t)p.plan.parts * p.plan.rows : 0);
+    gn_params_kernel<<<(unsigned)((2 * (int64_t)p.D + 15) / 16), 256, 0, stream>>>(p, p.rows > 0 ? p.plan.parts : 0);
     return hipGetLastError();
 }
 
 }  // namespace
-
-hipError_t launch_gnorm_backward(const GnArgs& p, hipStream_t stream) {
-#include "wkv7_gnorm_dispatch.h"
-}
 
 }  // namespace wkv7

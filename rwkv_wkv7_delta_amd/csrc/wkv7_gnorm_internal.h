@@ -30,11 +30,14 @@ struct GnArgs {
     const void* dy;
     void *dx, *dz;
     float *dgamma, *dbeta;       // null without theirs
-    float* part;                 // [parts * rows side by side][2][D]
+    float* part;                 // [parts][2][D]
     GnPlan plan;
 };
 
 hipError_t launch_gnorm_forward(const GnArgs& p, hipStream_t stream);
 hipError_t launch_gnorm_backward(const GnArgs& p, hipStream_t stream);
+// By token type, each in a translation unit of its own.
+hipError_t launch_gnorm_backward_bf16(const GnArgs& p, hipStream_t stream);
+hipError_t launch_gnorm_backward_f32(const GnArgs& p, hipStream_t stream);
 
 }  // namespace wkv7

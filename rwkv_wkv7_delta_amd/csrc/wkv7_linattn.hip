@@ -54,16 +54,17 @@ __device__ __forceinline__ float* state_at(float* base, const LaArgs& p, int b, 
 // dy: D <- e^{G_end} D + scale sum_t (e^{G_t} dy_t) q_t^T.
 // kSegment: what a segment leaves from zero, and its summed decay.  Else (the
 // reverse only) D behind every tile is written, and the gradient of the first state.
-// Four waves, each with 16 value rows (of 32: and half of the key columns).  Two tiles are
-// on their way from memory at any time: the products of one take a third of its loads' time.
-constexpr int kSweepThreads = 256;
+// Waves 0 to 3 hold the state, 16 value rows each (of 32: and half of the key columns), and
+// move it on; waves 4 to 7 bring the tiles: two on their way from memory, one on its way to
+// LDS while the others use the one before.
+constexpr int kSweepStage = 256;
 
 template <typename T, int N, int PB, bool kReverse, bool kSegment>
-__global__ __launch_bounds__(kSweepThreads) void la_sweep_kernel(const LaArgs p, const T* kk, const T* vv,
+__global__ __launch_bounds__(kLaThreads) void la_sweep_kernel(const LaArgs p, const T* kk, const T* vv,
                                                                  const float* first, float* last, T* marks) {
     typedef LaMat<T> M;
-    typedef LaStage<T, N, kSweepThreads> SK;
-    typedef LaStage<T, PB, kSweepThreads> SV;
+    typedef LaStage<T, N, kSweepStage, kSweepStage> SK;
+    typedef LaStage<T, PB, kSweepStage, kSweepStage> SV;
     constexpr int PT = PB / 16, NH = 4 / PT, NT = N / 16 / NH;
     constexpr int kBytes = kLaChunk * (SK::kStride + SV::kStride) * (int)sizeof(T);
     constexpr int BUF = kBytes <= 32 * 1024 ? 2 : 1;
@@ -78,13 +79,14 @@ __global__ __launch_bounds__(kSweepThreads) void la_sweep_kernel(const LaArgs p,
     const int64_t begin = (int64_t)seg * p.seg_len;
     const int64_t stop = seg == p.nseg - 1 ? row.len : begin + p.seg_len;
     const int end = (int)(stop < row.len ? stop : row.len);
-    const int ptile = wave % PT * 16, n0 = wave / PT * (NT * 16);
+    const bool holds = wave < 4;
+    const int ptile = wave % PT * 16, n0 = wave % 4 / PT * (NT * 16);
     const int prow = w.p0 + ptile + l16;
     f32x4 st[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) st[n] = zero4();
     const size_t states = (size_t)p.B * p.H * p.P * N;
-    if (!kSegment) {
+    if (holds && !kSegment) {
         const float* from = w.r > 0 ? p.seg_state + (w.r - 1) * states : first;
         if (from) {
             from = state_at<N>(const_cast<float*>(from), p, w.b, w.h, prow) + n0;
@@ -95,67 +97,76 @@ __global__ __launch_bounds__(kSweepThreads) void la_sweep_kernel(const LaArgs p,
     const int kh = w.h / (p.H / p.G);
     const int64_t krow = (int64_t)p.G * N, vrow = (int64_t)p.H * p.P;
     const int tiles = end > begin ? (int)((end - begin + kLaChunk - 1) / kLaChunk) : 0;
-    struct Ahead {
-        SK k;
-        SV v;
-        LaLog<T> g;
-    } even, odd_;
-    constexpr bool kDeep = SK::kLoads + SV::kLoads <= 12;
+    constexpr bool kDeep = SK::kLoads + SV::kLoads <= 16;
     const auto tile_of = [&](int i) { return kReverse ? tiles - 1 - i : i; };
-    // No condition on the loads (tiles that there are not have no bytes): how many are under
-    // way is then known to the code that waits for the older ones.
-    auto load = [&](int i, Ahead& r) {
-        const int64_t t0 = begin + (int64_t)tile_of(i) * kLaChunk;
-        const int n = i >= tiles ? 0 : (int)(end - t0 < kLaChunk ? end - t0 : kLaChunk);
-        const int64_t at = row.first + t0;
-        r.k.load(rows_of(kk + at * krow + kh * N, n, krow, N), (uint32_t)(krow * sizeof(T)));
-        r.v.load(rows_of(vv + at * vrow + (int64_t)w.h * p.P + w.p0, n, vrow, PB), (uint32_t)(vrow * sizeof(T)));
-        r.g.load(p, at, w.h, n);
-    };
-    auto put = [&](int buf, const Ahead& r) {
-        r.k.store(s_k[buf]);
-        r.v.store(s_v[buf]);
-        const bool odd = __builtin_amdgcn_ballot_w64(r.k.odd() || r.v.odd()) != 0;
-        if (lane == 0) s_d[buf].odd[wave] = odd;
-        if (wave == 0) put_decays(s_d[buf], r.g.get());
-    };
+    // Deep: by twos, the last perhaps a tile without tokens, which changes nothing.
+    const int turns = kDeep ? (tiles + 1) / 2 * 2 : tiles;
     double total = 0;
-    auto turn = [&](int i, Ahead& r) {
-        const int buf = BUF == 2 ? i & 1 : 0;
-        __syncthreads();
-        const LaDecay& d = s_d[buf];
-        if (!kSegment) {
-            // (of a tile that there is not: nothing)
-            const auto m = buffer_of(marks + (((row.ckpt + begin / kLaChunk + tile_of(i)) * p.H + w.h) * p.P + w.p0) * N,
-                                     i < tiles ? PB * N * (int)sizeof(T) : 0);
-            const uint32_t at = ((ptile + l16) * N + n0 + 4 * g) * (uint32_t)sizeof(T);
+    if (holds) {
+        for (int i = 0; i < turns; ++i) {
+            const int buf = BUF == 2 ? i & 1 : 0;
+            __syncthreads();
+            const LaDecay& d = s_d[buf];
+            if (!kSegment) {
+                // (of a tile that there is not: nothing)
+                const auto m = buffer_of(marks + (((row.ckpt + begin / kLaChunk + tile_of(i)) * p.H + w.h) * p.P + w.p0) * N,
+                                         i < tiles ? PB * N * (int)sizeof(T) : 0);
+                const uint32_t at = ((ptile + l16) * N + n0 + 4 * g) * (uint32_t)sizeof(T);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                if constexpr (sizeof(T) == 2)
-                    __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(vu2, cvt4(st[n])), m, at + 32 * n, 0, 0);
-                else
-                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, st[n]), m, at + 64 * n, 0, 0);
+                for (int n = 0; n < NT; ++n) {
+                    if constexpr (sizeof(T) == 2)
+                        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(vu2, cvt4(st[n])), m, at + 32 * n, 0, 0);
+                    else
+                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, st[n]), m, at + 64 * n, 0, 0);
+                }
             }
+            if (kSegment) total += d.sum;
+            move_state<T, NT>(st, s_k[buf] + n0, SK::kStride, s_v[buf] + ptile, SV::kStride, kReverse ? d.up : d.down,
+                              kReverse ? p.scale : 1.f, d.all, any_odd(d.odd), g, l16);
+            if (BUF == 1) __syncthreads();
         }
-        if (kSegment) total += d.sum;
-        move_state<T, NT>(st, s_k[buf] + n0, SK::kStride, s_v[buf] + ptile, SV::kStride, kReverse ? d.up : d.down,
-                          kReverse ? p.scale : 1.f, d.all, any_odd<4>(d.odd), g, l16);
-        if (BUF == 1) __syncthreads();
-        put(BUF == 2 ? buf ^ 1 : 0, r);
-        load(i + (kDeep ? 3 : 2), r);
-    };
-    if (tiles > 0) {
+    } else if (turns > 0) {
+        struct Ahead {
+            SK k;
+            SV v;
+            LaLog<T> g;
+        } even, odd_;
+        // No condition on the loads (tiles that there are not have no bytes): how many are
+        // under way is then known to the code that waits for the older ones.
+        auto load = [&](int i, Ahead& r) {
+            const int64_t t0 = begin + (int64_t)tile_of(i) * kLaChunk;
+            const int n = i >= tiles ? 0 : (int)(end - t0 < kLaChunk ? end - t0 : kLaChunk);
+            const int64_t at = row.first + t0;
+            r.k.load(rows_of(kk + at * krow + kh * N, n, krow, N), (uint32_t)(krow * sizeof(T)));
+            r.v.load(rows_of(vv + at * vrow + (int64_t)w.h * p.P + w.p0, n, vrow, PB), (uint32_t)(vrow * sizeof(T)));
+            r.g.load(p, at, w.h, n);
+        };
+        auto put = [&](int buf, const Ahead& r) {
+            r.k.store(s_k[buf]);
+            r.v.store(s_v[buf]);
+            const bool odd = __builtin_amdgcn_ballot_w64(r.k.odd() || r.v.odd()) != 0;
+            if (lane == 0) {
+                s_d[buf].odd[wave] = odd;
+                s_d[buf].odd[wave - 4] = 0;
+            }
+            if (wave == 4) put_decays(s_d[buf], r.g.get());
+        };
+        auto turn = [&](int i, Ahead& r) {
+            __syncthreads();
+            if (BUF == 1) __syncthreads();
+            put(BUF == 2 ? i & 1 ^ 1 : 0, r);
+            load(i + (kDeep ? 3 : 2), r);
+        };
         load(0, even);
         if (kDeep) load(1, odd_);
         put(0, even);
         load(kDeep ? 2 : 1, even);
-        // Deep: by twos, the last perhaps a tile without tokens, which changes nothing.
-        for (int i = 0; i < tiles; i += kDeep ? 2 : 1) {
+        for (int i = 0; i < turns; i += kDeep ? 2 : 1) {
             turn(i, kDeep ? odd_ : even);
             if (kDeep) turn(i + 1, even);
         }
     }
-    if (last && (kSegment || w.r == p.nseg - 1)) {
+    if (holds && last && (kSegment || w.r == p.nseg - 1)) {
         float* const to = state_at<N>(last + (kSegment ? w.r * states : 0), p, w.b, w.h, prow) + n0;
 #pragma unroll
         for (int n = 0; n < NT; ++n) *reinterpret_cast<f32x4*>(to + 16 * n + 4 * g) = st[n];
@@ -483,7 +494,7 @@ template <typename T, int N, int PB>
 hipError_t fwd_block(const LaArgs& p, hipStream_t stream) {
     const unsigned blocks = (unsigned)p.B * p.H * (p.P / PB);
     if (p.nseg > 1) {
-        la_sweep_kernel<T, N, PB, false, true><<<blocks * (p.nseg - 1), kSweepThreads, 0, stream>>>(
+        la_sweep_kernel<T, N, PB, false, true><<<blocks * (p.nseg - 1), kLaThreads, 0, stream>>>(
             p, static_cast<const T*>(p.k), static_cast<const T*>(p.v), nullptr, p.seg_state, nullptr);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
@@ -501,14 +512,14 @@ hipError_t adjoint_block(const LaBwdArgs& q, hipStream_t stream) {
     const T* const Q = static_cast<const T*>(p.q);
     const T* const dY = static_cast<const T*>(q.dy);
     if (p.nseg > 1) {
-        la_sweep_kernel<T, N, PB, true, true><<<blocks * (p.nseg - 1), kSweepThreads, 0, stream>>>(
+        la_sweep_kernel<T, N, PB, true, true><<<blocks * (p.nseg - 1), kLaThreads, 0, stream>>>(
             p, Q, dY, nullptr, p.seg_state, nullptr);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         la_join_kernel<<<(unsigned)(((size_t)p.B * p.H * p.P * N / 4 + 255) / 256), 256, 0, stream>>>(p, q.dsT);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    la_sweep_kernel<T, N, PB, true, false><<<blocks * p.nseg, kSweepThreads, 0, stream>>>(
+    la_sweep_kernel<T, N, PB, true, false><<<blocks * p.nseg, kLaThreads, 0, stream>>>(
         p, Q, dY, q.dsT, q.ds0, static_cast<T*>(q.adj));
     return hipGetLastError();
 }

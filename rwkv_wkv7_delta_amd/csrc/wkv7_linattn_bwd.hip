@@ -111,7 +111,7 @@ struct LaUnit {
 // one of either, whose triangles make up a square.  The sums over the heads that share a
 // key stay in registers.
 template <typename T, int N, int PB>
-__global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, unsigned units, int blocks) {
+__global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, int blocks) {
     typedef LaMat<T> M;
     typedef LaStage<T, N> SK;
     typedef LaStage<T, PB> SV;
@@ -125,10 +125,14 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, u
     const int w = wave % 4;
     const int shared = p.H / p.G, per = (shared + o.split - 1) / o.split, pblocks = p.P / PB;
     const int64_t krow = (int64_t)p.G * N, vrow = (int64_t)p.H * p.P;
-    const T* const V = static_cast<const T*>(p.v);
-    const T* const dY = static_cast<const T*>(o.dy);
-    const T* const CK = static_cast<const T*>(p.ckpt);
-    const T* const AD = static_cast<const T*>(o.adj);
+    // The pointers are read from the kernel's arguments where they are used: kept in scalar
+    // registers over the loop, they and the buffers made of them are more than there are.
+    typedef const __attribute__((address_space(4))) LaBwdArgs* Args;
+    const auto args = [&] {
+        Args a = (Args)__builtin_amdgcn_kernarg_segment_ptr();
+        asm volatile("" : "+s"(a));
+        return a;
+    };
     const int t = 16 * w + l16;   // the lane's token
     constexpr int kPer = 16 / (int)sizeof(T);
     // Results of the wave's 16 tokens, rows of W, n of the tile's written.
@@ -149,22 +153,43 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, u
     // stores were issued behind them).
     auto run = [&](auto queries_) {
     constexpr bool kQueries = decltype(queries_)::value;
-    unsigned id = blockIdx.x;
-    int64_t tile = -1;   // of unit `id`'s row, the last one taken
+    // Units are numbered row by row, tile by tile, part by part, group by group: this
+    // workgroup's, and the distance to its next one, digit by digit.
+    int at_kh, at_part, at_c, at_b, by_kh, by_part, by_c, by_b;
+    const auto digits = [&](unsigned i, int& kh, int& part, int& c, int& b) {
+        kh = (int)(i % p.G);
+        i /= p.G;
+        part = (int)(i % o.split);
+        i /= o.split;
+        c = (int)(i % blocks);
+        b = (int)(i / blocks);
+    };
+    digits(blockIdx.x, at_kh, at_part, at_c, at_b);
+    digits(gridDim.x, by_kh, by_part, by_c, by_b);
+    const auto skip = [&] {
+        at_kh += by_kh;
+        int over = at_kh >= p.G;
+        at_kh -= over ? p.G : 0;
+        at_part += by_part + over;
+        over = at_part >= o.split;
+        at_part -= over ? o.split : 0;
+        at_c += by_c + over;
+        over = at_c >= blocks;
+        at_c -= over ? blocks : 0;
+        at_b += by_b + over;
+    };
+    int64_t tile = -1;   // of the unit's row, the last one taken
     // The next unit with tokens.  A unit is every tile of a row whose number is c0 modulo
     // `blocks` (more than one only where a packed row is longer than the call says); tiles of
     // padding get their zeros here.
     auto advance = [&]() {
         LaUnit u;
         u.valid = false;
-        for (; id < units; id += gridDim.x, tile = -1) {
-            unsigned i = id;
-            u.kh = (int)(i % p.G);
-            i /= p.G;
-            u.part = (int)(i % o.split);
-            i /= o.split;
-            u.b = (int)(i / blocks);
-            const int c0 = (int)(i % blocks);
+        for (; at_b < p.B; skip(), tile = -1) {
+            u.kh = at_kh;
+            u.part = at_part;
+            u.b = at_b;
+            const int c0 = at_c;
             const LaRow row = la_row(p.rows, p.packed, p.tokens, p.T, u.b);
             tile = tile < 0 ? c0 : tile + blocks;
             if (tile * kLaChunk >= row.stored) continue;
@@ -183,21 +208,21 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, u
             }
             for (; u.step < u.steps; ++u.step) {
                 const int h = head_of_step(u), p0 = u.step % pblocks * PB;
-                T* const dvp = static_cast<T*>(o.dv) + u.at * vrow + (int64_t)h * p.P + p0;
+                T* const dvp = static_cast<T*>(args()->dv) + u.at * vrow + (int64_t)h * p.P + p0;
                 for (int e = threadIdx.x; e < u.n_out * (PB / kPer); e += kLaThreads)
                     *reinterpret_cast<vu4*>(dvp + e / (PB / kPer) * vrow + e % (PB / kPer) * kPer) = vu4{0, 0, 0, 0};
                 if (o.dg && p0 == 0 && (int)threadIdx.x < u.n_out)
-                    Elem<T>::store1(static_cast<T*>(o.dg) + (u.at + threadIdx.x) * p.H + h, 0.f);
+                    Elem<T>::store1(static_cast<T*>(args()->dg) + (u.at + threadIdx.x) * p.H + h, 0.f);
             }
             const int64_t kat = u.at * krow + u.kh * N;
             for (int e = threadIdx.x; e < u.n_out * N; e += kLaThreads) {
                 const int64_t k = kat + e / N * krow + e % N;
                 if (o.split > 1) {
                     const int64_t parts = (p.packed ? p.tokens : (int64_t)p.B * p.T) * krow * u.part;
-                    o.part_q[parts + k] = o.part_k[parts + k] = 0.f;
+                    args()->part_q[parts + k] = args()->part_k[parts + k] = 0.f;
                 } else {
-                    Elem<T>::store1(static_cast<T*>(o.dq) + k, 0.f);
-                    Elem<T>::store1(static_cast<T*>(o.dk) + k, 0.f);
+                    Elem<T>::store1(static_cast<T*>(args()->dq) + k, 0.f);
+                    Elem<T>::store1(static_cast<T*>(args()->dk) + k, 0.f);
                 }
             }
         }
@@ -212,14 +237,15 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, u
         const int64_t vat = u.at * vrow + (int64_t)h * p.P + p0;
         const int n = u.valid ? u.n_in : 0, n_qk = u.step == 0 ? n : 0;
         const uint32_t kb = (uint32_t)(krow * sizeof(T));
-        rq.load(rows_of(static_cast<const T*>(p.q) + u.at * krow + u.kh * N, n_qk, krow, N), kb);
-        rk.load(rows_of(static_cast<const T*>(p.k) + u.at * krow + u.kh * N, n_qk, krow, N), kb);
+        const Args a = args();
+        rq.load(rows_of(static_cast<const T*>(a->f.q) + u.at * krow + u.kh * N, n_qk, krow, N), kb);
+        rk.load(rows_of(static_cast<const T*>(a->f.k) + u.at * krow + u.kh * N, n_qk, krow, N), kb);
         if constexpr (kQueries) lg.load(p, u.at, h, n);
-        rv.load(rows_of(V + vat, n, vrow, PB), (uint32_t)(vrow * sizeof(T)));
-        ry.load(rows_of(dY + vat, n, vrow, PB), (uint32_t)(vrow * sizeof(T)));
+        rv.load(rows_of(static_cast<const T*>(a->f.v) + vat, n, vrow, PB), (uint32_t)(vrow * sizeof(T)));
+        ry.load(rows_of(static_cast<const T*>(a->dy) + vat, n, vrow, PB), (uint32_t)(vrow * sizeof(T)));
         const size_t sat = (((size_t)(u.ckpt + u.c) * p.H + h) * p.P + p0) * N;
-        rs.load(CK + sat, u.valid);
-        rd.load(AD + sat, u.valid);
+        rs.load(static_cast<const T*>(a->f.ckpt) + sat, u.valid);
+        rd.load(static_cast<const T*>(a->adj) + sat, u.valid);
     };
     // dg of a head once the sums over its tile are in LDS, by one wave.  Lane l: what counts
     // for token 63 - l, from behind it; what counts for token l, from before it.  In 64 bits:
@@ -235,7 +261,7 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, u
 #pragma unroll
         for (int j = 0; j < 8; ++j) both += sm.c[j];
         const float dg = (float)(x + __shfl(y, u) + all * both);
-        if (u < n_out) Elem<T>::store1(static_cast<T*>(o.dg) + (at + u) * p.H + h, u < n_in ? dg : 0.f);
+        if (u < n_out) Elem<T>::store1(static_cast<T*>(args()->dg) + (at + u) * p.H + h, u < n_in ? dg : 0.f);
     };
     LaUnit u = advance();
     if (!u.valid) return;
@@ -465,7 +491,7 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, u
                 for (int m = 0; m < PT; ++m)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) dv[m][r] = in ? dv[m][r] : 0.f;
-                store_rows(dv, static_cast<T*>(o.dv) + at * vrow + (int64_t)h * p.P + p0, n_out, vrow);
+                store_rows(dv, static_cast<T*>(args()->dv) + at * vrow + (int64_t)h * p.P + p0, n_out, vrow);
             }
             if (o.dg && head_last) {
                 // (what finish_dg reads of the head before)
@@ -508,13 +534,13 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, u
                 for (int r = 0; r < 4; ++r) x[e][r] = in ? dqk[e][r] : 0.f;
             if (o.split > 1) {
                 const int64_t parts = (p.packed ? p.tokens : (int64_t)p.B * p.T) * krow * u.part;
-                const auto to = rows_of((kQueries ? o.part_q : o.part_k) + parts + kat, n, krow, N);
+                const auto to = rows_of((kQueries ? args()->part_q : args()->part_k) + parts + kat, n, krow, N);
 #pragma unroll
                 for (int e = 0; e < NT; ++e)
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, x[e]), to,
                                                            t * (uint32_t)(krow * 4) + (16 * e + 4 * g) * 4, 0, 0);
             } else {
-                store_rows(x, static_cast<T*>(kQueries ? o.dq : o.dk) + kat, n, krow);
+                store_rows(x, static_cast<T*>(kQueries ? args()->dq : args()->dk) + kat, n, krow);
             }
         }
         // The next head's decays, where the other waves still compute.
@@ -566,7 +592,7 @@ hipError_t bwd_block(const LaBwdArgs& q, hipStream_t stream) {
     const unsigned units = (unsigned)p.B * blocks * p.G * q.split;
     // As many workgroups as run at once: two to a compute unit where LDS holds them.
     const unsigned most = sizeof(LaBwdShared<T, N, PB>) <= 80 * 1024 ? 512 : 256;
-    la_bwd_kernel<T, N, PB><<<units < most ? units : most, kLaThreads, 0, stream>>>(q, units, blocks);
+    la_bwd_kernel<T, N, PB><<<units < most ? units : most, kLaThreads, 0, stream>>>(q, blocks);
     if ((e = hipGetLastError()) != hipSuccess || q.split == 1) return e;
     const int64_t values = (p.packed ? p.tokens : (int64_t)p.B * p.T) * p.G * N;
     const unsigned half = (unsigned)((values / 4 + 255) / 256);

@@ -187,7 +187,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const T* p, int n, int
 }
 
 // A tile of up to 64 rows on its way from memory to LDS: 16 bytes per lane and load.
-template <typename T, int W, int kThreads = kLaThreads>
+template <typename T, int W, int kThreads = kLaThreads, int kFirst = 0>   // threads kFirst ..
 struct LaStage {
     static constexpr int kPieces = W * (int)sizeof(T) / 16;          // per row
     static constexpr int kRowsPer = kThreads / kPieces;            // rows of one load of the workgroup
@@ -197,14 +197,15 @@ struct LaStage {
     vu4 w[kLoads];
 
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t row_bytes) {
-        const uint32_t at = threadIdx.x / kPieces * row_bytes + threadIdx.x % kPieces * 16;
+        const uint32_t me = threadIdx.x - kFirst, at = me / kPieces * row_bytes + me % kPieces * 16;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
             w[i] = __builtin_bit_cast(vu4, __builtin_amdgcn_raw_buffer_load_b128(r, at + i * kRowsPer * row_bytes, 0, 0));
     }
     __device__ __forceinline__ void store(T* lds) const {
-        T* const p = lds + threadIdx.x / kPieces * kStride + threadIdx.x % kPieces * (16 / (int)sizeof(T));
-        if (kAll || threadIdx.x < kLaChunk * kPieces)
+        const uint32_t me = threadIdx.x - kFirst;
+        T* const p = lds + me / kPieces * kStride + me % kPieces * (16 / (int)sizeof(T));
+        if (kAll || me < kLaChunk * kPieces)
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) *reinterpret_cast<vu4*>(p + i * kRowsPer * kStride) = w[i];
     }
