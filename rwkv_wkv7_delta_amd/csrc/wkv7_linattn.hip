@@ -71,6 +71,9 @@ __global__ __launch_bounds__(kLaThreads) void la_sweep_kernel(const LaArgs p, co
     __shared__ __attribute__((aligned(16))) T s_k[BUF][kLaChunk * SK::kStride];
     __shared__ __attribute__((aligned(16))) T s_v[BUF][kLaChunk * SV::kStride];
     __shared__ LaDecay s_d[BUF];
+    // (checkpoints on their way to whole rows)
+    constexpr bool kMarks = !kSegment && NH == 1 && sizeof(T) == 2;
+    __shared__ __attribute__((aligned(16))) T s_own[4][kMarks ? LaRows16<T, N>::kSize : 8];
     const LaBlock w = la_block<PB>(p);
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int g = lane / 16, l16 = lane % 16;
@@ -111,14 +114,7 @@ __global__ __launch_bounds__(kLaThreads) void la_sweep_kernel(const LaArgs p, co
                 // (of a tile that there is not: nothing)
                 const auto m = buffer_of(marks + (((row.ckpt + begin / kLaChunk + tile_of(i)) * p.H + w.h) * p.P + w.p0) * N,
                                          i < tiles ? PB * N * (int)sizeof(T) : 0);
-                const uint32_t at = ((ptile + l16) * N + n0 + 4 * g) * (uint32_t)sizeof(T);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if constexpr (sizeof(T) == 2)
-                        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(vu2, cvt4(st[n])), m, at + 32 * n, 0, 0);
-                    else
-                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, st[n]), m, at + 64 * n, 0, 0);
-                }
+                store_mark<T, N>(s_own[wave], st, m, ptile, n0);
             }
             if (kSegment) total += d.sum;
             move_state<T, NT>(st, s_k[buf] + n0, SK::kStride, s_v[buf] + ptile, SV::kStride, kReverse ? d.up : d.down,
@@ -219,6 +215,7 @@ struct LaFwdShared {
     T v[kBuffers][kLaChunk * SV::kStride];
     T s[kBuffers][PB * SK::kStride];   // the state before the tile, [p][n], in the tokens' type
     T own[4][LaRows16<T, (N > PB ? N : PB)>::kSize];   // a wave's queries, then its results
+    T mark[4][sizeof(T) == 2 && PB == 64 ? LaRows16<T, N>::kSize : 8];   // a wave's state rows
     LaDecay d[kBuffers];
 };
 
@@ -381,14 +378,7 @@ __global__ __launch_bounds__(kLaThreads) void la_fwd_kernel(const LaArgs p) {
                 const auto m = buffer_of(static_cast<T*>(p.ckpt) +
                                              (((row.ckpt + begin / kLaChunk + c) * p.H + w.h) * p.P + w.p0) * N,
                                          p.ckpt && c < tiles ? PB * N * (int)sizeof(T) : 0);
-                const uint32_t mark = ((ptile + l16) * N + n0 + 4 * g) * (uint32_t)sizeof(T);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if constexpr (sizeof(T) == 2)
-                        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(vu2, cvt4(st[n])), m, mark + 32 * n, 0, 0);
-                    else
-                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, st[n]), m, mark + 64 * n, 0, 0);
-                }
+                store_mark<T, N>(sm.mark[wave - 4], st, m, ptile, n0);
                 move_state<T, NT>(st, sk + n0, SK::kStride, sv + ptile, SV::kStride, d.down, 1.f, d.all, odd, g, l16);
             }
             if (BUF == 1) __syncthreads();

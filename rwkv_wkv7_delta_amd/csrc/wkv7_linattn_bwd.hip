@@ -27,8 +27,11 @@ struct LaBwdShared {
     // A wave's results on their way to whole rows (fp32 rows go there by themselves).
     T own[sizeof(T) == 2 ? 8 : 1][sizeof(T) == 2 ? LaRows16<T, (N > PB ? N : PB)>::kSize : 16];
     LaDecay d[2];                                  // of this head and the next
-    // For dg: sums of M along its rows, by wave; a; M's sums down its columns; b; parts of <S, D>.
-    float row[4][kLaChunk], a[kLaChunk], col[kLaChunk], b[kLaChunk], c[8];
+    // For dg, of this head and the one before: sums of M along its rows, by wave; a; M's sums
+    // down its columns; b; parts of <S, D>.
+    struct {
+        float row[4][kLaChunk], a[kLaChunk], col[kLaChunk], b[kLaChunk], c[8];
+    } g[2];
     int odd[8];
 };
 
@@ -98,10 +101,11 @@ struct No {
 // What a workgroup has before it: a tile of one group of heads (or of a part of them), and of
 // these one head and PB of its value rows.
 struct LaUnit {
-    int b, kh, part, n_in, n_out, step, steps;
-    int64_t c, at;    // the tile's number in its row; its first token among all
-    int64_t ckpt;     // the row's first checkpoint
     bool valid;
+    int n_in, n_out;        // the tile's tokens, and places that are written
+    int part, step, steps, h;
+    int64_t at;             // the tile's first token among all
+    int64_t kat, vat, sat;  // where its keys, values and states are, in elements
 };
 
 // Tiles of 64 tokens stand alone, so a workgroup goes from one to the next (as many
@@ -123,8 +127,8 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, i
     const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int g = lane / 16, l16 = lane % 16;
     const int w = wave % 4;
-    const int shared = p.H / p.G, per = (shared + o.split - 1) / o.split, pblocks = p.P / PB;
-    const int64_t krow = (int64_t)p.G * N, vrow = (int64_t)p.H * p.P;
+    const int shared = p.H / p.G, per = (shared + o.split - 1) / o.split, pblocks = p.P / PB;   // (1, 2 or 4)
+    const int krow = p.G * N, vrow = p.H * p.P;
     // The pointers are read from the kernel's arguments where they are used: kept in scalar
     // registers over the loop, they and the buffers made of them are more than there are.
     typedef const __attribute__((address_space(4))) LaBwdArgs* Args;
@@ -148,7 +152,13 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, i
                 __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, x[e]), r, t * bytes + (16 * e + 4 * g) * 4, 0, 0);
         }
     };
-    const auto head_of_step = [&](const LaUnit& u) { return u.kh * shared + u.part * per + u.step / pblocks; };
+    const auto first_of_head = [&](const LaUnit& u) { return (u.step & (pblocks - 1)) == 0; };
+    const auto to_next_step = [&](LaUnit& u) {
+        ++u.step;
+        u.h += first_of_head(u);
+        u.vat += PB;
+        u.sat += PB * N;
+    };
     // A wave's whole way, by its role (so that the code that waits for loads knows how many
     // stores were issued behind them).
     auto run = [&](auto queries_) {
@@ -186,37 +196,34 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, i
         LaUnit u;
         u.valid = false;
         for (; at_b < p.B; skip(), tile = -1) {
-            u.kh = at_kh;
-            u.part = at_part;
-            u.b = at_b;
-            const int c0 = at_c;
-            const LaRow row = la_row(p.rows, p.packed, p.tokens, p.T, u.b);
-            tile = tile < 0 ? c0 : tile + blocks;
+            const LaRow row = la_row(p.rows, p.packed, p.tokens, p.T, at_b);
+            tile = tile < 0 ? at_c : tile + blocks;
             if (tile * kLaChunk >= row.stored) continue;
-            const int64_t t0 = tile * kLaChunk;
-            u.c = tile;
-            u.ckpt = row.ckpt;
+            const int t0 = (int)tile * kLaChunk, kh = at_kh;
+            u.part = at_part;
             u.at = row.first + t0;
-            u.n_in = (int)(row.len - t0 < kLaChunk ? (row.len > t0 ? row.len - t0 : 0) : kLaChunk);
-            u.n_out = (int)(row.stored - t0 < kLaChunk ? row.stored - t0 : kLaChunk);
+            u.n_in = row.len - t0 < kLaChunk ? (row.len > t0 ? row.len - t0 : 0) : kLaChunk;
+            u.n_out = row.stored - t0 < kLaChunk ? row.stored - t0 : kLaChunk;
             u.step = 0;
             const int heads = shared - u.part * per < per ? shared - u.part * per : per;
             u.steps = heads * pblocks;
+            u.h = kh * shared + u.part * per;
+            u.kat = u.at * krow + kh * N;
+            u.vat = u.at * vrow + u.h * p.P;
+            u.sat = ((row.ckpt + tile) * vrow + u.h * p.P) * N;
             if (u.n_in > 0) {
                 u.valid = true;
                 break;
             }
-            for (; u.step < u.steps; ++u.step) {
-                const int h = head_of_step(u), p0 = u.step % pblocks * PB;
-                T* const dvp = static_cast<T*>(args()->dv) + u.at * vrow + (int64_t)h * p.P + p0;
+            for (; u.step < u.steps; to_next_step(u)) {
+                T* const dvp = static_cast<T*>(args()->dv) + u.vat;
                 for (int e = threadIdx.x; e < u.n_out * (PB / kPer); e += kLaThreads)
-                    *reinterpret_cast<vu4*>(dvp + e / (PB / kPer) * vrow + e % (PB / kPer) * kPer) = vu4{0, 0, 0, 0};
-                if (o.dg && p0 == 0 && (int)threadIdx.x < u.n_out)
-                    Elem<T>::store1(static_cast<T*>(args()->dg) + (u.at + threadIdx.x) * p.H + h, 0.f);
+                    *reinterpret_cast<vu4*>(dvp + (int64_t)(e / (PB / kPer)) * vrow + e % (PB / kPer) * kPer) = vu4{0, 0, 0, 0};
+                if (o.dg && first_of_head(u) && (int)threadIdx.x < u.n_out)
+                    Elem<T>::store1(static_cast<T*>(args()->dg) + (u.at + threadIdx.x) * p.H + u.h, 0.f);
             }
-            const int64_t kat = u.at * krow + u.kh * N;
             for (int e = threadIdx.x; e < u.n_out * N; e += kLaThreads) {
-                const int64_t k = kat + e / N * krow + e % N;
+                const int64_t k = u.kat + (int64_t)(e / N) * krow + e % N;
                 if (o.split > 1) {
                     const int64_t parts = (p.packed ? p.tokens : (int64_t)p.B * p.T) * krow * u.part;
                     args()->part_q[parts + k] = args()->part_k[parts + k] = 0.f;
@@ -233,53 +240,60 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, i
     LaStateStage<T, N, PB> rs, rd;
     LaLog<T> lg;
     auto load = [&](const LaUnit& u) {
-        const int h = head_of_step(u), p0 = u.step % pblocks * PB;
-        const int64_t vat = u.at * vrow + (int64_t)h * p.P + p0;
         const int n = u.valid ? u.n_in : 0, n_qk = u.step == 0 ? n : 0;
-        const uint32_t kb = (uint32_t)(krow * sizeof(T));
+        const uint32_t kb = (uint32_t)krow * sizeof(T), vb = (uint32_t)vrow * sizeof(T);
         const Args a = args();
-        rq.load(rows_of(static_cast<const T*>(a->f.q) + u.at * krow + u.kh * N, n_qk, krow, N), kb);
-        rk.load(rows_of(static_cast<const T*>(a->f.k) + u.at * krow + u.kh * N, n_qk, krow, N), kb);
-        if constexpr (kQueries) lg.load(p, u.at, h, n);
-        rv.load(rows_of(static_cast<const T*>(a->f.v) + vat, n, vrow, PB), (uint32_t)(vrow * sizeof(T)));
-        ry.load(rows_of(static_cast<const T*>(a->dy) + vat, n, vrow, PB), (uint32_t)(vrow * sizeof(T)));
-        const size_t sat = (((size_t)(u.ckpt + u.c) * p.H + h) * p.P + p0) * N;
-        rs.load(static_cast<const T*>(a->f.ckpt) + sat, u.valid);
-        rd.load(static_cast<const T*>(a->adj) + sat, u.valid);
+        rq.load(rows_of(static_cast<const T*>(a->f.q) + u.kat, n_qk, krow, N), kb);
+        rk.load(rows_of(static_cast<const T*>(a->f.k) + u.kat, n_qk, krow, N), kb);
+        if constexpr (kQueries) lg.load(p, u.at, u.h, n);
+        rv.load(rows_of(static_cast<const T*>(a->f.v) + u.vat, n, vrow, PB), vb);
+        ry.load(rows_of(static_cast<const T*>(a->dy) + u.vat, n, vrow, PB), vb);
+        rs.load(static_cast<const T*>(a->f.ckpt) + u.sat, u.valid);
+        rd.load(static_cast<const T*>(a->adj) + u.sat, u.valid);
     };
     // dg of a head once the sums over its tile are in LDS, by one wave.  Lane l: what counts
     // for token 63 - l, from behind it; what counts for token l, from before it.  In 64 bits:
     // the rows and columns of M cancel where both lie on one side.
-    auto finish_dg = [&](int64_t at, int n_in, int n_out, int h, float all) {
+    struct Behind {   // the head whose dg is still to be written
+        int64_t at;
+        int h, n_in, n_out, buf;
+        float all;
+    };
+    auto finish_dg = [&](const Behind& k) {
         const int u = 63 - lane;
-        double x = (double)sm.a[u] - sm.col[u];
+        const auto& sg = sm.g[k.buf];
+        double x = (double)sg.a[u] - sg.col[u];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x += 16 * j <= u ? (double)sm.row[j][u] : 0.0;
+        for (int j = 0; j < 4; ++j) x += 16 * j <= u ? (double)sg.row[j][u] : 0.0;
         x = wave_running_sum(x);
-        const double y = wave_running_sum(lane > 0 ? (double)sm.b[lane - 1] : 0.0);
+        const double y = wave_running_sum(lane > 0 ? (double)sg.b[lane - 1] : 0.0);
         double both = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) both += sm.c[j];
-        const float dg = (float)(x + __shfl(y, u) + all * both);
-        if (u < n_out) Elem<T>::store1(static_cast<T*>(args()->dg) + (at + u) * p.H + h, u < n_in ? dg : 0.f);
+        for (int j = 0; j < 8; ++j) both += sg.c[j];
+        const float dg = (float)(x + __shfl(y, u) + k.all * both);
+        if (u < k.n_out) Elem<T>::store1(static_cast<T*>(args()->dg) + (k.at + u) * p.H + k.h, u < k.n_in ? dg : 0.f);
+    };
+    const auto after = [&](const LaUnit& u) {
+        LaUnit n = u;
+        if (!u.valid) return n;
+        to_next_step(n);
+        return n.step == n.steps ? advance() : n;
     };
     LaUnit u = advance();
     if (!u.valid) return;
+    LaUnit next = after(u);
     load(u);
     if (kQueries && wave == 0) put_decays(sm.d[0], lg.get());
-    int dbuf = 0, dg_h = -1, dg_in = 0, dg_out = 0;   // the head whose dg is still to be written
-    int64_t dg_at = 0;
-    float dg_all = 0.f;
-    f32x4 dqk[NT];   // dq of the lane's token, or dk
-    f32x4 rsum[4];   // M's rows 16 j + 4 g .., the lane's column
+    int dbuf = 0, gbuf = 0;
+    bool waits = false;   // a head's dg
+    Behind behind;
+    f32x4 dqk[NT];        // dq of the lane's token, or dk
     float asum = 0.f, bsum = 0.f, cdot = 0.f;
     bool odd_qk = false;
     while (u.valid) {
-        const int h = head_of_step(u), p0 = u.step % pblocks * PB;
-        const int64_t at = u.at;
         const int n_in = u.n_in, n_out = u.n_out;
         const bool in = t < n_in;
-        const bool head_first = p0 == 0, head_last = p0 + PB == p.P;
+        const bool head_first = first_of_head(u), head_last = ((u.step + 1) & (pblocks - 1)) == 0;
         __syncthreads();   // the tiles before have been read
         if (u.step == 0) {
             rq.store(sm.q);
@@ -288,24 +302,18 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, i
 #pragma unroll
             for (int n = 0; n < NT; ++n) dqk[n] = zero4();
         }
-        if (head_first) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) rsum[j] = zero4();
-            asum = bsum = cdot = 0.f;
-        }
+        if (head_first) asum = bsum = cdot = 0.f;
         rv.store(sm.v);
         ry.store(sm.dy);
         rs.store(sm.s);
         rd.store(sm.ds);
-        cdot += rs.dot(rd);
         const bool odd_lane = __builtin_amdgcn_ballot_w64(odd_qk || rv.odd() || ry.odd()) != 0;
         if (lane == 0) sm.odd[wave] = odd_lane;
-        LaUnit next = u;
-        if (++next.step == next.steps) next = advance();
+        cdot += rs.dot(rd);
         __syncthreads();
         load(next);
-        if (kQueries && dg_h >= 0 && wave == 1) finish_dg(dg_at, dg_in, dg_out, dg_h, dg_all);
-        dg_h = -1;
+        if (kQueries && waits && wave == 1) finish_dg(behind);
+        waits = false;
         {
             const LaDecay& d = sm.d[dbuf];
             const bool odd = any_odd(sm.odd);
@@ -447,8 +455,13 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, i
                                         m[r] = 4 * g + r > l16 ? m[r] : 0.f;
                                     }
                                 }
-                                rsum[j] += m;
                                 asum += (m[0] + m[1]) + (m[2] + m[3]);
+                                if (o.dg) {   // along the rows: over the 16 keys
+#pragma unroll
+                                    for (int r = 0; r < 4; ++r) m[r] = row16_sum(m[r]);
+                                    f32x4* const to = reinterpret_cast<f32x4*>(sm.g[gbuf].row[w] + 16 * j + 4 * g);
+                                    if (l16 == 0) *to = head_first ? m : *to + m;
+                                }
                             }
                             hb[u] = M::half(x);
                             ha[u] = M::half(y);
@@ -467,6 +480,10 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, i
                         dv[m] = M::mma(columns<T>(sm.dy + 32 * SV::kStride + 16 * m, SV::kStride, g, l16), wa[1], dv[m]);
                     }
                 } else {
+                    if (o.dg && head_first && l16 == 0)   // (the queries add M's rows up here)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (j >= w) *reinterpret_cast<f32x4*>(sm.g[gbuf].row[w] + 16 * j + 4 * g) = zero4();
                     for (int s = 0; s < n_in; ++s) {   // the query's token
                         float qk = 0.f, yv = 0.f;
 #pragma unroll 2
@@ -491,42 +508,29 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, i
                 for (int m = 0; m < PT; ++m)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) dv[m][r] = in ? dv[m][r] : 0.f;
-                store_rows(dv, static_cast<T*>(args()->dv) + at * vrow + (int64_t)h * p.P + p0, n_out, vrow);
+                store_rows(dv, static_cast<T*>(args()->dv) + u.vat, n_out, vrow);
             }
             if (o.dg && head_last) {
-                // (what finish_dg reads of the head before)
-                __syncthreads();
+                auto& sg = sm.g[gbuf];
                 const float a = sum_rows4(in ? asum : 0.f), cs = wave_sum(cdot);
-                if (lane == 0) sm.c[wave] = cs;
+                if (lane == 0) sg.c[wave] = cs;
                 if constexpr (kQueries) {
-                    if (g == 0) sm.a[t] = a;
+                    if (g == 0) sg.a[t] = a;
                 } else {
                     const float bs = sum_rows4(in ? bsum : 0.f);
                     if (g == 0) {
-                        sm.col[t] = a;
-                        sm.b[t] = bs;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (j >= w) {
-                            f32x4 x;
-#pragma unroll
-                            for (int r = 0; r < 4; ++r) x[r] = row16_sum(rsum[j][r]);
-                            if (l16 == 0) *reinterpret_cast<f32x4*>(sm.row[w] + 16 * j + 4 * g) = x;
-                        }
+                        sg.col[t] = a;
+                        sg.b[t] = bs;
                     }
                 }
-                dg_h = h;
-                dg_at = at;
-                dg_in = n_in;
-                dg_out = n_out;
-                dg_all = d.all;
+                behind = Behind{u.at, u.h, n_in, n_out, gbuf, d.all};
+                waits = true;
+                gbuf ^= 1;
             }
         }
         // ---- dq or dk, or this part's sums of them, behind the last step (before: no rows)
         {
             const int n = u.step + 1 == u.steps ? n_out : 0;
-            const int64_t kat = at * krow + u.kh * N;
             f32x4 x[NT];
 #pragma unroll
             for (int e = 0; e < NT; ++e)
@@ -534,25 +538,26 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, i
                 for (int r = 0; r < 4; ++r) x[e][r] = in ? dqk[e][r] : 0.f;
             if (o.split > 1) {
                 const int64_t parts = (p.packed ? p.tokens : (int64_t)p.B * p.T) * krow * u.part;
-                const auto to = rows_of((kQueries ? args()->part_q : args()->part_k) + parts + kat, n, krow, N);
+                const auto to = rows_of((kQueries ? args()->part_q : args()->part_k) + parts + u.kat, n, krow, N);
 #pragma unroll
                 for (int e = 0; e < NT; ++e)
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, x[e]), to,
-                                                           t * (uint32_t)(krow * 4) + (16 * e + 4 * g) * 4, 0, 0);
+                                                           t * (uint32_t)krow * 4 + (16 * e + 4 * g) * 4, 0, 0);
             } else {
-                store_rows(x, static_cast<T*>(kQueries ? args()->dq : args()->dk) + kat, n, krow);
+                store_rows(x, static_cast<T*>(kQueries ? args()->dq : args()->dk) + u.kat, n, krow);
             }
         }
         // The next head's decays, where the other waves still compute.
-        if (next.valid && next.step % pblocks == 0) {
+        if (next.valid && first_of_head(next)) {
             dbuf ^= 1;
             if (kQueries && wave == 0) put_decays(sm.d[dbuf], lg.get());
         }
         u = next;
+        next = after(u);
     }
-    if (dg_h >= 0) {
+    if (waits) {
         __syncthreads();
-        if (kQueries && wave == 1) finish_dg(dg_at, dg_in, dg_out, dg_h, dg_all);
+        if (kQueries && wave == 1) finish_dg(behind);
     }
     };
     if (wave < 4) run(Yes());

@@ -183,7 +183,7 @@ __device__ __forceinline__ LaRow la_row(const int32_t* rows, bool packed, int64_
 // stay below 2^31 bytes (sizes are limited for that).
 template <typename T>
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_of(const T* p, int n, int64_t stride, int width) {
-    return buffer_of(p, n > 0 ? (int)(((n - 1) * stride + width) * (int)sizeof(T)) : 0);
+    return buffer_of(p, n > 0 ? ((n - 1) * (int)stride + width) * (int)sizeof(T) : 0);
 }
 
 // A tile of up to 64 rows on its way from memory to LDS: 16 bytes per lane and load.
@@ -347,6 +347,25 @@ struct LaRows16 {
         }
     }
 };
+
+// The 16 value rows that a wave holds of a state, columns n0 .. of N, to a checkpoint of PB
+// rows (a buffer of them, or of nothing).
+template <typename T, int N, int NT>
+__device__ __forceinline__ void store_mark(T* lds, const f32x4 (&st)[NT], __amdgpu_buffer_rsrc_t r, int ptile, int n0) {
+    if constexpr (16 * NT == N && sizeof(T) == 2) {
+        LaRows16<T, N>::store(lds, st, r, N * sizeof(T), ptile);
+    } else {
+        const int lane = threadIdx.x % 64, g = lane / 16, l16 = lane % 16;
+        const uint32_t at = ((ptile + l16) * N + n0 + 4 * g) * (uint32_t)sizeof(T);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            if constexpr (sizeof(T) == 2)
+                __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(vu2, cvt4(st[n])), r, at + 32 * n, 0, 0);
+            else
+                __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, st[n]), r, at + 64 * n, 0, 0);
+        }
+    }
+}
 
 // By one whole wave.  A log decay of -infinity forgets everything: 2^-144270 is 0,
 // and sums that hold it stay exact to 2^-30.
