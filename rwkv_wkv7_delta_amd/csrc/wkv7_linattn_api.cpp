@@ -11,6 +11,8 @@ namespace {
 
 using wkv7::kLaChunk;
 
+constexpr int kUnits = 256;   // compute units of the device
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool req(const void* p) { return p != nullptr && aligned(p, 16); }
 bool opt(const void* p) { return p == nullptr || aligned(p, 16); }
@@ -28,7 +30,7 @@ bool size_ok(int32_t n) { return n == 32 || n == 64 || n == 128; }
 int64_t blocks_of(int64_t T) { return (T + kLaChunk - 1) / kLaChunk; }
 // Tiles of all rows, at most, and the rows of the checkpoint tensor.
 int64_t tiles_of(const wkv7_linattn_desc* d) {
-    return d->packed ? d->tokens / kLaChunk + d->B : (int64_t)d->B * blocks_of(d->T);
+    return d->packed ? (int64_t)d->tokens / kLaChunk + d->B : (int64_t)d->B * blocks_of(d->T);
 }
 int64_t tokens_of(const wkv7_linattn_desc* d) { return d->packed ? d->tokens : (int64_t)d->B * d->T; }
 
@@ -56,26 +58,33 @@ int check(const wkv7_linattn_desc* d) {
 struct Plan {
     int nseg, seg_len;
 };
-// Time segments where a launch without them (a workgroup per row, head and 64 value
-// rows) leaves compute units idle.
-Plan plan(const wkv7_linattn_desc* d, int units) {
+// Time segments.  A launch without them has one workgroup per row, head and 64 value rows,
+// which takes its tiles one after the other: where the workgroups are fewer than the compute
+// units, as many segments as fill them, if that is worth a first sweep over the states and
+// two more launches.  In tenths of a microsecond, measured where memory is not the limit: a
+// tile takes 20 (fp32 45) read out and 12 (20) in a sweep over states alone, the launches 150.
+// (1, 16384) tokens and 12 heads of 64 in bf16: 22 segments 56 us, 43 of them 65, 11 of them
+// 84; (4, 1024) tokens, 12 heads: forward in 5 segments 25 us, without 32, and the reverse
+// sweep 20 and 19.
+Plan plan(const wkv7_linattn_desc* d, bool read_out) {
     const Plan none{1, (int)(blocks_of(d->T) * kLaChunk)};
-    const int64_t wgs = (int64_t)d->B * d->H * (d->P / wkv7::la_value_block(d->P));
-    if (wgs == 0 || d->T == 0) return none;
-    int64_t n = units / wgs;
-    if (n > d->T / 128) n = d->T / 128;
-    if (n < 3) return none;
-    const int64_t len = blocks_of(((int64_t)d->T + n - 1) / n) * kLaChunk;
-    n = ((int64_t)d->T + len - 1) / len;
-    return n < 2 ? none : Plan{(int)n, (int)len};
+    const int64_t wgs = (int64_t)d->B * d->H * (d->P / wkv7::la_value_block(d->P)), tiles = blocks_of(d->T);
+    if (wgs == 0 || tiles < 2) return none;
+    int64_t n = (kUnits + wgs - 1) / wgs;
+    if (n > tiles) n = tiles;
+    if (n < 2) return none;
+    const int64_t each = (tiles + n - 1) / n;
+    n = (tiles + each - 1) / each;
+    const int64_t sweep = d->dtype == WKV7_BF16 ? 12 : 20, turn = !read_out ? sweep : d->dtype == WKV7_BF16 ? 20 : 45;
+    if (n < 2 || each * (sweep + turn) + 150 >= tiles * turn) return none;
+    return Plan{(int)n, (int)(each * kLaChunk)};
 }
-constexpr int kForwardUnits = 512, kSweepUnits = 512;
 
 // Parts that a group's heads are taken in, so that the tiles alone need not fill the device.
 int plan_split(const wkv7_linattn_desc* d) {
     const int64_t wgs = tiles_of(d) * d->G, shared = d->H / d->G;
     if (wgs == 0) return 1;
-    int64_t n = 512 / wgs;
+    int64_t n = 2 * kUnits / wgs;
     if (n > shared) n = shared;
     if (n < 2) return 1;
     const int64_t per = (shared + n - 1) / n;
@@ -116,12 +125,12 @@ size_t wkv7_linattn_ckpt_bytes(const wkv7_linattn_desc* desc) { return check(des
 
 size_t wkv7_linattn_forward_workspace_bytes(const wkv7_linattn_desc* desc) {
     if (check(desc) != WKV7_OK) return 0;
-    return segment_bytes(desc, plan(desc, kForwardUnits));
+    return segment_bytes(desc, plan(desc, true));
 }
 
 size_t wkv7_linattn_backward_workspace_bytes(const wkv7_linattn_desc* desc) {
     if (check(desc) != WKV7_OK) return 0;
-    return pad16(ckpt_bytes(desc)) + segment_bytes(desc, plan(desc, kSweepUnits)) +
+    return pad16(ckpt_bytes(desc)) + segment_bytes(desc, plan(desc, false)) +
            2 * part_bytes(desc, plan_split(desc));
 }
 
@@ -135,7 +144,7 @@ int wkv7_linattn_forward(const wkv7_linattn_desc* desc, const int32_t* rows, con
     if (!rows_ok(desc, rows) || (tokens && !(req(q) && req(k) && req(v) && req(g) && req(y))) ||
         !(opt(q) && opt(k) && opt(v) && opt(g) && opt(y) && opt(s0) && opt(sT) && opt(ckpt) && opt(workspace)))
         return WKV7_ERR_INVALID_ARG;
-    const Plan s = plan(desc, kForwardUnits);
+    const Plan s = plan(desc, true);
     const size_t need = segment_bytes(desc, s);
     if (need > 0 && (!workspace || workspace_bytes < need)) return WKV7_ERR_WORKSPACE;
     if (!tokens && !sT) return WKV7_OK;
@@ -157,7 +166,7 @@ int wkv7_linattn_backward(const wkv7_linattn_desc* desc, const int32_t* rows, co
         !(opt(q) && opt(k) && opt(v) && opt(g) && opt(dy) && opt(ckpt) && opt(dq) && opt(dk) && opt(dv) && opt(dg) &&
           opt(dsT) && opt(ds0) && opt(workspace)))
         return WKV7_ERR_INVALID_ARG;
-    const Plan s = plan(desc, kSweepUnits);
+    const Plan s = plan(desc, false);
     const int split = plan_split(desc);
     const size_t need = wkv7_linattn_backward_workspace_bytes(desc);
     if (need > 0 && (!workspace || workspace_bytes < need)) return WKV7_ERR_WORKSPACE;
