@@ -70,7 +70,7 @@ Plan plan(const wkv7_linattn_desc* d, bool read_out) {
     const Plan none{1, (int)(blocks_of(d->T) * kLaChunk)};
     const int64_t wgs = (int64_t)d->B * d->H * (d->P / wkv7::la_value_block(d->P)), tiles = blocks_of(d->T);
     if (wgs == 0 || tiles < 2) return none;
-    int64_t n = (kUnits + wgs - 1) / wgs;
+    int64_t n = kUnits / wgs;   // (one more, and some units have two: 37 us where 21 segments take 32)
     if (n > tiles) n = tiles;
     if (n < 2) return none;
     const int64_t each = (tiles + n - 1) / n;

@@ -17,20 +17,25 @@ namespace wkv7 {
 
 namespace {
 
+// Twelve waves: four for dq, four for dk, four for dv; the last eight bring the tiles.
+constexpr int kBwdThreads = 768, kBwdStage = 512, kBwdFirst = 256;
+template <typename T, int W>
+using LaBwdStage = LaStage<T, W, kBwdStage, kBwdFirst>;
+
 template <typename T, int N, int PB>
 struct LaBwdShared {
-    typedef LaStage<T, N> SK;
-    typedef LaStage<T, PB> SV;
+    typedef LaBwdStage<T, N> SK;
+    typedef LaBwdStage<T, PB> SV;
     T q[kLaChunk * SK::kStride], k[kLaChunk * SK::kStride];
     T v[kLaChunk * SV::kStride], dy[kLaChunk * SV::kStride];
     T s[PB * SK::kStride], ds[PB * SK::kStride];   // [p][n]
     // A wave's results on their way to whole rows (fp32 rows go there by themselves).
-    T own[sizeof(T) == 2 ? 8 : 1][sizeof(T) == 2 ? LaRows16<T, (N > PB ? N : PB)>::kSize : 16];
+    T own[sizeof(T) == 2 ? 12 : 1][sizeof(T) == 2 ? LaRows16<T, (N > PB ? N : PB)>::kSize : 16];
     LaDecay d[2];                                  // of this head and the next
-    // For dg, of this head and the one before: sums of M along its rows, by wave; a; M's sums
-    // down its columns; b; parts of <S, D>.
+    // For dg, of this head and the one before: sums of M down its columns, by wave; a and M's
+    // sums along its rows; b; parts of <S, D>.
     struct {
-        float row[4][kLaChunk], a[kLaChunk], col[kLaChunk], b[kLaChunk], c[8];
+        float col[4][kLaChunk], a[kLaChunk], b[kLaChunk], c[8];
     } g[2];
     int odd[8];
 };
@@ -39,7 +44,7 @@ struct LaBwdShared {
 template <typename T, int N, int PB>
 struct LaStateStage {
     static constexpr int kPieces = N * (int)sizeof(T) / 16;
-    static constexpr int kLoads = PB * kPieces / kLaThreads;
+    static constexpr int kLoads = PB * kPieces / kBwdStage;
     static constexpr int kStride = N + 16 / (int)sizeof(T);
     vu4 w[kLoads > 0 ? kLoads : 1];
     // Rows are one behind the other in memory; none where there is no tile.
@@ -47,12 +52,12 @@ struct LaStateStage {
         const auto r = buffer_of(p, some ? PB * N * (int)sizeof(T) : 0);
 #pragma unroll
         for (int i = 0; i < (kLoads > 0 ? kLoads : 1); ++i)
-            w[i] = __builtin_bit_cast(vu4, __builtin_amdgcn_raw_buffer_load_b128(r, (i * kLaThreads + threadIdx.x) * 16, 0, 0));
+            w[i] = __builtin_bit_cast(vu4, __builtin_amdgcn_raw_buffer_load_b128(r, (i * kBwdStage + threadIdx.x - kBwdFirst) * 16, 0, 0));
     }
     __device__ __forceinline__ void store(T* lds) const {
 #pragma unroll
         for (int i = 0; i < (kLoads > 0 ? kLoads : 1); ++i) {
-            const int at = i * kLaThreads + threadIdx.x;
+            const int at = i * kBwdStage + threadIdx.x - kBwdFirst;
             if (kLoads > 0 || at < PB * kPieces)
                 *reinterpret_cast<vu4*>(lds + at / kPieces * kStride + at % kPieces * (16 / (int)sizeof(T))) = w[i];
         }
@@ -60,7 +65,7 @@ struct LaStateStage {
     // The lane's part of <this, o>.
     __device__ __forceinline__ float dot(const LaStateStage& o) const {
         float x = 0.f;
-        if (kLoads > 0 || threadIdx.x < PB * kPieces) {
+        if (kLoads > 0 || (int)threadIdx.x - kBwdFirst < PB * kPieces) {
 #pragma unroll
             for (int i = 0; i < (kLoads > 0 ? kLoads : 1); ++i)
 #pragma unroll
@@ -79,8 +84,7 @@ struct LaStateStage {
 
 __device__ __forceinline__ float wave_sum(float x) { return sum_rows4(row16_sum(x)); }
 
-// Weights W of the tile that stands between a wave's tokens and the 16 of tile j, applied to
-// products x (and y): in lane (g, l16) register r, token 16 j + 4 g + r against the lane's own.
+// Decays between the lane's token and those of tile j: in register r, token 16 j + 4 g + r.
 __device__ __forceinline__ f32x4 decays(const LaDecay& d, int j, int g, float hi, float lo, bool later) {
     const f32x4 ohi = *reinterpret_cast<const f32x4*>(d.hi + 16 * j + 4 * g);
     const f32x4 olo = *reinterpret_cast<const f32x4*>(d.lo + 16 * j + 4 * g);
@@ -91,12 +95,12 @@ __device__ __forceinline__ f32x4 decays(const LaDecay& d, int j, int g, float hi
     return e;
 }
 
-struct Yes {
-    static constexpr bool value = true;
+// A wave's role.
+template <int kRole>
+struct Role {
+    static constexpr int value = kRole;
 };
-struct No {
-    static constexpr bool value = false;
-};
+constexpr int kDq = 0, kDk = 1, kDv = 2;
 
 // What a workgroup has before it: a tile of one group of heads (or of a part of them), and of
 // these one head and PB of its value rows.
@@ -110,15 +114,14 @@ struct LaUnit {
 
 // Tiles of 64 tokens stand alone, so a workgroup goes from one to the next (as many
 // workgroups as the device holds at once, in turn) with the next one's loads on their
-// way while it computes.  Waves 0 to 3 have the tokens 16 w .. as queries (dq, against the
-// keys before), waves 4 to 7 as keys (dk and dv, against the queries behind); on each SIMD
-// one of either, whose triangles make up a square.  The sums over the heads that share a
-// key stay in registers.
+// way while it computes.  Waves w, 4 + w and 8 + w have the tokens 16 w ..: as queries, for
+// dq, against the keys before; as keys, for dk and for dv, against the queries behind.  Each
+// SIMD has one of each.  The sums over the heads that share a key stay in registers.
 template <typename T, int N, int PB>
-__global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, int blocks) {
+__global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, int blocks) {
     typedef LaMat<T> M;
-    typedef LaStage<T, N> SK;
-    typedef LaStage<T, PB> SV;
+    typedef LaBwdStage<T, N> SK;
+    typedef LaBwdStage<T, PB> SV;
     typedef typename M::Frag Frag;
     typedef typename M::Half Half;
     constexpr int NT = N / 16, PT = PB / 16, KS = N / 32, PS = PB / 32;
@@ -161,8 +164,8 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, i
     };
     // A wave's whole way, by its role (so that the code that waits for loads knows how many
     // stores were issued behind them).
-    auto run = [&](auto queries_) {
-    constexpr bool kQueries = decltype(queries_)::value;
+    auto run = [&](auto role_) {
+    constexpr int kRole = decltype(role_)::value;
     // Units are numbered row by row, tile by tile, part by part, group by group: this
     // workgroup's, and the distance to its next one, digit by digit.
     int at_kh, at_part, at_c, at_b, by_kh, by_part, by_c, by_b;
@@ -217,12 +220,12 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, i
             }
             for (; u.step < u.steps; to_next_step(u)) {
                 T* const dvp = static_cast<T*>(args()->dv) + u.vat;
-                for (int e = threadIdx.x; e < u.n_out * (PB / kPer); e += kLaThreads)
+                for (int e = threadIdx.x; e < u.n_out * (PB / kPer); e += kBwdThreads)
                     *reinterpret_cast<vu4*>(dvp + (int64_t)(e / (PB / kPer)) * vrow + e % (PB / kPer) * kPer) = vu4{0, 0, 0, 0};
                 if (o.dg && first_of_head(u) && (int)threadIdx.x < u.n_out)
                     Elem<T>::store1(static_cast<T*>(args()->dg) + (u.at + threadIdx.x) * p.H + u.h, 0.f);
             }
-            for (int e = threadIdx.x; e < u.n_out * N; e += kLaThreads) {
+            for (int e = threadIdx.x; e < u.n_out * N; e += kBwdThreads) {
                 const int64_t k = u.kat + (int64_t)(e / N) * krow + e % N;
                 if (o.split > 1) {
                     const int64_t parts = (p.packed ? p.tokens : (int64_t)p.B * p.T) * krow * u.part;
@@ -243,9 +246,12 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, i
         const int n = u.valid ? u.n_in : 0, n_qk = u.step == 0 ? n : 0;
         const uint32_t kb = (uint32_t)krow * sizeof(T), vb = (uint32_t)vrow * sizeof(T);
         const Args a = args();
+        if constexpr (kRole == kDq) {
+            lg.load(p, u.at, u.h, n);
+            return;
+        }
         rq.load(rows_of(static_cast<const T*>(a->f.q) + u.kat, n_qk, krow, N), kb);
         rk.load(rows_of(static_cast<const T*>(a->f.k) + u.kat, n_qk, krow, N), kb);
-        if constexpr (kQueries) lg.load(p, u.at, u.h, n);
         rv.load(rows_of(static_cast<const T*>(a->f.v) + u.vat, n, vrow, PB), vb);
         ry.load(rows_of(static_cast<const T*>(a->dy) + u.vat, n, vrow, PB), vb);
         rs.load(static_cast<const T*>(a->f.ckpt) + u.sat, u.valid);
@@ -262,9 +268,9 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, i
     auto finish_dg = [&](const Behind& k) {
         const int u = 63 - lane;
         const auto& sg = sm.g[k.buf];
-        double x = (double)sg.a[u] - sg.col[u];
+        double x = sg.a[u];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x += 16 * j <= u ? (double)sg.row[j][u] : 0.0;
+        for (int j = 0; j < 4; ++j) x -= u < 16 * j + 16 ? (double)sg.col[j][u] : 0.0;
         x = wave_running_sum(x);
         const double y = wave_running_sum(lane > 0 ? (double)sg.b[lane - 1] : 0.0);
         double both = 0;
@@ -283,12 +289,12 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, i
     if (!u.valid) return;
     LaUnit next = after(u);
     load(u);
-    if (kQueries && wave == 0) put_decays(sm.d[0], lg.get());
+    if (kRole == kDq && wave == 0) put_decays(sm.d[0], lg.get());
     int dbuf = 0, gbuf = 0;
     bool waits = false;   // a head's dg
     Behind behind;
-    f32x4 dqk[NT];        // dq of the lane's token, or dk
-    float asum = 0.f, bsum = 0.f, cdot = 0.f;
+    f32x4 sum[NT];        // dq or dk of the lane's token
+    float asum = 0.f, cdot = 0.f;
     bool odd_qk = false;
     while (u.valid) {
         const int n_in = u.n_in, n_out = u.n_out;
@@ -296,272 +302,301 @@ __global__ __launch_bounds__(kLaThreads) void la_bwd_kernel(const LaBwdArgs o, i
         const bool head_first = first_of_head(u), head_last = ((u.step + 1) & (pblocks - 1)) == 0;
         __syncthreads();   // the tiles before have been read
         if (u.step == 0) {
-            rq.store(sm.q);
-            rk.store(sm.k);
-            odd_qk = rq.odd() || rk.odd();
+            if constexpr (kRole != kDq) {
+                rq.store(sm.q);
+                rk.store(sm.k);
+                odd_qk = rq.odd() || rk.odd();
+            }
 #pragma unroll
-            for (int n = 0; n < NT; ++n) dqk[n] = zero4();
+            for (int n = 0; n < NT; ++n) sum[n] = zero4();
         }
-        if (head_first) asum = bsum = cdot = 0.f;
-        rv.store(sm.v);
-        ry.store(sm.dy);
-        rs.store(sm.s);
-        rd.store(sm.ds);
-        const bool odd_lane = __builtin_amdgcn_ballot_w64(odd_qk || rv.odd() || ry.odd()) != 0;
-        if (lane == 0) sm.odd[wave] = odd_lane;
-        cdot += rs.dot(rd);
+        if (head_first) asum = cdot = 0.f;
+        if constexpr (kRole != kDq) {
+            rv.store(sm.v);
+            ry.store(sm.dy);
+            rs.store(sm.s);
+            rd.store(sm.ds);
+            const bool odd_lane = __builtin_amdgcn_ballot_w64(odd_qk || rv.odd() || ry.odd()) != 0;
+            if (lane == 0) sm.odd[wave - 4] = odd_lane;
+            cdot += rs.dot(rd);
+        }
         __syncthreads();
         load(next);
-        if (kQueries && waits && wave == 1) finish_dg(behind);
+        if (kRole == kDq && waits && wave == 1) finish_dg(behind);
         waits = false;
-        {
-            const LaDecay& d = sm.d[dbuf];
-            const bool odd = any_odd(sm.odd);
-            const float thi = d.hi[t], tlo = d.lo[t];
-            if constexpr (kQueries) {
-                // ---- dq_t: the state's part
-                const float up = d.up[t] * p.scale;
-                Frag yf[PS];   // dy_t, along the states' columns (the contraction's second order)
-#pragma unroll
-                for (int j = 0; j < PS; ++j) {
-                    const T* const y1 = sm.dy + t * SV::kStride + 32 * j + 4 * g;
-                    yf[j] = M::cat(M::four(y1), M::four(y1 + 16));
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    f32x4 x = zero4();
-#pragma unroll
-                    for (int j = 0; j < PS; ++j)
-                        x = M::mma(columns<T>(sm.s + 32 * j * SK::kStride + 16 * n, SK::kStride, g, l16), yf[j], x);
-                    x *= up;
-                    const f32x4 qn = M::wide(M::four(sm.q + t * SK::kStride + 16 * n + 4 * g));
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) asum = fmaf(qn[r], x[r], asum);
-                    dqk[n] += x;
-                }
-                if (!odd) {
-                    // ---- and the tile's: [s][t], s up to t
-                    Frag wt[2];
-#pragma unroll
-                    for (int j = 0; j < PS; ++j) yf[j] = M::rows(sm.dy + t * SV::kStride + 32 * j + 8 * g);
-#pragma unroll
-                    for (int j2 = 0; j2 < 2; ++j2) {
-                        Half h2[2];
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int j = 2 * j2 + u;
-                            f32x4 x = zero4();
-                            if (j <= w) {
-#pragma unroll
-                                for (int e = 0; e < PS; ++e)
-                                    x = M::mma(M::rows(sm.v + (16 * j + l16) * SV::kStride + 32 * e + 8 * g), yf[e], x);
-                                x *= decays(d, j, g, thi, tlo, false) * p.scale;
-                                if (j == w)   // the triangle's edge
-#pragma unroll
-                                    for (int r = 0; r < 4; ++r) x[r] = 4 * g + r <= l16 ? x[r] : 0.f;
-                            }
-                            // Rounded to the tokens' type, as the weights of the forward: half a step of
-                            // each, as large as the gradients' own rounding.
-                            h2[u] = M::half(x);
-                        }
-                        wt[j2] = M::cat(h2[0], h2[1]);
-                    }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        dqk[n] = M::mma(columns<T>(sm.k + 16 * n, SK::kStride, g, l16), wt[0], dqk[n]);
-                        if (w >= 2)
-                            dqk[n] = M::mma(columns<T>(sm.k + 32 * SK::kStride + 16 * n, SK::kStride, g, l16), wt[1], dqk[n]);
-                    }
-                } else {
-                    // An infinity or a NaN in the tile: pair by pair, each lane its token, so that it
-                    // meets no weight of 0 of a pair that does not exist.
-                    for (int s = 0; s < n_in; ++s) {
-                        float qk = 0.f, yv = 0.f;
+        const LaDecay& d = sm.d[dbuf];
+        const bool odd = any_odd(sm.odd);
+        const float thi = d.hi[t], tlo = d.lo[t];
+        // An infinity or a NaN in the tile (odd): pair by pair, each lane its token, so that it
+        // meets no weight of 0 of a pair that does not exist.  The products of token `late` as
+        // a query with `early` as a key, the second with the pair's weight.
+        const auto qk_of = [&](int late, int early) {
+            float x = 0.f;
 #pragma unroll 2
-                        for (int e = 0; e < N; ++e)
-                            qk = fmaf(Elem<T>::load1(sm.q + t * SK::kStride + e), Elem<T>::load1(sm.k + s * SK::kStride + e), qk);
+            for (int e = 0; e < N; ++e)
+                x = fmaf(Elem<T>::load1(sm.q + late * SK::kStride + e), Elem<T>::load1(sm.k + early * SK::kStride + e), x);
+            return x;
+        };
+        const auto yv_of = [&](int late, int early) {
+            float x = 0.f;
 #pragma unroll 2
-                        for (int e = 0; e < PB; ++e)
-                            yv = fmaf(Elem<T>::load1(sm.dy + t * SV::kStride + e), Elem<T>::load1(sm.v + s * SV::kStride + e), yv);
-                        yv *= exp2_raw((thi - d.hi[s]) + (tlo - d.lo[s])) * p.scale;
-                        if (in && s <= t) {
+            for (int e = 0; e < PB; ++e)
+                x = fmaf(Elem<T>::load1(sm.dy + late * SV::kStride + e), Elem<T>::load1(sm.v + early * SV::kStride + e), x);
+            return x;
+        };
+        const auto weight = [&](int late, int early) {
+            return exp2_raw((d.hi[late] - d.hi[early]) + (d.lo[late] - d.lo[early])) * p.scale;
+        };
+        if constexpr (kRole == kDq) {
+            // ---- the state's part
+            const float up = d.up[t] * p.scale;
+            Frag yf[PS];   // dy_t, along the states' columns (the contraction's second order)
 #pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                dqk[n] += M::wide(M::four(sm.k + s * SK::kStride + 16 * n + 4 * g)) * yv;
-                            if (s < t && g == 0) asum = fmaf(qk, yv, asum);   // M's row
-                        }
-                    }
-                }
-            } else {
-                // ---- dk_s and dv_s: the parts of the state's gradient
-                const float down = d.down[t];
-                f32x4 dv[PT];
-                Frag vf[PS], kf[KS];
+            for (int j = 0; j < PS; ++j) {
+                const T* const y1 = sm.dy + t * SV::kStride + 32 * j + 4 * g;
+                yf[j] = M::cat(M::four(y1), M::four(y1 + 16));
+            }
 #pragma unroll
-                for (int j = 0; j < PS; ++j) {
-                    const T* const v1 = sm.v + t * SV::kStride + 32 * j + 4 * g;
-                    vf[j] = M::cat(M::four(v1), M::four(v1 + 16));
-                }
+            for (int n = 0; n < NT; ++n) {
+                f32x4 x = zero4();
 #pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    f32x4 x = zero4();
+                for (int j = 0; j < PS; ++j)
+                    x = M::mma(columns<T>(sm.s + 32 * j * SK::kStride + 16 * n, SK::kStride, g, l16), yf[j], x);
+                x *= up;
+                const f32x4 qn = M::wide(M::four(sm.q + t * SK::kStride + 16 * n + 4 * g));
 #pragma unroll
-                    for (int j = 0; j < PS; ++j)
-                        x = M::mma(columns<T>(sm.ds + 32 * j * SK::kStride + 16 * n, SK::kStride, g, l16), vf[j], x);
-                    x *= down;
-                    const f32x4 kn = M::wide(M::four(sm.k + t * SK::kStride + 16 * n + 4 * g));
+                for (int r = 0; r < 4; ++r) asum = fmaf(qn[r], x[r], asum);
+                sum[n] += x;
+            }
+            if (!odd) {
+                // ---- and the tile's: [s][t], s up to t; and M
+                Frag wt[2], qf[KS];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) bsum = fmaf(kn[r], x[r], bsum);
-                    dqk[n] += x;
-                }
+                for (int j = 0; j < PS; ++j) yf[j] = M::rows(sm.dy + t * SV::kStride + 32 * j + 8 * g);
 #pragma unroll
-                for (int j = 0; j < KS; ++j) kf[j] = M::rows(sm.k + t * SK::kStride + 32 * j + 8 * g);
+                for (int j = 0; j < KS; ++j) qf[j] = M::rows(sm.q + t * SK::kStride + 32 * j + 8 * g);
 #pragma unroll
-                for (int m = 0; m < PT; ++m) {
-                    dv[m] = zero4();
+                for (int j2 = 0; j2 < 2; ++j2) {
+                    Half h2[2];
 #pragma unroll
-                    for (int j = 0; j < KS; ++j)
-                        dv[m] = M::mma(M::rows(sm.ds + (16 * m + l16) * SK::kStride + 32 * j + 8 * g), kf[j], dv[m]);
-                    dv[m] *= down;
-                }
-                if (!odd) {
-                    // ---- and the tile's: [t][s], t from s on
-                    Frag wb[2], wa[2];
+                    for (int u2 = 0; u2 < 2; ++u2) {
+                        const int j = 2 * j2 + u2;
+                        f32x4 x = zero4();
+                        if (j <= w) {
 #pragma unroll
-                    for (int j = 0; j < PS; ++j) vf[j] = M::rows(sm.v + t * SV::kStride + 32 * j + 8 * g);
+                            for (int e = 0; e < PS; ++e)
+                                x = M::mma(M::rows(sm.v + (16 * j + l16) * SV::kStride + 32 * e + 8 * g), yf[e], x);
+                            x *= decays(d, j, g, thi, tlo, false) * p.scale;
+                            if (j == w)   // the triangle's edge
 #pragma unroll
-                    for (int j2 = 0; j2 < 2; ++j2) {
-                        Half hb[2], ha[2];
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const int j = 2 * j2 + u;
-                            f32x4 x = zero4(), y = zero4();
-                            if (j >= w) {
-#pragma unroll
-                                for (int e = 0; e < PS; ++e)
-                                    x = M::mma(M::rows(sm.dy + (16 * j + l16) * SV::kStride + 32 * e + 8 * g), vf[e], x);
+                                for (int r = 0; r < 4; ++r) x[r] = 4 * g + r <= l16 ? x[r] : 0.f;
+                            if (o.dg) {
+                                f32x4 m = zero4();
 #pragma unroll
                                 for (int e = 0; e < KS; ++e)
-                                    y = M::mma(M::rows(sm.q + (16 * j + l16) * SK::kStride + 32 * e + 8 * g), kf[e], y);
-                                const f32x4 e = decays(d, j, g, thi, tlo, true) * p.scale;
-                                y *= e;
-                                f32x4 m = y * x;
-                                x *= e;
-                                if (j == w) {
+                                    m = M::mma(M::rows(sm.k + (16 * j + l16) * SK::kStride + 32 * e + 8 * g), qf[e], m);
+                                m *= x;
+                                if (j == w)   // (a token with itself is on no side of a decay)
 #pragma unroll
-                                    for (int r = 0; r < 4; ++r) {
-                                        y[r] = 4 * g + r >= l16 ? y[r] : 0.f;
-                                        x[r] = 4 * g + r >= l16 ? x[r] : 0.f;
-                                        m[r] = 4 * g + r > l16 ? m[r] : 0.f;
-                                    }
-                                }
+                                    for (int r = 0; r < 4; ++r) m[r] = 4 * g + r < l16 ? m[r] : 0.f;
                                 asum += (m[0] + m[1]) + (m[2] + m[3]);
-                                if (o.dg) {   // along the rows: over the 16 keys
 #pragma unroll
-                                    for (int r = 0; r < 4; ++r) m[r] = row16_sum(m[r]);
-                                    f32x4* const to = reinterpret_cast<f32x4*>(sm.g[gbuf].row[w] + 16 * j + 4 * g);
-                                    if (l16 == 0) *to = head_first ? m : *to + m;
-                                }
+                                for (int r = 0; r < 4; ++r) m[r] = row16_sum(m[r]);
+                                f32x4* const to = reinterpret_cast<f32x4*>(sm.g[gbuf].col[w] + 16 * j + 4 * g);
+                                if (l16 == 0) *to = head_first ? m : *to + m;
                             }
-                            hb[u] = M::half(x);
-                            ha[u] = M::half(y);
                         }
-                        wb[j2] = M::cat(hb[0], hb[1]);
-                        wa[j2] = M::cat(ha[0], ha[1]);
+                        // Rounded to the tokens' type, as the weights of the forward: half a step of
+                        // each, as large as the gradients' own rounding.
+                        h2[u2] = M::half(x);
                     }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        if (w < 2) dqk[n] = M::mma(columns<T>(sm.q + 16 * n, SK::kStride, g, l16), wb[0], dqk[n]);
-                        dqk[n] = M::mma(columns<T>(sm.q + 32 * SK::kStride + 16 * n, SK::kStride, g, l16), wb[1], dqk[n]);
-                    }
-#pragma unroll
-                    for (int m = 0; m < PT; ++m) {
-                        if (w < 2) dv[m] = M::mma(columns<T>(sm.dy + 16 * m, SV::kStride, g, l16), wa[0], dv[m]);
-                        dv[m] = M::mma(columns<T>(sm.dy + 32 * SV::kStride + 16 * m, SV::kStride, g, l16), wa[1], dv[m]);
-                    }
-                } else {
-                    if (o.dg && head_first && l16 == 0)   // (the queries add M's rows up here)
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            if (j >= w) *reinterpret_cast<f32x4*>(sm.g[gbuf].row[w] + 16 * j + 4 * g) = zero4();
-                    for (int s = 0; s < n_in; ++s) {   // the query's token
-                        float qk = 0.f, yv = 0.f;
-#pragma unroll 2
-                        for (int e = 0; e < N; ++e)
-                            qk = fmaf(Elem<T>::load1(sm.q + s * SK::kStride + e), Elem<T>::load1(sm.k + t * SK::kStride + e), qk);
-#pragma unroll 2
-                        for (int e = 0; e < PB; ++e)
-                            yv = fmaf(Elem<T>::load1(sm.dy + s * SV::kStride + e), Elem<T>::load1(sm.v + t * SV::kStride + e), yv);
-                        const float e = exp2_raw((d.hi[s] - thi) + (d.lo[s] - tlo)) * p.scale;
-                        if (in && s >= t) {
-#pragma unroll
-                            for (int n = 0; n < NT; ++n)
-                                dqk[n] += M::wide(M::four(sm.q + s * SK::kStride + 16 * n + 4 * g)) * (yv * e);
-#pragma unroll
-                            for (int m = 0; m < PT; ++m)
-                                dv[m] += M::wide(M::four(sm.dy + s * SV::kStride + 16 * m + 4 * g)) * (qk * e);
-                            if (s > t && g == 0) asum = fmaf(qk, yv * e, asum);
-                        }
-                    }
+                    wt[j2] = M::cat(h2[0], h2[1]);
                 }
 #pragma unroll
-                for (int m = 0; m < PT; ++m)
+                for (int n = 0; n < NT; ++n) {
+                    sum[n] = M::mma(columns<T>(sm.k + 16 * n, SK::kStride, g, l16), wt[0], sum[n]);
+                    if (w >= 2)
+                        sum[n] = M::mma(columns<T>(sm.k + 32 * SK::kStride + 16 * n, SK::kStride, g, l16), wt[1], sum[n]);
+                }
+            } else {
+                for (int s = 0; s < kLaChunk; ++s) {
+                    const bool pair = in && s <= t && s < n_in;
+                    float m = 0.f;
+                    if (pair) {
+                        const float yv = yv_of(t, s) * weight(t, s);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) dv[m][r] = in ? dv[m][r] : 0.f;
-                store_rows(dv, static_cast<T*>(args()->dv) + u.vat, n_out, vrow);
-            }
-            if (o.dg && head_last) {
-                auto& sg = sm.g[gbuf];
-                const float a = sum_rows4(in ? asum : 0.f), cs = wave_sum(cdot);
-                if (lane == 0) sg.c[wave] = cs;
-                if constexpr (kQueries) {
-                    if (g == 0) sg.a[t] = a;
-                } else {
-                    const float bs = sum_rows4(in ? bsum : 0.f);
-                    if (g == 0) {
-                        sg.col[t] = a;
-                        sg.b[t] = bs;
+                        for (int n = 0; n < NT; ++n)
+                            sum[n] += M::wide(M::four(sm.k + s * SK::kStride + 16 * n + 4 * g)) * yv;
+                        if (s < t && g == 0) m = qk_of(t, s) * yv;
+                    }
+                    asum += m;
+                    m = row16_sum(m);
+                    if (lane == 0) {
+                        float* const to = sm.g[gbuf].col[w] + s;
+                        *to = head_first ? m : *to + m;
                     }
                 }
-                behind = Behind{u.at, u.h, n_in, n_out, gbuf, d.all};
-                waits = true;
-                gbuf ^= 1;
             }
+        } else if constexpr (kRole == kDk) {
+            const float down = d.down[t];
+            Frag vf[PS];
+#pragma unroll
+            for (int j = 0; j < PS; ++j) {
+                const T* const v1 = sm.v + t * SV::kStride + 32 * j + 4 * g;
+                vf[j] = M::cat(M::four(v1), M::four(v1 + 16));
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                f32x4 x = zero4();
+#pragma unroll
+                for (int j = 0; j < PS; ++j)
+                    x = M::mma(columns<T>(sm.ds + 32 * j * SK::kStride + 16 * n, SK::kStride, g, l16), vf[j], x);
+                x *= down;
+                const f32x4 kn = M::wide(M::four(sm.k + t * SK::kStride + 16 * n + 4 * g));
+#pragma unroll
+                for (int r = 0; r < 4; ++r) asum = fmaf(kn[r], x[r], asum);   // b
+                sum[n] += x;
+            }
+            if (!odd) {
+                // ---- and the tile's: [t][s], t from s on
+                Frag wt[2];
+#pragma unroll
+                for (int j = 0; j < PS; ++j) vf[j] = M::rows(sm.v + t * SV::kStride + 32 * j + 8 * g);
+#pragma unroll
+                for (int j2 = 0; j2 < 2; ++j2) {
+                    Half h2[2];
+#pragma unroll
+                    for (int u2 = 0; u2 < 2; ++u2) {
+                        const int j = 2 * j2 + u2;
+                        f32x4 x = zero4();
+                        if (j >= w) {
+#pragma unroll
+                            for (int e = 0; e < PS; ++e)
+                                x = M::mma(M::rows(sm.dy + (16 * j + l16) * SV::kStride + 32 * e + 8 * g), vf[e], x);
+                            x *= decays(d, j, g, thi, tlo, true) * p.scale;
+                            if (j == w)
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) x[r] = 4 * g + r >= l16 ? x[r] : 0.f;
+                        }
+                        h2[u2] = M::half(x);
+                    }
+                    wt[j2] = M::cat(h2[0], h2[1]);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if (w < 2) sum[n] = M::mma(columns<T>(sm.q + 16 * n, SK::kStride, g, l16), wt[0], sum[n]);
+                    sum[n] = M::mma(columns<T>(sm.q + 32 * SK::kStride + 16 * n, SK::kStride, g, l16), wt[1], sum[n]);
+                }
+            } else {
+                for (int s = t; in && s < n_in; ++s) {   // the query's token
+                    const float yv = yv_of(s, t) * weight(s, t);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) sum[n] += M::wide(M::four(sm.q + s * SK::kStride + 16 * n + 4 * g)) * yv;
+                }
+            }
+        } else {
+            const float down = d.down[t];
+            f32x4 dv[PT];
+            Frag kf[KS];
+#pragma unroll
+            for (int j = 0; j < KS; ++j) kf[j] = M::rows(sm.k + t * SK::kStride + 32 * j + 8 * g);
+#pragma unroll
+            for (int m = 0; m < PT; ++m) {
+                dv[m] = zero4();
+#pragma unroll
+                for (int j = 0; j < KS; ++j)
+                    dv[m] = M::mma(M::rows(sm.ds + (16 * m + l16) * SK::kStride + 32 * j + 8 * g), kf[j], dv[m]);
+                dv[m] *= down;
+            }
+            if (!odd) {
+                Frag wt[2];
+#pragma unroll
+                for (int j2 = 0; j2 < 2; ++j2) {
+                    Half h2[2];
+#pragma unroll
+                    for (int u2 = 0; u2 < 2; ++u2) {
+                        const int j = 2 * j2 + u2;
+                        f32x4 x = zero4();
+                        if (j >= w) {
+#pragma unroll
+                            for (int e = 0; e < KS; ++e)
+                                x = M::mma(M::rows(sm.q + (16 * j + l16) * SK::kStride + 32 * e + 8 * g), kf[e], x);
+                            x *= decays(d, j, g, thi, tlo, true) * p.scale;
+                            if (j == w)
+#pragma unroll
+                                for (int r = 0; r < 4; ++r) x[r] = 4 * g + r >= l16 ? x[r] : 0.f;
+                        }
+                        h2[u2] = M::half(x);
+                    }
+                    wt[j2] = M::cat(h2[0], h2[1]);
+                }
+#pragma unroll
+                for (int m = 0; m < PT; ++m) {
+                    if (w < 2) dv[m] = M::mma(columns<T>(sm.dy + 16 * m, SV::kStride, g, l16), wt[0], dv[m]);
+                    dv[m] = M::mma(columns<T>(sm.dy + 32 * SV::kStride + 16 * m, SV::kStride, g, l16), wt[1], dv[m]);
+                }
+            } else {
+                for (int s = t; in && s < n_in; ++s) {
+                    const float qk = qk_of(s, t) * weight(s, t);
+#pragma unroll
+                    for (int m = 0; m < PT; ++m) dv[m] += M::wide(M::four(sm.dy + s * SV::kStride + 16 * m + 4 * g)) * qk;
+                }
+            }
+#pragma unroll
+            for (int m = 0; m < PT; ++m)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) dv[m][r] = in ? dv[m][r] : 0.f;
+            store_rows(dv, static_cast<T*>(args()->dv) + u.vat, n_out, vrow);
+        }
+        if (o.dg && head_last) {
+            auto& sg = sm.g[gbuf];
+            const float a = sum_rows4(in ? asum : 0.f);
+            if constexpr (kRole == kDq) {
+                if (g == 0) sg.a[t] = a;
+            } else {
+                const float cs = wave_sum(cdot);
+                if (lane == 0) sg.c[wave - 4] = cs;
+                if (kRole == kDk && g == 0) sg.b[t] = a;
+            }
+            behind = Behind{u.at, u.h, n_in, n_out, gbuf, d.all};
+            waits = true;
+            gbuf ^= 1;
         }
         // ---- dq or dk, or this part's sums of them, behind the last step (before: no rows)
-        {
+        if constexpr (kRole != kDv) {
             const int n = u.step + 1 == u.steps ? n_out : 0;
             f32x4 x[NT];
 #pragma unroll
             for (int e = 0; e < NT; ++e)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) x[e][r] = in ? dqk[e][r] : 0.f;
+                for (int r = 0; r < 4; ++r) x[e][r] = in ? sum[e][r] : 0.f;
             if (o.split > 1) {
                 const int64_t parts = (p.packed ? p.tokens : (int64_t)p.B * p.T) * krow * u.part;
-                const auto to = rows_of((kQueries ? args()->part_q : args()->part_k) + parts + u.kat, n, krow, N);
+                const auto to = rows_of((kRole == kDq ? args()->part_q : args()->part_k) + parts + u.kat, n, krow, N);
 #pragma unroll
                 for (int e = 0; e < NT; ++e)
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, x[e]), to,
                                                            t * (uint32_t)krow * 4 + (16 * e + 4 * g) * 4, 0, 0);
             } else {
-                store_rows(x, static_cast<T*>(kQueries ? args()->dq : args()->dk) + u.kat, n, krow);
+                store_rows(x, static_cast<T*>(kRole == kDq ? args()->dq : args()->dk) + u.kat, n, krow);
             }
         }
         // The next head's decays, where the other waves still compute.
         if (next.valid && first_of_head(next)) {
             dbuf ^= 1;
-            if (kQueries && wave == 0) put_decays(sm.d[dbuf], lg.get());
+            if (kRole == kDq && wave == 0) put_decays(sm.d[dbuf], lg.get());
         }
         u = next;
         next = after(u);
     }
     if (waits) {
         __syncthreads();
-        if (kQueries && wave == 1) finish_dg(behind);
+        if (kRole == kDq && wave == 1) finish_dg(behind);
     }
     };
-    if (wave < 4) run(Yes());
-    else run(No());
+    if (wave < 4) run(Role<kDq>());
+    else if (wave < 8) run(Role<kDk>());
+    else run(Role<kDv>());
 }
 
 // dq and dk: the sums over the parts of a group's heads, in order.  Four values a thread;
@@ -595,9 +630,8 @@ hipError_t bwd_block(const LaBwdArgs& q, hipStream_t stream) {
     if (e != hipSuccess) return e;
     const int blocks = p.T > 0 ? (int)(((int64_t)p.T + kLaChunk - 1) / kLaChunk) : 1;
     const unsigned units = (unsigned)p.B * blocks * p.G * q.split;
-    // As many workgroups as run at once: two to a compute unit where LDS holds them.
-    const unsigned most = sizeof(LaBwdShared<T, N, PB>) <= 80 * 1024 ? 512 : 256;
-    la_bwd_kernel<T, N, PB><<<units < most ? units : most, kLaThreads, 0, stream>>>(q, blocks);
+    const unsigned most = 256;   // one workgroup to a compute unit
+    la_bwd_kernel<T, N, PB><<<units < most ? units : most, kBwdThreads, 0, stream>>>(q, blocks);
     if ((e = hipGetLastError()) != hipSuccess || q.split == 1) return e;
     const int64_t values = (p.packed ? p.tokens : (int64_t)p.B * p.T) * p.G * N;
     const unsigned half = (unsigned)((values / 4 + 255) / 256);
