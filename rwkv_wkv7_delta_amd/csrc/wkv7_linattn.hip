@@ -53,7 +53,9 @@ __device__ __forceinline__ float* state_at(float* base, const LaArgs& p, int b, 
 // Forward (kReverse = false): S from k and v; reverse: its gradient D, from q and
 // dy: D <- e^{G_end} D + scale sum_t (e^{G_t} dy_t) q_t^T.
 // kSegment: what a segment leaves from zero, and its summed decay.  Else (the
-// reverse only) D behind every tile is written, and the gradient of the first state.
+// reverse only) D behind every tile is written, and the gradient of the first state; and
+// <S, D> with the tile's checkpoint S, from D's 32 bits: rounded as the checkpoints are, it
+// would make dg's error 1.7 times its own rounding.
 // Waves 0 to 3 hold the state, 16 value rows each (of 32: and half of the key columns), and
 // move it on; waves 4 to 7 bring the tiles: two on their way from memory, one on its way to
 // LDS while the others use the one before.
@@ -61,7 +63,7 @@ constexpr int kSweepStage = 256;
 
 template <typename T, int N, int PB, bool kReverse, bool kSegment>
 __global__ __launch_bounds__(kLaThreads) void la_sweep_kernel(const LaArgs p, const T* kk, const T* vv,
-                                                                 const float* first, float* last, T* marks) {
+                                                                 const float* first, float* last, T* marks, float* both) {
     typedef LaMat<T> M;
     typedef LaStage<T, N, kSweepStage, kSweepStage> SK;
     typedef LaStage<T, PB, kSweepStage, kSweepStage> SV;
@@ -106,14 +108,54 @@ __global__ __launch_bounds__(kLaThreads) void la_sweep_kernel(const LaArgs p, co
     const int turns = kDeep ? (tiles + 1) / 2 * 2 : tiles;
     double total = 0;
     if (holds) {
+        // The 16 value rows of a tile's checkpoint; one tile ahead.
+        vu4 part[kMarks ? 1 : NT];
+        LaRows16<T, N> whole;
+        const auto load_mark = [&](int i) __attribute__((always_inline)) {
+            const auto r = buffer_of(static_cast<const T*>(p.ckpt) +
+                                         (((row.ckpt + begin / kLaChunk + tile_of(i)) * p.H + w.h) * p.P + w.p0) * N,
+                                     both && i < tiles ? PB * N * (int)sizeof(T) : 0);
+            if constexpr (kMarks) {
+                whole.load(r, N * sizeof(T), ptile);
+            } else {
+                const uint32_t at = ((ptile + l16) * N + n0 + 4 * g) * (uint32_t)sizeof(T);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if constexpr (sizeof(T) == 2) {
+                        const vu2 x = __builtin_bit_cast(vu2, __builtin_amdgcn_raw_buffer_load_b64(r, at + 32 * n, 0, 0));
+                        part[n] = vu4{x[0], x[1], 0, 0};
+                    } else {
+                        part[n] = __builtin_bit_cast(vu4, __builtin_amdgcn_raw_buffer_load_b128(r, at + 64 * n, 0, 0));
+                    }
+                }
+            }
+        };
+        const auto mark = [&](int n) __attribute__((always_inline)) {   // as the wave holds D
+            if constexpr (kMarks) return M::wide(M::four(s_own[wave] + l16 * LaRows16<T, N>::kStride + 16 * n + 4 * g));
+            else if constexpr (sizeof(T) == 2) return unpack4(__builtin_bit_cast(bf16x4, vu2{part[n][0], part[n][1]}));
+            else return __builtin_bit_cast(f32x4, part[n]);
+        };
+        if (!kSegment) load_mark(0);
         for (int i = 0; i < turns; ++i) {
             const int buf = BUF == 2 ? i & 1 : 0;
             __syncthreads();
             const LaDecay& d = s_d[buf];
             if (!kSegment) {
                 // (of a tile that there is not: nothing)
-                const auto m = buffer_of(marks + (((row.ckpt + begin / kLaChunk + tile_of(i)) * p.H + w.h) * p.P + w.p0) * N,
-                                         i < tiles ? PB * N * (int)sizeof(T) : 0);
+                const int64_t tile = row.ckpt + begin / kLaChunk + tile_of(i);
+                const auto m = buffer_of(marks + ((tile * p.H + w.h) * p.P + w.p0) * N, i < tiles ? PB * N * (int)sizeof(T) : 0);
+                float x = 0.f;
+                if constexpr (kMarks) whole.put(s_own[wave]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const f32x4 e = mark(n);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) x = fmaf(e[q], st[n][q], x);
+                }
+                x = sum_rows4(row16_sum(x));
+                load_mark(i + 1);
+                const auto c = buffer_of(both + ((tile * p.H + w.h) * (p.P / PB) + w.p0 / PB) * 4, both && i < tiles ? 16 : 0);
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), c, lane == 0 ? 4 * wave : kNowhere, 0, 0);
                 store_mark<T, N>(s_own[wave], st, m, ptile, n0);
             }
             if (kSegment) total += d.sum;
@@ -485,7 +527,7 @@ hipError_t fwd_block(const LaArgs& p, hipStream_t stream) {
     const unsigned blocks = (unsigned)p.B * p.H * (p.P / PB);
     if (p.nseg > 1) {
         la_sweep_kernel<T, N, PB, false, true><<<blocks * (p.nseg - 1), kLaThreads, 0, stream>>>(
-            p, static_cast<const T*>(p.k), static_cast<const T*>(p.v), nullptr, p.seg_state, nullptr);
+            p, static_cast<const T*>(p.k), static_cast<const T*>(p.v), nullptr, p.seg_state, nullptr, nullptr);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         la_join_kernel<<<(unsigned)(((size_t)p.B * p.H * p.P * N / 4 + 255) / 256), 256, 0, stream>>>(p, p.s0);
@@ -503,14 +545,14 @@ hipError_t adjoint_block(const LaBwdArgs& q, hipStream_t stream) {
     const T* const dY = static_cast<const T*>(q.dy);
     if (p.nseg > 1) {
         la_sweep_kernel<T, N, PB, true, true><<<blocks * (p.nseg - 1), kLaThreads, 0, stream>>>(
-            p, Q, dY, nullptr, p.seg_state, nullptr);
+            p, Q, dY, nullptr, p.seg_state, nullptr, nullptr);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         la_join_kernel<<<(unsigned)(((size_t)p.B * p.H * p.P * N / 4 + 255) / 256), 256, 0, stream>>>(p, q.dsT);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     la_sweep_kernel<T, N, PB, true, false><<<blocks * p.nseg, kLaThreads, 0, stream>>>(
-        p, Q, dY, q.dsT, q.ds0, static_cast<T*>(q.adj));
+        p, Q, dY, q.dsT, q.ds0, static_cast<T*>(q.adj), q.both);
     return hipGetLastError();
 }
 

@@ -100,6 +100,10 @@ size_t ckpt_bytes(const wkv7_linattn_desc* d) {
     if (tokens_of(d) == 0) return 0;
     return (size_t)tiles_of(d) * d->H * d->P * d->N * (d->dtype == WKV7_BF16 ? 2 : 4);
 }
+size_t both_bytes(const wkv7_linattn_desc* d) {
+    if (d->fixed_decay || tokens_of(d) == 0) return 0;
+    return (size_t)tiles_of(d) * d->H * (d->P / wkv7::la_value_block(d->P)) * 16;
+}
 size_t part_bytes(const wkv7_linattn_desc* d, int split) {
     return split > 1 ? (size_t)split * tokens_of(d) * d->G * d->N * 4 : 0;
 }
@@ -130,7 +134,7 @@ size_t wkv7_linattn_forward_workspace_bytes(const wkv7_linattn_desc* desc) {
 
 size_t wkv7_linattn_backward_workspace_bytes(const wkv7_linattn_desc* desc) {
     if (check(desc) != WKV7_OK) return 0;
-    return pad16(ckpt_bytes(desc)) + segment_bytes(desc, plan(desc, false)) +
+    return pad16(ckpt_bytes(desc)) + both_bytes(desc) + segment_bytes(desc, plan(desc, false)) +
            2 * part_bytes(desc, plan_split(desc));
 }
 
@@ -171,10 +175,12 @@ int wkv7_linattn_backward(const wkv7_linattn_desc* desc, const int32_t* rows, co
     const size_t need = wkv7_linattn_backward_workspace_bytes(desc);
     if (need > 0 && (!workspace || workspace_bytes < need)) return WKV7_ERR_WORKSPACE;
     char* const adj = static_cast<char*>(workspace);
-    char* const seg = adj + pad16(ckpt_bytes(desc));
+    char* const both = adj + pad16(ckpt_bytes(desc));
+    char* const seg = both + both_bytes(desc);
     char* const part = seg + segment_bytes(desc, s);
     const wkv7::LaBwdArgs a{args(desc, rows, q, k, v, g, nullptr, nullptr, nullptr, const_cast<void*>(ckpt), s, seg),
-                            dy, dsT, dq, dk, dv, dg, ds0, adj, split, reinterpret_cast<float*>(part),
+                            dy, dsT, dq, dk, dv, dg, ds0, adj,
+                            both_bytes(desc) ? reinterpret_cast<float*>(both) : nullptr, split, reinterpret_cast<float*>(part),
                             reinterpret_cast<float*>(part + part_bytes(desc, split))};
     const hipStream_t hs = static_cast<hipStream_t>(stream);
     if (!tokens) return ds0 ? from_hip(wkv7::launch_la_adjoint(a, hs)) : WKV7_OK;

@@ -33,7 +33,7 @@ struct LaBwdShared {
     T own[sizeof(T) == 2 ? 12 : 1][sizeof(T) == 2 ? LaRows16<T, (N > PB ? N : PB)>::kSize : 16];
     LaDecay d[2];                                  // of this head and the next
     // For dg, of this head and the one before: sums of M down its columns, by wave; a and M's
-    // sums along its rows; b; parts of <S, D>.
+    // sums along its rows; b; the parts of <S, D>.
     struct {
         float col[4][kLaChunk], a[kLaChunk], b[kLaChunk], c[8];
     } g[2];
@@ -62,27 +62,7 @@ struct LaStateStage {
                 *reinterpret_cast<vu4*>(lds + at / kPieces * kStride + at % kPieces * (16 / (int)sizeof(T))) = w[i];
         }
     }
-    // The lane's part of <this, o>.
-    __device__ __forceinline__ float dot(const LaStateStage& o) const {
-        float x = 0.f;
-        if (kLoads > 0 || (int)threadIdx.x - kBwdFirst < PB * kPieces) {
-#pragma unroll
-            for (int i = 0; i < (kLoads > 0 ? kLoads : 1); ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if constexpr (sizeof(T) == 4) {
-                        x = fmaf(__uint_as_float(w[i][j]), __uint_as_float(o.w[i][j]), x);
-                    } else {
-                        x = fmaf(bf16_lo(w[i][j]), bf16_lo(o.w[i][j]), x);
-                        x = fmaf(bf16_hi(w[i][j]), bf16_hi(o.w[i][j]), x);
-                    }
-                }
-        }
-        return x;
-    }
 };
-
-__device__ __forceinline__ float wave_sum(float x) { return sum_rows4(row16_sum(x)); }
 
 // Decays between the lane's token and those of tile j: in register r, token 16 j + 4 g + r.
 __device__ __forceinline__ f32x4 decays(const LaDecay& d, int j, int g, float hi, float lo, bool later) {
@@ -105,10 +85,12 @@ constexpr int kDq = 0, kDk = 1, kDv = 2;
 // What a workgroup has before it: a tile of one group of heads (or of a part of them), and of
 // these one head and PB of its value rows.
 struct LaUnit {
-    bool valid;
+    // (no gaps between the members: copies of them would go through memory)
+    int valid, part, step, steps;
     int n_in, n_out;        // the tile's tokens, and places that are written
-    int part, step, steps, h;
+    int64_t h;
     int64_t at;             // the tile's first token among all
+    int64_t tile;           // its checkpoint's number
     int64_t kat, vat, sat;  // where its keys, values and states are, in elements
 };
 
@@ -131,11 +113,12 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
     const int g = lane / 16, l16 = lane % 16;
     const int w = wave % 4;
     const int shared = p.H / p.G, per = (shared + o.split - 1) / o.split, pblocks = p.P / PB;   // (1, 2 or 4)
+    const int parts = p.P < 64 ? 4 : p.P / 16;   // of <S, D>
     const int krow = p.G * N, vrow = p.H * p.P;
     // The pointers are read from the kernel's arguments where they are used: kept in scalar
     // registers over the loop, they and the buffers made of them are more than there are.
     typedef const __attribute__((address_space(4))) LaBwdArgs* Args;
-    const auto args = [&] {
+    const auto args = [&]() __attribute__((always_inline)) {
         Args a = (Args)__builtin_amdgcn_kernarg_segment_ptr();
         asm volatile("" : "+s"(a));
         return a;
@@ -143,7 +126,7 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
     const int t = 16 * w + l16;   // the lane's token
     constexpr int kPer = 16 / (int)sizeof(T);
     // Results of the wave's 16 tokens, rows of W, n of the tile's written.
-    const auto store_rows = [&](auto& x, T* to, int n, int64_t stride) {
+    const auto store_rows = [&](auto& x, T* to, int n, int64_t stride) __attribute__((always_inline)) {
         constexpr int W = 16 * (int)(sizeof(x) / sizeof(f32x4));
         const auto r = rows_of(to, n, stride, W);
         const uint32_t bytes = (uint32_t)(stride * (int64_t)sizeof(T));
@@ -155,8 +138,8 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
                 __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, x[e]), r, t * bytes + (16 * e + 4 * g) * 4, 0, 0);
         }
     };
-    const auto first_of_head = [&](const LaUnit& u) { return (u.step & (pblocks - 1)) == 0; };
-    const auto to_next_step = [&](LaUnit& u) {
+    const auto first_of_head = [&](const LaUnit& u) __attribute__((always_inline)) { return (u.step & (pblocks - 1)) == 0; };
+    const auto to_next_step = [&](LaUnit& u) __attribute__((always_inline)) {
         ++u.step;
         u.h += first_of_head(u);
         u.vat += PB;
@@ -164,12 +147,12 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
     };
     // A wave's whole way, by its role (so that the code that waits for loads knows how many
     // stores were issued behind them).
-    auto run = [&](auto role_) {
+    auto run = [&](auto role_) __attribute__((always_inline)) {
     constexpr int kRole = decltype(role_)::value;
     // Units are numbered row by row, tile by tile, part by part, group by group: this
     // workgroup's, and the distance to its next one, digit by digit.
     int at_kh, at_part, at_c, at_b, by_kh, by_part, by_c, by_b;
-    const auto digits = [&](unsigned i, int& kh, int& part, int& c, int& b) {
+    const auto digits = [&](unsigned i, int& kh, int& part, int& c, int& b) __attribute__((always_inline)) {
         kh = (int)(i % p.G);
         i /= p.G;
         part = (int)(i % o.split);
@@ -179,7 +162,7 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
     };
     digits(blockIdx.x, at_kh, at_part, at_c, at_b);
     digits(gridDim.x, by_kh, by_part, by_c, by_b);
-    const auto skip = [&] {
+    const auto skip = [&]() __attribute__((always_inline)) {
         at_kh += by_kh;
         int over = at_kh >= p.G;
         at_kh -= over ? p.G : 0;
@@ -195,9 +178,9 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
     // The next unit with tokens.  A unit is every tile of a row whose number is c0 modulo
     // `blocks` (more than one only where a packed row is longer than the call says); tiles of
     // padding get their zeros here.
-    auto advance = [&]() {
+    auto advance = [&]() __attribute__((always_inline)) {
         LaUnit u;
-        u.valid = false;
+        u.valid = 0;
         for (; at_b < p.B; skip(), tile = -1) {
             const LaRow row = la_row(p.rows, p.packed, p.tokens, p.T, at_b);
             tile = tile < 0 ? at_c : tile + blocks;
@@ -213,9 +196,10 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
             u.h = kh * shared + u.part * per;
             u.kat = u.at * krow + kh * N;
             u.vat = u.at * vrow + u.h * p.P;
-            u.sat = ((row.ckpt + tile) * vrow + u.h * p.P) * N;
+            u.tile = row.ckpt + tile;
+            u.sat = (u.tile * vrow + u.h * p.P) * N;
             if (u.n_in > 0) {
-                u.valid = true;
+                u.valid = 1;
                 break;
             }
             for (; u.step < u.steps; to_next_step(u)) {
@@ -228,8 +212,8 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
             for (int e = threadIdx.x; e < u.n_out * N; e += kBwdThreads) {
                 const int64_t k = u.kat + (int64_t)(e / N) * krow + e % N;
                 if (o.split > 1) {
-                    const int64_t parts = (p.packed ? p.tokens : (int64_t)p.B * p.T) * krow * u.part;
-                    args()->part_q[parts + k] = args()->part_k[parts + k] = 0.f;
+                    const int64_t skipped = (p.packed ? p.tokens : (int64_t)p.B * p.T) * krow * u.part;
+                    args()->part_q[skipped + k] = args()->part_k[skipped + k] = 0.f;
                 } else {
                     Elem<T>::store1(static_cast<T*>(args()->dq) + k, 0.f);
                     Elem<T>::store1(static_cast<T*>(args()->dk) + k, 0.f);
@@ -242,12 +226,16 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
     SV rv, ry;
     LaStateStage<T, N, PB> rs, rd;
     LaLog<T> lg;
-    auto load = [&](const LaUnit& u) {
+    float both1 = 0.f;   // (of the next unit)
+    auto load = [&](const LaUnit& u) __attribute__((always_inline)) {
         const int n = u.valid ? u.n_in : 0, n_qk = u.step == 0 ? n : 0;
         const uint32_t kb = (uint32_t)krow * sizeof(T), vb = (uint32_t)vrow * sizeof(T);
         const Args a = args();
         if constexpr (kRole == kDq) {
-            lg.load(p, u.at, u.h, n);
+            lg.load(p, u.at, (int)u.h, n);
+            // with a head's first step, its parts of <S, D>, one to a lane
+            const auto r = buffer_of(a->both + (u.tile * p.H + u.h) * parts, o.dg && n > 0 && first_of_head(u) ? 4 * parts : 0);
+            both1 = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, 4 * lane, 0, 0));
             return;
         }
         rq.load(rows_of(static_cast<const T*>(a->f.q) + u.kat, n_qk, krow, N), kb);
@@ -260,14 +248,13 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
     // dg of a head once the sums over its tile are in LDS, by one wave.  Lane l: what counts
     // for token 63 - l, from behind it; what counts for token l, from before it.  In 64 bits:
     // the rows and columns of M cancel where both lie on one side.
-    struct Behind {   // the head whose dg is still to be written
-        int64_t at;
-        int h, n_in, n_out, buf;
-        float all;
-    };
-    auto finish_dg = [&](const Behind& k) {
+    // (the head whose dg is still to be written)
+    int64_t behind_at = 0;
+    int behind_h = 0, behind_in = 0, behind_out = 0, behind_buf = 0;
+    float behind_all = 0.f;
+    auto finish_dg = [&]() __attribute__((always_inline)) {
         const int u = 63 - lane;
-        const auto& sg = sm.g[k.buf];
+        const auto& sg = sm.g[behind_buf];
         double x = sg.a[u];
 #pragma unroll
         for (int j = 0; j < 4; ++j) x -= u < 16 * j + 16 ? (double)sg.col[j][u] : 0.0;
@@ -275,11 +262,11 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
         const double y = wave_running_sum(lane > 0 ? (double)sg.b[lane - 1] : 0.0);
         double both = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) both += sg.c[j];
-        const float dg = (float)(x + __shfl(y, u) + k.all * both);
-        if (u < k.n_out) Elem<T>::store1(static_cast<T*>(args()->dg) + (k.at + u) * p.H + k.h, u < k.n_in ? dg : 0.f);
+        for (int j = 0; j < 8; ++j) both += sg.c[j];   // (0 behind the last)
+        const float dg = (float)(x + __shfl(y, u) + behind_all * both);
+        if (u < behind_out) Elem<T>::store1(static_cast<T*>(args()->dg) + (behind_at + u) * p.H + behind_h, u < behind_in ? dg : 0.f);
     };
-    const auto after = [&](const LaUnit& u) {
+    const auto after = [&](const LaUnit& u) __attribute__((always_inline)) {
         LaUnit n = u;
         if (!u.valid) return n;
         to_next_step(n);
@@ -292,9 +279,8 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
     if (kRole == kDq && wave == 0) put_decays(sm.d[0], lg.get());
     int dbuf = 0, gbuf = 0;
     bool waits = false;   // a head's dg
-    Behind behind;
     f32x4 sum[NT];        // dq or dk of the lane's token
-    float asum = 0.f, cdot = 0.f;
+    float asum = 0.f, csum = 0.f;
     bool odd_qk = false;
     while (u.valid) {
         const int n_in = u.n_in, n_out = u.n_out;
@@ -310,7 +296,8 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
 #pragma unroll
             for (int n = 0; n < NT; ++n) sum[n] = zero4();
         }
-        if (head_first) asum = cdot = 0.f;
+        if (head_first) asum = csum = 0.f;
+        csum += both1;
         if constexpr (kRole != kDq) {
             rv.store(sm.v);
             ry.store(sm.dy);
@@ -318,11 +305,10 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
             rd.store(sm.ds);
             const bool odd_lane = __builtin_amdgcn_ballot_w64(odd_qk || rv.odd() || ry.odd()) != 0;
             if (lane == 0) sm.odd[wave - 4] = odd_lane;
-            cdot += rs.dot(rd);
         }
         __syncthreads();
         load(next);
-        if (kRole == kDq && waits && wave == 1) finish_dg(behind);
+        if (kRole == kDq && waits && wave == 1) finish_dg();
         waits = false;
         const LaDecay& d = sm.d[dbuf];
         const bool odd = any_odd(sm.odd);
@@ -553,12 +539,16 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
             const float a = sum_rows4(in ? asum : 0.f);
             if constexpr (kRole == kDq) {
                 if (g == 0) sg.a[t] = a;
-            } else {
-                const float cs = wave_sum(cdot);
-                if (lane == 0) sg.c[wave - 4] = cs;
-                if (kRole == kDk && g == 0) sg.b[t] = a;
+                if (wave == 0 && lane < 8) sg.c[lane] = csum;
+            } else if (kRole == kDk && g == 0) {
+                sg.b[t] = a;
             }
-            behind = Behind{u.at, u.h, n_in, n_out, gbuf, d.all};
+            behind_at = u.at;
+            behind_h = (int)u.h;
+            behind_in = n_in;
+            behind_out = n_out;
+            behind_buf = gbuf;
+            behind_all = d.all;
             waits = true;
             gbuf ^= 1;
         }
@@ -571,8 +561,8 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
 #pragma unroll
                 for (int r = 0; r < 4; ++r) x[e][r] = in ? sum[e][r] : 0.f;
             if (o.split > 1) {
-                const int64_t parts = (p.packed ? p.tokens : (int64_t)p.B * p.T) * krow * u.part;
-                const auto to = rows_of((kRole == kDq ? args()->part_q : args()->part_k) + parts + u.kat, n, krow, N);
+                const int64_t skipped = (p.packed ? p.tokens : (int64_t)p.B * p.T) * krow * u.part;
+                const auto to = rows_of((kRole == kDq ? args()->part_q : args()->part_k) + skipped + u.kat, n, krow, N);
 #pragma unroll
                 for (int e = 0; e < NT; ++e)
                     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, x[e]), to,
@@ -591,7 +581,7 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
     }
     if (waits) {
         __syncthreads();
-        if (kRole == kDq && wave == 1) finish_dg(behind);
+        if (kRole == kDq && wave == 1) finish_dg();
     }
     };
     if (wave < 4) run(Role<kDq>());

@@ -39,6 +39,8 @@ struct LaBwdArgs {
     void *dq, *dk, *dv, *dg;    // dg null with constant decays
     float* ds0;                 // may be null
     void* adj;                  // gradient of the state behind every tile, laid out as the checkpoints
+    // Parts of <S, D> of every tile and head, fp32 [tiles][H][value blocks][4]; null without dg.
+    float* both;
     // Heads of a group in `split` parts (1: none), each with its own partial sums
     // of dq and dk, fp32 [split][tokens][G][N] both.
     int split;
