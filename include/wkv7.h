@@ -744,8 +744,8 @@ int wkv7_gnorm_backward(const wkv7_gnorm_desc* desc, const float* gamma, const f
  * A serving batch keeps the states of its sequences in a cache [planes][slots][row]
  * (planes: layers, or 1), row_bytes each of any type, 16-byte aligned at its start.
  * Rows of a multiple of 16 bytes move fastest.  slots <= 2^22, planes <= 2^20, and at
- * most 2^23 workgroups (rows moved x planes x 1024 pieces of a row, of 16, 4, 2 or 1
- * bytes as row_bytes allows).  Lists lie on the device and are not checked on the host.
+ * most 2^23 workgroups (rows moved x planes x 1024 pieces of 16 bytes of a row).
+ * Lists lie on the device and are not checked on the host.
  */
 
 /* In every plane, for i = 0 .. n - 1 in order: slot dst[i] of pool takes what slot src[i]

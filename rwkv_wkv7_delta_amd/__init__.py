@@ -17,7 +17,10 @@ Beside the recurrence stand the two operators of a state-space mixing layer
 (``mixers.py``): the short causal convolution (``conv_forward``,
 ``conv_backward``, ``conv_step``; at two taps the token shift) and the selective
 scan (``ssm_forward``, ``ssm_backward``, ``ssm_step``), whose training forward
-keeps state checkpoints in 32 or 8 bits.
+keeps state checkpoints in 32 or 8 bits; linear attention with one decay per head
+(``linattn.py``: ``linattn_forward``, ``linattn_backward``, ``linattn_step``), the
+group norm behind a read-out (``norm.py``: ``gnorm_forward``, ``gnorm_backward``) and
+the slots of a cache of states (``slots.py``: ``slots_copy``, ``slots_compact``).
 """
 
 from __future__ import annotations

@@ -32,7 +32,7 @@ int check(const wkv7_gnorm_desc* d) {
 // (four took more registers than there are in the backward).  As many groups side by side as 512 threads hold, of
 // several rows if a row has fewer.  Forward about 8192 workgroups; backward 512, each going
 // over as many rows as that leaves: each leaves a partial row of the sums for gamma and
-// beta (2048, a partial row for each row side by side: 318 us where 512 take @@, (16384, 2048)
+// beta (2048, a partial row for each row side by side: 318 us where 512 take 100, (16384, 2048)
 // in bf16).
 wkv7::GnPlan plan(const wkv7_gnorm_desc* d, bool backward) {
     wkv7::GnPlan p;

@@ -10,7 +10,8 @@
 // so each tensor is read once.  P lanes take a group, K pieces of V channels each; a
 // workgroup takes as many groups (of one or several rows) as make it full, always the
 // same channels, so that gamma, beta and the sums of their gradients stay where they
-// are over the rows.
+// are over the rows.  32768 rows of 40 groups of 64 with a gate behind, bf16: 101 us,
+// 5.0 TB/s (a copy of 1 GiB reaches 5.1).
 #pragma once
 
 #include "wkv7_gnorm_internal.h"

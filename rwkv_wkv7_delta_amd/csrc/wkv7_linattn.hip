@@ -8,6 +8,12 @@
 //   y_t = scale (e^{G_t} S q_t + sum_{s <= t} e^{G_t - G_s} (q_t . k_s) v_s)
 //   S  <- e^{G_end} S + sum_s (e^{G_end - G_s} v_s) k_s^T
 // which are plain matrix products: a scalar decay only scales their rows.
+//
+// Bound by HBM with as many workgroups as compute units: (8, 4096) tokens, 32 heads of 64,
+// bf16: 127 us, 4.3 TB/s; reading and writing the same bytes in the same order, without
+// arithmetic, takes 123.  With fewer, by a tile's chain of products, exponentials and one
+// barrier, 2 us (fp32 4.5).  A tile of 64 tokens: its products with the state and within
+// itself are as much work, 16 KiB of keys and values keep it in flight.
 
 #include "wkv7_linattn_device.h"
 
@@ -50,6 +56,8 @@ __device__ __forceinline__ float* state_at(float* base, const LaArgs& p, int b, 
 }
 
 // ---- the sweep over states alone ------------------------------------------------
+// (8, 4096) tokens, 40 heads of 64, bf16, in reverse with checkpoints: 191 us, 3.5 TB/s (what
+// 320 workgroups on 256 units reach in this order).
 // Forward (kReverse = false): S from k and v; reverse: its gradient D, from q and
 // dy: D <- e^{G_end} D + scale sum_t (e^{G_t} dy_t) q_t^T.
 // kSegment: what a segment leaves from zero, and its summed decay.  Else (the
@@ -470,7 +478,8 @@ __global__ __launch_bounds__(kLaThreads) void la_fwd_kernel(const LaArgs p) {
 
 // ---- one token ------------------------------------------------------------------
 // N / 4 lanes per state row, four columns each; 4096 / N rows a workgroup (four of
-// a lane's 16-byte loads in flight).  Bound by the states' bytes.
+// a lane's 16-byte loads in flight).  Bound by the states' bytes: 256 rows of 40 heads of
+// 64 x 64 take 73 us, 4.6 TB/s.
 template <typename T, int N>
 __global__ __launch_bounds__(256) void la_step_kernel(const LaStepArgs p) {
     constexpr int kLanes = N / 4, kRows = 4096 / N, kEach = 256 / kLanes;

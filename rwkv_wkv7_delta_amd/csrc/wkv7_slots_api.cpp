@@ -19,13 +19,11 @@ int check(int32_t planes, int32_t slots, int64_t row_bytes) {
     if (slots > (1 << 22) || planes > (1 << 20) || row_bytes > ((int64_t)1 << 40)) return WKV7_ERR_UNSUPPORTED;
     return WKV7_OK;
 }
-// At most 2^23 workgroups (of rows, planes and 1024 pieces of a row, of one byte at worst).
+// At most 2^23 workgroups (of rows, planes and 1024 pieces of 16 bytes of a row).
 bool grid_fits(int64_t rows, int32_t planes, int64_t row_bytes) {
-    const int64_t parts = (row_bytes + 1023) / 1024;
-    const int64_t small = row_bytes % 16 == 0 ? (parts + 15) / 16 : row_bytes % 4 == 0 ? (parts + 3) / 4
-                          : row_bytes % 2 == 0 ? (parts + 1) / 2 : parts;
-    if (rows == 0 || planes == 0 || small == 0) return true;
-    return rows * planes <= ((int64_t)1 << 23) / small;
+    const int64_t parts = (row_bytes + 16383) / 16384;
+    if (rows == 0 || planes == 0 || parts == 0) return true;
+    return rows * planes <= ((int64_t)1 << 23) / parts;
 }
 
 }  // namespace

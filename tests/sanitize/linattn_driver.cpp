@@ -68,8 +68,7 @@ hipError_t launch_gnorm_forward(const GnArgs& p, hipStream_t) { return gnorm(p);
 hipError_t launch_gnorm_backward(const GnArgs& p, hipStream_t) { return gnorm(p); }
 static hipError_t slots(const SlotsArgs& p, int64_t rows) {
     ++launches;
-    const int64_t piece = p.bytes % 16 == 0 ? 16 : p.bytes % 4 == 0 ? 4 : p.bytes % 2 == 0 ? 2 : 1;
-    check((p.bytes / piece + 1023) / 1024 * p.planes * rows * 256 <= kThreads, "slots threads");
+    check(((p.bytes + 15) / 16 + 1023) / 1024 * p.planes * rows * 256 <= kThreads, "slots threads");
     return hipSuccess;
 }
 hipError_t launch_slots_copy(const SlotsArgs& p, hipStream_t) { return slots(p, p.n); }

@@ -167,7 +167,11 @@ def test_linattn_workspace_and_sizes(L):
     many = wk.LinattnDesc(**dict(LA_OK, B=8, T=4096, H=32, G=32))
     assert L.wkv7_linattn_forward_workspace_bytes(C(many)) == 0
     assert L.wkv7_linattn_ckpt_bytes(C(many)) == 8 * 64 * 32 * 64 * 64 * 2
-    assert L.wkv7_linattn_backward_workspace_bytes(C(many)) == L.wkv7_linattn_ckpt_bytes(C(many))
+    # the gradient of the state behind every tile, and four parts of a product for each tile and head
+    back = L.wkv7_linattn_ckpt_bytes(C(many))
+    assert L.wkv7_linattn_backward_workspace_bytes(C(many)) == back + 8 * 64 * 32 * 16
+    many.fixed_decay = 1
+    assert L.wkv7_linattn_backward_workspace_bytes(C(many)) == back
     packed = wk.LinattnDesc(**dict(LA_OK, B=3, T=100, packed=1, tokens=130, N=32, dtype=wk.WKV7_F32))
     assert L.wkv7_linattn_ckpt_bytes(C(packed)) == (130 // 64 + 3) * 4 * 64 * 32 * 4
     assert wk.linattn_ckpt_shape(3, 100, 4, 64, 32, 130) == (5, 4, 64, 32)
