@@ -411,10 +411,12 @@ __global__ __launch_bounds__(kLaThreads) void la_fwd_kernel(const LaArgs p) {
                         for (int n = 0; n < N; ++n)
                             a = fmaf(Elem<T>::load1(sk + s * SK::kStride + n), Elem<T>::load1(own + l16 * SQ::kStride + n), a);
                         a *= exp2_raw((thi - d.hi[s]) + (tlo - d.lo[s]));
-                        if (s <= t)
 #pragma unroll
-                            for (int pt = 0; pt < PT; ++pt)
-                                o[pt] += M::wide(M::four(sv + s * SV::kStride + 16 * pt + 4 * g)) * a;
+                        for (int pt = 0; pt < PT; ++pt) {
+                            const f32x4 x = M::wide(M::four(sv + s * SV::kStride + 16 * pt + 4 * g)) * a;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) o[pt][q] += s <= t ? x[q] : 0.f;
+                        }
                     }
                 }
                 // nothing of a state that is not finite behind the row's last token

@@ -51,19 +51,19 @@ struct LaStateStage {
     static constexpr int kLoads = PB * kPieces / kBwdStage;
     static constexpr int kStride = N + 16 / (int)sizeof(T);
     vu4 w[kLoads > 0 ? kLoads : 1];
+    __device__ __forceinline__ static int piece(int i) { return (i * kBwdStage + threadIdx.x - kBwdFirst) % (PB * kPieces); }
     // Rows are one behind the other in memory; none where there is no tile.
     __device__ __forceinline__ void load(const T* p, bool some) {
         const auto r = buffer_of(p, some ? PB * N * (int)sizeof(T) : 0);
 #pragma unroll
         for (int i = 0; i < (kLoads > 0 ? kLoads : 1); ++i)
-            w[i] = __builtin_bit_cast(vu4, __builtin_amdgcn_raw_buffer_load_b128(r, (i * kBwdStage + threadIdx.x - kBwdFirst) * 16, 0, 0));
+            w[i] = __builtin_bit_cast(vu4, __builtin_amdgcn_raw_buffer_load_b128(r, piece(i) * 16, 0, 0));
     }
     __device__ __forceinline__ void store(T* lds) const {
 #pragma unroll
         for (int i = 0; i < (kLoads > 0 ? kLoads : 1); ++i) {
-            const int at = i * kBwdStage + threadIdx.x - kBwdFirst;
-            if (kLoads > 0 || at < PB * kPieces)
-                *reinterpret_cast<vu4*>(lds + at / kPieces * kStride + at % kPieces * (16 / (int)sizeof(T))) = w[i];
+            const int at = piece(i);
+            *reinterpret_cast<vu4*>(lds + at / kPieces * kStride + at % kPieces * (16 / (int)sizeof(T))) = w[i];
         }
     }
 };
@@ -128,7 +128,6 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
         return a;
     };
     const int t = 16 * w + l16;   // the lane's token
-    constexpr int kPer = 16 / (int)sizeof(T);
     // Results of the wave's 16 tokens, rows of W, n of the tile's written.
     const auto store_rows = [&](auto& x, T* to, int n, int64_t stride) __attribute__((always_inline)) {
         constexpr int W = 16 * (int)(sizeof(x) / sizeof(f32x4));
@@ -140,6 +139,17 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
 #pragma unroll
             for (int e = 0; e < W / 16; ++e)
                 __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, x[e]), r, t * bytes + (16 * e + 4 * g) * 4, 0, 0);
+        }
+    };
+    // n rows of W zeros, by all threads.
+    const auto zero_rows = [&](auto* to, int n, int64_t stride, int W) __attribute__((always_inline)) {
+        constexpr int kSize = (int)sizeof(*to);
+        const auto r = rows_of(to, n, stride, W);
+        const int pieces = W * kSize / 16;
+        for (int from = 0; from < kLaChunk * pieces; from += kBwdThreads) {
+            const int e = from + (int)threadIdx.x, row = e / pieces;
+            __builtin_amdgcn_raw_buffer_store_b128(vu4{0, 0, 0, 0}, r, row < kLaChunk
+                ? row * (uint32_t)(stride * kSize) + e % pieces * 16 : kNowhere, 0, 0);
         }
     };
     const auto first_of_head = [&](const LaUnit& u) __attribute__((always_inline)) { return (u.step & (pblocks - 1)) == 0; };
@@ -206,22 +216,22 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
                 u.valid = 1;
                 break;
             }
+            // (through buffers, which end behind the last row: the lanes stay together)
             for (; u.step < u.steps; to_next_step(u)) {
-                T* const dvp = static_cast<T*>(args()->dv) + u.vat;
-                for (int e = threadIdx.x; e < u.n_out * (PB / kPer); e += kBwdThreads)
-                    *reinterpret_cast<vu4*>(dvp + (int64_t)(e / (PB / kPer)) * vrow + e % (PB / kPer) * kPer) = vu4{0, 0, 0, 0};
-                if (o.dg && first_of_head(u) && (int)threadIdx.x < u.n_out)
-                    Elem<T>::store1(static_cast<T*>(args()->dg) + (u.at + threadIdx.x) * p.H + u.h, 0.f);
+                zero_rows(static_cast<T*>(args()->dv) + u.vat, u.n_out, vrow, PB);
+                if (!o.dg || !first_of_head(u)) continue;
+                const auto r = rows_of(static_cast<T*>(args()->dg) + u.at * p.H + u.h, u.n_out, p.H, 1);
+                const uint32_t at = threadIdx.x < kLaChunk ? threadIdx.x * p.H * (uint32_t)sizeof(T) : kNowhere;
+                if constexpr (sizeof(T) == 2) __builtin_amdgcn_raw_buffer_store_b16((unsigned short)0, r, at, 0, 0);
+                else __builtin_amdgcn_raw_buffer_store_b32(0u, r, at, 0, 0);
             }
-            for (int e = threadIdx.x; e < u.n_out * N; e += kBwdThreads) {
-                const int64_t k = u.kat + (int64_t)(e / N) * krow + e % N;
-                if (o.split > 1) {
-                    const int64_t skipped = (p.packed ? p.tokens : (int64_t)p.B * p.T) * krow * u.part;
-                    args()->part_q[skipped + k] = args()->part_k[skipped + k] = 0.f;
-                } else {
-                    Elem<T>::store1(static_cast<T*>(args()->dq) + k, 0.f);
-                    Elem<T>::store1(static_cast<T*>(args()->dk) + k, 0.f);
-                }
+            if (o.split > 1) {
+                const int64_t to = (p.packed ? p.tokens : (int64_t)p.B * p.T) * krow * u.part + u.kat;
+                zero_rows(args()->part_q + to, u.n_out, krow, N);
+                zero_rows(args()->part_k + to, u.n_out, krow, N);
+            } else {
+                zero_rows(static_cast<T*>(args()->dq) + u.kat, u.n_out, krow, N);
+                zero_rows(static_cast<T*>(args()->dk) + u.kat, u.n_out, krow, N);
             }
         }
         return u;
@@ -337,6 +347,16 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
         const auto weight = [&](int late, int early) {
             return exp2_raw((d.hi[late] - d.hi[early]) + (d.lo[late] - d.lo[early])) * p.scale;
         };
+        // A row times x, where there is such a pair: chosen, not branched around, so that all
+        // lanes stay together beside the matrix instructions.
+        const auto add = [&](bool pair, const T* from, float x, auto& to) __attribute__((always_inline)) {
+#pragma unroll
+            for (int n = 0; n < (int)(sizeof(to) / sizeof(f32x4)); ++n) {
+                const f32x4 y = M::wide(M::four(from + 16 * n + 4 * g)) * x;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) to[n][r] += pair ? y[r] : 0.f;
+            }
+        };
         if constexpr (kRole == kDq) {
             // ---- the state's part
             const float up = d.up[t] * p.scale;
@@ -393,7 +413,7 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
 #pragma unroll
                                 for (int r = 0; r < 4; ++r) m[r] = row16_sum(m[r]);
                                 f32x4* const to = reinterpret_cast<f32x4*>(sm.g[gbuf].col[w] + 16 * j + 4 * g);
-                                if (l16 == 0) *to = head_first ? m : *to + m;
+                                *to = head_first ? m : *to + m;   // (16 lanes alike: no branch)
                             }
                         }
                         // Rounded to the tokens' type, as the weights of the forward: half a step of
@@ -411,20 +431,14 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
             } else {
                 for (int s = 0; s < kLaChunk; ++s) {
                     const bool pair = in && s <= t && s < n_in;
-                    float m = 0.f;
-                    if (pair) {
-                        const float yv = yv_of(t, s) * weight(t, s);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            sum[n] += M::wide(M::four(sm.k + s * SK::kStride + 16 * n + 4 * g)) * yv;
-                        if (s < t && g == 0) m = qk_of(t, s) * yv;
-                    }
-                    asum += m;
+                    const float yv = yv_of(t, s) * weight(t, s);
+                    add(pair, sm.k + s * SK::kStride, yv, sum);
+                    float m = qk_of(t, s) * yv;
+                    m = pair && s < t ? m : 0.f;
+                    asum += g == 0 ? m : 0.f;
                     m = row16_sum(m);
-                    if (lane == 0) {
-                        float* const to = sm.g[gbuf].col[w] + s;
-                        *to = head_first ? m : *to + m;
-                    }
+                    float* const to = sm.g[gbuf].col[w] + s;
+                    *to = head_first ? m : *to + m;   // (64 lanes alike)
                 }
             }
         } else if constexpr (kRole == kDk) {
@@ -478,11 +492,8 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
                     sum[n] = M::mma(columns<T>(sm.q + 32 * SK::kStride + 16 * n, SK::kStride, g, l16), wt[1], sum[n]);
                 }
             } else {
-                for (int s = t; in && s < n_in; ++s) {   // the query's token
-                    const float yv = yv_of(s, t) * weight(s, t);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) sum[n] += M::wide(M::four(sm.q + s * SK::kStride + 16 * n + 4 * g)) * yv;
-                }
+                for (int s = 0; s < n_in; ++s)   // the query's token
+                    add(in && s >= t, sm.q + s * SK::kStride, yv_of(s, t) * weight(s, t), sum);
             }
         } else {
             const float down = d.down[t];
@@ -526,11 +537,8 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
                     dv[m] = M::mma(columns<T>(sm.dy + 32 * SV::kStride + 16 * m, SV::kStride, g, l16), wt[1], dv[m]);
                 }
             } else {
-                for (int s = t; in && s < n_in; ++s) {
-                    const float qk = qk_of(s, t) * weight(s, t);
-#pragma unroll
-                    for (int m = 0; m < PT; ++m) dv[m] += M::wide(M::four(sm.dy + s * SV::kStride + 16 * m + 4 * g)) * qk;
-                }
+                for (int s = 0; s < n_in; ++s)
+                    add(in && s >= t, sm.dy + s * SV::kStride, qk_of(s, t) * weight(s, t), dv);
             }
 #pragma unroll
             for (int m = 0; m < PT; ++m)

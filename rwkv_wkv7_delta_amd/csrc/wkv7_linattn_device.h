@@ -192,22 +192,22 @@ struct LaStage {
     static constexpr int kPieces = W * (int)sizeof(T) / 16;          // per row
     static constexpr int kRowsPer = kThreads / kPieces;            // rows of one load of the workgroup
     static constexpr int kLoads = kLaChunk > kRowsPer ? kLaChunk / kRowsPer : 1;
-    static constexpr bool kAll = kRowsPer <= kLaChunk;               // else the last threads have no piece
     static constexpr int kStride = W + 16 / (int)sizeof(T);          // elements of an LDS row: 16 bytes apart in the banks
     vu4 w[kLoads];
 
+    // (With more threads than pieces several take the same one: no branch around the store.)
+    __device__ __forceinline__ static uint32_t piece() { return (threadIdx.x - kFirst) % (kLaChunk * kPieces); }
     __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t r, uint32_t row_bytes) {
-        const uint32_t me = threadIdx.x - kFirst, at = me / kPieces * row_bytes + me % kPieces * 16;
+        const uint32_t me = piece(), at = me / kPieces * row_bytes + me % kPieces * 16;
 #pragma unroll
         for (int i = 0; i < kLoads; ++i)
             w[i] = __builtin_bit_cast(vu4, __builtin_amdgcn_raw_buffer_load_b128(r, at + i * kRowsPer * row_bytes, 0, 0));
     }
     __device__ __forceinline__ void store(T* lds) const {
-        const uint32_t me = threadIdx.x - kFirst;
+        const uint32_t me = piece();
         T* const p = lds + me / kPieces * kStride + me % kPieces * (16 / (int)sizeof(T));
-        if (kAll || me < kLaChunk * kPieces)
 #pragma unroll
-            for (int i = 0; i < kLoads; ++i) *reinterpret_cast<vu4*>(p + i * kRowsPer * kStride) = w[i];
+        for (int i = 0; i < kLoads; ++i) *reinterpret_cast<vu4*>(p + i * kRowsPer * kStride) = w[i];
     }
     // Whether any of the lane's values is infinite or NaN.
     __device__ __forceinline__ bool odd() const {
