@@ -654,8 +654,9 @@ size_t wkv7_linattn_ckpt_bytes(const wkv7_linattn_desc* desc);
 
 /* Device scratch: the forward's holds the states of its time segments, if there are
    any; the backward's as many bytes as the checkpoints (the gradient of the state
-   behind every tile), its own segments' states, and where heads share keys and tiles
-   are few, partial sums of dq and dk.  0 where none is needed. */
+   behind every tile), its own segments' states, parts of the products of states and
+   their gradients for dg, and where heads share keys and tiles are few, partial sums of
+   dq and dk.  0 where none is needed. */
 size_t wkv7_linattn_forward_workspace_bytes(const wkv7_linattn_desc* desc);
 size_t wkv7_linattn_backward_workspace_bytes(const wkv7_linattn_desc* desc);
 
@@ -690,7 +691,7 @@ int wkv7_linattn_backward(const wkv7_linattn_desc* desc, const int32_t* rows, co
 
 /* One token on resident states: q, k [B][G][N], v, y [B][H][P], g [B][H] or fp32 [H];
    state fp32 [nslots][H][P][N], read and overwritten where row b's slot is
-   slots[b] (int32 [B], 4-byte aligned; NULL: slot b, nslots at least B).  A row whose
+   slots[b] (int32 [B], B <= 65536, 4-byte aligned; NULL: slot b, nslots at least B).  A row whose
    slot is not in [0, nslots), or is an earlier row's, touches no state and gets y = 0.
    The descriptor is checked as for a prompt, T has no other effect; packed is refused. */
 int wkv7_linattn_step(const wkv7_linattn_desc* desc, const int32_t* slots, int32_t nslots, const void* q,
@@ -752,7 +753,7 @@ int wkv7_gnorm_backward(const wkv7_gnorm_desc* desc, const float* gamma, const f
    of `from` holds (pool itself, from_slots = slots, or a cache of from_slots slots that
    does not overlap it), or zeros where src[i] is -1.  A pair with a slot that does not
    exist is left out.  In order means: a pair reads what the pairs before it wrote, and of
-   two with one target the later stays.  Pairs that do not touch each other are copied at
+   two with one target the later stays.  n <= 65536.  Pairs that do not touch each other are copied at
    once; else one after the other, which takes longer. */
 int wkv7_slots_copy(int32_t planes, int32_t slots, int64_t row_bytes, int32_t n, const int32_t* src,
                     const int32_t* dst, const void* from, int32_t from_slots, void* pool, void* stream);

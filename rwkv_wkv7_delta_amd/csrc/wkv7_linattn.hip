@@ -10,10 +10,10 @@
 // which are plain matrix products: a scalar decay only scales their rows.
 //
 // Bound by HBM with as many workgroups as compute units: (8, 4096) tokens, 32 heads of 64,
-// bf16: 127 us, 4.3 TB/s; reading and writing the same bytes in the same order, without
+// bf16: 125 us, 4.3 TB/s; reading and writing the same bytes in the same order, without
 // arithmetic, takes 123.  With fewer, by a tile's chain of products, exponentials and one
-// barrier, 2 us (fp32 4.5).  A tile of 64 tokens: its products with the state and within
-// itself are as much work, 16 KiB of keys and values keep it in flight.
+// barrier, 2.4 us (fp32, N = 32, 5).  64 tokens a tile: at N = P = 64 its products with the
+// state and within itself are as much work as each other.
 
 #include "wkv7_linattn_device.h"
 
@@ -56,7 +56,7 @@ __device__ __forceinline__ float* state_at(float* base, const LaArgs& p, int b, 
 }
 
 // ---- the sweep over states alone ------------------------------------------------
-// (8, 4096) tokens, 40 heads of 64, bf16, in reverse with checkpoints: 191 us, 3.5 TB/s (what
+// (8, 4096) tokens, 40 heads of 64, bf16, in reverse with checkpoints: 194 us, 3.5 TB/s (what
 // 320 workgroups on 256 units reach in this order).
 // Forward (kReverse = false): S from k and v; reverse: its gradient D, from q and
 // dy: D <- e^{G_end} D + scale sum_t (e^{G_t} dy_t) q_t^T.

@@ -63,7 +63,7 @@ struct Plan {
 // units, as many segments as fill them, if that is worth a first sweep over the states and
 // two more launches.  In tenths of a microsecond, measured where memory is not the limit: a
 // tile takes 20 (fp32 45) read out and 12 (20) in a sweep over states alone, the launches 150.
-// (1, 16384) tokens and 12 heads of 64 in bf16: 22 segments 56 us, 43 of them 65, 11 of them
+// (1, 16384) tokens and 12 heads of 64 in bf16: 20 segments 55 us, 43 of them 65, 11 of them
 // 84; (4, 1024) tokens, 12 heads: forward in 5 segments 25 us, without 32, and the reverse
 // sweep 20 and 19.
 Plan plan(const wkv7_linattn_desc* d, bool read_out) {
@@ -192,6 +192,7 @@ int wkv7_linattn_step(const wkv7_linattn_desc* desc, const int32_t* slots, int32
     const int st = check(desc);
     if (st != WKV7_OK) return st;
     if (desc->packed || nslots < 0 || (!slots && nslots < desc->B)) return WKV7_ERR_INVALID_ARG;
+    if (slots && desc->B > 65536) return WKV7_ERR_UNSUPPORTED;   // (a row looks through those before it)
     if ((int64_t)desc->B * desc->H == 0) return WKV7_OK;
     if (!aligned(slots, 4) || !(req(q) && req(k) && req(v) && req(g) && req(state) && req(y)))
         return WKV7_ERR_INVALID_ARG;

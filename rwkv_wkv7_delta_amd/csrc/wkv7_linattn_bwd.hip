@@ -11,9 +11,9 @@
 // with M_is = W_is (q_i . k_s)(dy_i . v_s), a_i = q_i . (the state's part of dq_i),
 // b_s = k_s . (D's part of dk_s): sums within the tile only, however long the row is.
 //
-// (8, 4096) tokens, 40 heads of 64, bf16: 370 to 400 us, 4.0 TB/s, behind a sweep of 191.  Bound
-// by its tiles' way through LDS and about 9000 cycles of each wave's own work a tile, most of
-// it beside the loads: with dk and dv on the same waves 483 us.
+// (8, 4096) tokens, 40 heads of 64, bf16: 366 to 400 us, 3.9 TB/s, behind a sweep of 194.  Bound
+// by HBM and by the waves' own work (products, LDS, addresses), which overlap in part: with dk
+// and dv on the same waves 527 us, of which the arithmetic alone took 394, the bytes alone 352.
 
 #include "wkv7_linattn_device.h"
 

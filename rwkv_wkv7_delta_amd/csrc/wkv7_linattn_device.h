@@ -2,8 +2,8 @@
 // kernels.
 //
 // A tile is 64 tokens of one head; a workgroup is eight waves, two per SIMD, so that
-// one computes while the other waits for its operands.  Products go
-// through the matrix cores in 16 x 16 results, 32 deep: for bf16 tokens one
+// one computes while the other waits for its operands (twelve where there are
+// gradients).  Products go through the matrix cores in 16 x 16 results, 32 deep: for bf16 tokens one
 // 16x16x32 instruction, for fp32 tokens eight 16x16x4 ones.  Which 32 values of
 // the contraction a lane's eight operand elements stand for is the same for
 // both operands of every product here, one of

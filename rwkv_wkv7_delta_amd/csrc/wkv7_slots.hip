@@ -4,7 +4,7 @@
 // written once, 16 bytes a lane and access, four of them under way.  Rows of another size
 // than whole 16 bytes begin anywhere: their accesses are not aligned, and their last bytes go
 // one by one (7 planes of 50 moves of 60 002 bytes: 9 us, by pairs of bytes 17).
-// 12 planes of 48 copies of 192 KiB: 42 us, 5.3 TB/s; (a copy of 1 GiB reaches 5.1).
+// 12 planes of 48 copies of 192 KiB: 47 us, 4.8 TB/s (a copy of 1 GiB reaches 5.1).
 
 #include "wkv7_device.h"
 #include "wkv7_slots_internal.h"

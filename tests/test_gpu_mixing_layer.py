@@ -99,3 +99,50 @@ def test_serving_loop(wk):
     assert bool((cache[:, 3:] == 0).all())
     history = {(layer, int(moved[s])): h for (layer, s), h in history.items() if int(moved[s]) >= 0}
     decode([2, 0, 1])
+
+
+def test_captured_and_replayed(wk):
+    """A step, the norm with its gradients, copies and a compaction in one graph, replayed with
+    other values, lists and eager work in between; first on a stream of their own."""
+    import torch
+    L, S, B, H, N, P = 2, 6, 3, 2, 32, 64
+    gen = torch.Generator().manual_seed(5)
+    rand = lambda *s: torch.randn(*s, generator=gen).cuda()   # noqa: E731
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")   # noqa: E731
+    q, k, v, g, z = rand(B, H, N), rand(B, H, N), rand(B, H, P), -rand(B, H).abs(), rand(B, H * P)
+    gamma, beta, dy = rand(H * P), rand(H * P), rand(B, H * P)
+    slots, src, dst = dev([4, 0, 2]), dev([4, -1]), dev([5, 1])
+    keep = torch.tensor([True, False, True, False, True, True], device="cuda")
+
+    def work(cache):
+        o = [wk.linattn_step(q, k, v, g, cache[i], slots=slots).view(B, H * P) for i in range(L)]
+        y = wk.gnorm_forward(o[1], H, gamma, beta, z=z, silu=True)
+        grads = wk.gnorm_backward(o[1], dy, H, gamma, beta, z=z, silu=True)
+        wk.slots_copy(cache, src, dst)
+        return (*o, y, *grads, *wk.slots_compact(cache, keep, clear=True))
+
+    pool = rand(L, S, H, P, N)
+    cache, eager = pool.clone(), pool.clone()
+    want = work(pool.clone())
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = work(pool.clone())
+    torch.cuda.current_stream().wait_stream(side)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = work(cache)
+    cache.copy_(pool)
+    for i in range(4):
+        v.copy_(rand(B, H, P))
+        src[0] = i % 3
+        keep[i] = not bool(keep[i])
+        want = work(eager)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(outs, want):
+            assert torch.equal(a, b), i
+        assert torch.equal(cache, eager), i

@@ -153,6 +153,7 @@ def test_linattn_pointers(L):
     assert linattn(L, (BACKWARD,), dict(fixed_decay=1)) == bad                         # no dg then
     assert linattn(L, (STEP,), {}, nslots=0) == bad and linattn(L, (STEP,), {}, slots=FAKE, nslots=-1) == bad
     assert linattn(L, (STEP,), {}, slots=FAKE + 2) == bad
+    assert linattn(L, (STEP,), dict(B=65537), slots=FAKE, nslots=8) == {wk.WKV7_ERR_UNSUPPORTED}
 
 
 def test_linattn_workspace_and_sizes(L):
@@ -246,7 +247,7 @@ def test_slots_refusals(L):
     for over in (dict(n=-1), dict(from_slots=-1), dict(src=None), dict(dst=None), dict(src=FAKE + 2), dict(source=None),
                  dict(source=FAKE + 8), dict(from_slots=7)):   # the pool itself has as many slots as it has
         assert copy(**over) == bad, over
-    assert copy(n=1 << 22, row=1 << 20) == no and copy(source=FAKE * 4, from_slots=(1 << 22) + 1) == no
+    assert copy(n=65537, row=16) == no == copy(n=65536, row=1 << 24) and copy(source=FAKE * 4, from_slots=(1 << 22) + 1) == no
     for over in (dict(keep=None), dict(moved=None), dict(count=None), dict(moved=FAKE + 2), dict(count=FAKE + 2),
                  dict(clear=2), dict(ws=FAKE + 2)):
         assert compact(**over) == bad, over
