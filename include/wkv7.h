@@ -633,7 +633,8 @@ int wkv7_ssm_step(const wkv7_ssm_desc *desc, const wkv7_ssm_params *params, cons
  * [B + 1], required, not decreasing): row b has the tokens from starts[b] to
  * starts[b + 1] (both clamped to [0, tokens]); T is about the longest row's length
  * (the work is laid out for it; longer rows are taken whole all the same); outputs
- * of tokens that no row has are left as they were.  rows: 4-byte aligned.
+ * of tokens that no row has are left as they were (wkv7_linattn_clear_rest makes them
+ * 0).  rows: 4-byte aligned.  Without rows or heads the calls do nothing.
  * Sizes beyond these are refused (WKV7_ERR_UNSUPPORTED): T and tokens <= 2^31 - 65,
  * H P and G N <= 2^22, B H <= 2^21, B H P N <= 2^32, B ceil(T / 64) G <= 2^23, tokens
  * H P <= 2^40, and tiles H P N <= 2^40 with tiles = B ceil(T / 64), packed tokens / 64 + B.
@@ -688,6 +689,12 @@ int wkv7_linattn_backward(const wkv7_linattn_desc* desc, const int32_t* rows, co
                           const void* v, const void* g, const void* dy, const float* dsT, const void* ckpt, void* dq,
                           void* dk, void* dv, void* dg, float* ds0, void* workspace, size_t workspace_bytes,
                           void* stream);
+
+/* Packed rows: zeros in the places of tokens that no row has, which the calls above leave as
+   they were.  values: y or dv; queries: dq; keys: dk; decays: dg; each may be NULL.  Touches
+   no place of a row's token; in any order with the calls above. */
+int wkv7_linattn_clear_rest(const wkv7_linattn_desc* desc, const int32_t* starts, void* values, void* queries,
+                            void* keys, void* decays, void* stream);
 
 /* One token on resident states: q, k [B][G][N], v, y [B][H][P], g [B][H] or fp32 [H];
    state fp32 [nslots][H][P][N], read and overwritten where row b's slot is

@@ -57,7 +57,8 @@ EXPORTED = ("wkv7_abi_version", "wkv7_status_string", "wkv7_tape_bytes", "wkv7_c
             "wkv7_ssm_forward_workspace_bytes", "wkv7_ssm_backward_workspace_bytes",
             "wkv7_ssm_forward", "wkv7_ssm_backward", "wkv7_ssm_step", "wkv7_linattn_ckpt_bytes",
             "wkv7_linattn_forward_workspace_bytes", "wkv7_linattn_backward_workspace_bytes",
-            "wkv7_linattn_forward", "wkv7_linattn_backward", "wkv7_linattn_step", "wkv7_gnorm_forward",
+            "wkv7_linattn_forward", "wkv7_linattn_backward", "wkv7_linattn_clear_rest", "wkv7_linattn_step",
+            "wkv7_gnorm_forward",
             "wkv7_gnorm_backward_workspace_bytes", "wkv7_gnorm_backward", "wkv7_slots_copy",
             "wkv7_slots_compact_workspace_bytes", "wkv7_slots_compact")
 
@@ -192,6 +193,7 @@ def lib():
                 ("wkv7_linattn_backward_workspace_bytes", [LD], Z),
                 ("wkv7_linattn_forward", [LD] + [P] * 10 + [Z, P], ctypes.c_int),
                 ("wkv7_linattn_backward", [LD] + [P] * 14 + [Z, P], ctypes.c_int),
+                ("wkv7_linattn_clear_rest", [LD] + [P] * 6, ctypes.c_int),
                 ("wkv7_linattn_step", [LD, P, I] + [P] * 7, ctypes.c_int),
                 ("wkv7_gnorm_forward", [GD] + [P] * 6, ctypes.c_int),
                 ("wkv7_gnorm_backward_workspace_bytes", [GD], Z),

@@ -23,7 +23,7 @@ ARCH = "gfx950"
 SOURCES = ["wkv7_api.cpp", "wkv7_seq.hip", "wkv7_chunk_fwd.hip", "wkv7_bwd.hip", "wkv7_static.hip",
            "wkv7_epilogue.hip", "wkv7_chunk128.hip", "wkv7_ssm_api.cpp", "wkv7_ssm.hip",
            "wkv7_ssm_bwd.hip", "wkv7_conv.hip", "wkv7_linattn_api.cpp", "wkv7_linattn.hip",
-           "wkv7_linattn_bwd.hip", "wkv7_gnorm_api.cpp", "wkv7_gnorm.hip", "wkv7_gnorm_bwd_bf16.hip",
+           "wkv7_linattn_bwd.hip", "wkv7_linattn_rest.hip", "wkv7_gnorm_api.cpp", "wkv7_gnorm.hip", "wkv7_gnorm_bwd_bf16.hip",
            "wkv7_gnorm_bwd_f32.hip",
            "wkv7_slots_api.cpp", "wkv7_slots.hip"]
 

@@ -34,26 +34,7 @@ int64_t tiles_of(const wkv7_linattn_desc* d) {
 }
 int64_t tokens_of(const wkv7_linattn_desc* d) { return d->packed ? d->tokens : (int64_t)d->B * d->T; }
 
-int check(const wkv7_linattn_desc* d) {
-    if (!d) return WKV7_ERR_INVALID_ARG;
-    if (d->B < 0 || d->T < 0 || d->H < 0 || d->G < 1 || d->H % d->G != 0 || d->tokens < 0)
-        return WKV7_ERR_INVALID_ARG;
-    if ((d->packed != 0 && d->packed != 1) || (d->fixed_decay != 0 && d->fixed_decay != 1))
-        return WKV7_ERR_INVALID_ARG;
-    if (!(d->scale - d->scale == 0.f)) return WKV7_ERR_INVALID_ARG;   // not finite
-    if (!size_ok(d->N) || !size_ok(d->P)) return WKV7_ERR_UNSUPPORTED;
-    if (d->dtype != WKV7_F32 && d->dtype != WKV7_BF16) return WKV7_ERR_UNSUPPORTED;
-    // 64 token rows stay below 2^31 bytes, every grid at or below 2^31 threads.
-    if (d->T > INT32_MAX - 64 || d->tokens > INT32_MAX - 64 || (int64_t)d->H * d->P > (1 << 22) ||
-        (int64_t)d->G * d->N > (1 << 22))
-        return WKV7_ERR_UNSUPPORTED;
-    if (!product_fits(d->B, d->H, 4, 1, 1 << 23) || !product_fits(d->B, d->H, d->P, d->N, (int64_t)1 << 32) ||
-        !product_fits(d->B, blocks_of(d->T), d->G, 1, 1 << 23) ||
-        !product_fits(tiles_of(d), (int64_t)d->H * d->P, d->N, 1, (int64_t)1 << 40) ||
-        !product_fits(tokens_of(d), (int64_t)d->H * d->P, 1, 1, (int64_t)1 << 40))
-        return WKV7_ERR_UNSUPPORTED;
-    return WKV7_OK;
-}
+int check(const wkv7_linattn_desc* d) { return wkv7::la_check(d); }
 
 struct Plan {
     int nseg, seg_len;
@@ -122,6 +103,29 @@ bool rows_ok(const wkv7_linattn_desc* d, const int32_t* rows) {
 }
 
 }  // namespace
+
+namespace wkv7 {
+int la_check(const wkv7_linattn_desc* d) {
+    if (!d) return WKV7_ERR_INVALID_ARG;
+    if (d->B < 0 || d->T < 0 || d->H < 0 || d->G < 1 || d->H % d->G != 0 || d->tokens < 0)
+        return WKV7_ERR_INVALID_ARG;
+    if ((d->packed != 0 && d->packed != 1) || (d->fixed_decay != 0 && d->fixed_decay != 1))
+        return WKV7_ERR_INVALID_ARG;
+    if (!(d->scale - d->scale == 0.f)) return WKV7_ERR_INVALID_ARG;   // not finite
+    if (!size_ok(d->N) || !size_ok(d->P)) return WKV7_ERR_UNSUPPORTED;
+    if (d->dtype != WKV7_F32 && d->dtype != WKV7_BF16) return WKV7_ERR_UNSUPPORTED;
+    // 64 token rows stay below 2^31 bytes, every grid at or below 2^31 threads.
+    if (d->T > INT32_MAX - 64 || d->tokens > INT32_MAX - 64 || (int64_t)d->H * d->P > (1 << 22) ||
+        (int64_t)d->G * d->N > (1 << 22))
+        return WKV7_ERR_UNSUPPORTED;
+    if (!product_fits(d->B, d->H, 4, 1, 1 << 23) || !product_fits(d->B, d->H, d->P, d->N, (int64_t)1 << 32) ||
+        !product_fits(d->B, blocks_of(d->T), d->G, 1, 1 << 23) ||
+        !product_fits(tiles_of(d), (int64_t)d->H * d->P, d->N, 1, (int64_t)1 << 40) ||
+        !product_fits(tokens_of(d), (int64_t)d->H * d->P, 1, 1, (int64_t)1 << 40))
+        return WKV7_ERR_UNSUPPORTED;
+    return WKV7_OK;
+}
+}  // namespace wkv7
 
 extern "C" {
 

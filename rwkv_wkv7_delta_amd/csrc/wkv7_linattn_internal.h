@@ -6,7 +6,12 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "wkv7.h"
+
 namespace wkv7 {
+
+// The descriptor's status: WKV7_OK or why a call with it is refused.
+int la_check(const wkv7_linattn_desc* d);
 
 constexpr int kLaChunk = 64;   // tokens of a tile and of a checkpoint
 

@@ -9,7 +9,9 @@ memory with inputs.
 Rows of different lengths come padded, tokens [B, T] with ``lengths`` (int32 [B]:
 inputs behind a row's length are not used, outputs there are zero), or packed,
 tokens [total] with ``starts`` (int32 [B + 1]: row b has the tokens from starts[b]
-to starts[b + 1]) and ``max_len``, about the longest row's length.
+to starts[b + 1]) and ``max_len``, about the longest row's length; in the tensors that
+a call makes, the places of tokens that no row has are zero (a caller's ``out`` keeps
+what it held there).
 """
 
 from __future__ import annotations
@@ -77,6 +79,13 @@ def _ckpt_shape(d):
     return linattn_ckpt_shape(d.B, d.T, d.H, d.P, d.N, d.tokens if d.packed else None)
 
 
+def _clear_rest(d, starts, dev, values, queries=None, keys=None, decays=None):
+    """Zeros where a packed call writes nothing."""
+    if d.packed:
+        _call("wkv7_linattn_clear_rest", dev, ctypes.byref(d), _ptr(starts), _ptr(values), _ptr(queries), _ptr(keys),
+              _ptr(decays))
+
+
 def linattn_forward(q, k, v, g, *, s0=None, lengths=None, starts=None, max_len=None, scale: float = 1.0,
                     want_state: bool = True, want_ckpt: bool = False, out=None, workspace=None):
     """Linear attention (wkv7_linattn_forward), per head h of group h // (H // G), from S = s0:
@@ -102,6 +111,8 @@ def linattn_forward(q, k, v, g, *, s0=None, lengths=None, starts=None, max_len=N
     ws, wsb, _held = _scratch(workspace, lib().wkv7_linattn_forward_workspace_bytes(ctypes.byref(d)), dev)
     _call("wkv7_linattn_forward", dev, ctypes.byref(d), _ptr(rows), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(s0),
           _ptr(y), _ptr(sT), _ptr(ckpt), ws, wsb)
+    if out is None:
+        _clear_rest(d, rows, dev, y)
     return y, sT, ckpt
 
 
@@ -123,6 +134,7 @@ def linattn_backward(q, k, v, g, dy, ckpt, *, dsT=None, lengths=None, starts=Non
     ws, wsb, _held = _scratch(workspace, lib().wkv7_linattn_backward_workspace_bytes(ctypes.byref(d)), dev)
     _call("wkv7_linattn_backward", dev, ctypes.byref(d), _ptr(rows), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(dy),
           _ptr(dsT), _ptr(ckpt), *[_ptr(x) for x in grads], ws, wsb)
+    _clear_rest(d, rows, dev, grads.dv, grads.dq, grads.dk, grads.dg)
     return grads
 
 
