@@ -369,22 +369,28 @@ __device__ __forceinline__ void store_mark(T* lds, const f32x4 (&st)[NT], __amdg
 
 // By one whole wave.  A log decay of -infinity forgets everything: 2^-144270 is 0,
 // and sums that hold it stay exact to 2^-30.
+// A decay that is not a number, or infinite (a logarithm above 1e5), counts as 1 in the sums,
+// so that the pairs of tokens behind it keep their weights; what crosses it becomes NaN through
+// `up`, `down` and `all`: every token from it on reads the state before the tile, every one
+// before it meets the state's gradient behind it, and both are scaled by these.
 __device__ __forceinline__ void put_decays(LaDecay& d, float log_decay) {
     const int t = threadIdx.x % 64;
-    const double g = (double)fmaxf(log_decay, -1e5f) * 1.4426950408889634;
-    // a NaN stays one (fmaxf would drop it)
-    const double c = wave_running_sum(log_decay != log_decay ? (double)log_decay : g);
+    const bool bad = !(log_decay <= 1e5f);
+    const uint64_t odd = __builtin_amdgcn_ballot_w64(bad);
+    const float nan = __builtin_nanf("");
+    const double g = bad ? 0.0 : (double)fmaxf(log_decay, -1e5f) * 1.4426950408889634;
+    const double c = wave_running_sum(g);
     const uint64_t u = __builtin_bit_cast(uint64_t, c);
     const uint32_t l0 = __builtin_amdgcn_readlane((uint32_t)u, 63), l1 = __builtin_amdgcn_readlane((uint32_t)(u >> 32), 63);
     const double end = __builtin_bit_cast(double, (uint64_t)l1 << 32 | l0);
     const float hi = (float)c;
     d.hi[t] = hi;
     d.lo[t] = (float)(c - (double)hi);
-    d.up[t] = exp2_raw((float)c);
-    d.down[t] = exp2_raw((float)(end - c));
+    d.up[t] = odd << (63 - t) != 0 ? nan : exp2_raw((float)c);
+    d.down[t] = odd >> t >> 1 != 0 ? nan : exp2_raw((float)(end - c));
     if (t == 0) {
-        d.all = exp2_raw((float)end);
-        d.sum = end;
+        d.all = odd != 0 ? nan : exp2_raw((float)end);
+        d.sum = odd != 0 ? (double)nan : end;
     }
 }
 
