@@ -632,7 +632,8 @@ int wkv7_ssm_step(const wkv7_ssm_desc *desc, const wkv7_ssm_params *params, cons
  * outputs there are 0.  Or, with packed = 1, [tokens], with `rows` = starts (int32
  * [B + 1], required, not decreasing): row b has the tokens from starts[b] to
  * starts[b + 1] (both clamped to [0, tokens]); T is about the longest row's length
- * (the work is laid out for it; longer rows are taken whole all the same); outputs
+ * (the work is laid out for it, or for `tokens` if that is less; longer rows are
+ * taken whole all the same); outputs
  * of tokens that no row has are left as they were (wkv7_linattn_clear_rest makes them
  * 0).  rows: 4-byte aligned.  Without rows or heads the calls do nothing.
  * Sizes beyond these are refused (WKV7_ERR_UNSUPPORTED): T and tokens <= 2^31 - 65,

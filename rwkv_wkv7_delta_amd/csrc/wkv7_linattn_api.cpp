@@ -33,6 +33,9 @@ int64_t tiles_of(const wkv7_linattn_desc* d) {
     return d->packed ? (int64_t)d->tokens / kLaChunk + d->B : (int64_t)d->B * blocks_of(d->T);
 }
 int64_t tokens_of(const wkv7_linattn_desc* d) { return d->packed ? d->tokens : (int64_t)d->B * d->T; }
+// Tokens of a row that a launch is laid out for: no packed row has more than there are, and work
+// laid out for a model's whole context would be units and segments without tokens.
+int32_t longest(const wkv7_linattn_desc* d) { return d->packed && d->T > d->tokens ? d->tokens : d->T; }
 
 int check(const wkv7_linattn_desc* d) { return wkv7::la_check(d); }
 
@@ -48,8 +51,8 @@ struct Plan {
 // 84; (4, 1024) tokens, 12 heads: forward in 5 segments 25 us, without 32, and the reverse
 // sweep 20 and 19.
 Plan plan(const wkv7_linattn_desc* d, bool read_out) {
-    const Plan none{1, (int)(blocks_of(d->T) * kLaChunk)};
-    const int64_t wgs = (int64_t)d->B * d->H * (d->P / wkv7::la_value_block(d->P)), tiles = blocks_of(d->T);
+    const int64_t wgs = (int64_t)d->B * d->H * (d->P / wkv7::la_value_block(d->P)), tiles = blocks_of(longest(d));
+    const Plan none{1, (int)(tiles * kLaChunk)};
     if (wgs == 0 || tiles < 2) return none;
     int64_t n = kUnits / wgs;   // (one more, and some units have two: 37 us where 21 segments take 32)
     if (n > tiles) n = tiles;
@@ -92,7 +95,7 @@ size_t part_bytes(const wkv7_linattn_desc* d, int split) {
 wkv7::LaArgs args(const wkv7_linattn_desc* d, const int32_t* rows, const void* q, const void* k, const void* v,
                   const void* g, const float* s0, void* y, float* sT, void* ckpt, const Plan& s, void* seg) {
     char* const at = static_cast<char*>(seg);
-    return wkv7::LaArgs{d->B, d->T, d->H, d->G, d->N, d->P, d->dtype == WKV7_BF16, d->fixed_decay != 0,
+    return wkv7::LaArgs{d->B, longest(d), d->H, d->G, d->N, d->P, d->dtype == WKV7_BF16, d->fixed_decay != 0,
                         d->packed != 0, d->scale, d->tokens, rows, q, k, v, g, s0, y, sT, ckpt, s.nseg, s.seg_len,
                         reinterpret_cast<float*>(at),
                         reinterpret_cast<double*>(at ? at + (size_t)(s.nseg - 1) * state_bytes(d) : nullptr)};

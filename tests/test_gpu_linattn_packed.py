@@ -28,7 +28,7 @@ def test_tokens_of_no_row_are_zero(wk, H, G, N, P, starts, dtype):
     ins, _, dy, _, kw = make(41, 1, total, H, G, N, P, dtype)
     ins, dy = [x[0] for x in ins], dy[0]
     dev = torch.tensor(starts, dtype=torch.int32, device="cuda")
-    rows = dict(starts=dev, max_len=300, scale=kw["scale"])
+    rows = dict(starts=dev, max_len=64, scale=kw["scale"])   # (one plan for both)
     stale(*ins)
     y, _, ck = wk.linattn_forward(*ins, want_ckpt=True, **rows)
     stale(*ins)
@@ -76,3 +76,19 @@ def test_constant_decays_and_a_captured_graph(wk):
             assert torch.equal(a, b), starts
         for x in (got[0], *got[2:5]):
             assert bool((x[:starts[0]] == 0).all()) and bool((x[starts[-1]:] == 0).all())
+
+
+@pytest.mark.parametrize("max_len", [1 << 17, (1 << 29) - 64])
+def test_a_length_that_is_overstated(wk, max_len):
+    """A model's whole context, or the longest there is: the same results as the rows' own length."""
+    import torch
+    ins, _, dy, _, kw = make(43, 1, 63, 512, 1, 32, 32, "bf16")
+    ins, dy = [x[0] for x in ins], dy[0]
+    starts = torch.tensor([0, 63], dtype=torch.int32, device="cuda")
+    want = got = None
+    for n in (63, max_len):
+        rows = dict(starts=starts, max_len=n, scale=kw["scale"])
+        y, sT, ck = wk.linattn_forward(*ins, want_ckpt=True, **rows)
+        want, got = got, (y, sT, *wk.linattn_backward(*ins, dy, ck, **rows))
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
