@@ -700,7 +700,8 @@ int wkv7_linattn_clear_rest(const wkv7_linattn_desc* desc, const int32_t* starts
 
 /* One token on resident states: q, k [B][G][N], v, y [B][H][P], g [B][H] or fp32 [H];
    state fp32 [nslots][H][P][N], read and overwritten where row b's slot is
-   slots[b] (int32 [B], B <= 65536, 4-byte aligned; NULL: slot b, nslots at least B).  A row whose
+   slots[b] (int32 [B], B <= 65536, 4-byte aligned; NULL: slot b, nslots at least B; with nslots 0
+   state may be NULL).  A row whose
    slot is not in [0, nslots), or is an earlier row's, touches no state and gets y = 0.
    The descriptor is checked as for a prompt, T has no other effect; packed is refused. */
 int wkv7_linattn_step(const wkv7_linattn_desc* desc, const int32_t* slots, int32_t nslots, const void* q,

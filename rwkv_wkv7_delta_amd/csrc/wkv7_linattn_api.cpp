@@ -201,7 +201,8 @@ int wkv7_linattn_step(const wkv7_linattn_desc* desc, const int32_t* slots, int32
     if (desc->packed || nslots < 0 || (!slots && nslots < desc->B)) return WKV7_ERR_INVALID_ARG;
     if (slots && desc->B > 65536) return WKV7_ERR_UNSUPPORTED;   // (a row looks through those before it)
     if ((int64_t)desc->B * desc->H == 0) return WKV7_OK;
-    if (!aligned(slots, 4) || !(req(q) && req(k) && req(v) && req(g) && req(state) && req(y)))
+    // (a cache without slots has no memory: no row's slot exists)
+    if (!aligned(slots, 4) || !(req(q) && req(k) && req(v) && req(g) && req(y) && (nslots > 0 ? req(state) : opt(state))))
         return WKV7_ERR_INVALID_ARG;
     return from_hip(wkv7::launch_la_step(
         wkv7::LaStepArgs{desc->B, desc->H, desc->G, desc->N, desc->P, desc->dtype == WKV7_BF16,
