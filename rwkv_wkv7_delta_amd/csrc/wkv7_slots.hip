@@ -16,7 +16,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kAhead = 4;                  // pieces that a lane has on their way
 constexpr int kPart = kThreads * kAhead;   // pieces of a row that a workgroup takes
-constexpr int kSeen = 8192;                // slots of the map of targets: a bit each, hashed
+constexpr int kPairs = 1024;               // pairs of a list that have workgroups of their own
+constexpr int kSeen = 1 << 18;             // slots of the map of targets at a time: a bit each
 
 typedef uint32_t Piece __attribute__((ext_vector_type(4)));
 typedef Piece LoosePiece __attribute__((aligned(1)));
@@ -25,6 +26,9 @@ typedef Piece LoosePiece __attribute__((aligned(1)));
 __device__ __forceinline__ bool pair_ok(const SlotsArgs& p, int src, int dst) {
     return dst >= 0 && dst < p.slots && src >= -1 && src < p.from_slots;
 }
+
+// Words of the table of targets.
+__host__ __device__ inline int seen_words(int slots) { return ((slots < kSeen ? slots : kSeen) + 31) / 32; }
 
 // Pieces [c0, c0 + kPart) of row `src` of one plane to row `dst`; with the last of them the
 // row's bytes behind whole pieces.  A lane always has the same bytes of a row.
@@ -61,35 +65,45 @@ __device__ __forceinline__ void move_part(const SlotsArgs& p, int plane, int src
 // itself, so what it wrote for one pair is there for the next.  That is one row after the
 // other; where no target is named twice and none is a source, the pairs do not touch and
 // each has a workgroup of its own.  Every workgroup looks that up, the same way: it marks
-// the targets in a table of bits (by slot modulo its size: two slots that share a bit only
-// make the order be kept where it need not).
+// the targets in a table of bits, of as many slots as there are (of more than kSeen, 32 KiB
+// of LDS, kSeen at a time, the lists read again for each).  Of longer lists a workgroup takes
+// several pairs, so that the lists are not read more often than they are long: 65536 pairs of
+// rows of 4 KiB in a cache of 140000 slots 0.34 ms (with a workgroup for each pair 6.2), of 64
+// bytes in one of 2^22, sixteen tables, 2.5 ms (141).  With one table of 8192 bits for all
+// slots, where two far ones can share a bit, 1024 pairs of 4 KiB among 20000 slots went one
+// after the other, 687 us where these take 8.
 template <bool kWhole>
 __global__ __launch_bounds__(kThreads) void slots_copy_kernel(const SlotsArgs p, unsigned parts) {
-    __shared__ uint32_t s_seen[kSeen / 32];
+    extern __shared__ uint32_t s_seen[];
     __shared__ int s_met;
     const unsigned part = blockIdx.x % parts, rest = blockIdx.x / parts;
     const int plane = (int)(rest % p.planes), pair = (int)(rest / p.planes);
     const int64_t c0 = (int64_t)part * kPart;
     if (p.n > 1) {
-        for (int i = threadIdx.x; i < kSeen / 32; i += kThreads) s_seen[i] = 0;
         if (threadIdx.x == 0) s_met = 0;
-        __syncthreads();
-        bool met = false;
-        for (int i = threadIdx.x; i < p.n; i += kThreads) {
-            const int s = p.src[i], d = p.dst[i];
-            if (pair_ok(p, s, d)) {
-                const uint32_t bit = 1u << (d % 32), old = atomicOr(&s_seen[d / 32 % (kSeen / 32)], bit);
-                met |= (old & bit) != 0;
-            }
-        }
-        __syncthreads();
-        if (p.from == p.pool)
+        const int words = seen_words(p.slots);
+        for (int first = 0; first < p.slots; first += kSeen) {
+            for (int i = threadIdx.x; i < words; i += kThreads) s_seen[i] = 0;
+            __syncthreads();
+            const auto here = [&](int slot) { return slot >= first && slot - first < kSeen; };
+            bool met = false;
             for (int i = threadIdx.x; i < p.n; i += kThreads) {
                 const int s = p.src[i], d = p.dst[i];
-                if (pair_ok(p, s, d) && s >= 0 && s != d) met |= (s_seen[s / 32 % (kSeen / 32)] >> (s % 32) & 1) != 0;
+                if (pair_ok(p, s, d) && here(d)) {
+                    const uint32_t bit = 1u << (d % 32);
+                    met |= (atomicOr(&s_seen[(d - first) / 32], bit) & bit) != 0;
+                }
             }
-        if (met) s_met = 1;
-        __syncthreads();
+            __syncthreads();
+            if (p.from == p.pool)
+                for (int i = threadIdx.x; i < p.n; i += kThreads) {
+                    const int s = p.src[i], d = p.dst[i];
+                    if (pair_ok(p, s, d) && s != d && here(s)) met |= (s_seen[(s - first) / 32] >> (s % 32) & 1) != 0;
+                }
+            if (met) s_met = 1;
+            __syncthreads();
+            if (s_met) break;
+        }
         if (s_met) {
             if (pair != 0) return;
             for (int i = 0; i < p.n; ++i) {
@@ -99,8 +113,10 @@ __global__ __launch_bounds__(kThreads) void slots_copy_kernel(const SlotsArgs p,
             return;
         }
     }
-    const int s = p.src[pair], d = p.dst[pair];
-    if (pair_ok(p, s, d) && (s != d || p.from != p.pool)) move_part<kWhole>(p, plane, s, d, c0);
+    for (int64_t i = pair; i < p.n; i += gridDim.x / parts / p.planes) {
+        const int s = p.src[i], d = p.dst[i];
+        if (pair_ok(p, s, d) && (s != d || p.from != p.pool)) move_part<kWhole>(p, plane, s, d, c0);
+    }
 }
 
 // Which slots move: with `count` kept ones, those behind the first `count` places fill the
@@ -179,23 +195,25 @@ __global__ __launch_bounds__(kThreads) void slots_move_kernel(const SlotsArgs p,
 
 }  // namespace
 
-#define WKV7_SLOTS(kernel, rows)                                                              \
+#define WKV7_SLOTS(kernel, rows, lds)                                                         \
     {                                                                                         \
         const unsigned parts = (unsigned)(((p.bytes + 15) / 16 + kPart - 1) / kPart);         \
         const unsigned grid = parts * p.planes * (unsigned)(rows);                            \
-        if (p.bytes % 16 == 0) kernel<true><<<grid, kThreads, 0, stream>>>(p, parts);         \
-        else kernel<false><<<grid, kThreads, 0, stream>>>(p, parts);                          \
+        if (p.bytes % 16 == 0) kernel<true><<<grid, kThreads, lds, stream>>>(p, parts);       \
+        else kernel<false><<<grid, kThreads, lds, stream>>>(p, parts);                        \
         return hipGetLastError();                                                             \
     }
 
-hipError_t launch_slots_copy(const SlotsArgs& p, hipStream_t stream) WKV7_SLOTS(slots_copy_kernel, p.n)
+hipError_t launch_slots_copy(const SlotsArgs& p, hipStream_t stream) {
+    WKV7_SLOTS(slots_copy_kernel, p.n < kPairs ? p.n : kPairs, p.n > 1 ? seen_words(p.slots) * sizeof(uint32_t) : 0)
+}
 
 hipError_t launch_slots_compact(const SlotsArgs& p, hipStream_t stream) {
     slots_plan_kernel<<<1, kScan, 0, stream>>>(p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.planes == 0 || p.bytes == 0) return e;
     const int rows = p.clear ? p.slots : (p.slots + 1) / 2;
-    WKV7_SLOTS(slots_move_kernel, rows)
+    WKV7_SLOTS(slots_move_kernel, rows, 0)
 }
 
 }  // namespace wkv7
