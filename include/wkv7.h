@@ -670,10 +670,10 @@ size_t wkv7_linattn_backward_workspace_bytes(const wkv7_linattn_desc* desc);
  *   ckpt     wkv7_linattn_ckpt_bytes, or NULL
  * g is a log decay: 0 or below in use; -infinity forgets everything before the
  * token; NaN, infinity and what is above 1e5 make NaN of what they decay.  States are
- * fp32 to their last bits (with bf16 tokens too); a read-out's weights within 64
- * tokens, and the states it reads, are rounded to dtype.
+ * fp32 to their last bits (with bf16 tokens too); the weights within 64 tokens and
+ * the states that are read out keep 2^-17 of themselves.
  * An infinity or a NaN in a token reaches what the formulas take it to: its own and
- * later tokens' y of its heads, and their states.
+ * later tokens' y of its heads, and their states (an infinity perhaps as a NaN).
  */
 int wkv7_linattn_forward(const wkv7_linattn_desc* desc, const int32_t* rows, const void* q, const void* k,
                          const void* v, const void* g, const float* s0, void* y, float* sT, void* ckpt,

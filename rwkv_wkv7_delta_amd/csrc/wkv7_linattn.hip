@@ -26,11 +26,10 @@ namespace {
 // G is a multiple of 8).
 __device__ __forceinline__ int head_of(int i, int H, int G) { return i % G * (H / G) + i / G; }
 
-struct Yes {
-    static constexpr bool value = true;
-};
-struct No {
-    static constexpr bool value = false;
+// A wave's role: to read out its tokens against kBlocks tiles of 16, or (0) to hold the state.
+template <int kBlocks>
+struct Blocks {
+    static constexpr int value = kBlocks;
 };
 
 struct LaBlock {
@@ -249,22 +248,29 @@ __global__ __launch_bounds__(256) void la_join_kernel(const LaArgs p, const floa
 }
 
 // ---- prompts --------------------------------------------------------------------
-// A workgroup takes 64 (or all 32) value rows of a head's state over a segment.  Waves 0
-// to 3 read out: wave w the tokens 16 w .. of the tile.  Waves 4 to 7 hold the state and
-// move it on, 16 value rows each (of 32: and half of the columns), for the next tile while
-// the others read the one before from LDS.  Results are formed transposed, [s][t], [p][t],
-// [n][p], so that each feeds the next product from registers (wkv7_linattn_device.h).
+// A workgroup takes 64 (or all 32) value rows of a head's state over a segment.  Waves 4 to 7
+// hold the state, 16 value rows each (of 32: and half of the columns): each tile's queries read
+// it out from its registers, in terms, then it is moved on.  Waves 0 to 3 read out the tile
+// itself: wave w the tokens 16 w .. , to which it adds what the others read from the state, and
+// stores them.  Results are formed transposed, [s][t], [p][t], [n][p], so that each feeds the
+// next product from registers (wkv7_linattn_device.h); the state is both kinds of operand as it
+// is held.  (Handed on through LDS for the others to read, in two bf16 terms, the prompts below
+// took 152 us where this takes 140: four waves each read all of it.)
 template <typename T, int N, int PB>
 struct LaFwdShared {
     typedef LaStage<T, N> SK;
     typedef LaStage<T, PB> SV;
-    // Two of everything, and one barrier a tile, where two workgroups fit a unit's LDS.
-    static constexpr int kBytes = (kLaChunk * (SK::kStride + SV::kStride) + PB * SK::kStride) * (int)sizeof(T);
-    static constexpr int kBuffers = kBytes <= 28 * 1024 ? 2 : 1;
-    T k[kBuffers][kLaChunk * SK::kStride];
+    static constexpr int kHalves = 64 / PB;      // waves that share value rows, with N / kHalves columns each
+    static constexpr int kXStride = PB + 4;      // of a row of what is read from the state
+    // Two of everything, and one barrier a tile, where that takes at most 128 KiB (registers leave
+    // room for one workgroup on a unit in any case): (4, 2048) tokens, 32 heads of 128, bf16, 123
+    // KiB: 100 us, with one set 110; (8, 2048), 32 heads of 64, fp32, 139 KiB: 279 and 185.
+    static constexpr int kSet = kLaChunk * ((2 * SK::kStride + SV::kStride) * (int)sizeof(T) + kHalves * kXStride * 4);
+    static constexpr int kBuffers = 2 * kSet <= 128 * 1024 ? 2 : 1;
+    T k[kBuffers][kLaChunk * SK::kStride], q[kBuffers][kLaChunk * SK::kStride];
     T v[kBuffers][kLaChunk * SV::kStride];
-    T s[kBuffers][PB * SK::kStride];   // the state before the tile, [p][n], in the tokens' type
-    T own[4][LaRows16<T, (N > PB ? N : PB)>::kSize];   // a wave's queries, then its results
+    float x[kBuffers][kHalves][kLaChunk * kXStride];   // S q_t, [t][p]
+    T own[4][LaRows16<T, PB>::kSize];   // a wave's results
     T mark[4][sizeof(T) == 2 && PB == 64 ? LaRows16<T, N>::kSize : 8];   // a wave's state rows
     LaDecay d[kBuffers];
 };
@@ -314,11 +320,13 @@ __global__ __launch_bounds__(kLaThreads) void la_fwd_kernel(const LaArgs p) {
     // A wave's whole way over the segment, by its role: the code that waits for older loads
     // has to know how many younger loads and stores there are, so no role's are conditional
     // for another and tiles that there are not are loaded as nothing.
-    auto run = [&](auto reads_) {
-        constexpr bool kReads = decltype(reads_)::value;
+    auto run = [&](auto blocks_) {
+        constexpr int kBlocks = decltype(blocks_)::value;
+        constexpr bool kReads = kBlocks > 0;
         const int t = 16 * wave + l16;   // the read-out's token
-        T* const own = sm.own[wave % 4];
         Frag qf[KS];
+        f32x4 o[PT];
+        float tup = 0.f;
         auto load = [&](int c, Ahead& r) {
             const int n = tokens_of(c, end);
             const int64_t at = row.first + begin + (int64_t)c * kLaChunk;
@@ -335,47 +343,61 @@ __global__ __launch_bounds__(kLaThreads) void la_fwd_kernel(const LaArgs p) {
             const bool odd = __builtin_amdgcn_ballot_w64(r.k.odd() || r.v.odd()) != 0;
             if (lane == 0) sm.d[buf].odd[wave] = odd;
             if constexpr (kReads) {
-                if (wave == 0) put_decays(sm.d[buf], r.g.get());
+                if (kBlocks == 1) put_decays(sm.d[buf], r.g.get());
+                T* const own = sm.q[buf] + 16 * wave * SQ::kStride;
                 r.q.put(own);
 #pragma unroll
                 for (int i = 0; i < KS; ++i) qf[i] = M::rows(own + l16 * SQ::kStride + 32 * i + 8 * g);
             }
         };
-        auto put_state = [&](int buf) {
+        // Tile c's read-outs with what the state's waves found for them, to memory (before the
+        // first tile: no rows).
+        auto finish = [&](int c, int buf) {
+            const int n_in = tokens_of(c, end), n_out = c < 0 ? 0 : tokens_of(c, zero_end);
+            const int64_t at = row.first + begin + (int64_t)c * kLaChunk;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-                M::put(sm.s[buf] + (ptile + l16) * SK::kStride + n0 + 16 * n + 4 * g, st[n]);
+            for (int pt = 0; pt < PT; ++pt) {
+                const float* const x1 = sm.x[buf][0] + t * Shared::kXStride + 16 * pt + 4 * g;
+                f32x4 x = *reinterpret_cast<const f32x4*>(x1);
+                if constexpr (Shared::kHalves == 2) x += *reinterpret_cast<const f32x4*>(x1 + kLaChunk * Shared::kXStride);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) o[pt][q] = fmaf(x[q], tup, o[pt][q]) * p.scale;
+            }
+            // nothing of a state that is not finite behind the row's last token
+            if (n_in < kLaChunk)
+#pragma unroll
+                for (int pt = 0; pt < PT; ++pt)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) o[pt][q] = t < n_in ? o[pt][q] : 0.f;
+            LaRows16<T, PB>::store(sm.own[wave % 4], o,
+                                   rows_of(Y + at * vrow + (int64_t)w.h * p.P + w.p0, n_out, vrow, PB), vb, 16 * wave);
         };
         auto turn = [&](int c, Ahead& r) {
             const int buf = BUF == 2 ? c & 1 : 0, nxt = BUF == 2 ? buf ^ 1 : 0;
             __syncthreads();
             const T* const sk = sm.k[buf];
             const T* const sv = sm.v[buf];
+            const T* const sq = sm.q[buf];
             const LaDecay& d = sm.d[buf];
-            const int64_t at = row.first + begin + (int64_t)c * kLaChunk;
             const bool odd = any_odd(d.odd);
             if constexpr (kReads) {
+                if (BUF == 2) finish(c - 1, nxt);
                 const int n_in = tokens_of(c, end);
-                const float thi = d.hi[t], tlo = d.lo[t], tup = d.up[t];
-                f32x4 o[PT];
+                const float thi = d.hi[t], tlo = d.lo[t];
+                tup = d.up[t];
 #pragma unroll
-                for (int pt = 0; pt < PT; ++pt) {
-                    o[pt] = zero4();
-#pragma unroll
-                    for (int i = 0; i < KS; ++i)
-                        o[pt] = M::mma(M::rows(sm.s[buf] + (16 * pt + l16) * SK::kStride + 32 * i + 8 * g), qf[i], o[pt]);
-                }
+                for (int pt = 0; pt < PT; ++pt) o[pt] = zero4();
                 if (!odd) {
                     // [s][t] of the wave's tokens t against those up to them.
-                    Frag pf[2];
+                    Frag pf[2][M::kTerms];
 #pragma unroll
                     for (int j2 = 0; j2 < 2; ++j2) {
-                        typename M::Half h2[2];
+                        typename M::Half h2[2][M::kTerms];
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
                             const int j = 2 * j2 + u;
                             f32x4 a = zero4();
-                            if (j <= wave) {
+                            if (j < kBlocks) {
 #pragma unroll
                                 for (int i = 0; i < KS; ++i)
                                     a = M::mma(M::rows(sk + (16 * j + l16) * SK::kStride + 32 * i + 8 * g), qf[i], a);
@@ -383,33 +405,34 @@ __global__ __launch_bounds__(kLaThreads) void la_fwd_kernel(const LaArgs p) {
                                 const f32x4 slo = *reinterpret_cast<const f32x4*>(d.lo + 16 * j + 4 * g);
 #pragma unroll
                                 for (int q = 0; q < 4; ++q) a[q] *= exp2_raw((thi - shi[q]) + (tlo - slo[q]));
-                                if (j == wave)   // the triangle's edge
+                                if (j == kBlocks - 1)   // the triangle's edge
 #pragma unroll
                                     for (int q = 0; q < 4; ++q) a[q] = 4 * g + q <= l16 ? a[q] : 0.f;
                             }
-                            // Rounded to the tokens' type for the product with v: an error of half a
-                            // step of each weight, as large as y's own rounding.
-                            h2[u] = M::half(a);
+                            split_terms<T>(a, h2[u]);
                         }
-                        pf[j2] = M::cat(h2[0], h2[1]);
+#pragma unroll
+                        for (int e = 0; e < M::kTerms; ++e) pf[j2][e] = M::cat(h2[0][e], h2[1][e]);
                     }
 #pragma unroll
                     for (int pt = 0; pt < PT; ++pt) {
-                        o[pt] *= tup;
-                        o[pt] = M::mma(columns<T>(sv + 16 * pt, SV::kStride, g, l16), pf[0], o[pt]);
-                        if (wave >= 2)
-                            o[pt] = M::mma(columns<T>(sv + 32 * SV::kStride + 16 * pt, SV::kStride, g, l16), pf[1], o[pt]);
+                        const Frag v0 = columns<T>(sv + 16 * pt, SV::kStride, g, l16);
+#pragma unroll
+                        for (int e = M::kTerms - 1; e >= 0; --e) o[pt] = M::mma(v0, pf[0][e], o[pt]);
+                        if (kBlocks > 2) {
+                            const Frag v1 = columns<T>(sv + 32 * SV::kStride + 16 * pt, SV::kStride, g, l16);
+#pragma unroll
+                            for (int e = M::kTerms - 1; e >= 0; --e) o[pt] = M::mma(v1, pf[1][e], o[pt]);
+                        }
                     }
                 } else {
                     // An infinity or a NaN among the tile's keys and values: pair by pair, each lane its
                     // token, so that it meets no weight of 0 of a token before its own.
-#pragma unroll
-                    for (int pt = 0; pt < PT; ++pt) o[pt] *= tup;
                     for (int s = 0; s < n_in; ++s) {
                         float a = 0.f;
 #pragma unroll 2
                         for (int n = 0; n < N; ++n)
-                            a = fmaf(Elem<T>::load1(sk + s * SK::kStride + n), Elem<T>::load1(own + l16 * SQ::kStride + n), a);
+                            a = fmaf(Elem<T>::load1(sk + s * SK::kStride + n), Elem<T>::load1(sq + t * SK::kStride + n), a);
                         a *= exp2_raw((thi - d.hi[s]) + (tlo - d.lo[s]));
 #pragma unroll
                         for (int pt = 0; pt < PT; ++pt) {
@@ -419,22 +442,43 @@ __global__ __launch_bounds__(kLaThreads) void la_fwd_kernel(const LaArgs p) {
                         }
                     }
                 }
-                // nothing of a state that is not finite behind the row's last token
-#pragma unroll
-                for (int pt = 0; pt < PT; ++pt)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) o[pt][q] = t < n_in ? o[pt][q] * p.scale : 0.f;
-                LaRows16<T, PB>::store(own, o, rows_of(Y + at * vrow + (int64_t)w.h * p.P + w.p0, tokens_of(c, zero_end), vrow, PB),
-                                       vb, 16 * wave);
             } else {
+                // ---- the state read out, [p][t], as the lanes hold it
+                constexpr int kDepth = (NT + 1) / 2;   // (of 16 columns: the other half zeros)
+                Frag sf[kDepth][M::kTerms];
+#pragma unroll
+                for (int i = 0; i < kDepth; ++i) {
+                    typename M::Half h2[2][M::kTerms];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) split_terms<T>(2 * i + u < NT ? st[2 * i + u] : zero4(), h2[u]);
+#pragma unroll
+                    for (int e = 0; e < M::kTerms; ++e) sf[i][e] = M::cat(h2[0][e], h2[1][e]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    f32x4 x = zero4();
+#pragma unroll
+                    for (int i = 0; i < kDepth; ++i) {
+                        const T* const q1 = sq + (16 * j + l16) * SK::kStride + n0 + 32 * i + 4 * g;
+                        const Frag q2 = M::cat(M::four(q1), NT > 1 ? M::four(q1 + 16) : typename M::Half{});
+#pragma unroll
+                        for (int e = M::kTerms - 1; e >= 0; --e) x = M::mma(sf[i][e], q2, x);
+                    }
+                    *reinterpret_cast<f32x4*>(sm.x[buf][wave % 4 / PT] + (16 * j + l16) * Shared::kXStride + ptile + 4 * g) = x;
+                }
+                f32x4 was[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) was[n] = st[n];
+                move_state<T, NT>(st, sk + n0, SK::kStride, sv + ptile, SV::kStride, d.down, 1.f, d.all, odd, g, l16);
                 const auto m = buffer_of(static_cast<T*>(p.ckpt) +
                                              (((row.ckpt + begin / kLaChunk + c) * p.H + w.h) * p.P + w.p0) * N,
                                          p.ckpt && c < tiles ? PB * N * (int)sizeof(T) : 0);
-                store_mark<T, N>(sm.mark[wave - 4], st, m, ptile, n0);
-                move_state<T, NT>(st, sk + n0, SK::kStride, sv + ptile, SV::kStride, d.down, 1.f, d.all, odd, g, l16);
+                store_mark<T, N>(sm.mark[wave - 4], was, m, ptile, n0);
             }
-            if (BUF == 1) __syncthreads();
-            if constexpr (!kReads) put_state(nxt);
+            if (BUF == 1) {
+                __syncthreads();
+                if constexpr (kReads) finish(c, 0);
+            }
             put(nxt, r);
             load(c + (kDeep ? 3 : 2), r);
         };
@@ -447,7 +491,6 @@ __global__ __launch_bounds__(kLaThreads) void la_fwd_kernel(const LaArgs p) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) st[n] = *reinterpret_cast<const f32x4*>(from + 16 * n + 4 * g);
             }
-            put_state(0);
         }
         if (tiles > 0) {
             Ahead even, odd_;
@@ -456,15 +499,23 @@ __global__ __launch_bounds__(kLaThreads) void la_fwd_kernel(const LaArgs p) {
             put(0, even);
             load(kDeep ? 2 : 1, even);
             // Deep: by twos, the last perhaps a tile without tokens, which changes nothing.
-            for (int c = 0; c < tiles; c += kDeep ? 2 : 1) {
+            int c = 0;
+            for (; c < tiles; c += kDeep ? 2 : 1) {
                 turn(c, kDeep ? odd_ : even);
                 if (kDeep) turn(c + 1, even);
+            }
+            if (BUF == 2) {
+                __syncthreads();
+                if constexpr (kReads) finish(c - 1, c - 1 & 1);
             }
         }
     };
     const bool reads = wave < 4;
-    if (reads) run(Yes());
-    else run(No());
+    if (wave == 0) run(Blocks<1>());
+    else if (wave == 1) run(Blocks<2>());
+    else if (wave == 2) run(Blocks<3>());
+    else if (wave == 3) run(Blocks<4>());
+    else run(Blocks<0>());
     if (!reads && tail && p.sT) {
         float* const to = state_at<N>(p.sT, p, w.b, w.h, prow) + n0;
 #pragma unroll

@@ -347,6 +347,11 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
         const auto weight = [&](int late, int early) {
             return exp2_raw((d.hi[late] - d.hi[early]) + (d.lo[late] - d.lo[early])) * p.scale;
         };
+        // A product with weights in terms.
+        const auto weighted = [&](const Frag& rows, const Frag (&wt)[M::kTerms], f32x4& to) __attribute__((always_inline)) {
+#pragma unroll
+            for (int e = M::kTerms - 1; e >= 0; --e) to = M::mma(rows, wt[e], to);
+        };
         // A row times x, where there is such a pair: chosen, not branched around, so that all
         // lanes stay together beside the matrix instructions.
         const auto add = [&](bool pair, const T* from, float x, auto& to) __attribute__((always_inline)) {
@@ -380,14 +385,14 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
             }
             if (!odd) {
                 // ---- and the tile's: [s][t], s up to t; and M
-                Frag wt[2], qf[KS];
+                Frag wt[2][M::kTerms], qf[KS];
 #pragma unroll
                 for (int j = 0; j < PS; ++j) yf[j] = M::rows(sm.dy + t * SV::kStride + 32 * j + 8 * g);
 #pragma unroll
                 for (int j = 0; j < KS; ++j) qf[j] = M::rows(sm.q + t * SK::kStride + 32 * j + 8 * g);
 #pragma unroll
                 for (int j2 = 0; j2 < 2; ++j2) {
-                    Half h2[2];
+                    Half h2[2][M::kTerms];
 #pragma unroll
                     for (int u2 = 0; u2 < 2; ++u2) {
                         const int j = 2 * j2 + u2;
@@ -416,17 +421,15 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
                                 *to = head_first ? m : *to + m;   // (16 lanes alike: no branch)
                             }
                         }
-                        // Rounded to the tokens' type, as the weights of the forward: half a step of
-                        // each, as large as the gradients' own rounding.
-                        h2[u2] = M::half(x);
+                        split_terms<T>(x, h2[u2]);
                     }
-                    wt[j2] = M::cat(h2[0], h2[1]);
+#pragma unroll
+                    for (int e = 0; e < M::kTerms; ++e) wt[j2][e] = M::cat(h2[0][e], h2[1][e]);
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    sum[n] = M::mma(columns<T>(sm.k + 16 * n, SK::kStride, g, l16), wt[0], sum[n]);
-                    if (w >= 2)
-                        sum[n] = M::mma(columns<T>(sm.k + 32 * SK::kStride + 16 * n, SK::kStride, g, l16), wt[1], sum[n]);
+                    weighted(columns<T>(sm.k + 16 * n, SK::kStride, g, l16), wt[0], sum[n]);
+                    if (w >= 2) weighted(columns<T>(sm.k + 32 * SK::kStride + 16 * n, SK::kStride, g, l16), wt[1], sum[n]);
                 }
             } else {
                 for (int s = 0; s < kLaChunk; ++s) {
@@ -463,12 +466,12 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
             }
             if (!odd) {
                 // ---- and the tile's: [t][s], t from s on
-                Frag wt[2];
+                Frag wt[2][M::kTerms];
 #pragma unroll
                 for (int j = 0; j < PS; ++j) vf[j] = M::rows(sm.v + t * SV::kStride + 32 * j + 8 * g);
 #pragma unroll
                 for (int j2 = 0; j2 < 2; ++j2) {
-                    Half h2[2];
+                    Half h2[2][M::kTerms];
 #pragma unroll
                     for (int u2 = 0; u2 < 2; ++u2) {
                         const int j = 2 * j2 + u2;
@@ -482,14 +485,15 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
 #pragma unroll
                                 for (int r = 0; r < 4; ++r) x[r] = 4 * g + r >= l16 ? x[r] : 0.f;
                         }
-                        h2[u2] = M::half(x);
+                        split_terms<T>(x, h2[u2]);
                     }
-                    wt[j2] = M::cat(h2[0], h2[1]);
+#pragma unroll
+                    for (int e = 0; e < M::kTerms; ++e) wt[j2][e] = M::cat(h2[0][e], h2[1][e]);
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    if (w < 2) sum[n] = M::mma(columns<T>(sm.q + 16 * n, SK::kStride, g, l16), wt[0], sum[n]);
-                    sum[n] = M::mma(columns<T>(sm.q + 32 * SK::kStride + 16 * n, SK::kStride, g, l16), wt[1], sum[n]);
+                    if (w < 2) weighted(columns<T>(sm.q + 16 * n, SK::kStride, g, l16), wt[0], sum[n]);
+                    weighted(columns<T>(sm.q + 32 * SK::kStride + 16 * n, SK::kStride, g, l16), wt[1], sum[n]);
                 }
             } else {
                 for (int s = 0; s < n_in; ++s)   // the query's token
@@ -510,10 +514,10 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
                 dv[m] *= down;
             }
             if (!odd) {
-                Frag wt[2];
+                Frag wt[2][M::kTerms];
 #pragma unroll
                 for (int j2 = 0; j2 < 2; ++j2) {
-                    Half h2[2];
+                    Half h2[2][M::kTerms];
 #pragma unroll
                     for (int u2 = 0; u2 < 2; ++u2) {
                         const int j = 2 * j2 + u2;
@@ -527,14 +531,15 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
 #pragma unroll
                                 for (int r = 0; r < 4; ++r) x[r] = 4 * g + r >= l16 ? x[r] : 0.f;
                         }
-                        h2[u2] = M::half(x);
+                        split_terms<T>(x, h2[u2]);
                     }
-                    wt[j2] = M::cat(h2[0], h2[1]);
+#pragma unroll
+                    for (int e = 0; e < M::kTerms; ++e) wt[j2][e] = M::cat(h2[0][e], h2[1][e]);
                 }
 #pragma unroll
                 for (int m = 0; m < PT; ++m) {
-                    if (w < 2) dv[m] = M::mma(columns<T>(sm.dy + 16 * m, SV::kStride, g, l16), wt[0], dv[m]);
-                    dv[m] = M::mma(columns<T>(sm.dy + 32 * SV::kStride + 16 * m, SV::kStride, g, l16), wt[1], dv[m]);
+                    if (w < 2) weighted(columns<T>(sm.dy + 16 * m, SV::kStride, g, l16), wt[0], dv[m]);
+                    weighted(columns<T>(sm.dy + 32 * SV::kStride + 16 * m, SV::kStride, g, l16), wt[1], dv[m]);
                 }
             } else {
                 for (int s = 0; s < n_in; ++s)

@@ -27,6 +27,7 @@ template <> struct LaMat<bf16_t> {
     typedef bf16x8 Frag;
     typedef bf16x4 Half;
     static constexpr int kParts = 3;   // bf16 terms that carry a 32-bit operand
+    static constexpr int kTerms = 2;   // and those of a weight, or of a state that is read out
     static __device__ __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) { return mfma32(a, b, c); }
     static __device__ __forceinline__ Frag cat(Half a, Half b) { return cat8(a, b); }
     static __device__ __forceinline__ Half half(f32x4 x) { return cvt4(x); }
@@ -40,9 +41,8 @@ template <> struct LaMat<bf16_t> {
     static __device__ __forceinline__ Half four(const bf16_t* p) {
         return __builtin_bit_cast(bf16x4, *reinterpret_cast<const uint2*>(p));
     }
-    static __device__ __forceinline__ void put(bf16_t* p, f32x4 x) {
-        *reinterpret_cast<uint2*>(p) = __builtin_bit_cast(uint2, cvt4(x));
-    }
+    static __device__ __forceinline__ void put(bf16_t* p, f32x4 x) { put(p, cvt4(x)); }
+    static __device__ __forceinline__ void put(bf16_t* p, Half x) { *reinterpret_cast<uint2*>(p) = __builtin_bit_cast(uint2, x); }
 };
 
 template <> struct LaMat<float> {
@@ -50,7 +50,7 @@ template <> struct LaMat<float> {
         float v[8];
     };
     typedef f32x4 Half;
-    static constexpr int kParts = 1;
+    static constexpr int kParts = 1, kTerms = 1;
     static __device__ __forceinline__ f32x4 mma(const Frag& a, const Frag& b, f32x4 c) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[j], b.v[j], c, 0, 0, 0);
@@ -113,6 +113,30 @@ __device__ __forceinline__ void split_parts(const f32x4& lo, const f32x4& hi, ty
             f[i] = __builtin_bit_cast(typename M::Frag, w);
         }
         f[2] = M::cat(M::half(x[0]), M::half(x[1]));
+    }
+}
+
+// A weight within a tile, or a read-out's state, as kTerms halves that sum to it: with bf16
+// tokens what is cut off after 8 bits and the rest, rounded, so that 2^-17 of it is lost, a
+// 256th of the output's own rounding.  (Rounded to one bf16, they made outputs 1.4 times as
+// wrong as their rounding.)  An infinity becomes a NaN.
+template <typename T>
+__device__ __forceinline__ void split_terms(const f32x4& x, typename LaMat<T>::Half (&h)[LaMat<T>::kTerms]) {
+    typedef LaMat<T> M;
+    if constexpr (M::kTerms == 1) {
+        h[0] = x;
+    } else {
+        vu2 w;
+        f32x4 rest;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t a = __float_as_uint(x[2 * j]), b = __float_as_uint(x[2 * j + 1]);
+            w[j] = __builtin_amdgcn_perm(b, a, 0x07060302u);   // the upper halves
+            rest[2 * j] = x[2 * j] - __uint_as_float(a & 0xffff0000u);
+            rest[2 * j + 1] = x[2 * j + 1] - __uint_as_float(b & 0xffff0000u);
+        }
+        h[0] = __builtin_bit_cast(typename M::Half, w);
+        h[1] = M::half(rest);
     }
 }
 
