@@ -189,7 +189,7 @@ __global__ __launch_bounds__(kLaThreads) void la_sweep_kernel(const LaArgs p, co
         auto put = [&](int buf, const Ahead& r) {
             r.k.store(s_k[buf]);
             r.v.store(s_v[buf]);
-            const bool odd = __builtin_amdgcn_ballot_w64(r.k.odd() || r.v.odd()) != 0;
+            const bool odd = __builtin_amdgcn_ballot_w64((int)r.k.odd() | (int)r.v.odd()) != 0;
             if (lane == 0) {
                 s_d[buf].odd[wave] = odd;
                 s_d[buf].odd[wave - 4] = 0;
@@ -340,8 +340,8 @@ __global__ __launch_bounds__(kLaThreads) void la_fwd_kernel(const LaArgs p) {
         auto put = [&](int buf, const Ahead& r) {
             r.k.store(sm.k[buf]);
             r.v.store(sm.v[buf]);
-            const bool odd = __builtin_amdgcn_ballot_w64(r.k.odd() || r.v.odd()) != 0;
-            if (lane == 0) sm.d[buf].odd[wave] = odd;
+            const bool odd = __builtin_amdgcn_ballot_w64((int)r.k.odd() | (int)r.v.odd()) != 0;
+            sm.d[buf].odd[wave] = odd;   // (64 lanes alike: no branch)
             if constexpr (kReads) {
                 if (kBlocks == 1) put_decays(sm.d[buf], r.g.get());
                 T* const own = sm.q[buf] + 16 * wave * SQ::kStride;

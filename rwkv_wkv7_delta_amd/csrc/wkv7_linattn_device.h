@@ -412,10 +412,9 @@ __device__ __forceinline__ void put_decays(LaDecay& d, float log_decay) {
     d.lo[t] = (float)(c - (double)hi);
     d.up[t] = odd << (63 - t) != 0 ? nan : exp2_raw((float)c);
     d.down[t] = odd >> t >> 1 != 0 ? nan : exp2_raw((float)(end - c));
-    if (t == 0) {
-        d.all = odd != 0 ? nan : exp2_raw((float)end);
-        d.sum = odd != 0 ? (double)nan : end;
-    }
+    // (64 lanes alike: no branch)
+    d.all = odd != 0 ? nan : exp2_raw((float)end);
+    d.sum = odd != 0 ? (double)nan : end;
 }
 
 }  // namespace wkv7
