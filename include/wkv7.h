@@ -656,7 +656,7 @@ size_t wkv7_linattn_ckpt_bytes(const wkv7_linattn_desc* desc);
 
 /* Device scratch: the forward's holds the states of its time segments, if there are
    any; the backward's as many bytes as the checkpoints (the gradient of the state
-   behind every tile), its own segments' states, parts of the products of states and
+   behind every tile, with bf16 ten bits of it), its own segments' states, parts of the products of states and
    their gradients for dg, and where heads share keys and tiles are few, partial sums of
    dq and dk.  0 where none is needed. */
 size_t wkv7_linattn_forward_workspace_bytes(const wkv7_linattn_desc* desc);

@@ -61,8 +61,7 @@ __device__ __forceinline__ float* state_at(float* base, const LaArgs& p, int b, 
 // dy: D <- e^{G_end} D + scale sum_t (e^{G_t} dy_t) q_t^T.
 // kSegment: what a segment leaves from zero, and its summed decay.  Else (the
 // reverse only) D behind every tile is written, and the gradient of the first state; and
-// <S, D> with the tile's checkpoint S, from D's 32 bits: rounded as the checkpoints are, it
-// would make dg's error 1.7 times its own rounding.
+// <S, D> with the tile's checkpoint S, from D's 32 bits.
 // Waves 0 to 3 hold the state, 16 value rows each (of 32: and half of the key columns), and
 // move it on; waves 4 to 7 bring the tiles: two on their way from memory, one on its way to
 // LDS while the others use the one before.
@@ -147,10 +146,11 @@ __global__ __launch_bounds__(kLaThreads) void la_sweep_kernel(const LaArgs p, co
             const int buf = BUF == 2 ? i & 1 : 0;
             __syncthreads();
             const LaDecay& d = s_d[buf];
+            // (of a tile that there is not: nothing)
+            const int64_t tile = row.ckpt + begin / kLaChunk + tile_of(i);
+            const auto m = buffer_of(marks + ((tile * p.H + w.h) * p.P + w.p0) * N, i < tiles ? PB * N * (int)sizeof(T) : 0);
+            typename M::Half h[NT];
             if (!kSegment) {
-                // (of a tile that there is not: nothing)
-                const int64_t tile = row.ckpt + begin / kLaChunk + tile_of(i);
-                const auto m = buffer_of(marks + ((tile * p.H + w.h) * p.P + w.p0) * N, i < tiles ? PB * N * (int)sizeof(T) : 0);
                 float x = 0.f;
                 if constexpr (kMarks) whole.put(s_own[wave]);
 #pragma unroll
@@ -163,11 +163,17 @@ __global__ __launch_bounds__(kLaThreads) void la_sweep_kernel(const LaArgs p, co
                 load_mark(i + 1);
                 const auto c = buffer_of(both + ((tile * p.H + w.h) * (p.P / PB) + w.p0 / PB) * 4, both && i < tiles ? 16 : 0);
                 __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(x), c, lane == 0 ? 4 * wave : kNowhere, 0, 0);
-                store_mark<T, N>(s_own[wave], st, m, ptile, n0);
+                if constexpr (sizeof(T) == 2) {
+                    pack_adjoint(st, g, h);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) h[n] = st[n];
+                }
             }
             if (kSegment) total += d.sum;
             move_state<T, NT>(st, s_k[buf] + n0, SK::kStride, s_v[buf] + ptile, SV::kStride, kReverse ? d.up : d.down,
                               kReverse ? p.scale : 1.f, d.all, any_odd(d.odd), g, l16);
+            if (!kSegment) store_mark<T, N>(s_own[wave], h, m, ptile, n0);
             if (BUF == 1) __syncthreads();
         }
     } else if (turns > 0) {
@@ -466,9 +472,9 @@ __global__ __launch_bounds__(kLaThreads) void la_fwd_kernel(const LaArgs p) {
                     }
                     *reinterpret_cast<f32x4*>(sm.x[buf][wave % 4 / PT] + (16 * j + l16) * Shared::kXStride + ptile + 4 * g) = x;
                 }
-                f32x4 was[NT];
+                typename M::Half was[NT];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) was[n] = st[n];
+                for (int n = 0; n < NT; ++n) was[n] = M::half(st[n]);
                 move_state<T, NT>(st, sk + n0, SK::kStride, sv + ptile, SV::kStride, d.down, 1.f, d.all, odd, g, l16);
                 const auto m = buffer_of(static_cast<T*>(p.ckpt) +
                                              (((row.ckpt + begin / kLaChunk + c) * p.H + w.h) * p.P + w.p0) * N,

@@ -32,7 +32,7 @@ struct LaBwdShared {
     typedef LaBwdStage<T, PB> SV;
     T q[kLaChunk * SK::kStride], k[kLaChunk * SK::kStride];
     T v[kLaChunk * SV::kStride], dy[kLaChunk * SV::kStride];
-    T s[PB * SK::kStride], ds[PB * SK::kStride];   // [p][n]
+    T s[PB * SK::kStride], ds[LaMat<T>::kTerms][PB * SK::kStride];   // [p][n]; ds in terms
     // A wave's results on their way to whole rows (fp32 rows go there by themselves).
     T own[sizeof(T) == 2 ? 12 : 1][sizeof(T) == 2 ? LaRows16<T, (N > PB ? N : PB)>::kSize : 16];
     LaDecay d[2];                                  // of this head and the next
@@ -64,6 +64,27 @@ struct LaStateStage {
         for (int i = 0; i < (kLoads > 0 ? kLoads : 1); ++i) {
             const int at = piece(i);
             *reinterpret_cast<vu4*>(lds + at / kPieces * kStride + at % kPieces * (16 / (int)sizeof(T))) = w[i];
+        }
+    }
+    // An adjoint state as the sweep leaves it, in terms.
+    vu4 term[sizeof(T) == 2 ? (kLoads > 0 ? kLoads : 1) : 1][2];
+    __device__ __forceinline__ void unpack() {
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < (kLoads > 0 ? kLoads : 1); ++i) unpack_adjoint(w[i], term[i]);
+        }
+    }
+    __device__ __forceinline__ void store_terms(T (&lds)[LaMat<T>::kTerms][PB * kStride]) const {
+        if constexpr (sizeof(T) == 4) {
+            store(lds[0]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < (kLoads > 0 ? kLoads : 1); ++i)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int at = piece(i);
+                    *reinterpret_cast<vu4*>(lds[e] + at / kPieces * kStride + at % kPieces * 8) = term[i][e];
+                }
         }
     }
 };
@@ -300,6 +321,7 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
         const int n_in = u.n_in, n_out = u.n_out;
         const bool in = t < n_in;
         const bool head_first = first_of_head(u), head_last = ((u.step + 1) & (pblocks - 1)) == 0;
+        if constexpr (kRole != kDq) rd.unpack();
         __syncthreads();   // the tiles before have been read
         if (u.step == 0) {
             if constexpr (kRole != kDq) {
@@ -316,7 +338,7 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
             rv.store(sm.v);
             ry.store(sm.dy);
             rs.store(sm.s);
-            rd.store(sm.ds);
+            rd.store_terms(sm.ds);
             const bool odd_lane = __builtin_amdgcn_ballot_w64(odd_qk || rv.odd() || ry.odd()) != 0;
             if (lane == 0) sm.odd[wave - 4] = odd_lane;
         }
@@ -456,8 +478,10 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
             for (int n = 0; n < NT; ++n) {
                 f32x4 x = zero4();
 #pragma unroll
-                for (int j = 0; j < PS; ++j)
-                    x = M::mma(columns<T>(sm.ds + 32 * j * SK::kStride + 16 * n, SK::kStride, g, l16), vf[j], x);
+                for (int e = M::kTerms - 1; e >= 0; --e)
+#pragma unroll
+                    for (int j = 0; j < PS; ++j)
+                        x = M::mma(columns<T>(sm.ds[e] + 32 * j * SK::kStride + 16 * n, SK::kStride, g, l16), vf[j], x);
                 x *= down;
                 const f32x4 kn = M::wide(M::four(sm.k + t * SK::kStride + 16 * n + 4 * g));
 #pragma unroll
@@ -509,8 +533,10 @@ __global__ __launch_bounds__(kBwdThreads) void la_bwd_kernel(const LaBwdArgs o, 
             for (int m = 0; m < PT; ++m) {
                 dv[m] = zero4();
 #pragma unroll
-                for (int j = 0; j < KS; ++j)
-                    dv[m] = M::mma(M::rows(sm.ds + (16 * m + l16) * SK::kStride + 32 * j + 8 * g), kf[j], dv[m]);
+                for (int e = M::kTerms - 1; e >= 0; --e)
+#pragma unroll
+                    for (int j = 0; j < KS; ++j)
+                        dv[m] = M::mma(M::rows(sm.ds[e] + (16 * m + l16) * SK::kStride + 32 * j + 8 * g), kf[j], dv[m]);
                 dv[m] *= down;
             }
             if (!odd) {

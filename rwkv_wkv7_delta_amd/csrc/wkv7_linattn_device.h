@@ -355,8 +355,10 @@ struct LaRows16 {
         }
         settle();
     }
-    // Results [w][row] (row l16, columns 16 i + 4 g ..) of the rows row0 .. to memory.
-    static __device__ __forceinline__ void store(T* lds, const f32x4 (&x)[W / 16], __amdgpu_buffer_rsrc_t r,
+    // Results [w][row] (row l16, columns 16 i + 4 g ..) of the rows row0 .. to memory; of 32 bits
+    // (rounded) or as halves.
+    template <typename X>
+    static __device__ __forceinline__ void store(T* lds, const X (&x)[W / 16], __amdgpu_buffer_rsrc_t r,
                                                  uint32_t row_bytes, int row0) {
         const int lane = threadIdx.x % 64, g = lane / 16, l16 = lane % 16;
         settle();
@@ -372,10 +374,11 @@ struct LaRows16 {
     }
 };
 
-// The 16 value rows that a wave holds of a state, columns n0 .. of N, to a checkpoint of PB
-// rows (a buffer of them, or of nothing).
+// The 16 value rows that a wave holds of a state, as halves, columns n0 .. of N, to a
+// checkpoint of PB rows (a buffer of them, or of nothing).
 template <typename T, int N, int NT>
-__device__ __forceinline__ void store_mark(T* lds, const f32x4 (&st)[NT], __amdgpu_buffer_rsrc_t r, int ptile, int n0) {
+__device__ __forceinline__ void store_mark(T* lds, const typename LaMat<T>::Half (&st)[NT], __amdgpu_buffer_rsrc_t r,
+                                           int ptile, int n0) {
     if constexpr (16 * NT == N && sizeof(T) == 2) {
         LaRows16<T, N>::store(lds, st, r, N * sizeof(T), ptile);
     } else {
@@ -384,9 +387,87 @@ __device__ __forceinline__ void store_mark(T* lds, const f32x4 (&st)[NT], __amdg
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             if constexpr (sizeof(T) == 2)
-                __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(vu2, cvt4(st[n])), r, at + 32 * n, 0, 0);
+                __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(vu2, st[n]), r, at + 32 * n, 0, 0);
             else
                 __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(vu4, st[n]), r, at + 64 * n, 0, 0);
+        }
+    }
+}
+
+// ---- adjoint states between the backward's kernels ------------------------------------
+// With bf16 tokens a workspace of the checkpoints' size holds the gradients of the states, 16
+// bits a value, and one bf16 would leave dk and dv 1.4 times as wrong as their own rounding.
+// Eight neighbours along a row share an exponent instead: each is a half (relative to the
+// largest, which becomes 2^14 up to 2^15) whose last bit gives place to one bit of the 8 of
+// that exponent.  Ten significant bits down to 2^-28 of the largest of the eight, 2^-38 of
+// that below.  Where one of the eight is not finite (exponent 255) each is a bf16 instead; where
+// all are below 2^-112 they are read as such; below 2^-126 (exponent 0) they are zeros.
+constexpr int kAdjointBias = 127 + 14;
+constexpr uint32_t kAdjointBits = 0x00010001u;   // in the word of two
+
+// As the lanes hold state rows: eight are four of lane row g and four of lane row g + 1 (g even).
+template <int NT>
+__device__ __forceinline__ void pack_adjoint(const f32x4 (&x)[NT], int g, bf16x4 (&to)[NT]) {
+    uint32_t e[NT];
+    vu2 w[NT];
+    bool odd = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        // (the maximum that keeps a NaN)
+        const float m = __builtin_elementwise_maximum(
+            __builtin_elementwise_maximum(__builtin_elementwise_maximum(fabsf(x[n][0]), fabsf(x[n][1])), fabsf(x[n][2])),
+            fabsf(x[n][3]));
+        const auto both = __builtin_amdgcn_permlane16_swap(__float_as_uint(m), __float_as_uint(m), false, false);
+        e[n] = (both[0] > both[1] ? both[0] : both[1]) >> 23;
+        odd |= e[n] == 255;
+        const int by = e[n] == 0 ? -300 : kAdjointBias - (int)e[n];
+        // Cut off to eleven bits; with one added, the ten above the last are the nearest.
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            w[n][i] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(
+                          __builtin_ldexpf(x[n][2 * i], by), __builtin_ldexpf(x[n][2 * i + 1], by))) + kAdjointBits;
+    }
+    if (__builtin_amdgcn_ballot_w64(odd) != 0) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) w[n][i] = e[n] == 255 ? cvt2(x[n][2 * i], x[n][2 * i + 1]) : w[n][i];
+    }
+    // Bit j of the exponent to element j: bits 0 and 16 of each word.
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const uint32_t spread = (e[n] | e[n] << 15) >> 4 * (g & 1);
+        w[n][0] = (spread & kAdjointBits) | (w[n][0] & ~kAdjointBits);
+        w[n][1] = (spread >> 2 & kAdjointBits) | (w[n][1] & ~kAdjointBits);
+        to[n] = __builtin_bit_cast(bf16x4, w[n]);
+    }
+}
+
+// Eight packed values as two terms in the matrix cores' type, which hold their ten bits: the
+// first eight of them, and the rest.
+__device__ __forceinline__ void unpack_adjoint(const vu4& d, vu4 (&term)[2]) {
+    const uint32_t s = (d[0] & kAdjointBits) | (d[1] & kAdjointBits) << 2 | (d[2] & kAdjointBits) << 4 |
+                       (d[3] & kAdjointBits) << 6;
+    const int e = (int)((s | s >> 15) & 255u);
+    const float scale = __uint_as_float((uint32_t)(e - (kAdjointBias - 127)) << 23);
+    typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const h2 all = __builtin_bit_cast(h2, d[i] & 0xfffefffeu), top = __builtin_bit_cast(h2, d[i] & 0xfff8fff8u);
+        const float a = fmaf((float)top[0], scale, 0.f), b = fmaf((float)top[1], scale, 0.f);
+        term[0][i] = __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);   // the upper halves
+        term[1][i] = cvt2(fmaf((float)all[0], scale, -a), fmaf((float)all[1], scale, -b));
+    }
+    // bf16 values, and a scale that is no float (without values there is nothing to scale).
+    const bool tiny = (uint32_t)(e - 1) < kAdjointBias - 127;
+    if (__builtin_amdgcn_ballot_w64(e == 255 || tiny) != 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const h2 all = __builtin_bit_cast(h2, d[i] & 0xfffefffeu);
+            const float a = __builtin_ldexpf((float)all[0], e - kAdjointBias), b = __builtin_ldexpf((float)all[1], e - kAdjointBias);
+            const uint32_t one = cvt2(a, b);
+            term[0][i] = e == 255 ? d[i] & 0xfffefffeu : tiny ? one : term[0][i];
+            term[1][i] = e == 255 || tiny ? 0u : term[1][i];
         }
     }
 }

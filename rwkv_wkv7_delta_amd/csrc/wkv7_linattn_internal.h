@@ -43,7 +43,7 @@ struct LaBwdArgs {
     const float* dsT;           // may be null
     void *dq, *dk, *dv, *dg;    // dg null with constant decays
     float* ds0;                 // may be null
-    void* adj;                  // gradient of the state behind every tile, laid out as the checkpoints
+    void* adj;                  // gradient of the state behind every tile, laid out as the checkpoints (bf16: pack_adjoint)
     // Parts of <S, D> of every tile and head, fp32 [tiles][H][value blocks][4]; null without dg.
     float* both;
     // Heads of a group in `split` parts (1: none), each with its own partial sums

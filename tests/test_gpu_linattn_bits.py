@@ -34,3 +34,66 @@ def test_gradients_within_a_tile(wk, T, H, G, N, P):
     want = ref.reference(*ins, s0=s0, dy=dy, dsT=dsT, **rows_kw(kw))
     for name in ("dq", "dk", "dv", "dg"):
         ref.assert_within(getattr(g, name), want[name], t, 4 * ref.roundings(T, N, P), name, INNER)
+
+
+def off(got, want):
+    """How much farther from the definition than its own values rounded once, in 2-norms."""
+    import torch
+    want = want[0]
+    on = ~torch.isnan(want)
+    want, got = want[on], got.double().cpu()[on]
+    return float((got - want).norm() / (want.to(torch.bfloat16).double() - want).norm())
+
+
+@pytest.mark.parametrize("B,T,H,G,N,P,state", [(2, 200, 4, 4, 64, 64, True), (1, 130, 3, 1, 128, 128, True),
+                                               (2, 300, 4, 2, 32, 32, True), (1, 700, 2, 2, 64, 32, False),
+                                               (1, 256, 2, 2, 128, 32, True), (1, 900, 3, 3, 32, 64, False)])
+def test_gradients_over_tiles(wk, B, T, H, G, N, P, state):
+    """Between tiles the gradients of states keep ten bits, two more than outputs: 1 / 16 of their
+    squared error.  dq and dg are from the states of the checkpoints, which hold eight."""
+    ins, s0, dy, dsT, kw = make(83, B, T, H, G, N, P, "bf16", state=state)
+    y, _, ck = wk.linattn_forward(*ins, s0=s0, want_ckpt=True, **kw)
+    g = wk.linattn_backward(*ins, dy, ck, dsT=dsT, **kw)
+    want = ref.reference(*ins, s0=s0, dy=dy, dsT=dsT, **rows_kw(kw))
+    for name in ("dk", "dv"):
+        # 2^-10, and 2^-12 for the two steps of its rounding, in half steps of bf16
+        ref.assert_within(getattr(g, name), want[name], ins[2].dtype, 2 * ref.roundings(T, N, P), name, 1.25 / 4 + INNER)
+        assert off(getattr(g, name), want[name]) < 1.1, name
+    assert off(y, want["y"]) < 1.01
+
+
+@pytest.mark.parametrize("N,P", [(64, 64), (32, 32), (128, 64), (32, 128)])
+def test_gradients_of_states_far_apart(wk, N, P):
+    """Neighbours in a row of D that differ by up to 2^28, whole rows by any factor, zeros among them."""
+    import torch
+    ins, s0, dy, dsT, kw = make(84, 2, 70, 2, 1, N, P, "bf16")
+    gen = torch.Generator().manual_seed(1)
+    dsT = dsT * torch.exp2(torch.randint(-27, 1, dsT.shape, generator=gen)).cuda()
+    dsT = dsT * torch.exp2(torch.randint(-60, 50, dsT.shape[:-1], generator=gen))[..., None].cuda()
+    dsT[0, 0, 3], dsT[1, 1, :, 5] = 0.0, 0.0
+    ins[3][:] = -1e-3
+    dy = torch.zeros_like(dy)
+    _, _, ck = wk.linattn_forward(*ins, s0=s0, want_ckpt=True, **kw)
+    g = wk.linattn_backward(*ins, dy, ck, dsT=dsT, **kw)
+    want = ref.reference(*ins, s0=s0, dy=dy, dsT=dsT, **rows_kw(kw))
+    for name in ("dk", "dv"):
+        ref.assert_within(getattr(g, name), want[name], ins[2].dtype, 2 * ref.roundings(70, N, P), name, 1.25 / 4 + INNER)
+
+
+@pytest.mark.parametrize("N,P", [(64, 64), (32, 32), (128, 64)])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_a_gradient_of_a_state_that_is_not_finite(wk, bad, N, P):
+    """It stays in its column of dk and its row of dv; beside it bf16's own bits but one are kept."""
+    import torch
+    ins, s0, dy, dsT, kw = make(85, 1, 64, 2, 2, N, P, "bf16")
+    _, _, ck = wk.linattn_forward(*ins, s0=s0, want_ckpt=True, **kw)
+    dsT[0, 1, 4, 9] = bad
+    g = wk.linattn_backward(*ins, dy, ck, dsT=dsT, **kw)
+    want = ref.reference(*ins, s0=s0, dy=dy, dsT=dsT, **rows_kw(kw))
+    for name in ("dk", "dv"):
+        value, mag = want[name]
+        fine = torch.isfinite(value)
+        got = getattr(g, name).double().cpu()
+        assert torch.equal(torch.isfinite(got), fine), name
+        hide = lambda x: torch.where(fine, x, 0.0)   # noqa: E731
+        ref.assert_within(hide(got), (hide(value), hide(mag)), ins[2].dtype, ref.roundings(64, N, P), name, 3)
