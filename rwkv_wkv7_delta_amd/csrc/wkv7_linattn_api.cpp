@@ -46,10 +46,11 @@ struct Plan {
 // which takes its tiles one after the other: where the workgroups are fewer than the compute
 // units, as many segments as fill them, if that is worth a first sweep over the states and
 // two more launches.  In tenths of a microsecond, measured where memory is not the limit: a
-// tile takes 20 (fp32 45) read out and 12 (20) in a sweep over states alone, the launches 150.
-// (1, 16384) tokens and 12 heads of 64 in bf16: 20 segments 55 us, 43 of them 65, 11 of them
-// 84; (4, 1024) tokens, 12 heads: forward in 5 segments 25 us, without 32, and the reverse
-// sweep 20 and 19.
+// tile takes 20 (fp32 45) read out, 17 (25) in the reverse sweep, which leaves its state (25
+// and 43 at N = 128), and 12 (20) in a sweep over states alone, the launches 150.
+// (1, 16384) tokens and 12 heads of 64 in bf16: 20 segments 57 us, 43 of them 67, 11 of them
+// 82; (4, 1024) tokens, 12 heads: forward in 5 segments 24 us, without 34, and the gradients
+// with their reverse sweep in 5 segments 42, without 48.
 Plan plan(const wkv7_linattn_desc* d, bool read_out) {
     const int64_t wgs = (int64_t)d->B * d->H * (d->P / wkv7::la_value_block(d->P)), tiles = blocks_of(longest(d));
     const Plan none{1, (int)(tiles * kLaChunk)};
@@ -59,7 +60,8 @@ Plan plan(const wkv7_linattn_desc* d, bool read_out) {
     if (n < 2) return none;
     const int64_t each = (tiles + n - 1) / n;
     n = (tiles + each - 1) / each;
-    const int64_t sweep = d->dtype == WKV7_BF16 ? 12 : 20, turn = !read_out ? sweep : d->dtype == WKV7_BF16 ? 20 : 45;
+    const bool bf16 = d->dtype == WKV7_BF16, wide = d->N == 128;
+    const int64_t sweep = bf16 ? 12 : 20, turn = read_out ? (bf16 ? 20 : 45) : bf16 ? (wide ? 25 : 17) : wide ? 43 : 25;
     if (n < 2 || each * (sweep + turn) + 150 >= tiles * turn) return none;
     return Plan{(int)n, (int)(each * kLaChunk)};
 }

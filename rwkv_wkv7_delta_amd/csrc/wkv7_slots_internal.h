@@ -18,7 +18,7 @@ struct SlotsArgs {
     const uint8_t* keep;
     int32_t *moved, *count;
     bool clear;
-    int32_t* pairs;              // scratch: [2 slots + 2] sources, targets, their number, the kept slots'
+    int32_t* pairs;              // scratch: [2 slots + 1] sources, targets, their number
 };
 
 hipError_t launch_slots_copy(const SlotsArgs& p, hipStream_t stream);

@@ -44,7 +44,7 @@ def _inputs(q, k, v, g, lead: int, scale: float):
     shape = tuple(v.shape[:-2]) + (G, N)
     _same(q, "q", shape, v.dtype, dev)
     _same(k, "k", shape, v.dtype, dev)
-    fixed = g.dtype == torch.float32 and g.dim() == 1 and lead > 0
+    fixed = g.dtype == torch.float32 and g.dim() == 1
     if fixed:
         _same(g, "g", (H,), torch.float32, dev)
     else:
