@@ -262,7 +262,7 @@ __global__ __launch_bounds__(256) void la_join_kernel(const LaArgs p, const floa
 // next product from registers (wkv7_linattn_device.h); the state is both kinds of operand as it
 // is held.  (Handed on through LDS for the others to read, in two bf16 terms, the prompts below
 // took 152 us where this takes 140: four waves each read all of it.)
-template <typename T, int N, int PB>
+template <typename T, int N, int PB, bool kMarks>
 struct LaFwdShared {
     typedef LaStage<T, N> SK;
     typedef LaStage<T, PB> SV;
@@ -277,17 +277,18 @@ struct LaFwdShared {
     T v[kBuffers][kLaChunk * SV::kStride];
     float x[kBuffers][kHalves][kLaChunk * kXStride];   // S q_t, [t][p]
     T own[4][LaRows16<T, PB>::kSize];   // a wave's results
-    T mark[4][sizeof(T) == 2 && PB == 64 ? LaRows16<T, N>::kSize : 8];   // a wave's state rows
+    T mark[4][kMarks && sizeof(T) == 2 && PB == 64 ? LaRows16<T, N>::kSize : 8];   // a wave's state rows
     LaDecay d[kBuffers];
 };
 
-template <typename T, int N, int PB>
+// (kMarks: with checkpoints.)
+template <typename T, int N, int PB, bool kMarks>
 __global__ __launch_bounds__(kLaThreads) void la_fwd_kernel(const LaArgs p) {
     typedef LaMat<T> M;
     typedef LaStage<T, N> SK;
     typedef LaStage<T, PB> SV;
     typedef LaRows16<T, N> SQ;
-    typedef LaFwdShared<T, N, PB> Shared;
+    typedef LaFwdShared<T, N, PB, kMarks> Shared;
     typedef typename M::Frag Frag;
     constexpr int PT = PB / 16, NT = N / 16 * PT / 4, KS = N / 32, BUF = Shared::kBuffers;
     __shared__ __attribute__((aligned(16))) Shared sm;
@@ -333,15 +334,30 @@ __global__ __launch_bounds__(kLaThreads) void la_fwd_kernel(const LaArgs p) {
         Frag qf[KS];
         f32x4 o[PT];
         float tup = 0.f;
-        auto load = [&](int c, Ahead& r) {
-            const int n = tokens_of(c, end);
-            const int64_t at = row.first + begin + (int64_t)c * kLaChunk;
-            r.k.load(rows_of(static_cast<const T*>(p.k) + at * krow + kh * N, n, krow, N), kb);
-            r.v.load(rows_of(static_cast<const T*>(p.v) + at * vrow + (int64_t)w.h * p.P + w.p0, n, vrow, PB), vb);
+        // Where the next tile to be loaded is, the next one to be stored, and the next state;
+        // the tokens from there on.  Kept from turn to turn: formed anew from the tile's number
+        // they were a sixth of a wave's instructions.
+        int64_t at = row.first + begin;
+        int left = end - (int)begin;
+        const int64_t kat = at * krow + kh * N, vat = at * vrow + (int64_t)w.h * p.P + w.p0;
+        const T* at_k = static_cast<const T*>(p.k) + kat;
+        const T* at_q = static_cast<const T*>(p.q) + kat;
+        const T* at_v = static_cast<const T*>(p.v) + vat;
+        T* at_y = Y + vat;
+        T* at_mark = static_cast<T*>(p.ckpt) + (((row.ckpt + begin / kLaChunk) * p.H + w.h) * p.P + w.p0) * N;
+        auto load = [&](Ahead& r) {
+            const int n = left < 0 ? 0 : left < kLaChunk ? left : kLaChunk;
+            r.k.load(rows_of(at_k, n, krow, N), kb);
+            r.v.load(rows_of(at_v, n, vrow, PB), vb);
             if constexpr (kReads) {
-                r.q.load(rows_of(static_cast<const T*>(p.q) + at * krow + kh * N, n, krow, N), kb, 16 * wave);
-                r.g.load(p, at, w.h, n);
+                r.q.load(rows_of(at_q, n, krow, N), kb, 16 * wave);
+                if constexpr (kBlocks == 1) r.g.load(p, at, w.h, n);
             }
+            at += kLaChunk;
+            at_k += kLaChunk * krow;
+            at_q += kLaChunk * krow;
+            at_v += kLaChunk * vrow;
+            left -= kLaChunk;
         };
         auto put = [&](int buf, const Ahead& r) {
             r.k.store(sm.k[buf]);
@@ -360,7 +376,6 @@ __global__ __launch_bounds__(kLaThreads) void la_fwd_kernel(const LaArgs p) {
         // first tile: no rows).
         auto finish = [&](int c, int buf) {
             const int n_in = tokens_of(c, end), n_out = c < 0 ? 0 : tokens_of(c, zero_end);
-            const int64_t at = row.first + begin + (int64_t)c * kLaChunk;
 #pragma unroll
             for (int pt = 0; pt < PT; ++pt) {
                 const float* const x1 = sm.x[buf][0] + t * Shared::kXStride + 16 * pt + 4 * g;
@@ -376,7 +391,8 @@ __global__ __launch_bounds__(kLaThreads) void la_fwd_kernel(const LaArgs p) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) o[pt][q] = t < n_in ? o[pt][q] : 0.f;
             LaRows16<T, PB>::store(sm.own[wave % 4], o,
-                                   rows_of(Y + at * vrow + (int64_t)w.h * p.P + w.p0, n_out, vrow, PB), vb, 16 * wave);
+                                   rows_of(at_y, n_out, vrow, PB), vb, 16 * wave);
+            at_y += c < 0 ? 0 : kLaChunk * vrow;
         };
         auto turn = [&](int c, Ahead& r) {
             const int buf = BUF == 2 ? c & 1 : 0, nxt = BUF == 2 ? buf ^ 1 : 0;
@@ -476,17 +492,17 @@ __global__ __launch_bounds__(kLaThreads) void la_fwd_kernel(const LaArgs p) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) was[n] = M::half(st[n]);
                 move_state<T, NT>(st, sk + n0, SK::kStride, sv + ptile, SV::kStride, d.down, 1.f, d.all, odd, g, l16);
-                const auto m = buffer_of(static_cast<T*>(p.ckpt) +
-                                             (((row.ckpt + begin / kLaChunk + c) * p.H + w.h) * p.P + w.p0) * N,
-                                         p.ckpt && c < tiles ? PB * N * (int)sizeof(T) : 0);
-                store_mark<T, N>(sm.mark[wave - 4], was, m, ptile, n0);
+                if constexpr (kMarks) {
+                    store_mark<T, N>(sm.mark[wave - 4], was, buffer_of(at_mark, c < tiles ? PB * N * (int)sizeof(T) : 0), ptile, n0);
+                    at_mark += (int64_t)p.H * p.P * N;
+                }
             }
             if (BUF == 1) {
                 __syncthreads();
                 if constexpr (kReads) finish(c, 0);
             }
             put(nxt, r);
-            load(c + (kDeep ? 3 : 2), r);
+            load(r);
         };
         if constexpr (!kReads) {
 #pragma unroll
@@ -500,10 +516,10 @@ __global__ __launch_bounds__(kLaThreads) void la_fwd_kernel(const LaArgs p) {
         }
         if (tiles > 0) {
             Ahead even, odd_;
-            load(0, even);
-            if (kDeep) load(1, odd_);
+            load(even);
+            if (kDeep) load(odd_);
             put(0, even);
-            load(kDeep ? 2 : 1, even);
+            load(even);
             // Deep: by twos, the last perhaps a tile without tokens, which changes nothing.
             int c = 0;
             for (; c < tiles; c += kDeep ? 2 : 1) {
@@ -601,7 +617,8 @@ hipError_t fwd_block(const LaArgs& p, hipStream_t stream) {
         la_join_kernel<<<(unsigned)(((size_t)p.B * p.H * p.P * N / 4 + 255) / 256), 256, 0, stream>>>(p, p.s0);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    la_fwd_kernel<T, N, PB><<<blocks * p.nseg, kLaThreads, 0, stream>>>(p);
+    if (p.ckpt) la_fwd_kernel<T, N, PB, true><<<blocks * p.nseg, kLaThreads, 0, stream>>>(p);
+    else la_fwd_kernel<T, N, PB, false><<<blocks * p.nseg, kLaThreads, 0, stream>>>(p);
     return hipGetLastError();
 }
 
