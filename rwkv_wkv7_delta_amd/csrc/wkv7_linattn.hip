@@ -9,11 +9,12 @@
 //   S  <- e^{G_end} S + sum_s (e^{G_end - G_s} v_s) k_s^T
 // which are plain matrix products: a scalar decay only scales their rows.
 //
-// Bound by HBM with as many workgroups as compute units: (8, 4096) tokens, 32 heads of 64,
-// bf16: 125 us, 4.3 TB/s; reading and writing the same bytes in the same order, without
-// arithmetic, takes 123.  With fewer, by a tile's chain of products, exponentials and one
-// barrier, 2.4 us (fp32, N = 32, 5).  64 tokens a tile: at N = P = 64 its products with the
-// state and within itself are as much work as each other.
+// With as many workgroups as compute units, bound by HBM and by the waves' own instructions
+// alike: (8, 4096) tokens, 32 heads of 64, bf16: 126 to 130 us, 4.2 TB/s; reading and writing
+// the same bytes in the same order, without arithmetic, takes 123.  With fewer, by a tile's
+// products, exponentials and one barrier, 1.9 to 2.4 us (fp32, N = 32, P = 128: 4.2).  64 tokens a
+// tile: at N = P = 64 its products with the state and within itself are as much work as each
+// other.
 
 #include "wkv7_linattn_device.h"
 
@@ -55,7 +56,7 @@ __device__ __forceinline__ float* state_at(float* base, const LaArgs& p, int b, 
 }
 
 // ---- the sweep over states alone ------------------------------------------------
-// (8, 4096) tokens, 40 heads of 64, bf16, in reverse with checkpoints: 194 us, 3.5 TB/s (what
+// (8, 4096) tokens, 40 heads of 64, bf16, in reverse with checkpoints: 197 us, 3.4 TB/s (what
 // 320 workgroups on 256 units reach in this order).
 // Forward (kReverse = false): S from k and v; reverse: its gradient D, from q and
 // dy: D <- e^{G_end} D + scale sum_t (e^{G_t} dy_t) q_t^T.
@@ -260,8 +261,8 @@ __global__ __launch_bounds__(256) void la_join_kernel(const LaArgs p, const floa
 // itself: wave w the tokens 16 w .. , to which it adds what the others read from the state, and
 // stores them.  Results are formed transposed, [s][t], [p][t], [n][p], so that each feeds the
 // next product from registers (wkv7_linattn_device.h); the state is both kinds of operand as it
-// is held.  (Handed on through LDS for the others to read, in two bf16 terms, the prompts below
-// took 152 us where this takes 140: four waves each read all of it.)
+// is held.  (Handed on through LDS for the others to read, in two bf16 terms, it cost 12 us of the
+// prompts above: four waves each read all of it.)
 template <typename T, int N, int PB, bool kMarks>
 struct LaFwdShared {
     typedef LaStage<T, N> SK;
@@ -554,7 +555,9 @@ __global__ __launch_bounds__(kLaThreads) void la_fwd_kernel(const LaArgs p) {
 // ---- one token ------------------------------------------------------------------
 // N / 4 lanes per state row, four columns each; 4096 / N rows a workgroup (four of
 // a lane's 16-byte loads in flight).  Bound by the states' bytes: 256 rows of 40 heads of
-// 64 x 64 take 73 us, 4.6 TB/s.
+// 64 x 64 take 73 us, 4.6 TB/s.  With slots every wave looks through the rows before its own
+// for the same slot: 256, 4096 and 65536 rows of one head of 32 x 32 take 12, 21 and 2240 us,
+// without slots 11, 12 and 98.
 template <typename T, int N>
 __global__ __launch_bounds__(256) void la_step_kernel(const LaStepArgs p) {
     constexpr int kLanes = N / 4, kRows = 4096 / N, kEach = 256 / kLanes;

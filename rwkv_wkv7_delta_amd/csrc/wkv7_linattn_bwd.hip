@@ -11,9 +11,10 @@
 // with M_is = W_is (q_i . k_s)(dy_i . v_s), a_i = q_i . (the state's part of dq_i),
 // b_s = k_s . (D's part of dk_s): sums within the tile only, however long the row is.
 //
-// (8, 4096) tokens, 40 heads of 64, bf16: 366 to 400 us, 3.9 TB/s, behind a sweep of 194.  Bound
+// (8, 4096) tokens, 40 heads of 64, bf16: 377 to 415 us, 3.8 TB/s, behind a sweep of 197.  Bound
 // by HBM and by the waves' own work (products, LDS, addresses), which overlap in part: with dk
-// and dv on the same waves 527 us, of which the arithmetic alone took 394, the bytes alone 352.
+// and dv on the same waves 527 us, of which the arithmetic alone took 394, the bytes alone 352
+// (with weights and D in one bf16 term each; the second terms add 10 us, unpacking D 12).
 
 #include "wkv7_linattn_device.h"
 
