@@ -694,7 +694,7 @@ int wkv7_linattn_backward(const wkv7_linattn_desc* desc, const int32_t* rows, co
 
 /* Packed rows: zeros in the places of tokens that no row has, which the calls above leave as
    they were.  values: y or dv; queries: dq; keys: dk; decays: dg; each may be NULL.  Touches
-   no place of a row's token; in any order with the calls above. */
+   no place of a row's token; in any order with the calls above (starts do not fall). */
 int wkv7_linattn_clear_rest(const wkv7_linattn_desc* desc, const int32_t* starts, void* values, void* queries,
                             void* keys, void* decays, void* stream);
 

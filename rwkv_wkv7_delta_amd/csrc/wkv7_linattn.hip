@@ -334,6 +334,8 @@ __global__ __launch_bounds__(kLaThreads) void la_fwd_kernel(const LaArgs p) {
         const int t = 16 * wave + l16;   // the read-out's token
         Frag qf[KS];
         f32x4 o[PT];
+#pragma unroll
+        for (int pt = 0; pt < PT; ++pt) o[pt] = zero4();
         float tup = 0.f;
         // Where the next tile to be loaded is, the next one to be stored, and the next state;
         // the tokens from there on.  Kept from turn to turn: formed anew from the tile's number

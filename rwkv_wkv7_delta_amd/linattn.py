@@ -80,7 +80,7 @@ def _ckpt_shape(d):
 
 
 def _clear_rest(d, starts, dev, values, queries=None, keys=None, decays=None):
-    """Zeros where a packed call writes nothing."""
+    """Zeros where the packed call that follows writes nothing."""
     if d.packed:
         _call("wkv7_linattn_clear_rest", dev, ctypes.byref(d), _ptr(starts), _ptr(values), _ptr(queries), _ptr(keys),
               _ptr(decays))
@@ -109,10 +109,10 @@ def linattn_forward(q, k, v, g, *, s0=None, lengths=None, starts=None, max_len=N
     sT = torch.empty(state, device=dev, dtype=torch.float32) if want_state else None
     ckpt = torch.empty(_ckpt_shape(d), device=dev, dtype=v.dtype) if want_ckpt else None
     ws, wsb, _held = _scratch(workspace, lib().wkv7_linattn_forward_workspace_bytes(ctypes.byref(d)), dev)
-    _call("wkv7_linattn_forward", dev, ctypes.byref(d), _ptr(rows), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(s0),
-          _ptr(y), _ptr(sT), _ptr(ckpt), ws, wsb)
     if out is None:
         _clear_rest(d, rows, dev, y)
+    _call("wkv7_linattn_forward", dev, ctypes.byref(d), _ptr(rows), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(s0),
+          _ptr(y), _ptr(sT), _ptr(ckpt), ws, wsb)
     return y, sT, ckpt
 
 
@@ -132,9 +132,9 @@ def linattn_backward(q, k, v, g, dy, ckpt, *, dsT=None, lengths=None, starts=Non
     grads = LinattnGrads(new(q), new(k), new(v), None if d.fixed_decay else new(g),
                          torch.empty(state, device=dev, dtype=torch.float32) if want_ds0 else None)
     ws, wsb, _held = _scratch(workspace, lib().wkv7_linattn_backward_workspace_bytes(ctypes.byref(d)), dev)
+    _clear_rest(d, rows, dev, grads.dv, grads.dq, grads.dk, grads.dg)
     _call("wkv7_linattn_backward", dev, ctypes.byref(d), _ptr(rows), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(dy),
           _ptr(dsT), _ptr(ckpt), *[_ptr(x) for x in grads], ws, wsb)
-    _clear_rest(d, rows, dev, grads.dv, grads.dq, grads.dk, grads.dg)
     return grads
 
 

@@ -97,3 +97,18 @@ def test_a_gradient_of_a_state_that_is_not_finite(wk, bad, N, P):
         assert torch.equal(torch.isfinite(got), fine), name
         hide = lambda x: torch.where(fine, x, 0.0)   # noqa: E731
         ref.assert_within(hide(got), (hide(value), hide(mag)), ins[2].dtype, ref.roundings(64, N, P), name, 3)
+
+
+@pytest.mark.parametrize("power", [-100, -111, -114, -120, -124])
+def test_gradients_of_tiny_states(wk, power):
+    """Down to where a float's own exponents end, below 2^-112 to bf16's eight bits."""
+    import torch
+    ins, s0, dy, dsT, kw = make(86, 1, 64, 2, 2, 64, 64, "bf16", state=True)
+    ins[2].mul_(2.0 ** 100)
+    dsT = torch.ldexp(dsT.clamp(-0.9, 0.9), torch.tensor(power).cuda())
+    s0, dy = torch.zeros_like(s0), torch.zeros_like(dy)
+    _, _, ck = wk.linattn_forward(*ins, s0=s0, want_ckpt=True, **kw)
+    g = wk.linattn_backward(*ins, dy, ck, dsT=dsT, **kw)
+    want = ref.reference(*ins, s0=s0, dy=dy, dsT=dsT, **rows_kw(kw))
+    ref.assert_within(g.dk, want["dk"], ins[2].dtype, ref.roundings(64, 64, 64), "dk", 1 + INNER)
+    assert off(g.dk, want["dk"]) < (1.1 if power > -111 else 2)

@@ -92,3 +92,14 @@ def test_a_length_that_is_overstated(wk, max_len):
         want, got = got, (y, sT, *wk.linattn_backward(*ins, dy, ck, **rows))
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+def test_starts_that_fall(wk):
+    """What the rows' tokens get is not touched, also where starts fall, which they may not."""
+    import torch
+    ins, _, _, _, kw = make(44, 1, 128, 2, 2, 32, 32, "fp32")
+    ins = [x[0] for x in ins]
+    dev = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")   # noqa: E731
+    want, _, _ = wk.linattn_forward(*ins, starts=dev([0, 100]), max_len=100)
+    y, _, _ = wk.linattn_forward(*ins, starts=dev([0, 100, 50]), max_len=100)
+    assert torch.equal(y[:100], want[:100]) and bool((y[100:] == 0).all())
